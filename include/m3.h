@@ -297,6 +297,145 @@ M3_API m3_status m3_scan_fwd_noalloc(const m3_dims* dims, const m3_inputs* in,
                                      const m3_state* init, const m3_state* final_state,
                                      void* y, void* stream);
 
+/* ---- Linear attention with a decay for each head ----
+ * The core's recurrence with a constant scalar decay per head, no rotation and heads, key and
+ * value sizes of the caller's choice: per sequence and head h, with a = e^{log_decay[h]},
+ *     S_t = a S_{t-1} + k_t v_t^T   (K x V, fp32; S_{-1} = the initial state or zero)
+ *     o_t = scale S_t^T q_t
+ * in chunked form for prompts (m3_linattn_fwd), one token at a time (m3_linattn_step), and its
+ * gradients (m3_linattn_bwd). log_decay <= 0 is the use in view; 0 (no decay) and -inf (every
+ * token sees itself alone) are exact, and a positive one grows as the formula says. It is a
+ * constant of the layer: there is no gradient with respect to it.
+ *
+ * Heads: log_decay sets H = nheads; q, k and v may each have fewer heads (a divisor of H), and
+ * head h reads head h / (H / heads) of that tensor: grouped keys and values, or queries and keys
+ * shared by all heads. Gradients of shared heads are summed in fp32 before they are rounded.
+ *
+ * Packed sequences: with cu_seqlens (device, int32, nseq + 1 values, ascending from >= 0), the
+ * tensors hold seqlen rows in all and sequence i is rows [cu_seqlens[i], cu_seqlens[i + 1]).
+ * Rows outside every sequence are not read as tokens and their outputs are left as they were.
+ * Values outside [0, seqlen] are clamped to it and a descending pair is an empty sequence.
+ * Sequences of length 0 and 1 are allowed: the state after an empty one is its initial state. */
+
+/* A tensor of rows [nseq][seqlen][heads][dim] by its strides, in elements; the last dimension is
+ * contiguous. With cu_seqlens the batch stride is not used. Any element-aligned pointer and any
+ * strides (0 for an input, to broadcast); outputs must not overlap one another or an input. */
+typedef struct {
+    void* data;
+    int64_t batch, token, head;
+} m3_view;
+
+typedef struct {
+    int64_t nseq;      /* sequences, >= 0                                                  */
+    int64_t seqlen;    /* tokens of each, >= 0, or with cu_seqlens the rows of the tensors */
+    int64_t nheads;    /* H >= 1                                                           */
+    int64_t qheads;    /* heads of q, k and v: each divides H                              */
+    int64_t kheads;
+    int64_t vheads;
+    int64_t kdim;      /* K in [1, 256]                                                    */
+    int64_t vdim;      /* V in [1, 256]                                                    */
+    int32_t in_dtype;  /* m3_dtype of q, k, v, o and their gradients                       */
+    float scale;       /* finite                                                           */
+} m3_linattn_dims;
+
+typedef struct {
+    m3_view q, k, v;            /* read only                                               */
+    const float* log_decay;     /* [H]                                                     */
+    const int32_t* cu_seqlens;  /* [nseq + 1], or NULL: every sequence has seqlen tokens   */
+} m3_linattn_inputs;
+
+/* Workspace bytes of m3_linattn_fwd and m3_linattn_bwd for these dims (packed: whether
+ * cu_seqlens will be given), 0 where none is needed or the dims are invalid. Few long sequences
+ * are cut into segments that run in parallel, and each segment's end state is kept here; the
+ * backward keeps per-head gradients of shared heads here too. Depends on the current device's
+ * SM count. Any content; calls that may overlap need workspaces of their own. */
+M3_API size_t m3_linattn_workspace_bytes(const m3_linattn_dims* dims, int packed);
+M3_API size_t m3_linattn_bwd_workspace_bytes(const m3_linattn_dims* dims, int packed);
+
+/* Prompts. init, final: fp32 [nseq, H, K, V], or NULL for zero / not wanted; final may be init.
+ * o: the output [nseq][seqlen][H][V] by its view, in_dtype. workspace: 256-byte aligned, at least
+ * m3_linattn_workspace_bytes (NULL where that is 0). bf16 tensors whose pointers and strides are
+ * multiples of 16 bytes run on the tensor cores for K <= 128 (chunks of 128 tokens; products of
+ * bf16 operands with fp32 accumulators, the state exact to fp32); every other call runs in fp32
+ * on the CUDA cores. Asynchronous on `stream`. */
+M3_API m3_status m3_linattn_fwd(const m3_linattn_dims* dims, const m3_linattn_inputs* in,
+                                const float* init, float* final_state, const m3_view* o,
+                                void* workspace, size_t ws_bytes, void* stream);
+
+/* One token of every sequence: dims->seqlen must be 1, cu_seqlens NULL; the views' token strides
+ * are not used. state_in, state_out: fp32 [nstates, H, K, V], 16-byte aligned; state_out may be
+ * state_in (in place) but must not overlap it otherwise. slots NULL: sequence i has state i
+ * (nstates >= nseq). slots [nseq] (device, int32): sequence i has state slots[i]; a slot outside
+ * [0, nstates) skips that sequence (its o row is left as it was), and states of no sequence are
+ * left as they were. Sequences of one call must have slots of their own: of two that share one,
+ * that state and the outputs of both are undefined. o: [nseq][.][H][V], in_dtype. fp32
+ * arithmetic throughout. */
+M3_API m3_status m3_linattn_step(const m3_linattn_dims* dims, const m3_linattn_inputs* in,
+                                 const float* state_in, float* state_out, int64_t nstates,
+                                 const int32_t* slots, const m3_view* o, void* stream);
+
+/* Gradients of sum(o * d_o) + <final state, dfinal> for the call of m3_linattn_fwd with the same
+ * dims, inputs and init:
+ *     dq_t = scale S_t d_o_t,   dk_t = R_t v_t,   dv_t = R_t^T k_t,   dinit = a R_0,
+ *     R_t = a R_{t+1} + scale q_t d_o_t^T   (R_T such that a R_T = dfinal)
+ * d_o: [nseq][seqlen][H][V]. dq, dk, dv: in_dtype, laid out by their views with the heads of q,
+ * k and v. dfinal, dinit: fp32 [nseq, H, K, V], or NULL for zero / not wanted; dinit may be
+ * dfinal. The same tensor-core condition as m3_linattn_fwd, with K, V <= 128. Results do not
+ * depend on the order of execution. */
+typedef struct {
+    m3_view dq, dk, dv;
+} m3_linattn_grads;
+M3_API m3_status m3_linattn_bwd(const m3_linattn_dims* dims, const m3_linattn_inputs* in,
+                                const float* init, const m3_view* d_o, const float* dfinal,
+                                const m3_linattn_grads* grads, float* dinit, void* workspace,
+                                size_t ws_bytes, void* stream);
+
+/* Whether a bounded wait inside a linear attention kernel gave up on the current device since the
+ * last check: M3_OK or M3_ERR_TIMEOUT (the outputs of that call are then incomplete). Blocks
+ * until the device's work is done; clears the mark. */
+M3_API m3_status m3_linattn_check(void);
+
+/* ---- Group norm over a row's channels (channels last) with an activation ----
+ * Every row of C channels is normalised in G groups of C / G consecutive channels:
+ *     y = (x - mean) / sqrt(var + eps) * weight + bias     (M3_GN_CENTER)
+ *     y = x / sqrt(mean(x^2) + eps) * weight + bias        (without it: RMS)
+ *     out = y act(z) with a gate z, act(y) without;  act = SiLU with M3_GN_SILU, else identity.
+ * This is what follows the core's and linear attention's output in a block: one group per head,
+ * gated by the block's second branch (the paper's optional pre-gate grouped norm and its SiLU
+ * gate, Y' = Y * SiLU(Z)). Statistics and arithmetic in fp32, one rounding at the end. */
+#define M3_GN_CENTER 1u
+#define M3_GN_SILU 2u
+
+typedef struct {
+    int64_t batch;     /* >= 0                                      */
+    int64_t rows;      /* rows of each batch entry, >= 0            */
+    int64_t channels;  /* C >= 1                                    */
+    int64_t groups;    /* G >= 1, divides C                         */
+    int32_t in_dtype;  /* m3_dtype of x, z, out and their gradients */
+    float eps;         /* finite, >= 0                              */
+    uint32_t flags;    /* M3_GN_CENTER | M3_GN_SILU                 */
+} m3_group_norm_dims;
+
+/* Tensors [batch][rows][G][C / G] by their strides (m3_view: batch, token = row, head = group), so
+ * that linear attention's output is read as it lies and slices of wider rows are taken too.
+ * x; z: the gate, or data NULL for none; out may be x or z (the same view), and outputs must not
+ * overlap themselves or other tensors otherwise. weight, bias: fp32 [C], or NULL for one / zero. */
+M3_API m3_status m3_group_norm_fwd(const m3_group_norm_dims* dims, const m3_view* x,
+                                   const m3_view* z, const float* weight, const float* bias,
+                                   const m3_view* out, void* stream);
+
+/* Workspace bytes of m3_group_norm_bwd, 0 for invalid dims. Any content. */
+M3_API size_t m3_group_norm_bwd_workspace_bytes(const m3_group_norm_dims* dims);
+
+/* Gradients of sum(out * dout): dx, dz (in_dtype; dz required with z, else not used), dweight and
+ * dbias (fp32 [C], or NULL if not wanted; weight NULL counts as all ones). Sums over rows run in
+ * a fixed order. dx may be x or dout, dz may be z. workspace: 256-byte aligned. */
+M3_API m3_status m3_group_norm_bwd(const m3_group_norm_dims* dims, const m3_view* x,
+                                   const m3_view* z, const float* weight, const float* bias,
+                                   const m3_view* dout, const m3_view* dx, const m3_view* dz,
+                                   float* dweight, float* dbias, void* workspace, size_t ws_bytes,
+                                   void* stream);
+
 /* Static description of a status code. */
 M3_API const char* m3_status_str(m3_status s);
 

@@ -1,0 +1,648 @@
+// Group norm over a row's channels with an activation or gate, and its gradients.
+//
+// Bound by HBM: the forward reads x (and z) and writes out, the backward reads x, dout (and z) and
+// writes dx (and dz), each once. A group lives in the registers of LPG lanes of one warp (NV
+// 16-byte vectors a lane), so the statistics are a few shuffles, the deviations are squared from
+// registers (no E[x^2] - mean^2 cancellation) and nothing is read twice. Groups too large, or rows
+// not 16-byte aligned, take one CTA per group with scalar loads. Statistics, sums and arithmetic
+// are fp32; each output is rounded once.
+//
+// Backward, with xh = (x - mean) r, y = xh w + b, s = act(z) or act(y):
+//     dy = dout s (gate) or dout act'(y),  dz = dout y act'(z),  g = dy w,
+//     dx = r (g - xh mean(g xh) - mean(g) [centred]),  dw = sum_rows dy xh,  db = sum_rows dy.
+// Threads keep their columns and walk down the rows, so dw and db are summed in registers; a CTA's
+// shares go to the workspace and a second launch adds them in a fixed order.
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+
+#include "m3_common.cuh"
+#include "m3_internal.h"
+
+namespace m3 {
+namespace {
+
+// A tensor [batch][rows][G][D] by its strides, in elements.
+struct GnTensor {
+    void* p;
+    int64_t batch, row, group;
+};
+struct GnParams {
+    uint32_t rows, inner;                   // rows in all, and of each batch entry
+    int C, G, D;
+    GnTensor x, z, out, dout, dx, dz;
+    const float *w, *b;
+    float *dw, *db;
+    float* part;                            // backward: [shares][2][C]
+    uint32_t share_rows;                    // rows of one share
+    int shares;
+    float eps;
+};
+
+// A group's first element. T may be const.
+template <typename T>
+__device__ __forceinline__ T* at(const GnTensor& t, const GnParams& p, uint32_t row, int group) {
+    const uint32_t b = p.inner == p.rows ? 0u : row / p.inner;
+    return static_cast<T*>(t.p) + b * t.batch + static_cast<int64_t>(row - b * p.inner) * t.row + group * t.group;
+}
+
+constexpr int kThreads = 256;
+
+template <typename T>
+struct Vec;   // 16 bytes of T as floats
+template <>
+struct Vec<float> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ void load(const float* p, float* f) {
+        const float4 v = *reinterpret_cast<const float4*>(p);
+        f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+    }
+    static __device__ __forceinline__ void store(float* p, const float* f) {
+        *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void load(const __nv_bfloat16* p, float* f) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* f) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+// 1 / (1 + e^-v); e^-v = inf gives 0
+__device__ __forceinline__ float sigmoid(float v) { return __frcp_rn(1.f + __expf(-v)); }
+template <bool kSilu>
+__device__ __forceinline__ float act(float v) { return kSilu ? v * sigmoid(v) : v; }
+// act(v) and its slope
+template <bool kSilu>
+__device__ __forceinline__ void act_slope(float v, float* a, float* da) {
+    if (!kSilu) { *a = v; *da = 1.f; return; }
+    const float s = sigmoid(v);
+    *a = v * s;
+    *da = s * fmaf(v, 1.f - s, 1.f);
+}
+
+// the sum over the LPG lanes that hold a group
+template <int LPG>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+    for (int o = LPG / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// mean (0 without centring) and 1 / sqrt(var + eps) of the group in v[NV][N]; lanes beyond the
+// group's end hold zeros and cnt[i] = 0
+template <int LPG, int NV, int N, bool kCenter>
+__device__ __forceinline__ void stats(float (&v)[NV][N], const bool (&in)[NV], float inv, float eps, float* r) {
+    if (kCenter) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < N; ++e) s += v[i][e];
+        const float m = group_sum<LPG>(s) * inv;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < N; ++e) v[i][e] = in[i] ? v[i][e] - m : 0.f;
+    }
+    float q = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < N; ++e) q = fmaf(v[i][e], v[i][e], q);
+    *r = rsqrtf(fmaf(group_sum<LPG>(q), inv, eps));
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[i][e] *= *r;
+}
+
+template <typename T, int LPG, int NV, bool kCenter, bool kSilu, bool kGate>
+__global__ void __launch_bounds__(kThreads) gn_fwd_kernel(const GnParams p) {
+    constexpr int N = Vec<T>::N;
+    const int lane = threadIdx.x % LPG;
+    const uint32_t unit = (blockIdx.x * kThreads + threadIdx.x) / LPG, G = static_cast<uint32_t>(p.G);
+    const bool live = unit < p.rows * G;        // a warp's lanes stay together for the shuffles
+    const uint32_t row = live ? unit / G : 0u;
+    const int group = static_cast<int>(live ? unit - row * G : 0u), c0 = group * p.D;
+    const T* x = at<const T>(p.x, p, row, group);
+    const T* z = kGate ? at<const T>(p.z, p, row, group) : nullptr;
+    T* out = at<T>(p.out, p, row, group);
+    float v[NV][N], g[NV][N];
+    bool in[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int d = (i * LPG + lane) * N;
+        in[i] = live && d < p.D;
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[i][e] = g[i][e] = 0.f;
+        if (in[i]) {
+            Vec<T>::load(x + d, v[i]);
+            if (kGate) Vec<T>::load(z + d, g[i]);
+        }
+    }
+    float r;
+    stats<LPG, NV, N, kCenter>(v, in, 1.f / p.D, p.eps, &r);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (!in[i]) continue;
+        const int d = (i * LPG + lane) * N;
+        float o[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const float y = fmaf(v[i][e], p.w ? __ldg(p.w + c0 + d + e) : 1.f, p.b ? __ldg(p.b + c0 + d + e) : 0.f);
+            o[e] = kGate ? y * act<kSilu>(g[i][e]) : act<kSilu>(y);
+        }
+        Vec<T>::store(out + d, o);
+    }
+}
+
+// A CTA's threads lie side by side over `slab` columns (whole groups) and, where a slab is
+// narrower than the CTA, over several rows; they walk down the share's rows.
+template <typename T, int LPG, int NV, bool kCenter, bool kSilu, bool kGate>
+__global__ void __launch_bounds__(kThreads) gn_bwd_kernel(const GnParams p, int gx) {
+    constexpr int N = Vec<T>::N;
+    extern __shared__ float s_part[];
+    const int lane = threadIdx.x % LPG, grp = threadIdx.x / LPG;
+    const int gcol = grp % gx, ry = grp / gx, nry = (kThreads / LPG) / gx;
+    const int group = blockIdx.y * gx + gcol;
+    const bool col_ok = group < p.G && ry < nry;
+    const int c0 = group * p.D;
+    const uint32_t r0 = blockIdx.x * p.share_rows;
+    const uint32_t r1 = min(r0 + p.share_rows, p.rows);
+    float w[NV][N], b[NV][N], dw[NV][N], db[NV][N];
+    bool in[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int d = (i * LPG + lane) * N;
+        in[i] = col_ok && d < p.D;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            dw[i][e] = db[i][e] = 0.f;
+            w[i][e] = in[i] && p.w ? p.w[c0 + d + e] : 1.f;
+            b[i][e] = in[i] && p.b ? p.b[c0 + d + e] : 0.f;
+        }
+    }
+    const float inv = 1.f / p.D;
+    // every thread takes the same number of turns: the shuffles need whole warps
+    const uint32_t turns = (r1 - r0 + nry - 1) / nry;
+    for (uint32_t t = 0; t < turns; ++t) {
+        const uint32_t row = r0 + t * nry + ry;
+        const bool live = col_ok && row < r1;
+        const T *x = nullptr, *dout = nullptr, *zp = nullptr;
+        if (live) {
+            x = at<const T>(p.x, p, row, group);
+            dout = at<const T>(p.dout, p, row, group);
+            if (kGate) zp = at<const T>(p.z, p, row, group);
+        }
+        float v[NV][N], dy[NV][N], z[NV][N];
+        bool on[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int d = (i * LPG + lane) * N;
+            on[i] = live && in[i];
+#pragma unroll
+            for (int e = 0; e < N; ++e) v[i][e] = dy[i][e] = z[i][e] = 0.f;
+            if (on[i]) {
+                Vec<T>::load(x + d, v[i]);
+                Vec<T>::load(dout + d, dy[i]);
+                if (kGate) Vec<T>::load(zp + d, z[i]);
+            }
+        }
+        float r;
+        stats<LPG, NV, N, kCenter>(v, on, inv, p.eps, &r);
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const float y = fmaf(v[i][e], w[i][e], b[i][e]);
+                float a, da;
+                act_slope<kSilu>(kGate ? z[i][e] : y, &a, &da);
+                const float d = dy[i][e];
+                z[i][e] = d * y * da;                 // dz
+                const float g = on[i] ? (kGate ? d * a : d * da) : 0.f;
+                dw[i][e] = fmaf(g, v[i][e], dw[i][e]);
+                db[i][e] += g;
+                dy[i][e] = g * w[i][e];
+                s1 = fmaf(dy[i][e], v[i][e], s1);
+                s2 += dy[i][e];
+            }
+        }
+        s1 = group_sum<LPG>(s1) * inv;
+        s2 = kCenter ? group_sum<LPG>(s2) * inv : 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (!on[i]) continue;
+            const int d = (i * LPG + lane) * N;
+#pragma unroll
+            for (int e = 0; e < N; ++e) dy[i][e] = r * (dy[i][e] - v[i][e] * s1 - s2);
+            Vec<T>::store(at<T>(p.dx, p, row, group) + d, dy[i]);
+            if (kGate) Vec<T>::store(at<T>(p.dz, p, row, group) + d, z[i]);
+        }
+    }
+    if (!p.part) return;
+    // the CTA's rows are added group row by group row
+    const int width = gx * p.D;
+    float* sw = s_part;
+    float* sb = s_part + width;
+    for (int k = 0; k < nry; ++k) {
+        if (ry == k) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (!in[i]) continue;
+                const int c = gcol * p.D + (i * LPG + lane) * N;
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    sw[c + e] = k ? sw[c + e] + dw[i][e] : dw[i][e];
+                    sb[c + e] = k ? sb[c + e] + db[i][e] : db[i][e];
+                }
+            }
+        }
+        __syncthreads();
+    }
+    float* part = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.C;
+    const int col0 = blockIdx.y * width;
+    for (int c = threadIdx.x; c < width && col0 + c < p.C; c += kThreads) {
+        part[col0 + c] = sw[c];
+        part[p.C + col0 + c] = sb[c];
+    }
+}
+
+// dweight and dbias: the shares of one column added in order by 8 threads, then those by one
+__global__ void __launch_bounds__(kThreads) gn_shares_kernel(const GnParams p) {
+    __shared__ float s[8][33];
+    const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + cx;   // of 2 C columns
+    float sum = 0.f;
+    if (c < 2 * static_cast<int64_t>(p.C))
+        for (int k = ry; k < p.shares; k += 8) sum += p.part[static_cast<int64_t>(k) * 2 * p.C + c];
+    s[ry][cx] = sum;
+    __syncthreads();
+    if (ry == 0 && c < 2 * static_cast<int64_t>(p.C)) {
+#pragma unroll
+        for (int k = 1; k < 8; ++k) sum += s[k][cx];
+        float* dst = c < p.C ? p.dw : p.db;
+        if (dst) dst[c < p.C ? c : c - p.C] = sum;
+    }
+}
+
+// ---- any group size and alignment: one CTA per group, scalar loads
+
+__device__ __forceinline__ float block_sum(float v, float* s) {
+    v = warp_sum(v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.f;
+    for (int i = 0; i < kThreads / 32; ++i) v += s[i];
+    return v;
+}
+
+template <typename T, bool kCenter, bool kSilu, bool kGate>
+__global__ void __launch_bounds__(kThreads) gn_fwd_any_kernel(const GnParams p) {
+    __shared__ float s[kThreads / 32];
+    const uint32_t row = blockIdx.x / p.G;
+    const int group = static_cast<int>(blockIdx.x - row * p.G), c0 = group * p.D;
+    const T* x = at<const T>(p.x, p, row, group);
+    const T* z = kGate ? at<const T>(p.z, p, row, group) : nullptr;
+    T* out = at<T>(p.out, p, row, group);
+    float m = 0.f, q = 0.f;
+    if (kCenter) {
+        for (int d = threadIdx.x; d < p.D; d += kThreads) m += to_f(x[d]);
+        m = block_sum(m, s) / p.D;
+    }
+    for (int d = threadIdx.x; d < p.D; d += kThreads) {
+        const float v = to_f(x[d]) - m;
+        q = fmaf(v, v, q);
+    }
+    const float r = rsqrtf(block_sum(q, s) / p.D + p.eps);
+    for (int d = threadIdx.x; d < p.D; d += kThreads) {
+        const float y = fmaf((to_f(x[d]) - m) * r, p.w ? p.w[c0 + d] : 1.f, p.b ? p.b[c0 + d] : 0.f);
+        out[d] = from_f<T>(kGate ? y * act<kSilu>(to_f(z[d])) : act<kSilu>(y));
+    }
+}
+
+// one CTA per (share, group): its rows in turn; the columns' sums stay in the share's row of the
+// workspace, which only this CTA's thread of that column touches
+template <typename T, bool kCenter, bool kSilu, bool kGate>
+__global__ void __launch_bounds__(kThreads) gn_bwd_any_kernel(const GnParams p) {
+    __shared__ float s[kThreads / 32];
+    const uint32_t share = blockIdx.x / p.G;
+    const int group = static_cast<int>(blockIdx.x - share * p.G), c0 = group * p.D;
+    const uint32_t r0 = share * p.share_rows;
+    const uint32_t r1 = min(r0 + p.share_rows, p.rows);
+    float* part = p.part ? p.part + static_cast<int64_t>(share) * 2 * p.C + c0 : nullptr;
+    if (part)
+        for (int d = threadIdx.x; d < p.D; d += kThreads) part[d] = part[p.C + d] = 0.f;
+    for (uint32_t row = r0; row < r1; ++row) {
+        const T* x = at<const T>(p.x, p, row, group);
+        const T* dout = at<const T>(p.dout, p, row, group);
+        const T* z = kGate ? at<const T>(p.z, p, row, group) : nullptr;
+        T* dx = at<T>(p.dx, p, row, group);
+        T* dz = kGate ? at<T>(p.dz, p, row, group) : nullptr;
+        float m = 0.f, q = 0.f;
+        if (kCenter) {
+            for (int d = threadIdx.x; d < p.D; d += kThreads) m += to_f(x[d]);
+            m = block_sum(m, s) / p.D;
+        }
+        for (int d = threadIdx.x; d < p.D; d += kThreads) {
+            const float v = to_f(x[d]) - m;
+            q = fmaf(v, v, q);
+        }
+        const float r = rsqrtf(block_sum(q, s) / p.D + p.eps);
+        float s1 = 0.f, s2 = 0.f;
+        for (int pass = 0; pass < 2; ++pass) {
+            for (int d = threadIdx.x; d < p.D; d += kThreads) {
+                const float xh = (to_f(x[d]) - m) * r, w = p.w ? p.w[c0 + d] : 1.f;
+                const float y = fmaf(xh, w, p.b ? p.b[c0 + d] : 0.f), dd = to_f(dout[d]);
+                float a, da;
+                act_slope<kSilu>(kGate ? to_f(z[d]) : y, &a, &da);
+                const float dy = kGate ? dd * a : dd * da, g = dy * w;
+                if (pass == 0) {
+                    s1 = fmaf(g, xh, s1);
+                    s2 += g;
+                    if (part) {
+                        part[d] = fmaf(dy, xh, part[d]);
+                        part[p.C + d] += dy;
+                    }
+                } else {
+                    // this thread alone reads and writes element d from here on: dx may be x or dout
+                    dx[d] = from_f<T>(r * (g - xh * s1 - s2));
+                    if (kGate) dz[d] = from_f<T>(dd * y * da);
+                }
+            }
+            if (pass == 0) {
+                s1 = block_sum(s1, s) / p.D;
+                s2 = kCenter ? block_sum(s2, s) / p.D : 0.f;
+            }
+        }
+    }
+}
+
+// ---- dispatch
+
+template <bool kC, bool kS, bool kG>
+struct Flags {
+    static constexpr bool C = kC, S = kS, Z = kG;
+};
+template <typename F>
+auto with_flags(uint32_t flags, bool gate, F&& f) {
+    const bool c = flags & M3_GN_CENTER, s = flags & M3_GN_SILU;
+    if (c) {
+        if (s) return gate ? f(Flags<true, true, true>{}) : f(Flags<true, true, false>{});
+        return gate ? f(Flags<true, false, true>{}) : f(Flags<true, false, false>{});
+    }
+    if (s) return gate ? f(Flags<false, true, true>{}) : f(Flags<false, true, false>{});
+    return gate ? f(Flags<false, false, true>{}) : f(Flags<false, false, false>{});
+}
+
+template <int L, int V>
+struct Shape {
+    static constexpr int LPG = L, NV = V;
+};
+// lanes and vectors per group: the fewest lanes (from 4) that hold it in one vector each, then
+// more vectors; the caller has checked that 32 * 4 vectors are enough
+template <typename F>
+auto with_shape(int vecs, F&& f) {
+    if (vecs <= 4) return f(Shape<4, 1>{});
+    if (vecs <= 8) return f(Shape<8, 1>{});
+    if (vecs <= 16) return f(Shape<16, 1>{});
+    if (vecs <= 32) return f(Shape<32, 1>{});
+    if (vecs <= 64) return f(Shape<32, 2>{});
+    return f(Shape<32, 4>{});
+}
+
+bool ok16(const GnTensor& t, int es) {
+    return !t.p || ((reinterpret_cast<uintptr_t>(t.p) | static_cast<uintptr_t>(t.batch * es) |
+                     static_cast<uintptr_t>(t.row * es) | static_cast<uintptr_t>(t.group * es)) & 15u) == 0;
+}
+
+// 16-byte vectors of a group, or 0 where the vector form does not apply
+template <typename T>
+int vector_count(const GnParams& p) {
+    constexpr int N = Vec<T>::N, es = sizeof(T);
+    if (p.D % N != 0 || p.D / N > 128) return 0;
+    const bool ok = ok16(p.x, es) && ok16(p.z, es) && ok16(p.out, es) && ok16(p.dout, es) && ok16(p.dx, es) && ok16(p.dz, es);
+    return ok ? p.D / N : 0;
+}
+
+template <typename T>
+cudaError_t launch_fwd(const GnParams& p, uint32_t flags, cudaStream_t s) {
+    const int vecs = vector_count<T>(p);
+    with_flags(flags, p.z.p != nullptr, [&](auto f) {
+        using F = decltype(f);
+        if (vecs == 0) {
+            gn_fwd_any_kernel<T, F::C, F::S, F::Z><<<p.rows * static_cast<unsigned>(p.G), kThreads, 0, s>>>(p);
+            return 0;
+        }
+        return with_shape(vecs, [&](auto sh) {
+            using S = decltype(sh);
+            constexpr int per = kThreads / S::LPG;
+            gn_fwd_kernel<T, S::LPG, S::NV, F::C, F::S, F::Z>
+                <<<(p.rows * static_cast<unsigned>(p.G) + per - 1) / per, kThreads, 0, s>>>(p);
+            return 0;
+        });
+    });
+    return cudaGetLastError();
+}
+
+// Shares of the backward: as many as give every SM a few CTAs, at most one per row.
+int64_t share_count(int64_t rows, int64_t per_row_ctas) {
+    const int64_t want = (4 * static_cast<int64_t>(device_sm_count()) + per_row_ctas - 1) / per_row_ctas;
+    return rows < want ? (rows > 0 ? rows : 1) : want;
+}
+// the most shares any of the forms takes
+int64_t max_shares(int64_t rows) { return share_count(rows, 1); }
+
+template <typename T>
+cudaError_t launch_bwd(GnParams p, uint32_t flags, cudaStream_t s) {
+    const int vecs = vector_count<T>(p);
+    with_flags(flags, p.z.p != nullptr, [&](auto f) {
+        using F = decltype(f);
+        if (vecs == 0) {
+            const int64_t n = share_count(p.rows, p.G);
+            p.share_rows = static_cast<uint32_t>((p.rows + n - 1) / n);
+            p.shares = static_cast<int>((p.rows + p.share_rows - 1) / p.share_rows);
+            gn_bwd_any_kernel<T, F::C, F::S, F::Z><<<static_cast<unsigned>(p.shares * static_cast<int64_t>(p.G)), kThreads, 0, s>>>(p);
+            return 0;
+        }
+        return with_shape(vecs, [&](auto sh) {
+            using S = decltype(sh);
+            constexpr int per = kThreads / S::LPG;
+            // groups side by side: as many as the CTA's threads and 32 KB of column sums hold, the
+            // row's groups spread evenly over the slabs
+            const int most = per < 4096 / p.D ? per : 4096 / p.D;
+            const int gx = (p.G + (p.G + most - 1) / most - 1) / ((p.G + most - 1) / most);
+            const int nry = per / gx;
+            const unsigned slabs = static_cast<unsigned>((p.G + gx - 1) / gx);
+            const int64_t n = share_count((p.rows + nry - 1) / nry, slabs);
+            p.share_rows = static_cast<uint32_t>((p.rows + n - 1) / n);
+            p.shares = static_cast<int>((p.rows + p.share_rows - 1) / p.share_rows);
+            const size_t smem = static_cast<size_t>(gx) * p.D * 2 * sizeof(float);
+            gn_bwd_kernel<T, S::LPG, S::NV, F::C, F::S, F::Z>
+                <<<dim3(static_cast<unsigned>(p.shares), slabs), kThreads, smem, s>>>(p, gx);
+            return 0;
+        });
+    });
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !p.part) return e;
+    gn_shares_kernel<<<static_cast<unsigned>((2 * static_cast<int64_t>(p.C) + 31) / 32), kThreads, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+m3_status err(m3_status st, const char* fmt, ...) {
+    char msg[256];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(msg, sizeof(msg), fmt, ap);
+    va_end(ap);
+    return set_error(st, msg);
+}
+
+m3_status check(const m3_group_norm_dims* d) {
+    if (!d) return err(M3_ERR_INVALID_ARG, "dims is NULL");
+    if (d->in_dtype != M3_F32 && d->in_dtype != M3_BF16)
+        return err(M3_ERR_INVALID_ARG, "in_dtype %d is not M3_F32 or M3_BF16", d->in_dtype);
+    if (d->batch < 0 || d->rows < 0) return err(M3_ERR_INVALID_ARG, "batch and rows must be >= 0");
+    if (d->channels < 1 || d->groups < 1 || d->channels % d->groups != 0)
+        return err(M3_ERR_INVALID_ARG, "channels (%lld) must be a positive multiple of groups (%lld)",
+                   (long long)d->channels, (long long)d->groups);
+    if (!(d->eps >= 0.f) || !std::isfinite(d->eps)) return err(M3_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    if (d->flags & ~(M3_GN_CENTER | M3_GN_SILU))
+        return err(M3_ERR_INVALID_ARG, "unknown bits in flags (0x%x)", (unsigned)d->flags);
+    // (row, group) pairs are counted in 32 bits
+    const int64_t lim = 0x7fffffffLL - kThreads;
+    if (d->channels > (int64_t(1) << 24) || (d->batch > 0 && d->rows > lim / d->batch) ||
+        (d->batch > 0 && d->rows > 0 && d->groups > lim / (d->batch * d->rows)))
+        return err(M3_ERR_UNSUPPORTED, "batch * rows * groups exceeds 2^31");
+    return M3_OK;
+}
+
+m3_status check_ptr(const void* q, int64_t align, const char* name, bool need) {
+    if (!q) return need ? err(M3_ERR_INVALID_ARG, "%s is NULL", name) : M3_OK;
+    if (reinterpret_cast<uintptr_t>(q) % static_cast<uintptr_t>(align) != 0)
+        return err(M3_ERR_INVALID_ARG, "%s is not aligned to its element size", name);
+    return M3_OK;
+}
+
+m3_status check_view(const m3_view* v, int es, const char* name, bool need) {
+    return check_ptr(v ? v->data : nullptr, es, name, need);
+}
+
+GnTensor tensor(const m3_view* v) {
+    return v && v->data ? GnTensor{v->data, v->batch, v->token, v->head} : GnTensor{};
+}
+
+// Rows (and groups) of an output that share elements through equal strides.
+m3_status check_out(const m3_view* v, const m3_group_norm_dims* d, const char* name) {
+    const int64_t D = d->channels / d->groups;
+    const int64_t g = v->head < 0 ? -v->head : v->head, r = v->token < 0 ? -v->token : v->token;
+    if ((d->groups > 1 && g < D) || (d->rows > 1 && r < D) || (d->batch > 1 && v->batch == 0))
+        return err(M3_ERR_INVALID_ARG, "%s: rows or groups overlap", name);
+    return M3_OK;
+}
+
+GnParams make_params(const m3_group_norm_dims* d, const m3_view* x, const m3_view* z, const float* w, const float* b) {
+    GnParams p{};
+    p.rows = static_cast<uint32_t>(d->batch * d->rows);
+    p.inner = static_cast<uint32_t>(d->rows);
+    p.C = static_cast<int>(d->channels);
+    p.G = static_cast<int>(d->groups);
+    p.D = p.C / p.G;
+    p.eps = d->eps;
+    p.x = tensor(x);
+    p.z = tensor(z);
+    p.w = w;
+    p.b = b;
+    return p;
+}
+
+}  // namespace
+}  // namespace m3
+
+using namespace m3;
+
+extern "C" {
+
+m3_status m3_group_norm_fwd(const m3_group_norm_dims* dims, const m3_view* x, const m3_view* z,
+                            const float* weight, const float* bias, const m3_view* out, void* stream) {
+    set_error(M3_OK, "");
+    m3_status st = check(dims);
+    if (st != M3_OK) return st;
+    const bool bf16 = dims->in_dtype == M3_BF16;
+    const int es = bf16 ? 2 : 4;
+    const bool any = dims->batch > 0 && dims->rows > 0;
+    if ((st = check_view(x, es, "x", any)) != M3_OK || (st = check_view(z, es, "z", false)) != M3_OK ||
+        (st = check_ptr(weight, 4, "weight", false)) != M3_OK || (st = check_ptr(bias, 4, "bias", false)) != M3_OK ||
+        (st = check_view(out, es, "out", any)) != M3_OK)
+        return st;
+    if (!any) return M3_OK;
+    if ((st = check_out(out, dims, "out")) != M3_OK) return st;
+    GnParams p = make_params(dims, x, z, weight, bias);
+    p.out = tensor(out);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = bf16 ? launch_fwd<__nv_bfloat16>(p, dims->flags, s) : launch_fwd<float>(p, dims->flags, s);
+    return e == cudaSuccess ? M3_OK : err(M3_ERR_CUDA, "group norm launch: %s", cudaGetErrorString(e));
+}
+
+size_t m3_group_norm_bwd_workspace_bytes(const m3_group_norm_dims* dims) {
+    if (check(dims) != M3_OK) return 0;
+    const size_t n = static_cast<size_t>(max_shares(dims->batch * dims->rows)) * 2 * static_cast<size_t>(dims->channels) * 4;
+    return (n + 255) / 256 * 256;
+}
+
+m3_status m3_group_norm_bwd(const m3_group_norm_dims* dims, const m3_view* x, const m3_view* z, const float* weight,
+                            const float* bias, const m3_view* dout, const m3_view* dx, const m3_view* dz,
+                            float* dweight, float* dbias, void* workspace, size_t ws_bytes, void* stream) {
+    set_error(M3_OK, "");
+    m3_status st = check(dims);
+    if (st != M3_OK) return st;
+    const bool bf16 = dims->in_dtype == M3_BF16;
+    const int es = bf16 ? 2 : 4;
+    const bool any = dims->batch > 0 && dims->rows > 0, gate = z && z->data;
+    if ((st = check_view(x, es, "x", any)) != M3_OK || (st = check_view(z, es, "z", false)) != M3_OK ||
+        (st = check_view(dout, es, "dout", any)) != M3_OK || (st = check_view(dx, es, "dx", any)) != M3_OK ||
+        (st = check_view(dz, es, "dz", any && gate)) != M3_OK ||
+        (st = check_ptr(weight, 4, "weight", false)) != M3_OK || (st = check_ptr(bias, 4, "bias", false)) != M3_OK ||
+        (st = check_ptr(dweight, 4, "dweight", false)) != M3_OK || (st = check_ptr(dbias, 4, "dbias", false)) != M3_OK)
+        return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (!any) {
+        cudaError_t e = cudaSuccess;
+        if (dweight) e = cudaMemsetAsync(dweight, 0, dims->channels * 4, s);
+        if (e == cudaSuccess && dbias) e = cudaMemsetAsync(dbias, 0, dims->channels * 4, s);
+        return e == cudaSuccess ? M3_OK : err(M3_ERR_CUDA, "empty gradient: %s", cudaGetErrorString(e));
+    }
+    if ((st = check_out(dx, dims, "dx")) != M3_OK || (gate && (st = check_out(dz, dims, "dz")) != M3_OK)) return st;
+    const size_t need = m3_group_norm_bwd_workspace_bytes(dims);
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || ws_bytes < need)
+        return err(M3_ERR_INVALID_ARG, "workspace: NULL, misaligned or below %zu bytes", need);
+    GnParams p = make_params(dims, x, z, weight, bias);
+    p.dout = tensor(dout);
+    p.dx = tensor(dx);
+    p.dz = gate ? tensor(dz) : GnTensor{};
+    p.dw = dweight;
+    p.db = dbias;
+    p.part = (dweight || dbias) ? static_cast<float*>(workspace) : nullptr;
+    const cudaError_t e = bf16 ? launch_bwd<__nv_bfloat16>(p, dims->flags, s) : launch_bwd<float>(p, dims->flags, s);
+    return e == cudaSuccess ? M3_OK : err(M3_ERR_CUDA, "group norm backward launch: %s", cudaGetErrorString(e));
+}
+
+}  // extern "C"

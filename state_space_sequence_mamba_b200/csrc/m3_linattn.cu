@@ -1,0 +1,421 @@
+// Linear attention with a decay for each head: host side of its entry points (validation, the cut
+// into segments, workspace layout, dispatch) and the sum of shared heads' gradients.
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+
+#include "m3_common.cuh"
+#include "m3_internal.h"
+#include "m3_linattn.h"
+
+namespace m3 {
+
+// Segments trade work for parallelism: every cut sequence reads its k and v a second time (for the
+// segments' end states), so sequences are cut only while their number leaves CTA slots empty.
+// A segment has at least kMinSegTokens tokens.
+constexpr int64_t kMinSegTokens = 256;
+
+LinPlan lin_plan(int64_t nseq, int64_t L, bool packed, int64_t per_x, int64_t slots) {
+    LinPlan pl{};
+    const int64_t chunks = (L + 127) / 128, min_chunks = kMinSegTokens / 128;
+    if (!packed) {
+        int64_t want = slots / (nseq * per_x);
+        if (want > chunks / min_chunks) want = chunks / min_chunks;
+        if (want > kLinMaxSegs) want = kLinMaxSegs;
+        if (want < 1) want = 1;
+        const int64_t seg = (chunks + want - 1) / want;     // chunks of a segment
+        pl.seg_len = static_cast<int>((seg > 0 ? seg : 1) * 128);
+        pl.nseg = static_cast<int>(seg > 0 ? (chunks + seg - 1) / seg : 1);
+        pl.blocks_x = nseq * pl.nseg;
+        pl.cut = pl.nseg > 1;
+        return pl;
+    }
+    // the rows' share of one slot, whichever sequences they belong to
+    int64_t seg = (L * per_x + 128 * slots - 1) / (128 * slots);
+    if (seg < min_chunks) seg = min_chunks;
+    if (seg < (chunks + kLinMaxSegs - 1) / kLinMaxSegs) seg = (chunks + kLinMaxSegs - 1) / kLinMaxSegs;
+    pl.seg_len = static_cast<int>(seg * 128);
+    pl.nseg = 1;
+    // sum of max(1, ceil(len / seg_len)) over nseq sequences of at most L rows together
+    pl.blocks_x = L / pl.seg_len + nseq;
+    pl.cut = L > pl.seg_len;
+    return pl;
+}
+
+namespace {
+
+m3_status err(m3_status st, const char* fmt, ...) {
+    char msg[256];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(msg, sizeof(msg), fmt, ap);
+    va_end(ap);
+    return set_error(st, msg);
+}
+m3_status cuda_err(cudaError_t e, const char* where) {
+    return err(M3_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
+}
+
+constexpr int64_t kMaxGrid = 0x7fffffffLL;
+
+m3_status check_dims(const m3_linattn_dims* d) {
+    if (!d) return err(M3_ERR_INVALID_ARG, "dims is NULL");
+    if (d->in_dtype != M3_F32 && d->in_dtype != M3_BF16)
+        return err(M3_ERR_INVALID_ARG, "in_dtype %d is not M3_F32 or M3_BF16", d->in_dtype);
+    if (d->nseq < 0 || d->seqlen < 0) return err(M3_ERR_INVALID_ARG, "nseq and seqlen must be >= 0");
+    const int64_t H = d->nheads;
+    if (H < 1) return err(M3_ERR_INVALID_ARG, "nheads must be >= 1");
+    const int64_t hs[] = {d->qheads, d->kheads, d->vheads};
+    const char* names[] = {"qheads", "kheads", "vheads"};
+    for (int i = 0; i < 3; ++i)
+        if (hs[i] < 1 || H % hs[i] != 0)
+            return err(M3_ERR_INVALID_ARG, "%s (%lld) must divide nheads (%lld)", names[i],
+                       (long long)hs[i], (long long)H);
+    if (d->kdim < 1 || d->vdim < 1) return err(M3_ERR_INVALID_ARG, "kdim and vdim must be >= 1");
+    if (!std::isfinite(d->scale)) return err(M3_ERR_INVALID_ARG, "scale must be finite");
+    if (d->kdim > 256 || d->vdim > 256)
+        return err(M3_ERR_UNSUPPORTED, "kdim %lld or vdim %lld exceeds 256", (long long)d->kdim, (long long)d->vdim);
+    // token counts stay exact as fp32 exponents, indexes of one sequence fit 32 bits
+    if (d->seqlen > (int64_t(1) << 30) || H > 65536 || d->nseq > (int64_t(1) << 24))
+        return err(M3_ERR_UNSUPPORTED, "seqlen above 2^30, nheads above 65536 or nseq above 2^24");
+    return M3_OK;
+}
+
+m3_status check_view(const m3_view* v, const char* name, int es, bool need) {
+    if (!v || !v->data) return need ? err(M3_ERR_INVALID_ARG, "%s is NULL", name) : M3_OK;
+    if (reinterpret_cast<uintptr_t>(v->data) % static_cast<uintptr_t>(es) != 0)
+        return err(M3_ERR_INVALID_ARG, "%s is not aligned to its element size", name);
+    return M3_OK;
+}
+m3_status check_state(const float* q, const char* name) {
+    return reinterpret_cast<uintptr_t>(q) & 15u ? err(M3_ERR_INVALID_ARG, "%s is not 16-byte aligned", name) : M3_OK;
+}
+m3_status check_inputs(const m3_linattn_dims* d, const m3_linattn_inputs* in, bool any) {
+    if (!in) return err(M3_ERR_INVALID_ARG, "inputs is NULL");
+    const int es = d->in_dtype == M3_BF16 ? 2 : 4;
+    m3_status st;
+    if ((st = check_view(&in->q, "q", es, any)) != M3_OK || (st = check_view(&in->k, "k", es, any)) != M3_OK ||
+        (st = check_view(&in->v, "v", es, any)) != M3_OK)
+        return st;
+    if (!in->log_decay) return err(M3_ERR_INVALID_ARG, "log_decay is NULL");
+    if (reinterpret_cast<uintptr_t>(in->log_decay) & 3u) return err(M3_ERR_INVALID_ARG, "log_decay is misaligned");
+    if (reinterpret_cast<uintptr_t>(in->cu_seqlens) & 3u) return err(M3_ERR_INVALID_ARG, "cu_seqlens is misaligned");
+    return M3_OK;
+}
+
+LinTensor tensor(const m3_view& v, int64_t H, int64_t heads, bool packed) {
+    return LinTensor{v.data, packed ? 0 : v.batch, v.token, v.head, static_cast<int>(H / heads)};
+}
+
+LinParams make_params(const m3_linattn_dims* d, const m3_linattn_inputs* in) {
+    LinParams p{};
+    p.log_decay = in->log_decay;
+    p.cu = in->cu_seqlens;
+    p.nseq = static_cast<int>(d->nseq);
+    p.H = static_cast<int>(d->nheads);
+    p.L = d->seqlen;
+    return p;
+}
+
+int tiles_of(int64_t dim) { return static_cast<int>((dim + kLinTile - 1) / kLinTile); }
+
+// Tiles of the launches: forward, and the three gradients of the backward in one
+int fwd_tiles(const m3_linattn_dims* d) { return tiles_of(d->vdim); }
+int bwd_tiles(const m3_linattn_dims* d) { return 2 * tiles_of(d->kdim) + tiles_of(d->vdim); }
+int bwd_rows(const m3_linattn_dims* d) { return static_cast<int>(d->kdim > d->vdim ? d->kdim : d->vdim); }
+
+size_t seg_bytes(const m3_linattn_dims* d, bool packed, int rtiles, int rows, int slots) {
+    if (d->nseq == 0 || d->seqlen == 0) return 0;
+    const LinPlan pl = lin_plan(d->nseq, d->seqlen, packed, d->nheads * rtiles, slots);
+    return pl.cut ? static_cast<size_t>(pl.blocks_x) * d->nheads * rtiles * rows * kLinTile * 4 : 0;
+}
+// the larger of what the two forms take (which one runs depends on the tensors' alignment)
+size_t seg_bytes(const m3_linattn_dims* d, bool packed, int rtiles, int rows) {
+    const size_t a = seg_bytes(d, packed, rtiles, rows, lin_simt_slots());
+    const size_t b = seg_bytes(d, packed, rtiles, rows < 128 ? 128 : rows, lin_tc_slots());
+    return ((a > b ? a : b) + 255) / 256 * 256;
+}
+
+// fp32 per-head gradients of tensors whose heads are shared: [rows][H][dim] each
+size_t shared_bytes(const m3_linattn_dims* d, int which, bool packed) {
+    const int64_t heads = which == 0 ? d->qheads : which == 1 ? d->kheads : d->vheads;
+    const int64_t dim = which == 2 ? d->vdim : d->kdim;
+    if (heads == d->nheads) return 0;
+    const int64_t rows = packed ? d->seqlen : d->nseq * d->seqlen;
+    return (static_cast<size_t>(rows) * d->nheads * dim * 4 + 255) / 256 * 256;
+}
+
+// The sum over the H / heads heads that read one head of a tensor, in order, rounded once.
+template <typename T>
+__global__ void __launch_bounds__(256)
+fold_heads_kernel(const float* __restrict__ part, T* out, int64_t batch, int64_t token, int64_t head,
+                  int64_t L, int64_t total, int heads, int ratio, int dim, const int32_t* cu, int nseq) {
+    for (int64_t e = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; e < total;
+         e += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        const int c = static_cast<int>(e % dim);
+        const int64_t rh = e / dim;
+        const int g = static_cast<int>(rh % heads);
+        const int64_t row = rh / heads;
+        const int64_t b = cu ? 0 : row / L, t = cu ? row : row % L;
+        if (cu && (row < cu[0] || row >= cu[nseq])) continue;    // rows of no sequence are left alone
+        const float* src = part + (row * heads + g) * static_cast<int64_t>(ratio) * dim + c;
+        float s = 0.f;
+        for (int i = 0; i < ratio; ++i) s += src[static_cast<int64_t>(i) * dim];
+        out[b * batch + t * token + g * head + c] = from_f<T>(s);
+    }
+}
+
+cudaError_t fold_heads(const m3_linattn_dims* d, int which, const float* part, const m3_view& v,
+                       const int32_t* cu, cudaStream_t s) {
+    const int64_t heads = which == 0 ? d->qheads : which == 1 ? d->kheads : d->vheads;
+    const int64_t dim = which == 2 ? d->vdim : d->kdim;
+    const int64_t rows = cu ? d->seqlen : d->nseq * d->seqlen;
+    const int64_t total = rows * heads * dim;
+    if (total == 0) return cudaSuccess;
+    int64_t grid = (total + 255) / 256;
+    const int64_t most = 32LL * device_sm_count();
+    if (grid > most) grid = most;
+    const int ratio = static_cast<int>(d->nheads / heads);
+    if (d->in_dtype == M3_BF16)
+        fold_heads_kernel<__nv_bfloat16><<<static_cast<unsigned>(grid), 256, 0, s>>>(
+            part, static_cast<__nv_bfloat16*>(v.data), v.batch, v.token, v.head, d->seqlen, total,
+            static_cast<int>(heads), ratio, static_cast<int>(dim), cu, static_cast<int>(d->nseq));
+    else
+        fold_heads_kernel<float><<<static_cast<unsigned>(grid), 256, 0, s>>>(
+            part, static_cast<float*>(v.data), v.batch, v.token, v.head, d->seqlen, total,
+            static_cast<int>(heads), ratio, static_cast<int>(dim), cu, static_cast<int>(d->nseq));
+    return cudaGetLastError();
+}
+
+// Plans and launches the jobs of p in the form that takes them.
+m3_status run_jobs(LinParams& p, const m3_linattn_dims* d, int state_rows, char* ws, cudaStream_t s) {
+    const bool bf16 = d->in_dtype == M3_BF16, packed = p.cu != nullptr;
+    const bool tc = bf16 && lin_tc_supported(p);
+    const LinPlan pl = lin_plan(d->nseq, d->seqlen, packed, d->nheads * p.rtiles,
+                                tc ? lin_tc_slots() : lin_simt_slots());
+    p.seg_len = pl.seg_len;
+    p.nseg = pl.nseg;
+    p.blocks_x = pl.blocks_x;
+    p.seg = reinterpret_cast<float*>(ws);
+    p.seg_rows = tc && state_rows < 128 ? 128 : state_rows;
+    if (p.blocks_x > kMaxGrid / (d->nheads * p.rtiles))
+        return err(M3_ERR_UNSUPPORTED, "sequences * heads * column tiles exceed the grid limit");
+    const cudaError_t e = tc ? launch_lin_tc(p, pl.cut, s) : launch_lin_simt(p, bf16, pl.cut, s);
+    return e == cudaSuccess ? M3_OK : cuda_err(e, "linear attention launch");
+}
+
+// No token at all: the state passes through.
+m3_status pass_state(const m3_linattn_dims* d, const float* from, float* to, cudaStream_t s) {
+    if (!to || to == from) return M3_OK;
+    const size_t n = static_cast<size_t>(d->nseq) * d->nheads * d->kdim * d->vdim * 4;
+    if (n == 0) return M3_OK;
+    const cudaError_t e = from ? cudaMemcpyAsync(to, from, n, cudaMemcpyDeviceToDevice, s) : cudaMemsetAsync(to, 0, n, s);
+    return e == cudaSuccess ? M3_OK : cuda_err(e, "empty-sequence state copy");
+}
+
+// A copy of a state that the call overwrites while it may still read it.
+size_t state_bytes(const m3_linattn_dims* d) {
+    return (static_cast<size_t>(d->nseq) * d->nheads * d->kdim * d->vdim * 4 + 255) / 256 * 256;
+}
+m3_status keep_state(const m3_linattn_dims* d, const float* from, char* to, cudaStream_t s) {
+    const cudaError_t e = cudaMemcpyAsync(to, from, static_cast<size_t>(d->nseq) * d->nheads * d->kdim * d->vdim * 4,
+                                          cudaMemcpyDeviceToDevice, s);
+    return e == cudaSuccess ? M3_OK : cuda_err(e, "state copy");
+}
+
+m3_status check_workspace(void* ws, size_t have, size_t need) {
+    if (need > 0 && (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0 || have < need))
+        return err(M3_ERR_INVALID_ARG, "workspace: NULL, misaligned or below %zu bytes", need);
+    return M3_OK;
+}
+
+}  // namespace
+}  // namespace m3
+
+using namespace m3;
+
+extern "C" {
+
+size_t m3_linattn_workspace_bytes(const m3_linattn_dims* dims, int packed) {
+    if (check_dims(dims) != M3_OK) return 0;
+    const size_t n = seg_bytes(dims, packed != 0, fwd_tiles(dims), static_cast<int>(dims->kdim));
+    return n ? n + state_bytes(dims) : 0;
+}
+
+size_t m3_linattn_bwd_workspace_bytes(const m3_linattn_dims* dims, int packed) {
+    if (check_dims(dims) != M3_OK) return 0;
+    size_t n = seg_bytes(dims, packed != 0, bwd_tiles(dims), bwd_rows(dims));
+    for (int i = 0; i < 3; ++i) n += shared_bytes(dims, i, packed != 0);
+    return n + state_bytes(dims);
+}
+
+m3_status m3_linattn_fwd(const m3_linattn_dims* dims, const m3_linattn_inputs* in, const float* init,
+                         float* final_state, const m3_view* o, void* workspace, size_t ws_bytes,
+                         void* stream) {
+    set_error(M3_OK, "");
+    m3_status st = check_dims(dims);
+    if (st != M3_OK) return st;
+    const bool any = dims->nseq > 0 && dims->seqlen > 0;
+    if ((st = check_inputs(dims, in, any)) != M3_OK || (st = check_state(init, "init")) != M3_OK ||
+        (st = check_state(final_state, "final_state")) != M3_OK ||
+        (st = check_view(o, "o", dims->in_dtype == M3_BF16 ? 2 : 4, any)) != M3_OK)
+        return st;
+    const size_t need = m3_linattn_workspace_bytes(dims, in->cu_seqlens != nullptr);
+    if ((st = check_workspace(workspace, ws_bytes, need)) != M3_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (!any) return pass_state(dims, init, final_state, s);
+    LinParams p = make_params(dims, in);
+    const bool packed = in->cu_seqlens != nullptr;
+    const int64_t H = dims->nheads;
+    LinJob& j = p.job[0];
+    j.q = tensor(in->q, H, dims->qheads, packed);
+    j.k = tensor(in->k, H, dims->kheads, packed);
+    j.v = tensor(in->v, H, dims->vheads, packed);
+    j.y = o->data;
+    j.y_batch = packed ? 0 : o->batch; j.y_token = o->token; j.y_head = o->head;
+    j.Dk = static_cast<int>(dims->kdim);
+    j.Dv = static_cast<int>(dims->vdim);
+    j.tiles = fwd_tiles(dims);
+    j.p_scale = j.o_scale = dims->scale;
+    j.x_scale = 1.f;
+    j.init = init;
+    j.init_k = dims->vdim;
+    j.init_v = 1;
+    j.final_state = final_state;
+    p.njobs = 1;
+    p.rtiles = j.tiles;
+    if (init && init == final_state && need > 0) {  // cut: later segments read it while the last writes
+        char* copy = static_cast<char*>(workspace) + need - state_bytes(dims);
+        if ((st = keep_state(dims, init, copy, s)) != M3_OK) return st;
+        j.init = reinterpret_cast<const float*>(copy);
+    }
+    return run_jobs(p, dims, j.Dk, static_cast<char*>(workspace), s);
+}
+
+m3_status m3_linattn_bwd(const m3_linattn_dims* dims, const m3_linattn_inputs* in, const float* init,
+                         const m3_view* d_o, const float* dfinal, const m3_linattn_grads* grads,
+                         float* dinit, void* workspace, size_t ws_bytes, void* stream) {
+    set_error(M3_OK, "");
+    m3_status st = check_dims(dims);
+    if (st != M3_OK) return st;
+    const bool any = dims->nseq > 0 && dims->seqlen > 0;
+    const int es = dims->in_dtype == M3_BF16 ? 2 : 4;
+    if (!grads) return err(M3_ERR_INVALID_ARG, "grads is NULL");
+    if ((st = check_inputs(dims, in, any)) != M3_OK || (st = check_view(d_o, "d_o", es, any)) != M3_OK ||
+        (st = check_view(&grads->dq, "dq", es, any)) != M3_OK || (st = check_view(&grads->dk, "dk", es, any)) != M3_OK ||
+        (st = check_view(&grads->dv, "dv", es, any)) != M3_OK || (st = check_state(init, "init")) != M3_OK ||
+        (st = check_state(dfinal, "dfinal")) != M3_OK || (st = check_state(dinit, "dinit")) != M3_OK)
+        return st;
+    const bool packed = in->cu_seqlens != nullptr;
+    const size_t need = m3_linattn_bwd_workspace_bytes(dims, packed);
+    if ((st = check_workspace(workspace, ws_bytes, need)) != M3_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (!any) return pass_state(dims, dfinal, dinit, s);
+
+    LinParams p = make_params(dims, in);
+    const int64_t H = dims->nheads;
+    const int K = static_cast<int>(dims->kdim), V = static_cast<int>(dims->vdim);
+    const LinTensor q = tensor(in->q, H, dims->qheads, packed), k = tensor(in->k, H, dims->kheads, packed),
+                    v = tensor(in->v, H, dims->vheads, packed), g = tensor(*d_o, H, H, packed);
+    char* ws = static_cast<char*>(workspace);
+    char* seg = ws;
+    ws += seg_bytes(dims, packed, bwd_tiles(dims), bwd_rows(dims));
+    const m3_view* outs[3] = {&grads->dq, &grads->dk, &grads->dv};
+    float* part[3];
+    for (int i = 0; i < 3; ++i) {
+        const size_t n = shared_bytes(dims, i, packed);
+        part[i] = n ? reinterpret_cast<float*>(ws) : nullptr;
+        ws += n;
+    }
+    const LinTensor a[3] = {g, v, k}, b[3] = {v, g, q}, c[3] = {k, q, g};   // (do, v, k), (v, do, q), (k, q, do)
+    const int Dk[3] = {V, V, K}, Dv[3] = {K, K, V};
+    p.rtiles = 0;
+    for (int i = 0; i < 3; ++i) {
+        LinJob& j = p.job[i];
+        j.q = a[i]; j.k = b[i]; j.v = c[i];
+        j.Dk = Dk[i]; j.Dv = Dv[i];
+        j.tiles = tiles_of(Dv[i]);
+        p.rtiles += j.tiles;
+        j.reverse = i > 0;
+        j.p_scale = dims->scale;
+        // forward states carry plain sums, backward ones the scaled gradient beside dfinal
+        j.o_scale = i > 0 ? 1.f : dims->scale;
+        j.x_scale = i > 0 ? dims->scale : 1.f;
+        j.init = i > 0 ? dfinal : init;
+        j.init_k = i < 2 ? 1 : V;       // dq's and dk's states are the transposed ones
+        j.init_v = i < 2 ? V : 1;
+        if (part[i]) {
+            j.y = part[i];
+            j.y_f32 = 1;
+            j.y_head = Dv[i];
+            j.y_token = H * Dv[i];
+            j.y_batch = packed ? 0 : dims->seqlen * j.y_token;
+        } else {
+            j.y = outs[i]->data;
+            j.y_batch = packed ? 0 : outs[i]->batch; j.y_token = outs[i]->token; j.y_head = outs[i]->head;
+        }
+    }
+    p.job[2].final_state = dinit;
+    p.njobs = 3;
+    if (dfinal && dinit == dfinal) {    // other CTAs read it while one writes it
+        if ((st = keep_state(dims, dfinal, ws, s)) != M3_OK) return st;
+        p.job[1].init = p.job[2].init = reinterpret_cast<const float*>(ws);
+    }
+    if ((st = run_jobs(p, dims, bwd_rows(dims), seg, s)) != M3_OK) return st;
+    for (int i = 0; i < 3; ++i)
+        if (part[i]) {
+            const cudaError_t e = fold_heads(dims, i, part[i], *outs[i], in->cu_seqlens, s);
+            if (e != cudaSuccess) return cuda_err(e, "gradient sum launch");
+        }
+    return M3_OK;
+}
+
+m3_status m3_linattn_step(const m3_linattn_dims* dims, const m3_linattn_inputs* in, const float* state_in,
+                          float* state_out, int64_t nstates, const int32_t* slots, const m3_view* o,
+                          void* stream) {
+    set_error(M3_OK, "");
+    m3_status st = check_dims(dims);
+    if (st != M3_OK) return st;
+    if (dims->seqlen != 1) return err(M3_ERR_INVALID_ARG, "a step needs seqlen == 1");
+    const bool any = dims->nseq > 0;
+    if ((st = check_inputs(dims, in, any)) != M3_OK) return st;
+    if (in->cu_seqlens) return err(M3_ERR_INVALID_ARG, "a step takes no cu_seqlens");
+    if (nstates < 0 || (!slots && nstates < dims->nseq))
+        return err(M3_ERR_INVALID_ARG, "nstates (%lld) is below nseq (%lld)", (long long)nstates, (long long)dims->nseq);
+    if (reinterpret_cast<uintptr_t>(slots) & 3u) return err(M3_ERR_INVALID_ARG, "slots is misaligned");
+    if (any && nstates > 0 && (!state_in || !state_out)) return err(M3_ERR_INVALID_ARG, "state_in and state_out are required");
+    if ((st = check_state(state_in, "state_in")) != M3_OK || (st = check_state(state_out, "state_out")) != M3_OK ||
+        (st = check_view(o, "o", dims->in_dtype == M3_BF16 ? 2 : 4, any)) != M3_OK)
+        return st;
+    if (dims->nseq * dims->nheads > kMaxGrid / 4) return err(M3_ERR_UNSUPPORTED, "nseq * nheads exceeds the grid limit");
+    if (!any || nstates == 0) return M3_OK;
+    LinStep p{};
+    p.q = tensor(in->q, dims->nheads, dims->qheads, false);
+    p.k = tensor(in->k, dims->nheads, dims->kheads, false);
+    p.v = tensor(in->v, dims->nheads, dims->vheads, false);
+    p.log_decay = in->log_decay;
+    p.state_in = state_in;
+    p.state_out = state_out;
+    p.nstates = nstates;
+    p.slots = slots;
+    p.o = o->data;
+    p.o_batch = o->batch;
+    p.o_head = o->head;
+    p.nseq = dims->nseq;
+    p.H = static_cast<int>(dims->nheads);
+    p.K = static_cast<int>(dims->kdim);
+    p.V = static_cast<int>(dims->vdim);
+    p.scale = dims->scale;
+    const cudaError_t e = launch_lin_step(p, dims->in_dtype == M3_BF16, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? M3_OK : cuda_err(e, "linear attention step launch");
+}
+
+m3_status m3_linattn_check(void) {
+    set_error(M3_OK, "");
+    int flag = 0;
+    const cudaError_t e = lin_tc_timeout(&flag);
+    if (e != cudaSuccess) return cuda_err(e, "timeout mark");
+    return flag ? err(M3_ERR_TIMEOUT, "a bounded wait inside a linear attention kernel gave up") : M3_OK;
+}
+
+}  // extern "C"

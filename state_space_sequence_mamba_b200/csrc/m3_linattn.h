@@ -1,0 +1,186 @@
+// Internal declarations of linear attention with a decay for each head: the pass that the
+// forward and each gradient run, and its launchers.
+//
+// One pass. Per sequence and head, with a = e^{log_decay}:
+//     y_t = p_scale sum_{s <= t} a^{t - s} (q_t . k_s) v_s + o_scale a^{t + 1} H_in^T q_t
+//     H_out = a^n H_in + x_scale sum_s a^{n - 1 - s} k_s v_s^T
+// run over the tokens in order or (reverse) from the last one back. The forward is
+// (q, k, v) -> o; dq is (do, v, k); dk and dv are (v, do, q) and (k, q, do) in reverse: the
+// gradients of a bilinear recurrence are the same recurrence with the operands exchanged.
+// The state's columns (of v and y) are independent, so a pass is cut into 64-column tiles.
+// Long sequences are cut into segments: a first launch runs each segment's state from zero
+// (state_only), and in the second every segment sums its predecessors' end states, decayed.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace m3 {
+
+constexpr int kLinTile = 64;        // columns of v and y one CTA owns
+constexpr int kLinMaxSegs = 64;     // segments of one sequence of a batch
+
+struct LinTensor {
+    const void* p;
+    int64_t batch, token, head;     // strides in elements
+    int ratio;                      // head h reads head h / ratio
+};
+
+struct LinJob {
+    LinTensor q, k, v;
+    void* y;
+    int64_t y_batch, y_token, y_head;   // head h writes at h * y_head
+    int y_f32;                      // y is fp32 (a per-head gradient still to be summed)
+    int Dk, Dv, tiles;              // tiles = ceil(Dv / 64)
+    int reverse;
+    float p_scale, o_scale, x_scale;
+    // state before the first token in processing order: element (k, v) of unit u at
+    // init[u * Dk * Dv + k * init_k + v * init_v]; in reverse it enters the last token's
+    // adjoint undecayed (the recurrence's R_T with a R_T = init)
+    const float* init;
+    int64_t init_k, init_v;
+    float* final_state;             // [unit][Dk][Dv], in reverse times a once more; or null
+};
+
+struct LinParams {
+    const float* log_decay;
+    const int32_t* cu;              // packed sequences, or null
+    int nseq, H;
+    int64_t L;                      // tokens of each sequence, or rows in all
+    int seg_len;                    // tokens of a segment (a multiple of 128)
+    int nseg;                       // segments of every sequence (batches)
+    int64_t blocks_x;               // (sequence, segment) pairs, or (packed) a bound of theirs
+    int njobs, rtiles;              // rtiles = all jobs' tiles
+    float* seg;                     // segment end states, [blocks_x][H][rtiles][seg_rows][64]
+    int seg_rows;
+    LinJob job[3];
+};
+
+// Cuts of nseq sequences of L tokens (packed: L rows in all) for `slots` CTAs on the device.
+struct LinPlan {
+    int seg_len, nseg;
+    int64_t blocks_x;
+    bool cut;                       // some sequence may have more than one segment
+};
+LinPlan lin_plan(int64_t nseq, int64_t L, bool packed, int64_t per_x, int64_t slots);
+
+// fp32 on the CUDA cores, any dims and strides.
+int lin_simt_slots();
+cudaError_t launch_lin_simt(const LinParams& p, bool bf16, bool cut, cudaStream_t s);
+// bf16 on the tensor cores: Dk <= 128, 16-byte aligned tensors.
+int lin_tc_slots();
+bool lin_tc_supported(const LinParams& p);
+cudaError_t launch_lin_tc(const LinParams& p, bool cut, cudaStream_t s);
+cudaError_t lin_tc_timeout(int* flag);   // reads and clears the timeout mark (blocks)
+
+struct LinStep {
+    LinTensor q, k, v;
+    const float* log_decay;
+    const float* state_in;
+    float* state_out;
+    int64_t nstates;
+    const int32_t* slots;
+    void* o;
+    int64_t o_batch, o_head;
+    int64_t nseq;
+    int H, K, V;
+    float scale;
+};
+cudaError_t launch_lin_step(const LinStep& p, bool bf16, cudaStream_t s);
+
+#ifdef __CUDACC__
+// What a CTA's (sequence, segment) index stands for.
+struct LinWhere {
+    int seq, seg, nseg;
+    int64_t row0;       // the sequence's first row (token index inside its batch entry)
+    int64_t batch;      // batch entry of the tensors
+    int64_t len;        // tokens of the sequence
+    bool valid;
+};
+
+// Sequence and segment of block x. Packed: the running count of segments, 32 sequences at a
+// time (all lanes of a warp call this together).
+__device__ __forceinline__ LinWhere lin_locate(const LinParams& p, int64_t x) {
+    LinWhere w{};
+    if (!p.cu) {
+        w.seq = static_cast<int>(x / p.nseg);
+        w.seg = static_cast<int>(x % p.nseg);
+        w.nseg = p.nseg;
+        w.batch = w.seq;
+        w.len = p.L;
+        w.valid = w.seq < p.nseq;
+        return w;
+    }
+    const int lane = threadIdx.x & 31;
+    int64_t before = 0;
+    for (int base = 0; base < p.nseq; base += 32) {
+        const int i = base + lane;
+        int64_t s = 0, e = 0;
+        int64_t n = 0;
+        if (i < p.nseq) {
+            s = p.cu[i];
+            e = p.cu[i + 1];
+            s = s < 0 ? 0 : (s > p.L ? p.L : s);
+            e = e < s ? s : (e > p.L ? p.L : e);
+            n = (e - s + p.seg_len - 1) / p.seg_len;
+            if (n < 1) n = 1;
+        }
+        int64_t incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, before + incl > x);
+        if (hit) {
+            const int src = __ffs(hit) - 1;
+            w.seq = base + src;
+            w.seg = static_cast<int>(x - before - __shfl_sync(0xffffffffu, incl - n, src));
+            w.nseg = static_cast<int>(__shfl_sync(0xffffffffu, n, src));
+            w.row0 = __shfl_sync(0xffffffffu, s, src);
+            w.len = __shfl_sync(0xffffffffu, e - s, src);
+            w.valid = true;
+            return w;
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return w;
+}
+
+// a^n from log2(a): exact at n = 0 whatever a is (a = 0 included).
+__device__ __forceinline__ float lin_pow(float g2, float n) { return n == 0.f ? 1.f : exp2f(g2 * n); }
+
+// Element (r, c) of the state with which segment w.seg of job j starts (processing order), except
+// that in reverse the first segment's state still lacks no decay (see LinJob::init).
+// order: 0 = first in processing order.
+__device__ __forceinline__ float lin_start_state(const LinParams& p, const LinJob& j, const LinWhere& w,
+                                                 int64_t x, int h, int rt, int tile, float g2, int r, int c) {
+    const int order = j.reverse ? w.nseg - 1 - w.seg : w.seg;
+    const int64_t seg0 = static_cast<int64_t>(w.seg) * p.seg_len;
+    float acc = 0.f;
+    if (j.init && r < j.Dk && tile * kLinTile + c < j.Dv) {
+        // tokens already processed before this segment
+        const int64_t done = j.reverse ? (order == 0 ? 0 : w.len - (seg0 + p.seg_len)) : seg0;
+        const float f = lin_pow(g2, static_cast<float>(j.reverse && done > 0 ? done - 1 : done));
+        const int64_t unit = static_cast<int64_t>(w.seq) * p.H + h;
+        if (f != 0.f)
+            acc = f * j.init[unit * j.Dk * j.Dv + r * j.init_k +
+                             static_cast<int64_t>(tile * kLinTile + c) * j.init_v];
+    }
+    for (int o = 0; o < order; ++o) {
+        const int sg = j.reverse ? w.nseg - 1 - o : o;
+        // tokens between that segment's end and this one's start
+        int64_t gap;
+        if (!j.reverse) gap = seg0 - static_cast<int64_t>(sg + 1) * p.seg_len;
+        else gap = static_cast<int64_t>(sg) * p.seg_len - (seg0 + p.seg_len);
+        const float f = lin_pow(g2, static_cast<float>(gap));
+        if (f == 0.f) continue;
+        const float* e = p.seg + (((x - w.seg + sg) * p.H + h) * p.rtiles + rt) *
+                                     static_cast<int64_t>(p.seg_rows) * kLinTile;
+        acc = fmaf(f, e[static_cast<int64_t>(r) * kLinTile + c], acc);
+    }
+    return acc;
+}
+#endif
+
+}  // namespace m3

@@ -1,0 +1,152 @@
+// One token of linear attention for every sequence: S <- a S + k v^T, o = scale S^T q.
+//
+// Bound by HBM: the fp32 state (K V 4 bytes per sequence and head) is read once and written once,
+// 5 flops per 8 bytes. A CTA owns a sequence's head and a block of TX float4 columns of its state;
+// its 256 threads stand on 256 / TX rows, so a warp reads and writes whole runs of a row, and each
+// thread issues the loads of up to 8 rows before it uses the first. The products with q are summed
+// over the thread's rows in registers, then over the row groups through shared memory, in a
+// fixed order.
+#include "m3_common.cuh"
+#include "m3_internal.h"
+#include "m3_linattn.h"
+
+namespace m3 {
+namespace {
+
+constexpr int kThreads = 256, kRowsAhead = 8;
+
+template <typename T, int TX>
+__global__ void __launch_bounds__(kThreads)
+lin_step_kernel(const LinStep p, int tiles) {
+    constexpr int RY = kThreads / TX;
+    __shared__ float s_q[256], s_k[256];
+    __shared__ float4 s_o[kThreads];
+    const int tid = threadIdx.x, cx = tid % TX, ry = tid / TX;
+    const int64_t unit = blockIdx.x / tiles;
+    const int tile = static_cast<int>(blockIdx.x - unit * tiles);
+    const int64_t i = unit / p.H;
+    const int h = static_cast<int>(unit - i * p.H);
+    const int64_t st = p.slots ? p.slots[i] : i;
+    if (st < 0 || st >= p.nstates) return;
+    const T* q = static_cast<const T*>(p.q.p) + i * p.q.batch + (h / p.q.ratio) * p.q.head;
+    const T* k = static_cast<const T*>(p.k.p) + i * p.k.batch + (h / p.k.ratio) * p.k.head;
+    const T* v = static_cast<const T*>(p.v.p) + i * p.v.batch + (h / p.v.ratio) * p.v.head;
+    const float a = expf(p.log_decay[h]);
+    const int64_t base = (st * p.H + h) * p.K * static_cast<int64_t>(p.V);
+    const int col = 4 * (tile * TX + cx);
+    const bool on = col < p.V;
+    // TX is a multiple-of-4 column kernel: V % 4 == 0 (see the launch)
+    const float4* src = reinterpret_cast<const float4*>(p.state_in + base + col);
+    float4* dst = reinterpret_cast<float4*>(p.state_out + base + col);
+    const int row4 = p.V / 4;
+    float4 vv = make_float4(0.f, 0.f, 0.f, 0.f), o = vv;
+    float4 first[kRowsAhead];
+    // the state's first rows are on their way before anything else is waited for
+#pragma unroll
+    for (int u = 0; u < kRowsAhead; ++u) {
+        const int r = ry + u * RY;
+        first[u] = (on && r < p.K) ? __ldcs(src + static_cast<int64_t>(r) * row4) : vv;
+    }
+    for (int d = tid; d < p.K; d += kThreads) {
+        s_q[d] = to_f(q[d]);
+        s_k[d] = to_f(k[d]);
+    }
+    if (on) vv = make_float4(to_f(v[col]), to_f(v[col + 1]), to_f(v[col + 2]), to_f(v[col + 3]));
+    __syncthreads();
+    for (int r0 = ry; r0 < p.K; r0 += kRowsAhead * RY) {
+        if (r0 != ry) {
+#pragma unroll
+            for (int u = 0; u < kRowsAhead; ++u) {
+                const int r = r0 + u * RY;
+                if (on && r < p.K) first[u] = __ldcs(src + static_cast<int64_t>(r) * row4);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kRowsAhead; ++u) {
+            const int r = r0 + u * RY;
+            if (on && r < p.K) {
+                const float kr = s_k[r], qr = s_q[r];
+                float4 s = first[u];
+                s.x = fmaf(a, s.x, kr * vv.x); s.y = fmaf(a, s.y, kr * vv.y);
+                s.z = fmaf(a, s.z, kr * vv.z); s.w = fmaf(a, s.w, kr * vv.w);
+                __stcs(dst + static_cast<int64_t>(r) * row4, s);
+                o.x = fmaf(qr, s.x, o.x); o.y = fmaf(qr, s.y, o.y);
+                o.z = fmaf(qr, s.z, o.z); o.w = fmaf(qr, s.w, o.w);
+            }
+        }
+    }
+    s_o[tid] = o;
+    __syncthreads();
+    // halves of the row groups added until one is left
+#pragma unroll
+    for (int half = RY / 2; half > 0; half /= 2) {
+        if (ry < half) {
+            const float4 b = s_o[tid + half * TX];
+            o.x += b.x; o.y += b.y; o.z += b.z; o.w += b.w;
+            s_o[tid] = o;
+        }
+        __syncthreads();
+    }
+    if (ry == 0 && on) {
+        T* y = static_cast<T*>(p.o) + i * p.o_batch + h * p.o_head + col;
+        y[0] = from_f<T>(p.scale * o.x); y[1] = from_f<T>(p.scale * o.y);
+        y[2] = from_f<T>(p.scale * o.z); y[3] = from_f<T>(p.scale * o.w);
+    }
+}
+
+// V not a multiple of 4: one thread per column, rows in turn.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) lin_step_any_kernel(const LinStep p) {
+    __shared__ float s_q[256], s_k[256];
+    const int tid = threadIdx.x;
+    const int64_t unit = blockIdx.x, i = unit / p.H;
+    const int h = static_cast<int>(unit - i * p.H);
+    const int64_t st = p.slots ? p.slots[i] : i;
+    if (st < 0 || st >= p.nstates) return;
+    const T* q = static_cast<const T*>(p.q.p) + i * p.q.batch + (h / p.q.ratio) * p.q.head;
+    const T* k = static_cast<const T*>(p.k.p) + i * p.k.batch + (h / p.k.ratio) * p.k.head;
+    const T* v = static_cast<const T*>(p.v.p) + i * p.v.batch + (h / p.v.ratio) * p.v.head;
+    for (int d = tid; d < p.K; d += kThreads) {
+        s_q[d] = to_f(q[d]);
+        s_k[d] = to_f(k[d]);
+    }
+    __syncthreads();
+    if (tid >= p.V) return;
+    const float a = expf(p.log_decay[h]), vv = to_f(v[tid]);
+    const int64_t base = (st * p.H + h) * p.K * static_cast<int64_t>(p.V) + tid;
+    float o = 0.f;
+    for (int r = 0; r < p.K; ++r) {
+        const int64_t at = base + static_cast<int64_t>(r) * p.V;
+        const float s = fmaf(a, p.state_in[at], s_k[r] * vv);
+        p.state_out[at] = s;
+        o = fmaf(s_q[r], s, o);
+    }
+    static_cast<T*>(p.o)[i * p.o_batch + h * p.o_head + tid] = from_f<T>(p.scale * o);
+}
+
+template <typename T>
+cudaError_t launch_t(const LinStep& p, cudaStream_t s) {
+    const int64_t units = p.nseq * p.H;
+    if (p.V % 4 != 0) {
+        lin_step_any_kernel<T><<<static_cast<unsigned>(units), kThreads, 0, s>>>(p);
+        return cudaGetLastError();
+    }
+    const int c4 = p.V / 4;
+    if (c4 > 8) {
+        const int tiles = (c4 + 15) / 16;
+        lin_step_kernel<T, 16><<<static_cast<unsigned>(units * tiles), kThreads, 0, s>>>(p, tiles);
+    } else if (c4 > 4) {
+        lin_step_kernel<T, 8><<<static_cast<unsigned>(units), kThreads, 0, s>>>(p, 1);
+    } else {
+        lin_step_kernel<T, 4><<<static_cast<unsigned>(units), kThreads, 0, s>>>(p, 1);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_lin_step(const LinStep& p, bool bf16, cudaStream_t s) {
+    return bf16 ? launch_t<__nv_bfloat16>(p, s) : launch_t<float>(p, s);
+}
+
+}  // namespace m3
