@@ -103,8 +103,18 @@ m3_status check_inputs(const m3_linattn_dims* d, const m3_linattn_inputs* in, bo
     return M3_OK;
 }
 
-LinTensor tensor(const m3_view& v, int64_t H, int64_t heads, bool packed) {
-    return LinTensor{v.data, packed ? 0 : v.batch, v.token, v.head, static_cast<int>(H / heads)};
+// A dimension of one entry has stride 0, whatever the caller's says.
+LinTensor tensor(const m3_linattn_dims* d, const m3_view& v, int64_t heads, bool packed) {
+    return LinTensor{v.data, packed || d->nseq == 1 ? 0 : v.batch, d->seqlen == 1 ? 0 : v.token,
+                     heads == 1 ? 0 : v.head, static_cast<int>(d->nheads / heads)};
+}
+
+void set_output(LinJob& j, const m3_linattn_dims* d, const m3_view& v, int64_t heads, bool packed) {
+    const LinTensor t = tensor(d, v, heads, packed);
+    j.y = v.data;
+    j.y_batch = t.batch;
+    j.y_token = t.token;
+    j.y_head = t.head;
 }
 
 LinParams make_params(const m3_linattn_dims* d, const m3_linattn_inputs* in) {
@@ -266,13 +276,11 @@ m3_status m3_linattn_fwd(const m3_linattn_dims* dims, const m3_linattn_inputs* i
     if (!any) return pass_state(dims, init, final_state, s);
     LinParams p = make_params(dims, in);
     const bool packed = in->cu_seqlens != nullptr;
-    const int64_t H = dims->nheads;
     LinJob& j = p.job[0];
-    j.q = tensor(in->q, H, dims->qheads, packed);
-    j.k = tensor(in->k, H, dims->kheads, packed);
-    j.v = tensor(in->v, H, dims->vheads, packed);
-    j.y = o->data;
-    j.y_batch = packed ? 0 : o->batch; j.y_token = o->token; j.y_head = o->head;
+    j.q = tensor(dims, in->q, dims->qheads, packed);
+    j.k = tensor(dims, in->k, dims->kheads, packed);
+    j.v = tensor(dims, in->v, dims->vheads, packed);
+    set_output(j, dims, *o, dims->nheads, packed);
     j.Dk = static_cast<int>(dims->kdim);
     j.Dv = static_cast<int>(dims->vdim);
     j.tiles = fwd_tiles(dims);
@@ -315,8 +323,8 @@ m3_status m3_linattn_bwd(const m3_linattn_dims* dims, const m3_linattn_inputs* i
     LinParams p = make_params(dims, in);
     const int64_t H = dims->nheads;
     const int K = static_cast<int>(dims->kdim), V = static_cast<int>(dims->vdim);
-    const LinTensor q = tensor(in->q, H, dims->qheads, packed), k = tensor(in->k, H, dims->kheads, packed),
-                    v = tensor(in->v, H, dims->vheads, packed), g = tensor(*d_o, H, H, packed);
+    const LinTensor q = tensor(dims, in->q, dims->qheads, packed), k = tensor(dims, in->k, dims->kheads, packed),
+                    v = tensor(dims, in->v, dims->vheads, packed), g = tensor(dims, *d_o, H, packed);
     char* ws = static_cast<char*>(workspace);
     char* seg = ws;
     ws += seg_bytes(dims, packed, bwd_tiles(dims), bwd_rows(dims));
@@ -351,8 +359,7 @@ m3_status m3_linattn_bwd(const m3_linattn_dims* dims, const m3_linattn_inputs* i
             j.y_token = H * Dv[i];
             j.y_batch = packed ? 0 : dims->seqlen * j.y_token;
         } else {
-            j.y = outs[i]->data;
-            j.y_batch = packed ? 0 : outs[i]->batch; j.y_token = outs[i]->token; j.y_head = outs[i]->head;
+            set_output(j, dims, *outs[i], H, packed);
         }
     }
     p.job[2].final_state = dinit;
@@ -390,9 +397,9 @@ m3_status m3_linattn_step(const m3_linattn_dims* dims, const m3_linattn_inputs* 
     if (dims->nseq * dims->nheads > kMaxGrid / 4) return err(M3_ERR_UNSUPPORTED, "nseq * nheads exceeds the grid limit");
     if (!any || nstates == 0) return M3_OK;
     LinStep p{};
-    p.q = tensor(in->q, dims->nheads, dims->qheads, false);
-    p.k = tensor(in->k, dims->nheads, dims->kheads, false);
-    p.v = tensor(in->v, dims->nheads, dims->vheads, false);
+    p.q = tensor(dims, in->q, dims->qheads, false);
+    p.k = tensor(dims, in->k, dims->kheads, false);
+    p.v = tensor(dims, in->v, dims->vheads, false);
     p.log_decay = in->log_decay;
     p.state_in = state_in;
     p.state_out = state_out;
