@@ -92,51 +92,48 @@ cudaError_t launch_lin_step(const LinStep& p, bool bf16, cudaStream_t s);
 // What a CTA's (sequence, segment) index stands for.
 struct LinWhere {
     int seq, seg, nseg;
-    int64_t row0;       // the sequence's first row (token index inside its batch entry)
-    int64_t batch;      // batch entry of the tensors
-    int64_t len;        // tokens of the sequence
+    int row0;           // the sequence's first row (token index inside its batch entry)
+    int batch;          // batch entry of the tensors
+    int len;            // tokens of the sequence
     bool valid;
 };
 
 // Sequence and segment of block x. Packed: the running count of segments, 32 sequences at a
 // time (all lanes of a warp call this together).
-__device__ __forceinline__ LinWhere lin_locate(const LinParams& p, int64_t x) {
+__device__ __forceinline__ LinWhere lin_locate(const LinParams& p, unsigned x) {
     LinWhere w{};
     if (!p.cu) {
-        w.seq = static_cast<int>(x / p.nseg);
-        w.seg = static_cast<int>(x % p.nseg);
+        const unsigned nseg = static_cast<unsigned>(p.nseg), seq = x / nseg;
+        w.seq = w.batch = static_cast<int>(seq);
+        w.seg = static_cast<int>(x - seq * nseg);
         w.nseg = p.nseg;
-        w.batch = w.seq;
-        w.len = p.L;
+        w.len = static_cast<int>(p.L);
         w.valid = w.seq < p.nseq;
         return w;
     }
-    const int lane = threadIdx.x & 31;
-    int64_t before = 0;
+    const int lane = threadIdx.x & 31, L = static_cast<int>(p.L);
+    int64_t before = 0;         // offsets that overlap may add up to anything
+#pragma unroll 1
     for (int base = 0; base < p.nseq; base += 32) {
         const int i = base + lane;
-        int64_t s = 0, e = 0;
-        int64_t n = 0;
+        int s = 0, e = 0, n = 0;
         if (i < p.nseq) {
-            s = p.cu[i];
-            e = p.cu[i + 1];
-            s = s < 0 ? 0 : (s > p.L ? p.L : s);
-            e = e < s ? s : (e > p.L ? p.L : e);
-            n = (e - s + p.seg_len - 1) / p.seg_len;
-            if (n < 1) n = 1;
+            s = min(max(p.cu[i], 0), L);
+            e = min(max(p.cu[i + 1], s), L);
+            n = max((e - s + p.seg_len - 1) / p.seg_len, 1);
         }
-        int64_t incl = n;
+        int incl = n;           // at most 32 (2^30 / 128 + 1)
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+            const int up = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += up;
         }
-        const unsigned hit = __ballot_sync(0xffffffffu, before + incl > x);
+        const unsigned hit = __ballot_sync(0xffffffffu, before + incl > static_cast<int64_t>(x));
         if (hit) {
             const int src = __ffs(hit) - 1;
             w.seq = base + src;
-            w.seg = static_cast<int>(x - before - __shfl_sync(0xffffffffu, incl - n, src));
-            w.nseg = static_cast<int>(__shfl_sync(0xffffffffu, n, src));
+            w.seg = static_cast<int>(x - before) - __shfl_sync(0xffffffffu, incl - n, src);
+            w.nseg = __shfl_sync(0xffffffffu, n, src);
             w.row0 = __shfl_sync(0xffffffffu, s, src);
             w.len = __shfl_sync(0xffffffffu, e - s, src);
             w.valid = true;

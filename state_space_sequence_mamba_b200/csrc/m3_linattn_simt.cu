@@ -57,8 +57,8 @@ lin_simt_kernel(const __grid_constant__ LinParams p) {
     constexpr int RI = C / 16;      // rows a thread owns in the S and y products
     extern __shared__ __align__(16) float sm[];
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const int64_t per_x = static_cast<int64_t>(p.H) * p.rtiles;
-    const int64_t x = blockIdx.x / per_x;
+    const unsigned per_x = static_cast<unsigned>(p.H) * p.rtiles;
+    const unsigned x = blockIdx.x / per_x;
     const int rem = static_cast<int>(blockIdx.x - x * per_x);
     const int h = rem / p.rtiles, rt = rem % p.rtiles;
     int ji = 0, tile = rt;
@@ -199,7 +199,7 @@ lin_simt_kernel(const __grid_constant__ LinParams p) {
     }
     __syncthreads();
     if (kStateOnly) {
-        float* e = p.seg + ((x * p.H + h) * p.rtiles + rt) * static_cast<int64_t>(p.seg_rows) * kVT;
+        float* e = p.seg + ((static_cast<int64_t>(x) * p.H + h) * p.rtiles + rt) * p.seg_rows * kVT;
         for (int i = tid; i < j.Dk * kVT; i += kThreads) e[i] = sh[(i / kVT) * kVS + i % kVT];
         return;
     }
