@@ -8,9 +8,10 @@
 //     O2 = P v                                     M128 N64  K=128  (A = P in TMEM)
 //     y  = o_scale a^{e(i)} O1 + O2
 //     H  <- a^n H + k^T v',  v' = x_scale a^{w(j)} v      M128 N=64 parts K=128
-// The mask's powers of a multiply the scores in fp32, in two factors per 16 columns that are both at
+// The mask's powers of a multiply the scores in fp32, in two factors per 32 columns that are both at
 // most 1 for a <= 1 (a^{t - last column} of the thread's row, a^{last - column} of the column), so
-// nothing overflows however strong the decay; the diagonal blocks take a^{t - j} from a table. q, k and v enter the products as stored. Roundings to bf16: P and H as operands of the
+// nothing overflows however strong the decay; the diagonal blocks take theirs from the same table,
+// shifted by the row. q, k and v enter the products as stored. Roundings to bf16: P and H as operands of the
 // output's products (the output is rounded to bf16 itself), and v' as the sum of bf16 parts: two
 // (2^-17) for a state that only feeds bf16 operands, three (2^-25) for one that is returned. The
 // parts lie side by side as one operand of 128 or 192 columns, so k is read once for all of them,
@@ -63,10 +64,11 @@ enum {
     B_P, B_P1, B_H0, B_VP,              // operands written: P, the state's, v'
     B_SFREE, B_SFREE1, B_OFREE, B_HFREE,            // accumulators read: S and O2, O1, k^T v'
     B_QKFREE, B_QKFREE1, B_VFREE, B_VFREE1,         // stages free for the next load
+    B_CLEAN,                            // rows behind the last token zeroed (once)
     B_DRAIN, B_DRAIN1, B_DRAIN2, kNumBars
 };
 __host__ __device__ constexpr uint32_t bar_count(int b) {
-    return (b == B_H0 || b == B_VP || b == B_HFREE) ? 8
+    return (b == B_H0 || b == B_VP || b == B_HFREE || b == B_CLEAN) ? 8
          : (b == B_P || b == B_P1 || b == B_SFREE || b == B_SFREE1 || b == B_OFREE) ? 4
          : (b == B_QKFREE || b == B_QKFREE1) ? 3      // S, O1 and k^T v' done
          : (b == B_VFREE || b == B_VFREE1) ? 9        // read by the v' warps, O2 done
@@ -84,18 +86,16 @@ struct LinTcParams {
     int parts[3];               // bf16 parts of v'
 };
 
-// Waits for the phase of `bar` with the given parity, giving up when another role has or after
-// kMaxPolls polls (the thread is suspended for up to a microsecond in each: about a second). No
-// clock is read: the loop stays small, and it is in the code a dozen times.
+// Waits for the phase of `bar` with the given parity, giving up after kMaxPolls polls (the thread is
+// suspended for up to a microsecond in each: about a second). The loop is in the code a dozen times,
+// so it reads neither a clock nor the flag: a role that gave up makes the others run out of polls too.
 constexpr int kMaxPolls = 1 << 21;
 constexpr long long kDrainCycles = 200000000LL;
 __device__ __forceinline__ bool lwait(uint64_t* bar, int parity, volatile int* abort_flag) {
     const uint32_t a = smem_u32(bar);
 #pragma unroll 1
-    for (int i = 0; i < kMaxPolls; ++i) {
+    for (int i = 0; i < kMaxPolls; ++i)
         if (mbar_try_wait_sleep(a, parity & 1, 1000u)) return true;
-        if (*abort_flag) return false;
-    }
     *abort_flag = 1;
     return false;
 }
@@ -143,6 +143,20 @@ __device__ __forceinline__ void tma_prefetch_4d(const void* tmap, int c0, int c1
                  :: "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3) : "memory");
 }
 
+// The 72 registers a thread that 28 warps leave are dealt out again by what the roles hold. Spills are
+// what to avoid: beside 227 KB of shared memory the L1 cache is too small to hold them.
+constexpr int kRegsLaunch = 72, kRegsRow = 96, kRegsState = 64, kRegsIssue = 40;
+static_assert(2 * kRegsRow + 2 * kRegsState + 2 * kRegsLaunch + kRegsIssue == 7 * kRegsLaunch,
+              "an increase beyond what the block was launched with would wait for ever");
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N));
+}
+
 // 32 bytes to global memory (32-byte aligned)
 __device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
@@ -158,7 +172,9 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ __align__(8) uint64_t bars[kNumBars];
     __shared__ __align__(16) float pw[kC + 4];
-    __shared__ __align__(16) float cf[16];
+    // a^{31 - k} (reverse: a^{k - 31}), zero where the exponent is negative: entries 31 - r + i are row r
+    // of the mask's diagonal blocks, a^{31 - i} (a^i) the columns' factors of the others
+    __shared__ float mask[64];
     __shared__ uint32_t tslot;
     __shared__ volatile int s_abort;
 
@@ -197,7 +213,10 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
     }
     if (warp == kLoadWarp) tmem_alloc(&tslot, kTmemCols);
     if (tid <= kC) pw[tid] = lin_pow(g2, static_cast<float>(tid));
-    if (tid >= 256 && tid < 272) cf[tid - 256] = lin_pow(g2, static_cast<float>(rev ? tid - 256 : 271 - tid));
+    if (tid >= 256 && tid < 320) {
+        const int d = rev ? tid - 287 : 287 - tid;
+        mask[tid - 256] = d >= 0 ? lin_pow(g2, static_cast<float>(d)) : 0.f;
+    }
     if (slabs == 1) {   // the state's rows 64 .. 127: zeros (never loaded)
         for (int i = tid; i < static_cast<int>(kSlab / 16); i += kThreads) {
             *reinterpret_cast<uint4*>(sm + S_K + kSlab + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
@@ -213,12 +232,13 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
 
     if (warp < kRowWarps) {
         // ================= rows: S -> P, then y =================
+        if constexpr (!kStateOnly) regs_inc<kRegsRow>();
         if (!kStateOnly) {
             const int g = warp >> 2, rw = warp & 3, t = 32 * rw + lane;
             const uint32_t ls = tmem + ((32u * rw) << 16) + T_S + 128u * g;     // S, P and (+64) O2
             const uint32_t lo = tmem + ((32u * rw) << 16) + T_O1;
             const float ps = j.p_scale;
-            const int sgn = rev ? 1 : -1, back = rev ? 0 : 15;
+            const int sgn = rev ? 1 : -1;
             const int es = j.y_f32 ? 4 : 2;
             const int cols = j.Dv - tile * kVT;
             uint8_t* ybase = static_cast<uint8_t*>(j.y) +
@@ -230,54 +250,27 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
                 const int t0 = chunk_t0(c), n = chunk_n(c);
                 if (!lwait_warp(&bars[B_S + g], c >> 1, &s_abort)) break;
                 fence_after_sync();
-                // sixteen columns at a time, as far as columns hold tokens
+                // 32 columns at a time, as far as columns hold tokens (scores behind the last are zero)
 #pragma unroll 1
-                for (int b = 0; 16 * b < n; ++b) {
-                    uint32_t pk[8];
-                    const int ahead = sgn * ((b >> 1) - rw);    // 0: the diagonal block of 32 x 32
+                for (int b = 0; 32 * b < n; ++b) {
+                    uint32_t pk[16];
+                    const int ahead = sgn * (b - rw);           // 0: the diagonal block
                     if (ahead < 0) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) pk[i] = 0u;
+                        for (int i = 0; i < 16; ++i) pk[i] = 0u;
                     } else {
-                        float v[16];
-                        tmem_ld_32x32b_x16(ls + 16u * b, v);
+                        float v[32];
+                        tmem_ld_32x32b_x32(ls + 32u * b, v);
+                        const float* m = mask + (ahead > 0 ? (rev ? 31 : 0) : 31 - lane);
+                        const float f = ahead > 0 ? ps * pw[sgn * (32 * b - t) - (rev ? 0 : 31)] : ps;
                         tmem_wait_ld();
-                        if (ahead > 0 && 16 * b + 16 <= n) {
-                            const float f = ps * pw[sgn * (16 * b - t) - back];
 #pragma unroll
-                            for (int i = 0; i < 16; i += 4) {
-                                const float4 c4 = *reinterpret_cast<const float4*>(cf + i);
-                                pk[i / 2] = pack2(v[i] * f * c4.x, v[i + 1] * f * c4.y);
-                                pk[i / 2 + 1] = pack2(v[i + 2] * f * c4.z, v[i + 3] * f * c4.w);
-                            }
-                        } else {
-                            // d = the distance of the piece's column 0, last = the last column that holds a
-                            // token; the mask by sign bits (a select of a loaded value becomes a branch)
-                            const int d = sgn * (16 * b - t), last = n - 1 - 16 * b;
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const int di = d + sgn * i;
-                                const int off = (di | (last - i)) >> 31;
-                                v[i] = __int_as_float(__float_as_int(v[i] * (ps * pw[max(di, 0)])) & ~off);
-                            }
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) pk[i] = pack2(v[2 * i], v[2 * i + 1]);
-                        }
+                        for (int i = 0; i < 16; ++i) pk[i] = pack2(v[2 * i] * f * m[2 * i], v[2 * i + 1] * f * m[2 * i + 1]);
                     }
-                    // piece b of P lies over S's piece b / 2, which has been read
-                    tmem_st_32x32b_x8(ls + 8u * b, pk);
+                    // block b of P lies over S's block b / 2, which has been read
+                    tmem_st_32x32b_x16(ls + 16u * b, pk);
                 }
                 tmem_wait_st();
-                if (n < kC) {
-                    // rows of v behind the last token, as far as the product reads: another sequence's,
-                    // or anything (their scores are zero, but zero times NaN is not)
-                    if (!lwait_warp(&bars[B_V + g], c >> 1, &s_abort)) break;
-                    if (t >= n)
-#pragma unroll 1
-                        for (int i = 0; i < 8; ++i)
-                            *reinterpret_cast<uint4*>(sm + S_V + g * kSlab + t * 128 + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
-                    fence_proxy_async();
-                }
                 fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[B_P + g]);
@@ -287,31 +280,35 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
                 if (!lwait_warp(&bars[B_O1 + g], c >> 1, &s_abort) || !lwait_warp(&bars[B_O2 + g], c >> 1, &s_abort)) break;
                 fence_after_sync();
 #pragma unroll 1
-                for (int q = 0; q < 4; ++q) {
-                    float a[16], o[16];
-                    tmem_ld_32x32b_x16(lo + 16u * q, a);
-                    tmem_ld_32x32b_x16(ls + T_O2 + 16u * q, o);
+                for (int q = 0; q < 2; ++q) {
+                    float a[32], o[32];
+                    tmem_ld_32x32b_x32(lo + 32u * q, a);
+                    tmem_ld_32x32b_x32(ls + T_O2 + 32u * q, o);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] = fmaf(f1, a[i], o[i]);
-                    const int left = t < n ? cols - 16 * q : 0;
+                    for (int i = 0; i < 32; ++i) o[i] = fmaf(f1, a[i], o[i]);
+                    const int left = t < n ? cols - 32 * q : 0;
                     if (j.y_f32) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t u[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) u[k] = __float_as_uint(o[8 * i + k]);
+                            if (8 * i < left) store32(y + 128 * q + 32 * i, u);     // always whole sectors
+                        }
+                    } else {
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             uint32_t u[8];
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) u[k] = __float_as_uint(o[8 * i + k]);
-                            if (8 * i < left) store32(y + 64 * q + 32 * i, u);      // always whole sectors
-                        }
-                    } else {
-                        uint32_t u[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) u[k] = pack2(o[2 * k], o[2 * k + 1]);
-                        if (wide && left >= 16) {
-                            store32(y + 32 * q, u);
-                        } else {
-                            if (left > 0) *reinterpret_cast<uint4*>(y + 32 * q) = make_uint4(u[0], u[1], u[2], u[3]);
-                            if (left > 8) *reinterpret_cast<uint4*>(y + 32 * q + 16) = make_uint4(u[4], u[5], u[6], u[7]);
+                            for (int k = 0; k < 8; ++k) u[k] = pack2(o[16 * i + 2 * k], o[16 * i + 2 * k + 1]);
+                            uint8_t* at = y + 64 * q + 32 * i;
+                            if (wide && left >= 16 * i + 16) {
+                                store32(at, u);
+                            } else {
+                                if (left > 16 * i) *reinterpret_cast<uint4*>(at) = make_uint4(u[0], u[1], u[2], u[3]);
+                                if (left > 16 * i + 8) *reinterpret_cast<uint4*>(at + 16) = make_uint4(u[4], u[5], u[6], u[7]);
+                            }
                         }
                     }
                 }
@@ -325,6 +322,7 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
         }
     } else if (warp < kPartWarp0) {
         // ================= the state: half of row r (32 columns) in a thread's registers =================
+        if constexpr (!kStateOnly) regs_dec<kRegsState>();
         const int r = 32 * (warp & 3) + lane, c0 = (warp - kStateWarp0) >> 2 << 5;
         const uint32_t lb = tmem + ((32u * (warp & 3)) << 16) + T_H + c0;
         const int cols = j.Dv - tile * kVT - c0;        // of this thread's that exist
@@ -453,10 +451,28 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
         // the chunk before still reads theirs.
         const int r = 32 * (warp & 3) + lane, half = (warp - kPartWarp0) >> 2;
 #pragma unroll 1
-        for (int c = 0; c < nupdates; ++c) {
+        for (int c = 0; c < nchunks; ++c) {
             const int st = c & 1, n = chunk_n(c);
-            const float wt = r < n ? j.x_scale * pw[rev ? r : n - 1 - r] : 0.f;
+            if (c >= nupdates && n == kC) break;
             if (!lwait_warp(&bars[B_V + st], c >> 1, &s_abort)) break;
+            if (n < kC) {
+                // Rows of k and v behind the last token, another sequence's or anything, become zeros before
+                // a product reads them: their weights are, but zero times NaN is not.
+                if (!lwait_warp(&bars[B_QK + st], c >> 1, &s_abort)) break;
+                if (r >= n) {
+#pragma unroll 1
+                    for (int i = 0; i < 8; ++i) {
+                        *reinterpret_cast<uint4*>(sm + S_K + (2 * st + half) * kSlab + r * 128 + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
+                        if (i < 4)
+                            *reinterpret_cast<uint4*>(sm + S_V + st * kSlab + swz128(r, 32 * half + 8 * i)) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[B_CLEAN]);
+                if (c >= nupdates) break;
+            }
+            const float wt = r < n ? j.x_scale * pw[rev ? r : n - 1 - r] : 0.f;
             uint32_t p0[16], p1[16], p2[16];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -465,24 +481,13 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[B_VFREE + st]);
-            // rows behind the last token, another sequence's or anything, are zeros: their weights are,
-            // but zero times NaN is not. k's too, as far as the product reads.
-            const uint32_t keep = r < n ? 0xFFFFFFFFu : 0u;
 #pragma unroll
             for (int u = 0; u < 16; ++u) {
-                const uint32_t raw = p0[u] & keep;
-                const float a = wt * lo_f(raw), b = wt * hi_f(raw);
+                const float a = wt * lo_f(p0[u]), b = wt * hi_f(p0[u]);
                 p0[u] = pack2(a, b);
                 const float a1 = a - lo_f(p0[u]), b1 = b - hi_f(p0[u]);
                 p1[u] = pack2(a1, b1);
                 p2[u] = pack2(a1 - lo_f(p1[u]), b1 - hi_f(p1[u]));
-            }
-            if (n < kC) {
-                if (!lwait_warp(&bars[B_QK + st], c >> 1, &s_abort)) break;
-                if (r >= n)
-#pragma unroll 1
-                    for (int i = 0; i < 8; ++i)
-                        *reinterpret_cast<uint4*>(sm + S_K + (2 * st + half) * kSlab + r * 128 + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
             }
             if (c > 0 && !lwait_warp(&bars[B_DH], c - 1, &s_abort)) break;
 #pragma unroll
@@ -497,160 +502,164 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[B_VP]);
         }
-    } else if (warp == kLoadWarp) {
-        // ================= TMA loads (one lane) =================
-        if (lane == 0) {
-            const void* mq = &maps.m[tp.map[ji][0]];
-            const void* mk = &maps.m[tp.map[ji][1]];
-            const void* mv = &maps.m[tp.map[ji][2]];
-            const int hq = h / tp.head_ratio[ji][0], hk = h / tp.head_ratio[ji][1], hv = h / tp.head_ratio[ji][2];
-            const int bq = tp.batched[ji][0] ? w.batch : 0, bk = tp.batched[ji][1] ? w.batch : 0;
-            const int bv = tp.batched[ji][2] ? w.batch : 0, row0 = w.row0;
-            const int loads = kStateOnly ? nupdates : nchunks;
-            int done = 0;
+    } else {
+        if constexpr (!kStateOnly) regs_dec<kRegsIssue>();
+        if (warp == kLoadWarp) {
+            // ================= TMA loads (one lane) =================
+            if (lane == 0) {
+                const void* mq = &maps.m[tp.map[ji][0]];
+                const void* mk = &maps.m[tp.map[ji][1]];
+                const void* mv = &maps.m[tp.map[ji][2]];
+                const int hq = h / tp.head_ratio[ji][0], hk = h / tp.head_ratio[ji][1], hv = h / tp.head_ratio[ji][2];
+                const int bq = tp.batched[ji][0] ? w.batch : 0, bk = tp.batched[ji][1] ? w.batch : 0;
+                const int bv = tp.batched[ji][2] ? w.batch : 0, row0 = w.row0;
+                const int loads = kStateOnly ? nupdates : nchunks;
+                int done = 0;
 #pragma unroll 1
-            for (int c = 0; c < loads; ++c) {
-                const int st = c & 1, at = row0 + chunk_t0(c);
-                if (c > 1 && !lwait(&bars[B_QKFREE + st], (c >> 1) - 1, &s_abort)) break;
-                mbar_arrive_expect_tx(&bars[B_QK + st], (kStateOnly ? 1 : 2) * slabs * kSlab);
-#pragma unroll 1
-                for (int s = 0; s < slabs; ++s) {
-                    tma_load_4d(sm + S_K + (2 * st + s) * kSlab, mk, &bars[B_QK + st], 64 * s, hk, at, bk);
-                    if (!kStateOnly) tma_load_4d(sm + S_Q + (2 * st + s) * kSlab, mq, &bars[B_QK + st], 64 * s, hq, at, bq);
-                }
-                if (c > 1 && !lwait(&bars[B_VFREE + st], (c >> 1) - 1, &s_abort)) {
-                    (void)mbar_wait(&bars[B_QK + st], (c >> 1) & 1, kDrainCycles);
-                    break;
-                }
-                mbar_arrive_expect_tx(&bars[B_V + st], kSlab);
-                tma_load_4d(sm + S_V + st * kSlab, mv, &bars[B_V + st], tile * kVT, hv, at, bv);
-                done = c + 1;
-                if (c + 1 < loads) {    // the next chunk on its way to L2
-                    const int tn = row0 + chunk_t0(c + 1);
+                for (int c = 0; c < loads; ++c) {
+                    const int st = c & 1, at = row0 + chunk_t0(c);
+                    if (c > 1 && !lwait(&bars[B_QKFREE + st], (c >> 1) - 1, &s_abort)) break;
+                    mbar_arrive_expect_tx(&bars[B_QK + st], (kStateOnly ? 1 : 2) * slabs * kSlab);
 #pragma unroll 1
                     for (int s = 0; s < slabs; ++s) {
-                        tma_prefetch_4d(mk, 64 * s, hk, tn, bk);
-                        if (!kStateOnly) tma_prefetch_4d(mq, 64 * s, hq, tn, bq);
+                        tma_load_4d(sm + S_K + (2 * st + s) * kSlab, mk, &bars[B_QK + st], 64 * s, hk, at, bk);
+                        if (!kStateOnly) tma_load_4d(sm + S_Q + (2 * st + s) * kSlab, mq, &bars[B_QK + st], 64 * s, hq, at, bq);
                     }
-                    tma_prefetch_4d(mv, tile * kVT, hv, tn, bv);
+                    if (c > 1 && !lwait(&bars[B_VFREE + st], (c >> 1) - 1, &s_abort)) {
+                        (void)mbar_wait(&bars[B_QK + st], (c >> 1) & 1, kDrainCycles);
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&bars[B_V + st], kSlab);
+                    tma_load_4d(sm + S_V + st * kSlab, mv, &bars[B_V + st], tile * kVT, hv, at, bv);
+                    done = c + 1;
+                    if (c + 1 < loads) {    // the next chunk on its way to L2
+                        const int tn = row0 + chunk_t0(c + 1);
+#pragma unroll 1
+                        for (int s = 0; s < slabs; ++s) {
+                            tma_prefetch_4d(mk, 64 * s, hk, tn, bk);
+                            if (!kStateOnly) tma_prefetch_4d(mq, 64 * s, hq, tn, bq);
+                        }
+                        tma_prefetch_4d(mv, tile * kVT, hv, tn, bv);
+                    }
+                }
+                // every copy has landed before the CTA exits (at once, unless a wait gave up)
+                for (int c = done > 2 ? done - 2 : 0; c < done; ++c) {
+                    (void)mbar_wait(&bars[B_QK + (c & 1)], (c >> 1) & 1, kDrainCycles);
+                    (void)mbar_wait(&bars[B_V + (c & 1)], (c >> 1) & 1, kDrainCycles);
                 }
             }
-            // every copy has landed before the CTA exits (at once, unless a wait gave up)
-            for (int c = done > 2 ? done - 2 : 0; c < done; ++c) {
-                (void)mbar_wait(&bars[B_QK + (c & 1)], (c >> 1) & 1, kDrainCycles);
-                (void)mbar_wait(&bars[B_V + (c & 1)], (c >> 1) & 1, kDrainCycles);
-            }
-        }
-        __syncwarp();
-    } else if (warp == kOutWarp) {
-        // ================= S and O2 (issued by the first lane) =================
-        // Every commit is waited for by somebody: one that arrived after the CTA's end would write
-        // into the next one's barriers.
-        if (!kStateOnly) {
-            const uint32_t el = lane == 0;
-            constexpr uint32_t id_s = idesc_bf16(128, 128, false, false);
-            constexpr uint32_t id_o = idesc_bf16(128, 64, false, true);
-            bool issued = false;
+            __syncwarp();
+        } else if (warp == kOutWarp) {
+            // ================= S and O2 (issued by the first lane) =================
+            // Every commit is waited for by somebody: one that arrived after the CTA's end would write
+            // into the next one's barriers.
+            if (!kStateOnly) {
+                const uint32_t el = lane == 0;
+                constexpr uint32_t id_s = idesc_bf16(128, 128, false, false);
+                constexpr uint32_t id_o = idesc_bf16(128, 64, false, true);
+                bool issued = false;
 #pragma unroll 1
-            for (int c = -1; c < nchunks; ++c) {
-                if (c + 1 < nchunks) {
-                    const int st = (c + 1) & 1, ph = (c + 1) >> 1;
-                    if (!lwait_warp(&bars[B_QK + st], ph, &s_abort)) break;
-                    if (c > 0 && !lwait_warp(&bars[B_SFREE + st], ph - 1, &s_abort)) break;
+                for (int c = -1; c < nchunks; ++c) {
+                    if (c + 1 < nchunks) {
+                        const int st = (c + 1) & 1, ph = (c + 1) >> 1;
+                        if (!lwait_warp(&bars[B_QK + st], ph, &s_abort)) break;
+                        if (c > 0 && !lwait_warp(&bars[B_SFREE + st], ph - 1, &s_abort)) break;
+                        if (chunk_n(c + 1) < kC && !lwait_warp(&bars[B_CLEAN], 0, &s_abort)) break;
+                        fence_after_sync();
+                        issued = true;
+                        const uint32_t loQ = desc_lo(smem_u32(sm + S_Q + 2 * st * kSlab), 16);
+                        const uint32_t loK = desc_lo(smem_u32(sm + S_K + 2 * st * kSlab), 16);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (k < ksteps) mma_el(el, tmem + T_S + 128u * st, desc_pack(loQ + (kmajor_off(k, kSlab) >> 4), hi),
+                                     desc_pack(loK + (kmajor_off(k, kSlab) >> 4), hi), id_s, k > 0);
+                        commit_el(el, &bars[B_S + st]);
+                        if (c + 3 < nchunks) commit_el(el, &bars[B_QKFREE + st]);
+                    }
+                    if (c >= 0) {
+                        const int st = c & 1, ph = c >> 1, steps = (chunk_n(c) + 15) / 16;
+                        if (!lwait_warp(&bars[B_P + st], ph, &s_abort) || !lwait_warp(&bars[B_V + st], ph, &s_abort)) break;
+                        fence_after_sync();
+                        const uint32_t loV = desc_lo(smem_u32(sm + S_V + st * kSlab), kSlab);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (k < steps) mma_ts_el(el, tmem + T_S + 128u * st + T_O2, tmem + T_S + 128u * st + 8u * k,
+                                        desc_pack(loV + (mnmajor_off(k) >> 4), hi), id_o, k > 0);
+                        commit_el(el, &bars[B_O2 + st]);
+                        if (c + 2 < nchunks) commit_el(el, &bars[B_VFREE + st]);
+                    }
+                }
+                if (s_abort && issued) {    // products in flight end before their TMEM is released
+                    commit_el(el, &bars[B_DRAIN]);
+                    (void)mbar_wait(&bars[B_DRAIN], 0, kDrainCycles);
+                }
+            }
+        } else if (warp == kReadWarp) {
+            // ================= O1 (issued by the first lane) =================
+            if (!kStateOnly) {
+                const uint32_t el = lane == 0;
+                constexpr uint32_t id_o = idesc_bf16(128, 64, false, true);
+                const uint32_t loH = desc_lo(smem_u32(sm + S_H), kSlab);
+                bool issued = false;
+#pragma unroll 1
+                for (int c = 0; c < nchunks; ++c) {
+                    const int st = c & 1;
+                    if (!lwait_warp(&bars[B_QK + st], c >> 1, &s_abort) || !lwait_warp(&bars[B_H0], c, &s_abort) ||
+                        (c > 0 && !lwait_warp(&bars[B_OFREE], c - 1, &s_abort)))
+                        break;
                     fence_after_sync();
                     issued = true;
                     const uint32_t loQ = desc_lo(smem_u32(sm + S_Q + 2 * st * kSlab), 16);
-                    const uint32_t loK = desc_lo(smem_u32(sm + S_K + 2 * st * kSlab), 16);
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        if (k < ksteps) mma_el(el, tmem + T_S + 128u * st, desc_pack(loQ + (kmajor_off(k, kSlab) >> 4), hi),
-                                 desc_pack(loK + (kmajor_off(k, kSlab) >> 4), hi), id_s, k > 0);
-                    commit_el(el, &bars[B_S + st]);
-                    if (c + 3 < nchunks) commit_el(el, &bars[B_QKFREE + st]);
+                        if (k < ksteps)
+                            mma_el(el, tmem + T_O1, desc_pack(loQ + (kmajor_off(k, kSlab) >> 4), hi),
+                                     desc_pack(loH + (mnmajor_off(k) >> 4), hi), id_o, k > 0);
+                    commit_el(el, &bars[B_O1 + st]);
+                    if (c + 2 < nchunks) commit_el(el, &bars[B_QKFREE + st]);
                 }
-                if (c >= 0) {
-                    const int st = c & 1, ph = c >> 1, steps = (chunk_n(c) + 15) / 16;
-                    if (!lwait_warp(&bars[B_P + st], ph, &s_abort) || !lwait_warp(&bars[B_V + st], ph, &s_abort)) break;
+                if (s_abort && issued) {
+                    commit_el(el, &bars[B_DRAIN1]);
+                    (void)mbar_wait(&bars[B_DRAIN1], 0, kDrainCycles);
+                }
+            }
+        } else {
+            // ================= k^T v' (issued by the first lane) =================
+            {
+                const uint32_t el = lane == 0;
+                const uint32_t id_h = parts > 2 ? idesc_bf16(128, 192, true, true) : idesc_bf16(128, 128, true, true);
+                const uint32_t loVP = desc_lo(smem_u32(sm + S_VP), kSlab);
+                bool issued = false;
+#pragma unroll 1
+                for (int c = 0; c < nupdates; ++c) {
+                    const int st = c & 1, steps = (chunk_n(c) + 15) / 16;
+                    // before the first product the accumulator held the state before the segment
+                    const int freed = kStateOnly ? c - 1 : c;
+                    if (!lwait_warp(&bars[B_QK + st], c >> 1, &s_abort) || !lwait_warp(&bars[B_VP], c, &s_abort) ||
+                        (freed >= 0 && !lwait_warp(&bars[B_HFREE], freed, &s_abort)))
+                        break;
                     fence_after_sync();
-                    const uint32_t loV = desc_lo(smem_u32(sm + S_V + st * kSlab), kSlab);
+                    issued = true;
+                    const uint32_t loK = desc_lo(smem_u32(sm + S_K + 2 * st * kSlab), kSlab);
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        if (k < steps) mma_ts_el(el, tmem + T_S + 128u * st + T_O2, tmem + T_S + 128u * st + 8u * k,
-                                    desc_pack(loV + (mnmajor_off(k) >> 4), hi), id_o, k > 0);
-                    commit_el(el, &bars[B_O2 + st]);
-                    if (c + 2 < nchunks) commit_el(el, &bars[B_VFREE + st]);
-                }
-            }
-            if (s_abort && issued) {    // products in flight end before their TMEM is released
-                commit_el(el, &bars[B_DRAIN]);
-                (void)mbar_wait(&bars[B_DRAIN], 0, kDrainCycles);
-            }
-        }
-    } else if (warp == kReadWarp) {
-        // ================= O1 (issued by the first lane) =================
-        if (!kStateOnly) {
-            const uint32_t el = lane == 0;
-            constexpr uint32_t id_o = idesc_bf16(128, 64, false, true);
-            const uint32_t loH = desc_lo(smem_u32(sm + S_H), kSlab);
-            bool issued = false;
-#pragma unroll 1
-            for (int c = 0; c < nchunks; ++c) {
-                const int st = c & 1;
-                if (!lwait_warp(&bars[B_QK + st], c >> 1, &s_abort) || !lwait_warp(&bars[B_H0], c, &s_abort) ||
-                    (c > 0 && !lwait_warp(&bars[B_OFREE], c - 1, &s_abort)))
-                    break;
-                fence_after_sync();
-                issued = true;
-                const uint32_t loQ = desc_lo(smem_u32(sm + S_Q + 2 * st * kSlab), 16);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (k < ksteps)
-                        mma_el(el, tmem + T_O1, desc_pack(loQ + (kmajor_off(k, kSlab) >> 4), hi),
-                                 desc_pack(loH + (mnmajor_off(k) >> 4), hi), id_o, k > 0);
-                commit_el(el, &bars[B_O1 + st]);
-                if (c + 2 < nchunks) commit_el(el, &bars[B_QKFREE + st]);
-            }
-            if (s_abort && issued) {
-                commit_el(el, &bars[B_DRAIN1]);
-                (void)mbar_wait(&bars[B_DRAIN1], 0, kDrainCycles);
-            }
-        }
-    } else {
-        // ================= k^T v' (issued by the first lane) =================
-        {
-            const uint32_t el = lane == 0;
-            const uint32_t id_h = parts > 2 ? idesc_bf16(128, 192, true, true) : idesc_bf16(128, 128, true, true);
-            const uint32_t loVP = desc_lo(smem_u32(sm + S_VP), kSlab);
-            bool issued = false;
-#pragma unroll 1
-            for (int c = 0; c < nupdates; ++c) {
-                const int st = c & 1, steps = (chunk_n(c) + 15) / 16;
-                // before the first product the accumulator held the state before the segment
-                const int freed = kStateOnly ? c - 1 : c;
-                if (!lwait_warp(&bars[B_QK + st], c >> 1, &s_abort) || !lwait_warp(&bars[B_VP], c, &s_abort) ||
-                    (freed >= 0 && !lwait_warp(&bars[B_HFREE], freed, &s_abort)))
-                    break;
-                fence_after_sync();
-                issued = true;
-                const uint32_t loK = desc_lo(smem_u32(sm + S_K + 2 * st * kSlab), kSlab);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (k < steps)
-                        mma_el(el, tmem + T_H, desc_pack(loK + (mnmajor_off(k) >> 4), hi),
-                                 desc_pack(loVP + (mnmajor_off(k) >> 4), hi), id_h, k > 0);
-                commit_el(el, &bars[B_DH]);
-                if (c + 2 < nchunks) {
-                    commit_el(el, &bars[B_QKFREE + st]);
-                    if (kStateOnly && el) { // nobody else reads a stage
-                        mbar_arrive(&bars[B_QKFREE + st]);
-                        mbar_arrive(&bars[B_QKFREE + st]);
-                        mbar_arrive(&bars[B_VFREE + st]);
+                        if (k < steps)
+                            mma_el(el, tmem + T_H, desc_pack(loK + (mnmajor_off(k) >> 4), hi),
+                                     desc_pack(loVP + (mnmajor_off(k) >> 4), hi), id_h, k > 0);
+                    commit_el(el, &bars[B_DH]);
+                    if (c + 2 < nchunks) {
+                        commit_el(el, &bars[B_QKFREE + st]);
+                        if (kStateOnly && el) { // nobody else reads a stage
+                            mbar_arrive(&bars[B_QKFREE + st]);
+                            mbar_arrive(&bars[B_QKFREE + st]);
+                            mbar_arrive(&bars[B_VFREE + st]);
+                        }
                     }
                 }
-            }
-            if (s_abort && issued) {
-                commit_el(el, &bars[B_DRAIN2]);
-                (void)mbar_wait(&bars[B_DRAIN2], 0, kDrainCycles);
+                if (s_abort && issued) {
+                    commit_el(el, &bars[B_DRAIN2]);
+                    (void)mbar_wait(&bars[B_DRAIN2], 0, kDrainCycles);
+                }
             }
         }
     }
@@ -738,6 +747,12 @@ cudaError_t launch_lin_tc(const LinParams& p, bool cut, cudaStream_t s) {
     }
     e = cudaFuncSetAttribute(lin_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
+    // the roles' shares add up to a launch with exactly these
+    static const int regs = [] {
+        cudaFuncAttributes a{};
+        return cudaFuncGetAttributes(&a, lin_tc_kernel<false>) == cudaSuccess ? a.numRegs : 0;
+    }();
+    if (regs != kRegsLaunch) return cudaErrorInvalidConfiguration;
     lin_tc_kernel<false><<<grid, kThreads, kSmem, s>>>(tp, maps);
     return cudaGetLastError();
 }
