@@ -366,8 +366,8 @@ M3_API m3_status m3_linattn_fwd(const m3_linattn_dims* dims, const m3_linattn_in
  * are not used. state_in, state_out: fp32 [nstates, H, K, V], 16-byte aligned; state_out may be
  * state_in (in place) but must not overlap it otherwise. slots NULL: sequence i has state i
  * (nstates >= nseq). slots [nseq] (device, int32): sequence i has state slots[i]; a slot outside
- * [0, nstates) skips that sequence (its o row is left as it was), and states of no sequence are
- * left as they were. Sequences of one call must have slots of their own: of two that share one,
+ * [0, nstates) skips that sequence (its o row is zero), and states of no sequence are left as they
+ * were. Sequences of one call must have slots of their own: of two that share one,
  * that state and the outputs of both are undefined. o: [nseq][.][H][V], in_dtype. fp32
  * arithmetic throughout. */
 M3_API m3_status m3_linattn_step(const m3_linattn_dims* dims, const m3_linattn_inputs* in,

@@ -7,7 +7,6 @@ implementation.
 from __future__ import annotations
 
 import ctypes
-import math
 import os
 
 import torch
@@ -405,120 +404,44 @@ def scan_bwd(x, B, C, theta, dt, A, lam, dy, B_bias=None, C_bias=None, init: Sta
 
 
 # ---- linear attention with a decay for each head, and the grouped norm behind it ----
-# These calls run on the tensors' device and, unless a stream is given, on its current stream.
-# Outputs and workspaces they allocate are allocated on the stream they run on.
+# Marshalled in C++ (csrc/m3_torch.cpp), since these calls' kernels may be as short as the
+# marshalling. They run on the tensors' device and, unless a stream is given, on its current
+# stream; what they allocate is allocated on the stream they run on. Wrong shapes, types, strides
+# and devices raise ValueError, the library's own refusals M3Error.
 
-class _On:
-    """The tensors' device and the call's stream made current while it allocates and launches."""
-
-    __slots__ = ("ctx", "handle")
-
-    def __init__(self, device, stream):
-        self.ctx = None
-        if stream is not None:
-            if stream.device != device:
-                raise ValueError(f"stream on {stream.device}, tensors on {device}")
-            if stream != torch.cuda.current_stream(device) or device.index != torch.cuda.current_device():
-                self.ctx = torch.cuda.stream(stream)
-            self.handle = stream.cuda_stream
-        else:
-            if device.index != torch.cuda.current_device():
-                self.ctx = torch.cuda.device(device)
-            self.handle = torch.cuda.current_stream(device).cuda_stream
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+_native = None
 
 
-def _same(ref, *tensors):
-    """Every tensor on ref's CUDA device."""
-    if not ref.is_cuda:
-        raise ValueError("tensors must be on a CUDA device")
-    for t in tensors:
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"tensors on {ref.device} and {t.device}")
+def _ext():
+    """The native marshalling module, bound to the loaded library. Raises if it is missing."""
+    global _native
+    if _native is None:
+        lib = load_library()
+        try:
+            from . import _m3torch
+        except ImportError as e:
+            raise ImportError(f"{os.path.join(_HERE, '_m3torch.so')} does not load: build it with "
+                              "`python -m state_space_sequence_mamba_b200.build`") from e
+        _m3torch.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
+            "m3_linattn_workspace_bytes", "m3_linattn_bwd_workspace_bytes", "m3_linattn_fwd",
+            "m3_linattn_step", "m3_linattn_bwd", "m3_group_norm_fwd",
+            "m3_group_norm_bwd_workspace_bytes", "m3_group_norm_bwd")))
+        _native = _m3torch
+    return _native
 
 
-def _view(t, name, shape, dtype, step=False):
-    """A tensor [b, L, heads, dim] (a step's: [b, heads, dim]) by its strides."""
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
-    st = t.stride()
-    if st[-1] != 1 and shape[-1] > 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    return View(t.data_ptr(), st[0], 0, st[1]) if step else View(t.data_ptr(), *st[:3])
-
-
-def _out_view(t, name, shape, dtype, step=False):
-    v = _view(t, name, shape, dtype, step)
-    if any(s == 0 for s, n in zip(t.stride(), shape) if n > 1):
-        raise ValueError(f"{name} is written and must not be expanded")
-    return v
-
-
-def _f32(t, name, shape):
-    """The pointer of a contiguous fp32 tensor, or None."""
-    if t is None:
-        return None
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != torch.float32:
-        raise ValueError(f"{name} must be float32")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _i32(t, name, n):
-    if t is None:
-        return None
-    if t.dtype != torch.int32 or t.dim() != 1 or (n is not None and t.shape[0] != n) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 vector" + (f" of {n}" if n is not None else ""))
-    return t.data_ptr()
-
-
-def _linattn_args(q, k, v, log_decay, scale, cu_seqlens, step=False):
-    """Dims and inputs of a call, checked: q [b, L, Hq, K], k [b, L, Hk, K], v [b, L, Hv, V]."""
-    _same(q, k, v, log_decay, cu_seqlens)
-    nd = 3 if step else 4
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        if t.dim() != nd:
-            raise ValueError(f"{name} must have {nd} dimensions, has {t.dim()}")
-    if log_decay.dim() != 1:
-        raise ValueError("log_decay must be a vector of one value per head")
-    H, lead, K, V = log_decay.shape[0], tuple(q.shape[:nd - 2]), q.shape[-1], v.shape[-1]
-    dt, code = q.dtype, _dtype_code(q.dtype)
-    ins = LinattnInputs(_view(q, "q", (*lead, q.shape[-2], K), dt, step),
-                        _view(k, "k", (*lead, k.shape[-2], K), dt, step),
-                        _view(v, "v", (*lead, v.shape[-2], V), dt, step),
-                        _f32(log_decay, "log_decay", (H,)), _i32(cu_seqlens, "cu_seqlens", None))
-    nseq, L = lead[0], 1 if step else lead[1]
-    if cu_seqlens is not None:
-        if nseq != 1:
-            raise ValueError("packed sequences lie in tensors of batch 1")
-        nseq = cu_seqlens.shape[0] - 1
-        if nseq < 0:
-            raise ValueError("cu_seqlens needs at least one value")
-    return LinattnDims(nseq, L, H, q.shape[-2], k.shape[-2], v.shape[-2], K, V, code, scale), ins
-
-
-def _workspace(given, need, device):
-    """(tensor that keeps it alive, pointer, bytes)"""
-    if given is None:
-        if need == 0:
-            return None, None, 0
-        given = torch.empty(need, dtype=torch.uint8, device=device)
-    elif given.device != device or not given.is_contiguous():
-        raise ValueError("workspace must be contiguous and on the tensors' device")
-    return given, given.data_ptr(), given.numel() * given.element_size()
+def _run(name, stream, ref, *args):
+    f = getattr(_native or _ext(), name)
+    if stream is None:
+        r = f(*args)
+    else:
+        if stream.device != ref.device:
+            raise ValueError(f"stream on {stream.device}, tensors on {ref.device}")
+        with torch.cuda.stream(stream):
+            r = f(*args)
+    if type(r) is int:
+        _check(r)
+    return r
 
 
 def linattn_workspace_bytes(dims: LinattnDims, packed=False, backward=False) -> int:
@@ -537,52 +460,16 @@ def linattn_fwd(q, k, v, log_decay, scale=1.0, init=None, final=True, o=None, cu
     ``final=True`` allocates the final state, ``False``/None skips it, or pass a tensor (it may be
     ``init``). ``o`` [b, L, H, V] is allocated unless given (packed: zeroed, since rows behind the
     last sequence are not written). Returns (o, final state or None)."""
-    lib = load_library()
-    dims, ins = _linattn_args(q, k, v, log_decay, scale, cu_seqlens)
-    dev = q.device
-    _same(q, init, o, final if torch.is_tensor(final) else None)
-    states = (dims.nseq, dims.nheads, dims.kdim, dims.vdim)
-    with _On(dev, stream) as handle:
-        shape = (q.shape[0], q.shape[1], dims.nheads, dims.vdim)
-        if o is None:
-            o = (torch.empty if cu_seqlens is None else torch.zeros)(shape, dtype=q.dtype, device=dev)
-        if final is True:
-            final = torch.empty(states, device=dev)
-        elif final is False:
-            final = None
-        need = lib.m3_linattn_workspace_bytes(ctypes.byref(dims), cu_seqlens is not None)
-        keep, ws, n = _workspace(workspace, need, dev)
-        rc = lib.m3_linattn_fwd(ctypes.byref(dims), ctypes.byref(ins), _f32(init, "init", states),
-                                _f32(final, "final", states),
-                                ctypes.byref(_out_view(o, "o", shape, q.dtype)), ws, n, handle)
-    _check(rc)
-    return o, final
+    return _run("linattn_fwd", stream, q, q, k, v, log_decay, scale, init, final, o, cu_seqlens, workspace)
 
 
 def linattn_step(q, k, v, log_decay, state, state_out=None, slots=None, scale=1.0, o=None,
                  stream=None):
     """m3_linattn_step: one token of every sequence. q [b, Hq, K], k [b, Hk, K], v [b, Hv, V];
     ``state`` [b, H, K, V] fp32, or with ``slots`` [b] int32 a pool [n, H, K, V] of which sequence
-    i has state slots[i] (outside [0, n): the sequence is skipped and its o row left as it was; a
-    freshly allocated ``o`` is zeroed then). ``state_out`` defaults to ``state`` (in place).
-    Returns (o [b, H, V], state_out)."""
-    lib = load_library()
-    dims, ins = _linattn_args(q, k, v, log_decay, scale, None, step=True)
-    if state_out is None:
-        state_out = state
-    _same(q, state, state_out, slots, o)
-    b = q.shape[0]
-    states = (state.shape[0] if slots is not None else b, dims.nheads, dims.kdim, dims.vdim)
-    with _On(q.device, stream) as handle:
-        shape = (b, dims.nheads, dims.vdim)
-        if o is None:
-            o = (torch.empty if slots is None else torch.zeros)(shape, dtype=q.dtype, device=q.device)
-        rc = lib.m3_linattn_step(ctypes.byref(dims), ctypes.byref(ins), _f32(state, "state", states),
-                                 _f32(state_out, "state_out", states), states[0],
-                                 _i32(slots, "slots", b),
-                                 ctypes.byref(_out_view(o, "o", shape, q.dtype, True)), handle)
-    _check(rc)
-    return o, state_out
+    i has state slots[i] (outside [0, n): the sequence is skipped and its o row is zero).
+    ``state_out`` defaults to ``state`` (in place). Returns (o [b, H, V], state_out)."""
+    return _run("linattn_step", stream, q, q, k, v, log_decay, scale, state, state_out, slots, o)
 
 
 def linattn_bwd(q, k, v, log_decay, do, scale=1.0, init=None, dfinal=None, cu_seqlens=None,
@@ -592,28 +479,10 @@ def linattn_bwd(q, k, v, log_decay, do, scale=1.0, init=None, dfinal=None, cu_se
     and shapes (packed: allocated ones are zeroed, since rows behind the last sequence are not
     written). Returns a dict of dq, dk, dv and dinit ([n, H, K, V] fp32; None without
     ``want_init``; pass a tensor as ``want_init`` to have it written there)."""
-    lib = load_library()
-    dims, ins = _linattn_args(q, k, v, log_decay, scale, cu_seqlens)
-    dev = q.device
-    dinit = want_init if torch.is_tensor(want_init) else None
-    _same(q, do, init, dfinal, dinit, *(grads or ()))
-    states = (dims.nseq, dims.nheads, dims.kdim, dims.vdim)
-    with _On(dev, stream) as handle:
-        if grads is None:
-            new = torch.empty if cu_seqlens is None else torch.zeros
-            grads = tuple(new(t.shape, dtype=t.dtype, device=dev) for t in (q, k, v))
-        if want_init is True:
-            dinit = torch.empty(states, device=dev)
-        gc = LinattnGrads(*(_out_view(g, n, tuple(t.shape), q.dtype)
-                            for g, n, t in zip(grads, ("dq", "dk", "dv"), (q, k, v))))
-        need = lib.m3_linattn_bwd_workspace_bytes(ctypes.byref(dims), cu_seqlens is not None)
-        keep, ws, n = _workspace(workspace, need, dev)
-        dov = _view(do, "do", (q.shape[0], q.shape[1], dims.nheads, dims.vdim), q.dtype)
-        rc = lib.m3_linattn_bwd(ctypes.byref(dims), ctypes.byref(ins), _f32(init, "init", states),
-                                ctypes.byref(dov), _f32(dfinal, "dfinal", states),
-                                ctypes.byref(gc), _f32(dinit, "dinit", states), ws, n, handle)
-    _check(rc)
-    return dict(dq=grads[0], dk=grads[1], dv=grads[2], dinit=dinit)
+    dq, dk, dv = grads if grads is not None else (None, None, None)
+    r = _run("linattn_bwd", stream, q, q, k, v, log_decay, scale, do, init, dfinal, cu_seqlens,
+             dq, dk, dv, want_init, workspace)
+    return dict(dq=r[0], dk=r[1], dv=r[2], dinit=r[3])
 
 
 def linattn_check(device=None):
@@ -622,79 +491,13 @@ def linattn_check(device=None):
         _check(load_library().m3_linattn_check())
 
 
-def _one_stride(sizes, strides):
-    """The stride at which the elements of these dimensions lie, None if there is no such."""
-    step, span = 0, None
-    for n, s in zip(reversed(sizes), reversed(strides)):
-        if n == 1:
-            continue
-        if span is None:
-            step, span = s, s * n
-        elif s != span:
-            return None
-        else:
-            span *= n
-    return step
-
-
-def _gn_views(groups, ref, **tensors):
-    """(batch, rows) and the views of tensors [..., C] of ref's shape and type: their leading
-    dimensions cut where each part of every tensor's lies at one stride."""
-    shape, dtype = ref.shape, ref.dtype
-    lead, C = shape[:-1], shape[-1]
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if t.shape != shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        if t.dtype != dtype:
-            raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
-        if t.stride(-1) != 1 and C > 1:
-            raise ValueError(f"{name}: the channels must be contiguous")
-    D = C // groups if groups > 0 else C
-    if all(t is None or t.is_contiguous() for t in tensors.values()):
-        return (1, ref.numel() // C), [None if t is None else ctypes.byref(View(t.data_ptr(), 0, C, D))
-                                       for t in tensors.values()]
-    for cut in range(len(lead) + 1):
-        views = []
-        for t in tensors.values():
-            if t is None:
-                views.append(None)
-                continue
-            outer, inner = (_one_stride(lead[a:b], t.stride()[a:b]) for a, b in ((0, cut), (cut, len(lead))))
-            if outer is None or inner is None:
-                break
-            views.append(ctypes.byref(View(t.data_ptr(), outer, inner, D)))
-        else:
-            return (math.prod(lead[:cut]), math.prod(lead[cut:])), views
-    raise ValueError("rows must lie at one stride, or at one in every batch entry")
-
-
-def _gn_args(x, groups, weight, bias, center, silu, eps, **tensors):
-    if x.dim() < 1 or x.shape[-1] < 1:
-        raise ValueError("x needs a last dimension of channels")
-    C = x.shape[-1]
-    flags = (M3_GN_CENTER if center else 0) | (M3_GN_SILU if silu else 0)
-    sizes, views = _gn_views(groups, x, x=x, **tensors)
-    return (ctypes.byref(GroupNormDims(*sizes, C, groups, _dtype_code(x.dtype), eps, flags)),
-            _f32(weight, "weight", (C,)), _f32(bias, "bias", (C,)), *views)
-
-
 def group_norm_fwd(x, groups, weight=None, bias=None, z=None, center=True, silu=True, eps=1e-5,
                    out=None, stream=None):
     """m3_group_norm_fwd: x [..., C] normalised over each row's groups of C / groups channels,
     times weight plus bias (fp32 [C], optional), then times silu(z) with a gate ``z`` [..., C],
     or through silu without one (``silu=False``: times z, or as it is). ``center=False`` divides
     by the root mean square instead. Rows may be slices of wider ones. Returns out."""
-    lib = load_library()
-    _same(x, weight, bias, z, out)
-    with _On(x.device, stream) as handle:
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        dims, w, b, xv, zv, ov = _gn_args(x, groups, weight, bias, center, silu, eps, z=z, out=out)
-        rc = lib.m3_group_norm_fwd(dims, xv, zv, w, b, ov, handle)
-    _check(rc)
-    return out
+    return _run("group_norm_fwd", stream, x, x, groups, weight, bias, z, center, silu, eps, out)
 
 
 def group_norm_bwd(dout, x, groups, weight=None, bias=None, z=None, center=True, silu=True,
@@ -702,20 +505,6 @@ def group_norm_bwd(dout, x, groups, weight=None, bias=None, z=None, center=True,
     """m3_group_norm_bwd: gradients of sum(out * dout) for group_norm_fwd on the same arguments.
     Returns a dict of dx, dz (None without z), dweight and dbias (fp32 [C]; None without weight
     or bias)."""
-    lib = load_library()
-    _same(x, dout, weight, bias, z, dx, dz)
-    with _On(x.device, stream) as handle:
-        if dx is None:
-            dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        if dz is None and z is not None:
-            dz = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        dw = torch.empty_like(weight) if weight is not None else None
-        db = torch.empty_like(bias) if bias is not None else None
-        dims, w, b, xv, zv, dov, dxv, dzv = _gn_args(x, groups, weight, bias, center, silu, eps, z=z,
-                                                     dout=dout, dx=dx, dz=dz if z is not None else None)
-        keep, ws, n = _workspace(workspace, lib.m3_group_norm_bwd_workspace_bytes(dims), x.device)
-        rc = lib.m3_group_norm_bwd(dims, xv, zv, w, b, dov, dxv, dzv,
-                                   None if dw is None else dw.data_ptr(),
-                                   None if db is None else db.data_ptr(), ws, n, handle)
-    _check(rc)
-    return dict(dx=dx, dz=dz if z is not None else None, dweight=dw, dbias=db)
+    r = _run("group_norm_bwd", stream, x, dout, x, groups, weight, bias, z, center, silu, eps, dx, dz,
+             workspace)
+    return dict(dx=r[0], dz=r[1], dweight=r[2], dbias=r[3])

@@ -1,4 +1,5 @@
-"""Builds ``libm3.so`` (the C ABI of include/m3.h) in-tree with nvcc for sm_100a.
+"""Builds ``libm3.so`` (the C ABI of include/m3.h) in-tree with nvcc for sm_100a, and
+``_m3torch.so``, which hands torch tensors to it, with g++.
 
 Usage: ``python -m state_space_sequence_mamba_b200.build [--force] [-v]``.
 No GPU is needed: nvcc cross-compiles.
@@ -9,11 +10,14 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libm3.so")
+TORCH_SRC = os.path.join(CSRC, "m3_torch.cpp")
+TORCH_EXT = os.path.join(HERE, "_m3torch.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -34,7 +38,47 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _ext_stale() -> bool:
+    if not os.path.exists(TORCH_EXT):
+        return True
+    t = os.path.getmtime(TORCH_EXT)
+    return any(os.path.getmtime(d) > t for d in (TORCH_SRC, os.path.join(ROOT, "include", "m3.h"), __file__))
+
+
+def _start_ext(tmp):
+    """The g++ process that writes the torch binding to ``tmp``."""
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    inc = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), os.path.join(ROOT, "include"), sysconfig.get_paths()["include"]]
+    lib = os.path.join(base, "lib")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{d}" for d in inc), TORCH_SRC, "-o", tmp, f"-L{lib}",
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    return cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    ext = None
+    if force or _ext_stale():
+        ext_tmp = TORCH_EXT + f".tmp{os.getpid()}"
+        ext = _start_ext(ext_tmp)
+    try:
+        _build_lib(force, verbose)
+    finally:
+        out, _ = ext[1].communicate() if ext else (b"", None)
+    if ext:
+        if verbose or ext[1].returncode != 0:
+            sys.stdout.write(out.decode())
+        if ext[1].returncode != 0:
+            raise RuntimeError("g++ failed: " + " ".join(ext[0]))
+        os.replace(ext_tmp, TORCH_EXT)
+    return LIB
+
+
+def _build_lib(force: bool, verbose: bool) -> str:
     if not force and not _stale():
         return LIB
     objs = []

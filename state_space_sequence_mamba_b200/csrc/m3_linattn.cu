@@ -395,7 +395,7 @@ m3_status m3_linattn_step(const m3_linattn_dims* dims, const m3_linattn_inputs* 
         (st = check_view(o, "o", dims->in_dtype == M3_BF16 ? 2 : 4, any)) != M3_OK)
         return st;
     if (dims->nseq * dims->nheads > kMaxGrid / 4) return err(M3_ERR_UNSUPPORTED, "nseq * nheads exceeds the grid limit");
-    if (!any || nstates == 0) return M3_OK;
+    if (!any) return M3_OK;
     LinStep p{};
     p.q = tensor(dims, in->q, dims->qheads, false);
     p.k = tensor(dims, in->k, dims->kheads, false);

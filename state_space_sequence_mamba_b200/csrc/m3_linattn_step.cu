@@ -27,7 +27,12 @@ lin_step_kernel(const LinStep p, int tiles) {
     const int64_t i = unit / p.H;
     const int h = static_cast<int>(unit - i * p.H);
     const int64_t st = p.slots ? p.slots[i] : i;
-    if (st < 0 || st >= p.nstates) return;
+    T* y = static_cast<T*>(p.o) + i * p.o_batch + h * p.o_head;
+    if (st < 0 || st >= p.nstates) {        // no state: the row is zero
+        const int c = tile * 4 * TX + tid;
+        if (tid < 4 * TX && c < p.V) y[c] = from_f<T>(0.f);
+        return;
+    }
     const T* q = static_cast<const T*>(p.q.p) + i * p.q.batch + (h / p.q.ratio) * p.q.head;
     const T* k = static_cast<const T*>(p.k.p) + i * p.k.batch + (h / p.k.ratio) * p.k.head;
     const T* v = static_cast<const T*>(p.v.p) + i * p.v.batch + (h / p.v.ratio) * p.v.head;
@@ -88,9 +93,8 @@ lin_step_kernel(const LinStep p, int tiles) {
         __syncthreads();
     }
     if (ry == 0 && on) {
-        T* y = static_cast<T*>(p.o) + i * p.o_batch + h * p.o_head + col;
-        y[0] = from_f<T>(p.scale * o.x); y[1] = from_f<T>(p.scale * o.y);
-        y[2] = from_f<T>(p.scale * o.z); y[3] = from_f<T>(p.scale * o.w);
+        y[col] = from_f<T>(p.scale * o.x); y[col + 1] = from_f<T>(p.scale * o.y);
+        y[col + 2] = from_f<T>(p.scale * o.z); y[col + 3] = from_f<T>(p.scale * o.w);
     }
 }
 
@@ -102,7 +106,11 @@ __global__ void __launch_bounds__(kThreads) lin_step_any_kernel(const LinStep p)
     const int64_t unit = blockIdx.x, i = unit / p.H;
     const int h = static_cast<int>(unit - i * p.H);
     const int64_t st = p.slots ? p.slots[i] : i;
-    if (st < 0 || st >= p.nstates) return;
+    T* y = static_cast<T*>(p.o) + i * p.o_batch + h * p.o_head;
+    if (st < 0 || st >= p.nstates) {        // no state: the row is zero
+        if (tid < p.V) y[tid] = from_f<T>(0.f);
+        return;
+    }
     const T* q = static_cast<const T*>(p.q.p) + i * p.q.batch + (h / p.q.ratio) * p.q.head;
     const T* k = static_cast<const T*>(p.k.p) + i * p.k.batch + (h / p.k.ratio) * p.k.head;
     const T* v = static_cast<const T*>(p.v.p) + i * p.v.batch + (h / p.v.ratio) * p.v.head;
@@ -121,7 +129,7 @@ __global__ void __launch_bounds__(kThreads) lin_step_any_kernel(const LinStep p)
         p.state_out[at] = s;
         o = fmaf(s_q[r], s, o);
     }
-    static_cast<T*>(p.o)[i * p.o_batch + h * p.o_head + tid] = from_f<T>(p.scale * o);
+    y[tid] = from_f<T>(p.scale * o);
 }
 
 template <typename T>

@@ -295,7 +295,7 @@ def test_step(cuda_dev, shape, dtype):
             assert torch.equal(o2[i], o[i]) and torch.equal(pool[slots[i]], S[i])
             before[slots[i]] = pool[slots[i]]
         else:
-            assert bool((o2[i] == 7.0).all())
+            assert bool((o2[i] == 0.0).all())
     assert torch.equal(pool, before)
 
 
