@@ -53,9 +53,9 @@ struct Vec;   // 16 bytes of T as floats
 template <>
 struct Vec<float> {
     static constexpr int N = 4;
-    static __device__ __forceinline__ void load(const float* p, float* f) {
-        const float4 v = *reinterpret_cast<const float4*>(p);
-        f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+    static __device__ __forceinline__ void unpack(const uint4& v, float* f) {
+        f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y);
+        f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
     }
     static __device__ __forceinline__ void store(float* p, const float* f) {
         *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
@@ -64,8 +64,7 @@ struct Vec<float> {
 template <>
 struct Vec<__nv_bfloat16> {
     static constexpr int N = 8;
-    static __device__ __forceinline__ void load(const __nv_bfloat16* p, float* f) {
-        const uint4 v = *reinterpret_cast<const uint4*>(p);
+    static __device__ __forceinline__ void unpack(const uint4& v, float* f) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -84,8 +83,8 @@ struct Vec<__nv_bfloat16> {
     }
 };
 
-// 1 / (1 + e^-v); e^-v = inf gives 0
-__device__ __forceinline__ float sigmoid(float v) { return __frcp_rn(1.f + __expf(-v)); }
+// 1 / (1 + e^-v); e^-v = inf gives 0. The approximate divide is within 2 units in the last place.
+__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
 template <bool kSilu>
 __device__ __forceinline__ float act(float v) { return kSilu ? v * sigmoid(v) : v; }
 // act(v) and its slope
@@ -133,98 +132,119 @@ __device__ __forceinline__ void stats(float (&v)[NV][N], const bool (&in)[NV], f
         for (int e = 0; e < N; ++e) v[i][e] *= *r;
 }
 
-template <typename T, int LPG, int NV, bool kCenter, bool kSilu, bool kGate>
-__global__ void __launch_bounds__(kThreads) gn_fwd_kernel(const GnParams p) {
-    constexpr int N = Vec<T>::N;
-    const int lane = threadIdx.x % LPG;
-    const uint32_t unit = (blockIdx.x * kThreads + threadIdx.x) / LPG, G = static_cast<uint32_t>(p.G);
-    const bool live = unit < p.rows * G;        // a warp's lanes stay together for the shuffles
-    const uint32_t row = live ? unit / G : 0u;
-    const int group = static_cast<int>(live ? unit - row * G : 0u), c0 = group * p.D;
-    const T* x = at<const T>(p.x, p, row, group);
-    const T* z = kGate ? at<const T>(p.z, p, row, group) : nullptr;
-    T* out = at<T>(p.out, p, row, group);
-    float v[NV][N], g[NV][N];
-    bool in[NV];
+// The row walk of both directions. A CTA's threads lie side by side over gx whole groups and, where
+// those are narrower than the CTA, over nry rows; they keep their columns (and so the weights) and
+// walk down the share's rows, the next row's loads in flight while one is worked on (two rows ahead
+// measured the same: 45.3 against 43.8 us forward, 82.0 against 84.4 backward, on 8192 x 4096).
+template <typename T, int LPG, int NV>
+struct Walk {
+    static constexpr int N = Vec<T>::N;
+    int lane, ry, nry, group, c0;
+    uint32_t row, r1, turns;
+    bool col_ok, in[NV];
+    __device__ __forceinline__ Walk(const GnParams& p, int gx) {
+        lane = threadIdx.x % LPG;
+        const int grp = threadIdx.x / LPG;
+        nry = (kThreads / LPG) / gx;
+        ry = grp / gx;
+        group = blockIdx.y * gx + grp % gx;
+        col_ok = group < p.G && ry < nry;
+        c0 = group * p.D;
+        const uint32_t r0 = blockIdx.x * p.share_rows;
+        r1 = min(r0 + p.share_rows, p.rows);
+        row = r0 + ry;
+        turns = (r1 - r0 + nry - 1) / nry;      // the same for every thread: the shuffles need whole warps
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int d = (i * LPG + lane) * N;
-        in[i] = live && d < p.D;
-#pragma unroll
-        for (int e = 0; e < N; ++e) v[i][e] = g[i][e] = 0.f;
-        if (in[i]) {
-            Vec<T>::load(x + d, v[i]);
-            if (kGate) Vec<T>::load(z + d, g[i]);
-        }
+        for (int i = 0; i < NV; ++i) in[i] = col_ok && (i * LPG + lane) * N < p.D;
     }
-    float r;
-    stats<LPG, NV, N, kCenter>(v, in, 1.f / p.D, p.eps, &r);
+    __device__ __forceinline__ int col(int i) const { return (i * LPG + lane) * N; }
+    // this thread's vectors of one row, zeros where it has none
+    __device__ __forceinline__ void fetch(const GnParams& p, const GnTensor& t, uint32_t r, uint4 (&raw)[NV]) const {
+        const bool live = col_ok && r < r1;
+        const T* src = live ? at<const T>(t, p, r, group) : nullptr;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        if (!in[i]) continue;
-        const int d = (i * LPG + lane) * N;
-        float o[N];
+        for (int i = 0; i < NV; ++i)
+            raw[i] = live && in[i] ? __ldcs(reinterpret_cast<const uint4*>(src + col(i))) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ __forceinline__ void weights(const float* src, float other, float (&w)[NV][N]) const {
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            const float y = fmaf(v[i][e], p.w ? __ldg(p.w + c0 + d + e) : 1.f, p.b ? __ldg(p.b + c0 + d + e) : 0.f);
-            o[e] = kGate ? y * act<kSilu>(g[i][e]) : act<kSilu>(y);
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < N; ++e) w[i][e] = src && in[i] ? __ldg(src + c0 + col(i) + e) : other;
+    }
+};
+
+template <typename T, int LPG, int NV, bool kCenter, bool kSilu, bool kGate>
+__global__ void __launch_bounds__(kThreads) gn_fwd_kernel(const GnParams p, int gx) {
+    constexpr int N = Vec<T>::N;
+    Walk<T, LPG, NV> k(p, gx);
+    uint4 rx[NV], rz[NV];
+    k.fetch(p, p.x, k.row, rx);
+    if (kGate) k.fetch(p, p.z, k.row, rz);
+    float w[NV][N], b[NV][N];
+    k.weights(p.w, 1.f, w);
+    k.weights(p.b, 0.f, b);
+    const float inv = 1.f / p.D;
+    for (uint32_t t = 0; t < k.turns; ++t, k.row += k.nry) {
+        float v[NV][N], g[NV][N];
+        bool on[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            on[i] = k.in[i] && k.row < k.r1;
+            Vec<T>::unpack(rx[i], v[i]);
+            if (kGate) Vec<T>::unpack(rz[i], g[i]);
         }
-        Vec<T>::store(out + d, o);
+        k.fetch(p, p.x, k.row + k.nry, rx);
+        if (kGate) k.fetch(p, p.z, k.row + k.nry, rz);
+        float r;
+        stats<LPG, NV, N, kCenter>(v, on, inv, p.eps, &r);
+        if (!(k.col_ok && k.row < k.r1)) continue;
+        T* out = at<T>(p.out, p, k.row, k.group);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (!on[i]) continue;
+            float o[N];
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const float y = fmaf(v[i][e], w[i][e], b[i][e]);
+                o[e] = kGate ? y * act<kSilu>(g[i][e]) : act<kSilu>(y);
+            }
+            Vec<T>::store(out + k.col(i), o);
+        }
     }
 }
 
-// A CTA's threads lie side by side over `slab` columns (whole groups) and, where a slab is
-// narrower than the CTA, over several rows; they walk down the share's rows.
 template <typename T, int LPG, int NV, bool kCenter, bool kSilu, bool kGate>
 __global__ void __launch_bounds__(kThreads) gn_bwd_kernel(const GnParams p, int gx) {
     constexpr int N = Vec<T>::N;
     extern __shared__ float s_part[];
-    const int lane = threadIdx.x % LPG, grp = threadIdx.x / LPG;
-    const int gcol = grp % gx, ry = grp / gx, nry = (kThreads / LPG) / gx;
-    const int group = blockIdx.y * gx + gcol;
-    const bool col_ok = group < p.G && ry < nry;
-    const int c0 = group * p.D;
-    const uint32_t r0 = blockIdx.x * p.share_rows;
-    const uint32_t r1 = min(r0 + p.share_rows, p.rows);
+    Walk<T, LPG, NV> k(p, gx);
+    uint4 rx[NV], rz[NV], rd[NV];
+    k.fetch(p, p.x, k.row, rx);
+    k.fetch(p, p.dout, k.row, rd);
+    if (kGate) k.fetch(p, p.z, k.row, rz);
     float w[NV][N], b[NV][N], dw[NV][N], db[NV][N];
-    bool in[NV];
+    k.weights(p.w, 1.f, w);
+    k.weights(p.b, 0.f, b);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int d = (i * LPG + lane) * N;
-        in[i] = col_ok && d < p.D;
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            dw[i][e] = db[i][e] = 0.f;
-            w[i][e] = in[i] && p.w ? p.w[c0 + d + e] : 1.f;
-            b[i][e] = in[i] && p.b ? p.b[c0 + d + e] : 0.f;
-        }
-    }
+        for (int e = 0; e < N; ++e) dw[i][e] = db[i][e] = 0.f;
     const float inv = 1.f / p.D;
-    // every thread takes the same number of turns: the shuffles need whole warps
-    const uint32_t turns = (r1 - r0 + nry - 1) / nry;
-    for (uint32_t t = 0; t < turns; ++t) {
-        const uint32_t row = r0 + t * nry + ry;
-        const bool live = col_ok && row < r1;
-        const T *x = nullptr, *dout = nullptr, *zp = nullptr;
-        if (live) {
-            x = at<const T>(p.x, p, row, group);
-            dout = at<const T>(p.dout, p, row, group);
-            if (kGate) zp = at<const T>(p.z, p, row, group);
-        }
+    for (uint32_t t = 0; t < k.turns; ++t, k.row += k.nry) {
         float v[NV][N], dy[NV][N], z[NV][N];
         bool on[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int d = (i * LPG + lane) * N;
-            on[i] = live && in[i];
-#pragma unroll
-            for (int e = 0; e < N; ++e) v[i][e] = dy[i][e] = z[i][e] = 0.f;
-            if (on[i]) {
-                Vec<T>::load(x + d, v[i]);
-                Vec<T>::load(dout + d, dy[i]);
-                if (kGate) Vec<T>::load(zp + d, z[i]);
-            }
+            on[i] = k.in[i] && k.row < k.r1;
+            Vec<T>::unpack(rx[i], v[i]);
+            Vec<T>::unpack(rd[i], dy[i]);
+            if (kGate) Vec<T>::unpack(rz[i], z[i]);
         }
+        const uint32_t row = k.row;
+        k.fetch(p, p.x, row + k.nry, rx);
+        k.fetch(p, p.dout, row + k.nry, rd);
+        if (kGate) k.fetch(p, p.z, row + k.nry, rz);
         float r;
         stats<LPG, NV, N, kCenter>(v, on, inv, p.eps, &r);
         float s1 = 0.f, s2 = 0.f;
@@ -236,7 +256,7 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_kernel(const GnParams p, int 
                 float a, da;
                 act_slope<kSilu>(kGate ? z[i][e] : y, &a, &da);
                 const float d = dy[i][e];
-                z[i][e] = d * y * da;                 // dz
+                if (kGate) z[i][e] = d * y * da;      // dz
                 const float g = on[i] ? (kGate ? d * a : d * da) : 0.f;
                 dw[i][e] = fmaf(g, v[i][e], dw[i][e]);
                 db[i][e] += g;
@@ -247,14 +267,16 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_kernel(const GnParams p, int 
         }
         s1 = group_sum<LPG>(s1) * inv;
         s2 = kCenter ? group_sum<LPG>(s2) * inv : 0.f;
+        if (!(k.col_ok && row < k.r1)) continue;
+        T* dx = at<T>(p.dx, p, row, k.group);
+        T* dz = kGate ? at<T>(p.dz, p, row, k.group) : nullptr;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (!on[i]) continue;
-            const int d = (i * LPG + lane) * N;
 #pragma unroll
             for (int e = 0; e < N; ++e) dy[i][e] = r * (dy[i][e] - v[i][e] * s1 - s2);
-            Vec<T>::store(at<T>(p.dx, p, row, group) + d, dy[i]);
-            if (kGate) Vec<T>::store(at<T>(p.dz, p, row, group) + d, z[i]);
+            Vec<T>::store(dx + k.col(i), dy[i]);
+            if (kGate) Vec<T>::store(dz + k.col(i), z[i]);
         }
     }
     if (!p.part) return;
@@ -262,16 +284,16 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_kernel(const GnParams p, int 
     const int width = gx * p.D;
     float* sw = s_part;
     float* sb = s_part + width;
-    for (int k = 0; k < nry; ++k) {
-        if (ry == k) {
+    for (int y = 0; y < k.nry; ++y) {
+        if (k.ry == y) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                if (!in[i]) continue;
-                const int c = gcol * p.D + (i * LPG + lane) * N;
+                if (!k.in[i]) continue;
+                const int c = (k.group - blockIdx.y * gx) * p.D + k.col(i);
 #pragma unroll
                 for (int e = 0; e < N; ++e) {
-                    sw[c + e] = k ? sw[c + e] + dw[i][e] : dw[i][e];
-                    sb[c + e] = k ? sb[c + e] + db[i][e] : db[i][e];
+                    sw[c + e] = y ? sw[c + e] + dw[i][e] : dw[i][e];
+                    sb[c + e] = y ? sb[c + e] + db[i][e] : db[i][e];
                 }
             }
         }
@@ -443,8 +465,37 @@ int vector_count(const GnParams& p) {
     return ok ? p.D / N : 0;
 }
 
+// Shares of the rows: as many as give every SM `per_sm` CTAs, at most one per (CTA's) row.
+int64_t share_count(int64_t rows, int64_t per_row_ctas, int per_sm) {
+    const int64_t want = (per_sm * static_cast<int64_t>(device_sm_count()) + per_row_ctas - 1) / per_row_ctas;
+    return rows < want ? (rows > 0 ? rows : 1) : want;
+}
+// One wave of CTAs: what the registers let an SM hold (64 and 102 a thread at groups of 64). More, shorter
+// shares were slower: 46.1 us with 16 CTAs an SM forward, 90.8 with 4 backward.
+constexpr int kFwdPerSm = 4, kBwdPerSm = 2;
+// the most shares any form of the backward takes
+int64_t max_shares(int64_t rows) { return share_count(rows, 1, kBwdPerSm); }
+
+// Groups side by side in a CTA: as many as its threads and 32 KB of column sums hold, the row's groups
+// spread evenly over the slabs.
+int groups_per_cta(const GnParams& p, int per) {
+    const int most = per < 4096 / p.D ? per : 4096 / p.D;
+    const int slabs = (p.G + most - 1) / most;
+    return (p.G + slabs - 1) / slabs;
+}
+
+// The walk's grid: fills in the shares.
+dim3 walk_grid(GnParams& p, int gx, int per, int per_sm) {
+    const int nry = per / gx;
+    const unsigned slabs = static_cast<unsigned>((p.G + gx - 1) / gx);
+    const int64_t turns = (p.rows + nry - 1) / nry, n = share_count(turns, slabs, per_sm);
+    p.share_rows = static_cast<uint32_t>((turns + n - 1) / n * nry);
+    p.shares = static_cast<int>((p.rows + p.share_rows - 1) / p.share_rows);
+    return dim3(static_cast<unsigned>(p.shares), slabs);
+}
+
 template <typename T>
-cudaError_t launch_fwd(const GnParams& p, uint32_t flags, cudaStream_t s) {
+cudaError_t launch_fwd(GnParams p, uint32_t flags, cudaStream_t s) {
     const int vecs = vector_count<T>(p);
     with_flags(flags, p.z.p != nullptr, [&](auto f) {
         using F = decltype(f);
@@ -455,21 +506,14 @@ cudaError_t launch_fwd(const GnParams& p, uint32_t flags, cudaStream_t s) {
         return with_shape(vecs, [&](auto sh) {
             using S = decltype(sh);
             constexpr int per = kThreads / S::LPG;
-            gn_fwd_kernel<T, S::LPG, S::NV, F::C, F::S, F::Z>
-                <<<(p.rows * static_cast<unsigned>(p.G) + per - 1) / per, kThreads, 0, s>>>(p);
+            const int gx = groups_per_cta(p, per);
+            const dim3 grid = walk_grid(p, gx, per, kFwdPerSm);
+            gn_fwd_kernel<T, S::LPG, S::NV, F::C, F::S, F::Z><<<grid, kThreads, 0, s>>>(p, gx);
             return 0;
         });
     });
     return cudaGetLastError();
 }
-
-// Shares of the backward: as many as give every SM a few CTAs, at most one per row.
-int64_t share_count(int64_t rows, int64_t per_row_ctas) {
-    const int64_t want = (4 * static_cast<int64_t>(device_sm_count()) + per_row_ctas - 1) / per_row_ctas;
-    return rows < want ? (rows > 0 ? rows : 1) : want;
-}
-// the most shares any of the forms takes
-int64_t max_shares(int64_t rows) { return share_count(rows, 1); }
 
 template <typename T>
 cudaError_t launch_bwd(GnParams p, uint32_t flags, cudaStream_t s) {
@@ -477,7 +521,7 @@ cudaError_t launch_bwd(GnParams p, uint32_t flags, cudaStream_t s) {
     with_flags(flags, p.z.p != nullptr, [&](auto f) {
         using F = decltype(f);
         if (vecs == 0) {
-            const int64_t n = share_count(p.rows, p.G);
+            const int64_t n = share_count(p.rows, p.G, kBwdPerSm);
             p.share_rows = static_cast<uint32_t>((p.rows + n - 1) / n);
             p.shares = static_cast<int>((p.rows + p.share_rows - 1) / p.share_rows);
             gn_bwd_any_kernel<T, F::C, F::S, F::Z><<<static_cast<unsigned>(p.shares * static_cast<int64_t>(p.G)), kThreads, 0, s>>>(p);
@@ -486,18 +530,10 @@ cudaError_t launch_bwd(GnParams p, uint32_t flags, cudaStream_t s) {
         return with_shape(vecs, [&](auto sh) {
             using S = decltype(sh);
             constexpr int per = kThreads / S::LPG;
-            // groups side by side: as many as the CTA's threads and 32 KB of column sums hold, the
-            // row's groups spread evenly over the slabs
-            const int most = per < 4096 / p.D ? per : 4096 / p.D;
-            const int gx = (p.G + (p.G + most - 1) / most - 1) / ((p.G + most - 1) / most);
-            const int nry = per / gx;
-            const unsigned slabs = static_cast<unsigned>((p.G + gx - 1) / gx);
-            const int64_t n = share_count((p.rows + nry - 1) / nry, slabs);
-            p.share_rows = static_cast<uint32_t>((p.rows + n - 1) / n);
-            p.shares = static_cast<int>((p.rows + p.share_rows - 1) / p.share_rows);
+            const int gx = groups_per_cta(p, per);
+            const dim3 grid = walk_grid(p, gx, per, kBwdPerSm);
             const size_t smem = static_cast<size_t>(gx) * p.D * 2 * sizeof(float);
-            gn_bwd_kernel<T, S::LPG, S::NV, F::C, F::S, F::Z>
-                <<<dim3(static_cast<unsigned>(p.shares), slabs), kThreads, smem, s>>>(p, gx);
+            gn_bwd_kernel<T, S::LPG, S::NV, F::C, F::S, F::Z><<<grid, kThreads, smem, s>>>(p, gx);
             return 0;
         });
     });
