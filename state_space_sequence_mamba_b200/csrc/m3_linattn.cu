@@ -155,45 +155,86 @@ size_t shared_bytes(const m3_linattn_dims* d, int which, bool packed) {
     return (static_cast<size_t>(rows) * d->nheads * dim * 4 + 255) / 256 * 256;
 }
 
-// The sum over the H / heads heads that read one head of a tensor, in order, rounded once.
+// The sum over the H / heads heads that read one head of a tensor, in order, rounded once: up to
+// three tensors in one launch (blockIdx.y), eight columns a thread where the dimension allows.
+struct Fold {
+    const float* part;
+    void* out;
+    int64_t batch, token, head;
+    int heads, ratio, dim, vec;
+    int64_t units;          // rows * heads * (dim / vec)
+};
+struct Folds {
+    Fold f[3];
+    const int32_t* cu;
+    int64_t L;
+    int nseq;
+};
 template <typename T>
-__global__ void __launch_bounds__(256)
-fold_heads_kernel(const float* __restrict__ part, T* out, int64_t batch, int64_t token, int64_t head,
-                  int64_t L, int64_t total, int heads, int ratio, int dim, const int32_t* cu, int nseq) {
-    for (int64_t e = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; e < total;
+__global__ void __launch_bounds__(256) fold_heads_kernel(const __grid_constant__ Folds p) {
+    const Fold& f = p.f[blockIdx.y];
+    const int per = f.dim / f.vec;
+    for (int64_t e = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; e < f.units;
          e += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const int c = static_cast<int>(e % dim);
-        const int64_t rh = e / dim;
-        const int g = static_cast<int>(rh % heads);
-        const int64_t row = rh / heads;
-        const int64_t b = cu ? 0 : row / L, t = cu ? row : row % L;
-        if (cu && (row < cu[0] || row >= cu[nseq])) continue;    // rows of no sequence are left alone
-        const float* src = part + (row * heads + g) * static_cast<int64_t>(ratio) * dim + c;
-        float s = 0.f;
-        for (int i = 0; i < ratio; ++i) s += src[static_cast<int64_t>(i) * dim];
-        out[b * batch + t * token + g * head + c] = from_f<T>(s);
+        const int c = static_cast<int>(e % per) * f.vec;
+        const int64_t rh = e / per;
+        const int g = static_cast<int>(rh % f.heads);
+        const int64_t row = rh / f.heads;
+        if (p.cu && (row < p.cu[0] || row >= p.cu[p.nseq])) continue;   // rows of no sequence are left alone
+        const int64_t b = p.cu ? 0 : row / p.L, t = p.cu ? row : row % p.L;
+        const float* src = f.part + (row * f.heads + g) * static_cast<int64_t>(f.ratio) * f.dim + c;
+        T* out = static_cast<T*>(f.out) + b * f.batch + t * f.token + g * f.head + c;
+        if (f.vec == 8) {
+            float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+            for (int i = 0; i < f.ratio; ++i) {
+                const float4 lo = __ldcs(reinterpret_cast<const float4*>(src + static_cast<int64_t>(i) * f.dim));
+                const float4 hi = __ldcs(reinterpret_cast<const float4*>(src + static_cast<int64_t>(i) * f.dim + 4));
+                s[0] += lo.x; s[1] += lo.y; s[2] += lo.z; s[3] += lo.w;
+                s[4] += hi.x; s[5] += hi.y; s[6] += hi.z; s[7] += hi.w;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) out[i] = from_f<T>(s[i]);
+        } else {
+            float s = 0.f;
+            for (int i = 0; i < f.ratio; ++i) s += src[static_cast<int64_t>(i) * f.dim];
+            *out = from_f<T>(s);
+        }
     }
 }
 
-cudaError_t fold_heads(const m3_linattn_dims* d, int which, const float* part, const m3_view& v,
+cudaError_t fold_heads(const m3_linattn_dims* d, float* const (&part)[3], const m3_view* const (&v)[3],
                        const int32_t* cu, cudaStream_t s) {
-    const int64_t heads = which == 0 ? d->qheads : which == 1 ? d->kheads : d->vheads;
-    const int64_t dim = which == 2 ? d->vdim : d->kdim;
+    Folds p{};
+    p.cu = cu;
+    p.L = d->seqlen;
+    p.nseq = static_cast<int>(d->nseq);
     const int64_t rows = cu ? d->seqlen : d->nseq * d->seqlen;
-    const int64_t total = rows * heads * dim;
-    if (total == 0) return cudaSuccess;
-    int64_t grid = (total + 255) / 256;
-    const int64_t most = 32LL * device_sm_count();
-    if (grid > most) grid = most;
-    const int ratio = static_cast<int>(d->nheads / heads);
-    if (d->in_dtype == M3_BF16)
-        fold_heads_kernel<__nv_bfloat16><<<static_cast<unsigned>(grid), 256, 0, s>>>(
-            part, static_cast<__nv_bfloat16*>(v.data), v.batch, v.token, v.head, d->seqlen, total,
-            static_cast<int>(heads), ratio, static_cast<int>(dim), cu, static_cast<int>(d->nseq));
-    else
-        fold_heads_kernel<float><<<static_cast<unsigned>(grid), 256, 0, s>>>(
-            part, static_cast<float*>(v.data), v.batch, v.token, v.head, d->seqlen, total,
-            static_cast<int>(heads), ratio, static_cast<int>(dim), cu, static_cast<int>(d->nseq));
+    int n = 0;
+    int64_t most = 0;
+    for (int i = 0; i < 3; ++i) {
+        if (!part[i]) continue;
+        Fold& f = p.f[n++];
+        const int64_t heads = i == 0 ? d->qheads : i == 1 ? d->kheads : d->vheads;
+        f.part = part[i];
+        f.out = v[i]->data;
+        f.batch = v[i]->batch;
+        f.token = v[i]->token;
+        f.head = v[i]->head;
+        f.heads = static_cast<int>(heads);
+        f.ratio = static_cast<int>(d->nheads / heads);
+        f.dim = static_cast<int>(i == 2 ? d->vdim : d->kdim);
+        f.vec = f.dim % 8 == 0 ? 8 : 1;
+        f.units = rows * heads * (f.dim / f.vec);
+        most = f.units > most ? f.units : most;
+    }
+    if (n == 0 || most == 0) return cudaSuccess;
+    int64_t grid = (most + 255) / 256;
+    const int64_t lim = 16LL * device_sm_count();
+    if (grid > lim) grid = lim;
+    const dim3 g(static_cast<unsigned>(grid), static_cast<unsigned>(n));
+    if (d->in_dtype == M3_BF16) fold_heads_kernel<__nv_bfloat16><<<g, 256, 0, s>>>(p);
+    else fold_heads_kernel<float><<<g, 256, 0, s>>>(p);
     return cudaGetLastError();
 }
 
@@ -369,11 +410,8 @@ m3_status m3_linattn_bwd(const m3_linattn_dims* dims, const m3_linattn_inputs* i
         p.job[1].init = p.job[2].init = reinterpret_cast<const float*>(ws);
     }
     if ((st = run_jobs(p, dims, bwd_rows(dims), seg, s)) != M3_OK) return st;
-    for (int i = 0; i < 3; ++i)
-        if (part[i]) {
-            const cudaError_t e = fold_heads(dims, i, part[i], *outs[i], in->cu_seqlens, s);
-            if (e != cudaSuccess) return cuda_err(e, "gradient sum launch");
-        }
+    const cudaError_t e = fold_heads(dims, part, outs, in->cu_seqlens, s);
+    if (e != cudaSuccess) return cuda_err(e, "gradient sum launch");
     return M3_OK;
 }
 

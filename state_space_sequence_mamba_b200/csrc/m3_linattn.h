@@ -12,6 +12,7 @@
 // (state_only), and in the second every segment sums its predecessors' end states, decayed.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -87,6 +88,19 @@ struct LinStep {
     float scale;
 };
 cudaError_t launch_lin_step(const LinStep& p, bool bf16, cudaStream_t s);
+
+// Raises a kernel's limit of dynamic shared memory to `bytes` (the kernel's largest), once per device.
+template <typename K>
+cudaError_t allow_smem(K* kernel, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (bit && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 #ifdef __CUDACC__
 // What a CTA's (sequence, segment) index stands for.

@@ -214,21 +214,23 @@ lin_simt_kernel(const __grid_constant__ LinParams p) {
     }
 }
 
+template <typename T, int C, bool kStateOnly>
+cudaError_t launch_one(const LinParams& p, int Dk, cudaStream_t s) {
+    static std::atomic<uint64_t> done{0};
+    auto k = lin_simt_kernel<T, C, kStateOnly>;
+    const cudaError_t e = allow_smem(k, simt_smem(C == 64 ? 128 : 256, C).bytes, done);
+    if (e != cudaSuccess) return e;
+    k<<<static_cast<unsigned>(p.blocks_x * p.H * p.rtiles), kThreads, simt_smem(Dk, C).bytes, s>>>(p);
+    return cudaGetLastError();
+}
+
 template <typename T, int C>
 cudaError_t launch_t(const LinParams& p, int Dk, bool cut, cudaStream_t s) {
-    const int bytes = simt_smem(Dk, C).bytes;
-    const unsigned grid = static_cast<unsigned>(p.blocks_x * p.H * p.rtiles);
-    cudaError_t e;
     if (cut) {
-        auto k0 = lin_simt_kernel<T, C, true>;
-        if ((e = cudaFuncSetAttribute(k0, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
-        k0<<<grid, kThreads, bytes, s>>>(p);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        const cudaError_t e = launch_one<T, C, true>(p, Dk, s);
+        if (e != cudaSuccess) return e;
     }
-    auto k1 = lin_simt_kernel<T, C, false>;
-    if ((e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
-    k1<<<grid, kThreads, bytes, s>>>(p);
-    return cudaGetLastError();
+    return launch_one<T, C, false>(p, Dk, s);
 }
 
 }  // namespace

@@ -188,6 +188,7 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
     const LinJob& j = p.job[ji];
     const LinWhere w = lin_locate(p, x);
     if (!w.valid) return;
+    if (kStateOnly) grid_dep_launch_dependents();
     const bool rev = j.reverse;
     const int order = rev ? w.nseg - 1 - w.seg : w.seg;
     const bool last_seg = order == w.nseg - 1;
@@ -335,6 +336,7 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
             const int before = rev ? (order == 0 ? 0 : w.len - (seg0 + p.seg_len)) : seg0;
             const float fi = lin_pow(g2, static_cast<float>(rev && before > 0 ? before - 1 : before));
             const bool live = r < j.Dk, given = j.init && live && fi != 0.f;
+            if (order > 0) grid_dep_wait();     // the segments' end states are there
             const float* src = given ? j.init + (static_cast<int64_t>(w.seq) * p.H + h) * j.Dk * j.Dv + r * j.init_k +
                                            (tile * kVT + c0) * j.init_v
                                      : nullptr;
@@ -453,11 +455,12 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
 #pragma unroll 1
         for (int c = 0; c < nchunks; ++c) {
             const int st = c & 1, n = chunk_n(c);
-            if (c >= nupdates && n == kC) break;
+            if (c >= nupdates && (n == kC || !p.cu)) break;
             if (!lwait_warp(&bars[B_V + st], c >> 1, &s_abort)) break;
-            if (n < kC) {
-                // Rows of k and v behind the last token, another sequence's or anything, become zeros before
-                // a product reads them: their weights are, but zero times NaN is not.
+            if (n < kC && p.cu) {
+                // Packed: rows of k and v behind the last token, another sequence's or anything, become zeros
+                // before a product reads them: their weights are, but zero times NaN is not. (In a batch they
+                // lie outside the tensor map, whose loads fill in zeros.)
                 if (!lwait_warp(&bars[B_QK + st], c >> 1, &s_abort)) break;
                 if (r >= n) {
 #pragma unroll 1
@@ -564,7 +567,7 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
                         const int st = (c + 1) & 1, ph = (c + 1) >> 1;
                         if (!lwait_warp(&bars[B_QK + st], ph, &s_abort)) break;
                         if (c > 0 && !lwait_warp(&bars[B_SFREE + st], ph - 1, &s_abort)) break;
-                        if (chunk_n(c + 1) < kC && !lwait_warp(&bars[B_CLEAN], 0, &s_abort)) break;
+                        if (p.cu && chunk_n(c + 1) < kC && !lwait_warp(&bars[B_CLEAN], 0, &s_abort)) break;
                         fence_after_sync();
                         issued = true;
                         const uint32_t loQ = desc_lo(smem_u32(sm + S_Q + 2 * st * kSlab), 16);
@@ -664,6 +667,8 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
         }
     }
 
+    // no CTA ends before the launch before it: what comes after this grid comes after both
+    if (!kStateOnly && tid == 0) grid_dep_wait();
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
@@ -737,24 +742,25 @@ cudaError_t launch_lin_tc(const LinParams& p, bool cut, cudaStream_t s) {
             if (!encode_tmap(&maps.m[m], true, 4, t.p, d, st, box, true)) return cudaErrorInvalidValue;
         }
     }
-    const unsigned grid = static_cast<unsigned>(p.blocks_x * p.H * p.rtiles);
-    cudaError_t e;
-    if (cut) {
-        e = cudaFuncSetAttribute(lin_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-        if (e != cudaSuccess) return e;
-        lin_tc_kernel<true><<<grid, kThreads, kSmem, s>>>(tp, maps);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
-    e = cudaFuncSetAttribute(lin_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
-    // the roles' shares add up to a launch with exactly these
+    // the roles' register shares add up to a launch with exactly these
     static const int regs = [] {
         cudaFuncAttributes a{};
         return cudaFuncGetAttributes(&a, lin_tc_kernel<false>) == cudaSuccess ? a.numRegs : 0;
     }();
     if (regs != kRegsLaunch) return cudaErrorInvalidConfiguration;
-    lin_tc_kernel<false><<<grid, kThreads, kSmem, s>>>(tp, maps);
-    return cudaGetLastError();
+    const unsigned grid = static_cast<unsigned>(p.blocks_x * p.H * p.rtiles);
+    static std::atomic<uint64_t> done_state{0}, done{0};
+    cudaError_t e = allow_smem(lin_tc_kernel<false>, kSmem, done);
+    if (e != cudaSuccess) return e;
+    if (!cut) {
+        lin_tc_kernel<false><<<grid, kThreads, kSmem, s>>>(tp, maps);
+        return cudaGetLastError();
+    }
+    if ((e = allow_smem(lin_tc_kernel<true>, kSmem, done_state)) != cudaSuccess) return e;
+    lin_tc_kernel<true><<<grid, kThreads, kSmem, s>>>(tp, maps);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    // may start while the end states' kernel runs; whoever reads them waits for it
+    return launch_after_rms(lin_tc_kernel<false>, grid, kThreads, kSmem, s, tp, maps);
 }
 
 cudaError_t lin_tc_timeout(int* flag) {
