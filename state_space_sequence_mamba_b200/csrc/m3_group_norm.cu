@@ -18,6 +18,7 @@
 
 #include "m3_common.cuh"
 #include "m3_internal.h"
+#include "m3_sm100.cuh"
 
 namespace m3 {
 namespace {
@@ -218,6 +219,7 @@ template <typename T, int LPG, int NV, bool kCenter, bool kSilu, bool kGate>
 __global__ void __launch_bounds__(kThreads) gn_bwd_kernel(const GnParams p, int gx) {
     constexpr int N = Vec<T>::N;
     extern __shared__ float s_part[];
+    sm100::grid_dep_launch_dependents();
     Walk<T, LPG, NV> k(p, gx);
     uint4 rx[NV], rz[NV], rd[NV];
     k.fetch(p, p.x, k.row, rx);
@@ -307,21 +309,24 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_kernel(const GnParams p, int 
     }
 }
 
-// dweight and dbias: the shares of one column added in order by 8 threads, then those by one
-__global__ void __launch_bounds__(kThreads) gn_shares_kernel(const GnParams p) {
-    __shared__ float s[8][33];
+// dweight and dbias: the shares of one column added in order by 32 threads, then those by a tree
+__global__ void __launch_bounds__(1024) gn_shares_kernel(const GnParams p) {
+    __shared__ float s[32][33];
     const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + cx;   // of 2 C columns
+    sm100::grid_dep_wait();     // may have started while the shares were formed
     float sum = 0.f;
     if (c < 2 * static_cast<int64_t>(p.C))
-        for (int k = ry; k < p.shares; k += 8) sum += p.part[static_cast<int64_t>(k) * 2 * p.C + c];
+#pragma unroll 4
+        for (int k = ry; k < p.shares; k += 32) sum += __ldcg(p.part + static_cast<int64_t>(k) * 2 * p.C + c);
     s[ry][cx] = sum;
     __syncthreads();
-    if (ry == 0 && c < 2 * static_cast<int64_t>(p.C)) {
-#pragma unroll
-        for (int k = 1; k < 8; ++k) sum += s[k][cx];
-        float* dst = c < p.C ? p.dw : p.db;
-        if (dst) dst[c < p.C ? c : c - p.C] = sum;
+    // warp ry takes column ry
+    sum = warp_sum(s[cx][ry]);
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + ry;
+    if (cx == 0 && col < 2 * static_cast<int64_t>(p.C)) {
+        float* dst = col < p.C ? p.dw : p.db;
+        if (dst) dst[col < p.C ? col : col - p.C] = sum;
     }
 }
 
@@ -366,6 +371,7 @@ __global__ void __launch_bounds__(kThreads) gn_fwd_any_kernel(const GnParams p) 
 template <typename T, bool kCenter, bool kSilu, bool kGate>
 __global__ void __launch_bounds__(kThreads) gn_bwd_any_kernel(const GnParams p) {
     __shared__ float s[kThreads / 32];
+    sm100::grid_dep_launch_dependents();
     const uint32_t share = blockIdx.x / p.G;
     const int group = static_cast<int>(blockIdx.x - share * p.G), c0 = group * p.D;
     const uint32_t r0 = share * p.share_rows;
@@ -539,8 +545,7 @@ cudaError_t launch_bwd(GnParams p, uint32_t flags, cudaStream_t s) {
     });
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !p.part) return e;
-    gn_shares_kernel<<<static_cast<unsigned>((2 * static_cast<int64_t>(p.C) + 31) / 32), kThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_after_rms(gn_shares_kernel, static_cast<unsigned>((2 * static_cast<int64_t>(p.C) + 31) / 32), 1024, 0, s, p);
 }
 
 m3_status err(m3_status st, const char* fmt, ...) {

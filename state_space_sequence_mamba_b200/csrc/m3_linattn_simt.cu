@@ -41,13 +41,37 @@ __device__ __forceinline__ void fma4(float4& a, float s, const float4& b) {
     a.z = fmaf(s, b.z, a.z); a.w = fmaf(s, b.w, a.w);
 }
 
-// rows [0, n) of a tensor into fp32 shared rows of `width` (>= dim) floats, zeros elsewhere
-template <typename T>
-__device__ __forceinline__ void stage(float* dst, int stride, const T* src, int64_t token, int n, int C,
-                                      int dim, int width) {
-    for (int e = threadIdx.x; e < C * width; e += kThreads) {
-        const int r = e / width, c = e - r * width;
-        dst[r * stride + c] = (r < n && c < dim) ? to_f(src[r * token + c]) : 0.f;
+// four consecutive elements as floats
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u),
+                       __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
+}
+
+// rows [0, n) of a tensor into fp32 shared rows of `width` floats (a multiple of 4, >= dim), zeros
+// elsewhere: 16 threads side by side, four elements each; vec: rows can be read in fours
+template <typename T, int C>
+__device__ __forceinline__ void stage(float* dst, int stride, const T* src, int64_t token, int n, int dim,
+                                      int width, bool vec, int tx, int ty) {
+#pragma unroll
+    for (int a = 0; a < C / 16; ++a) {
+        const int r = ty + 16 * a;
+        const T* row = src + r * token;
+        for (int c = 4 * tx; c < width; c += 64) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < n) {
+                if (vec && c + 4 <= dim) {
+                    v = load4(row + c);
+                } else {
+                    if (c < dim) v.x = to_f(row[c]);
+                    if (c + 1 < dim) v.y = to_f(row[c + 1]);
+                    if (c + 2 < dim) v.z = to_f(row[c + 2]);
+                    if (c + 3 < dim) v.w = to_f(row[c + 3]);
+                }
+            }
+            *reinterpret_cast<float4*>(dst + r * stride + c) = v;
+        }
     }
 }
 
@@ -85,6 +109,10 @@ lin_simt_kernel(const __grid_constant__ LinParams p) {
     const T* v = static_cast<const T*>(j.v.p) + w.batch * j.v.batch + (h / j.v.ratio) * j.v.head + w.row0 * j.v.token +
                  tile * kVT;
     const int vdim = j.Dv - tile * kVT < kVT ? j.Dv - tile * kVT : kVT;
+    auto fours = [](const T* base, int64_t token) {
+        return ((reinterpret_cast<uintptr_t>(base) | static_cast<uintptr_t>(token * sizeof(T))) & (4 * sizeof(T) - 1)) == 0;
+    };
+    const bool vq = fours(q, j.q.token), vk = fours(k, j.k.token), vv4 = fours(v, j.v.token);
     const int64_t ntok = seg_end - seg0;
     const int nchunks = static_cast<int>((ntok + C - 1) / C);
     const int hrows = (L.Dp + 63) / 64;     // 64-row blocks of the state
@@ -95,9 +123,9 @@ lin_simt_kernel(const __grid_constant__ LinParams p) {
         // in reverse the given state meets the sequence's last token undecayed
         const int off = (j.reverse && order == 0 && cc == 0) ? 1 : 0;
         __syncthreads();
-        if (!kStateOnly) stage(sq, L.qs, q + t0 * j.q.token, j.q.token, n, C, j.Dk, L.Dp);
-        stage(sk, L.qs, k + t0 * j.k.token, j.k.token, n, C, j.Dk, L.Dp);
-        stage(sv, kVS, v + t0 * j.v.token, j.v.token, n, C, vdim, kVT);
+        if (!kStateOnly) stage<T, C>(sq, L.qs, q + t0 * j.q.token, j.q.token, n, j.Dk, L.Dp, vq, tx, ty);
+        stage<T, C>(sk, L.qs, k + t0 * j.k.token, j.k.token, n, j.Dk, L.Dp, vk, tx, ty);
+        stage<T, C>(sv, kVS, v + t0 * j.v.token, j.v.token, n, vdim, kVT, vv4, tx, ty);
         __syncthreads();
         if (!kStateOnly) {
             float s[RI][RI];

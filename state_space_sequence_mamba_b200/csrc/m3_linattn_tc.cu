@@ -138,11 +138,6 @@ __device__ __forceinline__ void commit_el(uint32_t el, uint64_t* bar) {
         :: "r"(smem_u32(bar)), "r"(el) : "memory");
 }
 
-__device__ __forceinline__ void tma_prefetch_4d(const void* tmap, int c0, int c1, int c2, int c3) {
-    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];"
-                 :: "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3) : "memory");
-}
-
 // The 72 registers a thread that 28 warps leave are dealt out again by what the roles hold. Spills are
 // what to avoid: beside 227 KB of shared memory the L1 cache is too small to hold them.
 constexpr int kRegsLaunch = 72, kRegsRow = 96, kRegsState = 64, kRegsIssue = 40;
@@ -207,23 +202,48 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
     auto chunk_n = [&](int c) { const int n = seg_end - chunk_t0(c); return n < kC ? n : kC; };
 
     // ---------------- set-up ----------------
-    if (tid == 0) {
-        for (int i = 0; i < kNumBars; ++i) mbar_init(&bars[i], bar_count(i));
-        fence_mbar_init();
+    if (tid == 32 * kOutWarp) {     // the maps on their way while the barriers are set up
+        for (int a = 0; a < 3; ++a)
+            asm volatile("prefetch.tensormap [%0];" :: "l"(&maps.m[tp.map[ji][a]]) : "memory");
         s_abort = 0;
     }
-    if (warp == kLoadWarp) tmem_alloc(&tslot, kTmemCols);
+    // what the first loads need, before anything else: they are issued ahead of the block's barrier
+    auto load = [&](int c) {
+        const int st = c & 1, at = w.row0 + chunk_t0(c);
+        const int hq = h / tp.head_ratio[ji][0], hk = h / tp.head_ratio[ji][1], hv = h / tp.head_ratio[ji][2];
+        const int bq = tp.batched[ji][0] ? w.batch : 0, bk = tp.batched[ji][1] ? w.batch : 0, bv = tp.batched[ji][2] ? w.batch : 0;
+        if (c > 1 && !lwait(&bars[B_QKFREE + st], (c >> 1) - 1, &s_abort)) return false;
+        mbar_arrive_expect_tx(&bars[B_QK + st], (kStateOnly ? 1 : 2) * slabs * kSlab);
+#pragma unroll 1
+        for (int s = 0; s < slabs; ++s) {
+            tma_load_4d(sm + S_K + (2 * st + s) * kSlab, &maps.m[tp.map[ji][1]], &bars[B_QK + st], 64 * s, hk, at, bk);
+            if (!kStateOnly)
+                tma_load_4d(sm + S_Q + (2 * st + s) * kSlab, &maps.m[tp.map[ji][0]], &bars[B_QK + st], 64 * s, hq, at, bq);
+        }
+        if (c > 1 && !lwait(&bars[B_VFREE + st], (c >> 1) - 1, &s_abort)) {
+            (void)mbar_wait(&bars[B_QK + st], (c >> 1) & 1, kDrainCycles);
+            return false;
+        }
+        mbar_arrive_expect_tx(&bars[B_V + st], kSlab);
+        tma_load_4d(sm + S_V + st * kSlab, &maps.m[tp.map[ji][2]], &bars[B_V + st], tile * kVT, hv, at, bv);
+        return true;
+    };
+    const int nloads = kStateOnly ? nupdates : nchunks;
+    if (warp == kLoadWarp) {
+        if (lane == 0) {
+            for (int i = 0; i < kNumBars; ++i) mbar_init(&bars[i], bar_count(i));
+            fence_mbar_init();
+            fence_proxy_async();
+#pragma unroll 1
+            for (int c = 0; c < 2 && c < nloads; ++c) load(c);
+        }
+        __syncwarp();
+        tmem_alloc(&tslot, kTmemCols);
+    }
     if (tid <= kC) pw[tid] = lin_pow(g2, static_cast<float>(tid));
     if (tid >= 256 && tid < 320) {
         const int d = rev ? tid - 287 : 287 - tid;
         mask[tid - 256] = d >= 0 ? lin_pow(g2, static_cast<float>(d)) : 0.f;
-    }
-    if (slabs == 1) {   // the state's rows 64 .. 127: zeros (never loaded)
-        for (int i = tid; i < static_cast<int>(kSlab / 16); i += kThreads) {
-            *reinterpret_cast<uint4*>(sm + S_K + kSlab + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
-            *reinterpret_cast<uint4*>(sm + S_K + 3 * kSlab + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
-        }
-        fence_proxy_async();
     }
     fence_before_sync();
     __syncthreads();
@@ -510,40 +530,11 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
         if (warp == kLoadWarp) {
             // ================= TMA loads (one lane) =================
             if (lane == 0) {
-                const void* mq = &maps.m[tp.map[ji][0]];
-                const void* mk = &maps.m[tp.map[ji][1]];
-                const void* mv = &maps.m[tp.map[ji][2]];
-                const int hq = h / tp.head_ratio[ji][0], hk = h / tp.head_ratio[ji][1], hv = h / tp.head_ratio[ji][2];
-                const int bq = tp.batched[ji][0] ? w.batch : 0, bk = tp.batched[ji][1] ? w.batch : 0;
-                const int bv = tp.batched[ji][2] ? w.batch : 0, row0 = w.row0;
-                const int loads = kStateOnly ? nupdates : nchunks;
-                int done = 0;
+                int done = nloads < 2 ? nloads : 2;
 #pragma unroll 1
-                for (int c = 0; c < loads; ++c) {
-                    const int st = c & 1, at = row0 + chunk_t0(c);
-                    if (c > 1 && !lwait(&bars[B_QKFREE + st], (c >> 1) - 1, &s_abort)) break;
-                    mbar_arrive_expect_tx(&bars[B_QK + st], (kStateOnly ? 1 : 2) * slabs * kSlab);
-#pragma unroll 1
-                    for (int s = 0; s < slabs; ++s) {
-                        tma_load_4d(sm + S_K + (2 * st + s) * kSlab, mk, &bars[B_QK + st], 64 * s, hk, at, bk);
-                        if (!kStateOnly) tma_load_4d(sm + S_Q + (2 * st + s) * kSlab, mq, &bars[B_QK + st], 64 * s, hq, at, bq);
-                    }
-                    if (c > 1 && !lwait(&bars[B_VFREE + st], (c >> 1) - 1, &s_abort)) {
-                        (void)mbar_wait(&bars[B_QK + st], (c >> 1) & 1, kDrainCycles);
-                        break;
-                    }
-                    mbar_arrive_expect_tx(&bars[B_V + st], kSlab);
-                    tma_load_4d(sm + S_V + st * kSlab, mv, &bars[B_V + st], tile * kVT, hv, at, bv);
+                for (int c = done; c < nloads; ++c) {
+                    if (!load(c)) break;
                     done = c + 1;
-                    if (c + 1 < loads) {    // the next chunk on its way to L2
-                        const int tn = row0 + chunk_t0(c + 1);
-#pragma unroll 1
-                        for (int s = 0; s < slabs; ++s) {
-                            tma_prefetch_4d(mk, 64 * s, hk, tn, bk);
-                            if (!kStateOnly) tma_prefetch_4d(mq, 64 * s, hq, tn, bq);
-                        }
-                        tma_prefetch_4d(mv, tile * kVT, hv, tn, bv);
-                    }
                 }
                 // every copy has landed before the CTA exits (at once, unless a wait gave up)
                 for (int c = done > 2 ? done - 2 : 0; c < done; ++c) {
