@@ -49,30 +49,35 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
                        __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
 }
 
-// rows [0, n) of a tensor into fp32 shared rows of `width` floats (a multiple of 4, >= dim), zeros
-// elsewhere: 16 threads side by side, four elements each; vec: rows can be read in fours
-template <typename T, int C>
-__device__ __forceinline__ void stage(float* dst, int stride, const T* src, int64_t token, int n, int dim,
-                                      int width, bool vec, int tx, int ty) {
-#pragma unroll
-    for (int a = 0; a < C / 16; ++a) {
-        const int r = ty + 16 * a;
-        const T* row = src + r * token;
-        for (int c = 4 * tx; c < width; c += 64) {
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < n) {
-                if (vec && c + 4 <= dim) {
-                    v = load4(row + c);
-                } else {
-                    if (c < dim) v.x = to_f(row[c]);
-                    if (c + 1 < dim) v.y = to_f(row[c + 1]);
-                    if (c + 2 < dim) v.z = to_f(row[c + 2]);
-                    if (c + 3 < dim) v.w = to_f(row[c + 3]);
-                }
-            }
-            *reinterpret_cast<float4*>(dst + r * stride + c) = v;
-        }
+// four elements of a row from column c on, zeros beyond its `dim` (vec: the row can be read in fours)
+template <typename T>
+__device__ __forceinline__ float4 fetch4(const T* row, int c, int dim, bool vec) {
+    if (vec && c + 4 <= dim) return load4(row + c);
+    float v[4];
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        const float x = c + i < dim ? to_f(row[c + i]) : 0.f;
+        v[0] = i == 0 ? x : v[0]; v[1] = i == 1 ? x : v[1];
+        v[2] = i == 2 ? x : v[2]; v[3] = i == 3 ? x : v[3];
     }
+    return make_float4(v[0], v[1], v[2], v[3]);
+}
+
+// the first `left` of four elements (vec: the address takes all four at once)
+__device__ __forceinline__ void put4(float* p, const float (&o)[4]) { *reinterpret_cast<float4*>(p) = make_float4(o[0], o[1], o[2], o[3]); }
+__device__ __forceinline__ void put4(__nv_bfloat16* p, const float (&o)[4]) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(o[0], o[1]), b = __floats2bfloat162_rn(o[2], o[3]);
+    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+template <typename T>
+__device__ __forceinline__ void store4(T* p, const float (&o)[4], int left, bool vec) {
+    if (vec && left >= 4) {
+        put4(p, o);
+        return;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+        if (u < left) p[u] = from_f<T>(o[u]);
 }
 
 template <typename T, int C, bool kStateOnly>
@@ -99,10 +104,10 @@ lin_simt_kernel(const __grid_constant__ LinParams p) {
     float *sq = sm + L.q, *sk = sm + L.k, *sv = sm + L.v, *sp = sm + L.p, *sh = sm + L.h, *pw = sm + L.pw;
     const float g2 = p.log_decay[h] * 1.4426950408889634f;
     for (int i = tid; i <= C; i += kThreads) pw[i] = lin_pow(g2, static_cast<float>(i));
+    const bool blank = kStateOnly || (order == 0 && !j.init);      // no state before this segment
     for (int e = tid; e < L.Dp * kVT; e += kThreads) {
         const int r = e / kVT, c = e % kVT;
-        sh[r * kVS + c] = (kStateOnly || r >= j.Dk) ? 0.f
-                          : lin_start_state(p, j, w, x, h, rt, tile, g2, r, c);
+        sh[r * kVS + c] = blank || r >= j.Dk ? 0.f : lin_start_state(p, j, w, x, h, rt, tile, g2, r, c);
     }
     const T* q = static_cast<const T*>(j.q.p) + w.batch * j.q.batch + (h / j.q.ratio) * j.q.head + w.row0 * j.q.token;
     const T* k = static_cast<const T*>(j.k.p) + w.batch * j.k.batch + (h / j.k.ratio) * j.k.head + w.row0 * j.k.token;
@@ -113,6 +118,10 @@ lin_simt_kernel(const __grid_constant__ LinParams p) {
         return ((reinterpret_cast<uintptr_t>(base) | static_cast<uintptr_t>(token * sizeof(T))) & (4 * sizeof(T) - 1)) == 0;
     };
     const bool vq = fours(q, j.q.token), vk = fours(k, j.k.token), vv4 = fours(v, j.v.token);
+    const int64_t y0 = w.batch * j.y_batch + w.row0 * j.y_token + h * j.y_head + tile * kVT;
+    const int es = j.y_f32 ? 4 : static_cast<int>(sizeof(T));
+    const bool yv = ((reinterpret_cast<uintptr_t>(j.y) | static_cast<uintptr_t>(y0 * es) | static_cast<uintptr_t>(j.y_token * es)) &
+                     (4 * es - 1)) == 0;
     const int64_t ntok = seg_end - seg0;
     const int nchunks = static_cast<int>((ntok + C - 1) / C);
     const int hrows = (L.Dp + 63) / 64;     // 64-row blocks of the state
@@ -123,9 +132,31 @@ lin_simt_kernel(const __grid_constant__ LinParams p) {
         // in reverse the given state meets the sequence's last token undecayed
         const int off = (j.reverse && order == 0 && cc == 0) ? 1 : 0;
         __syncthreads();
-        if (!kStateOnly) stage<T, C>(sq, L.qs, q + t0 * j.q.token, j.q.token, n, j.Dk, L.Dp, vq, tx, ty);
-        stage<T, C>(sk, L.qs, k + t0 * j.k.token, j.k.token, n, j.Dk, L.Dp, vk, tx, ty);
-        stage<T, C>(sv, kVS, v + t0 * j.v.token, j.v.token, n, vdim, kVT, vv4, tx, ty);
+        // q, k and v rows as fp32, zeros behind the last token and column: 16 threads side by side, four
+        // elements each, every load of a sweep issued before the first is stored
+#pragma unroll 1
+        for (int c = 4 * tx; c < L.Dp || c < kVT; c += 64) {
+            float4 fq[RI], fk[RI], fv[RI];
+#pragma unroll
+            for (int a = 0; a < RI; ++a) {
+                const int r = ty + 16 * a;
+                fq[a] = fk[a] = fv[a] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (r < n) {
+                    if (!kStateOnly && c < j.Dk) fq[a] = fetch4(q + (t0 + r) * j.q.token, c, j.Dk, vq);
+                    if (c < j.Dk) fk[a] = fetch4(k + (t0 + r) * j.k.token, c, j.Dk, vk);
+                    if (c < vdim) fv[a] = fetch4(v + (t0 + r) * j.v.token, c, vdim, vv4);
+                }
+            }
+#pragma unroll
+            for (int a = 0; a < RI; ++a) {
+                const int r = ty + 16 * a;
+                if (c < L.Dp) {
+                    if (!kStateOnly) *reinterpret_cast<float4*>(sq + r * L.qs + c) = fq[a];
+                    *reinterpret_cast<float4*>(sk + r * L.qs + c) = fk[a];
+                }
+                if (c < kVT) *reinterpret_cast<float4*>(sv + r * kVS + c) = fv[a];
+            }
+        }
         __syncthreads();
         if (!kStateOnly) {
             float s[RI][RI];
@@ -133,6 +164,7 @@ lin_simt_kernel(const __grid_constant__ LinParams p) {
             for (int a = 0; a < RI; ++a)
 #pragma unroll
                 for (int b = 0; b < RI; ++b) s[a][b] = 0.f;
+#pragma unroll 1
             for (int d = 0; d < L.Dp; d += 4) {
                 float4 qa[RI], kb[RI];
 #pragma unroll
@@ -158,10 +190,13 @@ lin_simt_kernel(const __grid_constant__ LinParams p) {
                     sp[i * (C + 4) + jj] = (d >= 0 && jj < n) ? s[a][b] * (j.p_scale * pw[d]) : 0.f;
                 }
             __syncthreads();
+            // columns of P that hold tokens; no state yet (a fresh sequence's first chunk): nothing to read
+            const int nr = (n + 3) & ~3, hd4 = (cc == 0 && blank) ? 0 : L.Dp;
             float4 yi[RI], yh[RI];
 #pragma unroll
             for (int a = 0; a < RI; ++a) yi[a] = yh[a] = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int jj = 0; jj < C; jj += 4) {
+#pragma unroll 2
+            for (int jj = 0; jj < nr; jj += 4) {
                 float4 vv[4];
 #pragma unroll
                 for (int u = 0; u < 4; ++u) vv[u] = *reinterpret_cast<const float4*>(sv + (jj + u) * kVS + 4 * tx);
@@ -172,7 +207,8 @@ lin_simt_kernel(const __grid_constant__ LinParams p) {
                     fma4(yi[a], pp.z, vv[2]); fma4(yi[a], pp.w, vv[3]);
                 }
             }
-            for (int d = 0; d < L.Dp; d += 4) {
+#pragma unroll 1
+            for (int d = 0; d < hd4; d += 4) {
                 float4 hh[4];
 #pragma unroll
                 for (int u = 0; u < 4; ++u) hh[u] = *reinterpret_cast<const float4*>(sh + (d + u) * kVS + 4 * tx);
@@ -190,16 +226,14 @@ lin_simt_kernel(const __grid_constant__ LinParams p) {
                 const float f = j.o_scale * pw[(j.reverse ? n - i : i + 1) - off];
                 const float o[4] = {fmaf(f, yh[a].x, yi[a].x), fmaf(f, yh[a].y, yi[a].y),
                                     fmaf(f, yh[a].z, yi[a].z), fmaf(f, yh[a].w, yi[a].w)};
-                const int64_t at = w.batch * j.y_batch + (w.row0 + t0 + i) * j.y_token + h * j.y_head + tile * kVT + 4 * tx;
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    if (4 * tx + u < vdim) {
-                        if (j.y_f32) static_cast<float*>(j.y)[at + u] = o[u];
-                        else static_cast<T*>(j.y)[at + u] = from_f<T>(o[u]);
-                    }
+                const int64_t at = y0 + (t0 + i) * j.y_token + 4 * tx;
+                if (j.y_f32) store4(static_cast<float*>(j.y) + at, o, vdim - 4 * tx, yv);
+                else store4(static_cast<T*>(j.y) + at, o, vdim - 4 * tx, yv);
             }
             __syncthreads();     // the state has been read
         }
+        // the last chunk's update only for a state that somebody wants
+        if (!kStateOnly && cc + 1 == nchunks && !(j.final_state && order == w.nseg - 1)) break;
         const float hd = pw[n - off];
         for (int b = 0; b < hrows; ++b) {
             const int k0 = 64 * b + 4 * ty;
@@ -207,6 +241,7 @@ lin_simt_kernel(const __grid_constant__ LinParams p) {
             float4 acc[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
             for (int i = 0; i < n; ++i) {
                 const float wt = pw[j.reverse ? i : n - 1 - i];
                 const float4 kk = *reinterpret_cast<const float4*>(sk + i * L.qs + k0);
