@@ -12,29 +12,27 @@ namespace m3 {
 
 // Segments trade work for parallelism: every cut sequence reads its k and v a second time (for the
 // segments' end states), so sequences are cut only while their number leaves CTA slots empty.
-// A segment has at least kMinSegTokens tokens.
-constexpr int64_t kMinSegTokens = 256;
-
-LinPlan lin_plan(int64_t nseq, int64_t L, bool packed, int64_t per_x, int64_t slots) {
+LinPlan lin_plan(int64_t nseq, int64_t L, bool packed, int64_t per_x, const LinForm& form) {
     LinPlan pl{};
-    const int64_t chunks = (L + 127) / 128, min_chunks = kMinSegTokens / 128;
+    const int64_t chunks = (L + form.chunk - 1) / form.chunk;
     if (!packed) {
-        int64_t want = slots / (nseq * per_x);
-        if (want > chunks / min_chunks) want = chunks / min_chunks;
+        int64_t want = form.slots / (nseq * per_x);
+        if (want > chunks / form.min_chunks) want = chunks / form.min_chunks;
         if (want > kLinMaxSegs) want = kLinMaxSegs;
         if (want < 1) want = 1;
-        const int64_t seg = (chunks + want - 1) / want;     // chunks of a segment
-        pl.seg_len = static_cast<int>((seg > 0 ? seg : 1) * 128);
-        pl.nseg = static_cast<int>(seg > 0 ? (chunks + seg - 1) / seg : 1);
+        const int64_t seg = chunks > 0 ? (chunks + want - 1) / want : 1;    // chunks of a segment
+        pl.seg_len = static_cast<int>(seg * form.chunk);
+        pl.nseg = static_cast<int>(chunks > 0 ? (chunks + seg - 1) / seg : 1);
         pl.blocks_x = nseq * pl.nseg;
         pl.cut = pl.nseg > 1;
         return pl;
     }
     // the rows' share of one slot, whichever sequences they belong to
-    int64_t seg = (L * per_x + 128 * slots - 1) / (128 * slots);
-    if (seg < min_chunks) seg = min_chunks;
-    if (seg < (chunks + kLinMaxSegs - 1) / kLinMaxSegs) seg = (chunks + kLinMaxSegs - 1) / kLinMaxSegs;
-    pl.seg_len = static_cast<int>(seg * 128);
+    int64_t seg = (L * per_x + form.chunk * static_cast<int64_t>(form.slots) - 1) / (form.chunk * static_cast<int64_t>(form.slots));
+    const int64_t least = (chunks + kLinMaxSegs - 1) / kLinMaxSegs;
+    if (seg < least) seg = least;
+    if (seg < form.min_chunks) seg = form.min_chunks;
+    pl.seg_len = static_cast<int>(seg * form.chunk);
     pl.nseg = 1;
     // sum of max(1, ceil(len / seg_len)) over nseq sequences of at most L rows together
     pl.blocks_x = L / pl.seg_len + nseq;
@@ -134,15 +132,15 @@ int fwd_tiles(const m3_linattn_dims* d) { return tiles_of(d->vdim); }
 int bwd_tiles(const m3_linattn_dims* d) { return 2 * tiles_of(d->kdim) + tiles_of(d->vdim); }
 int bwd_rows(const m3_linattn_dims* d) { return static_cast<int>(d->kdim > d->vdim ? d->kdim : d->vdim); }
 
-size_t seg_bytes(const m3_linattn_dims* d, bool packed, int rtiles, int rows, int slots) {
+size_t seg_bytes(const m3_linattn_dims* d, bool packed, int rtiles, int rows, const LinForm& form) {
     if (d->nseq == 0 || d->seqlen == 0) return 0;
-    const LinPlan pl = lin_plan(d->nseq, d->seqlen, packed, d->nheads * rtiles, slots);
+    const LinPlan pl = lin_plan(d->nseq, d->seqlen, packed, d->nheads * rtiles, form);
     return pl.cut ? static_cast<size_t>(pl.blocks_x) * d->nheads * rtiles * rows * kLinTile * 4 : 0;
 }
 // the larger of what the two forms take (which one runs depends on the tensors' alignment)
 size_t seg_bytes(const m3_linattn_dims* d, bool packed, int rtiles, int rows) {
-    const size_t a = seg_bytes(d, packed, rtiles, rows, lin_simt_slots());
-    const size_t b = seg_bytes(d, packed, rtiles, rows < 128 ? 128 : rows, lin_tc_slots());
+    const size_t a = seg_bytes(d, packed, rtiles, rows, lin_simt_form());
+    const size_t b = seg_bytes(d, packed, rtiles, rows < 128 ? 128 : rows, lin_tc_form());
     return ((a > b ? a : b) + 255) / 256 * 256;
 }
 
@@ -243,7 +241,7 @@ m3_status run_jobs(LinParams& p, const m3_linattn_dims* d, int state_rows, char*
     const bool bf16 = d->in_dtype == M3_BF16, packed = p.cu != nullptr;
     const bool tc = bf16 && lin_tc_supported(p);
     const LinPlan pl = lin_plan(d->nseq, d->seqlen, packed, d->nheads * p.rtiles,
-                                tc ? lin_tc_slots() : lin_simt_slots());
+                                tc ? lin_tc_form() : lin_simt_form());
     p.seg_len = pl.seg_len;
     p.nseg = pl.nseg;
     p.blocks_x = pl.blocks_x;

@@ -48,7 +48,7 @@ struct LinParams {
     const int32_t* cu;              // packed sequences, or null
     int nseq, H;
     int64_t L;                      // tokens of each sequence, or rows in all
-    int seg_len;                    // tokens of a segment (a multiple of 128)
+    int seg_len;                    // tokens of a segment (a multiple of the form's chunk)
     int nseg;                       // segments of every sequence (batches)
     int64_t blocks_x;               // (sequence, segment) pairs, or (packed) a bound of theirs
     int njobs, rtiles;              // rtiles = all jobs' tiles
@@ -57,19 +57,23 @@ struct LinParams {
     LinJob job[3];
 };
 
-// Cuts of nseq sequences of L tokens (packed: L rows in all) for `slots` CTAs on the device.
+// Cuts of nseq sequences of L tokens (packed: L rows in all) into segments of at least min_chunks
+// chunks, for `slots` CTAs on the device.
 struct LinPlan {
     int seg_len, nseg;
     int64_t blocks_x;
     bool cut;                       // some sequence may have more than one segment
 };
-LinPlan lin_plan(int64_t nseq, int64_t L, bool packed, int64_t per_x, int64_t slots);
+struct LinForm {
+    int slots, chunk, min_chunks;
+};
+LinPlan lin_plan(int64_t nseq, int64_t L, bool packed, int64_t per_x, const LinForm& form);
 
 // fp32 on the CUDA cores, any dims and strides.
-int lin_simt_slots();
+LinForm lin_simt_form();
 cudaError_t launch_lin_simt(const LinParams& p, bool bf16, bool cut, cudaStream_t s);
 // bf16 on the tensor cores: Dk <= 128, 16-byte aligned tensors.
-int lin_tc_slots();
+LinForm lin_tc_form();
 bool lin_tc_supported(const LinParams& p);
 cudaError_t launch_lin_tc(const LinParams& p, bool cut, cudaStream_t s);
 cudaError_t lin_tc_timeout(int* flag);   // reads and clears the timeout mark (blocks)
@@ -161,37 +165,6 @@ __device__ __forceinline__ LinWhere lin_locate(const LinParams& p, unsigned x) {
 // a^n from log2(a): exact at n = 0 whatever a is (a = 0 included).
 __device__ __forceinline__ float lin_pow(float g2, float n) { return n == 0.f ? 1.f : exp2f(g2 * n); }
 
-// Element (r, c) of the state with which segment w.seg of job j starts (processing order), except
-// that in reverse the first segment's state still lacks no decay (see LinJob::init).
-// order: 0 = first in processing order.
-__device__ __forceinline__ float lin_start_state(const LinParams& p, const LinJob& j, const LinWhere& w,
-                                                 int64_t x, int h, int rt, int tile, float g2, int r, int c) {
-    const int order = j.reverse ? w.nseg - 1 - w.seg : w.seg;
-    const int64_t seg0 = static_cast<int64_t>(w.seg) * p.seg_len;
-    float acc = 0.f;
-    if (j.init && r < j.Dk && tile * kLinTile + c < j.Dv) {
-        // tokens already processed before this segment
-        const int64_t done = j.reverse ? (order == 0 ? 0 : w.len - (seg0 + p.seg_len)) : seg0;
-        const float f = lin_pow(g2, static_cast<float>(j.reverse && done > 0 ? done - 1 : done));
-        const int64_t unit = static_cast<int64_t>(w.seq) * p.H + h;
-        if (f != 0.f)
-            acc = f * j.init[unit * j.Dk * j.Dv + r * j.init_k +
-                             static_cast<int64_t>(tile * kLinTile + c) * j.init_v];
-    }
-    for (int o = 0; o < order; ++o) {
-        const int sg = j.reverse ? w.nseg - 1 - o : o;
-        // tokens between that segment's end and this one's start
-        int64_t gap;
-        if (!j.reverse) gap = seg0 - static_cast<int64_t>(sg + 1) * p.seg_len;
-        else gap = static_cast<int64_t>(sg) * p.seg_len - (seg0 + p.seg_len);
-        const float f = lin_pow(g2, static_cast<float>(gap));
-        if (f == 0.f) continue;
-        const float* e = p.seg + (((x - w.seg + sg) * p.H + h) * p.rtiles + rt) *
-                                     static_cast<int64_t>(p.seg_rows) * kLinTile;
-        acc = fmaf(f, e[static_cast<int64_t>(r) * kLinTile + c], acc);
-    }
-    return acc;
-}
 #endif
 
 }  // namespace m3

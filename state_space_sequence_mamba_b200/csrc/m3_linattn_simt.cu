@@ -5,36 +5,41 @@
 // memory as fp32. Per chunk of n tokens (i, j: positions in processing order's own direction)
 //     P = (q k^T) masked by p_scale a^{|i - j|},  y = P v + o_scale a^{e(i)} q H,
 //     H <- a^n H + sum_j x_scale a^{w(j)} k_j v_j^T,
-// all three as register-tiled products of 256 threads (4 x 4 outputs a thread and step, operands
-// read as float4). With C = 64 a token and head cost 2 (64 Dk + 64 64 + 2 Dk 64) flops, so a
-// chunk is bound by the FMA pipe and shared-memory reads, not by DRAM. Measured on b1 L4096 H16
-// K128 V64 fp32: see the figures beside the launch.
+// as register-tiled products of 256 threads (4 x 4 outputs a thread, operands read as float4; q k^T
+// and q H share one sweep over q). With C = 64 a token and head cost 2 (64 Dk + 64 64 + 2 Dk 64)
+// flops, so a chunk is bound by the FMA pipe and by shared-memory reads, not by DRAM. Rows are not
+// padded but swizzled, and P takes q's place, so that two CTAs of Dk = 128 fit an SM (112 KB each).
 #include "m3_common.cuh"
 #include "m3_internal.h"
 #include "m3_linattn.h"
+#include "m3_sm100.cuh"
 
 namespace m3 {
 namespace {
 
-constexpr int kThreads = 256, kVT = kLinTile, kVS = kVT + 4;
+constexpr int kThreads = 256, kVT = kLinTile;
 
 struct SimtSmem {
-    int Dp, qs;      // Dk padded to 8, its row stride
-    int q, k, v, p, h, pw, bytes;
+    int Dp;          // Dk padded to 16 or a multiple of 32
+    int mask;        // of the swizzle of k's rows: within 16 or 32 columns
+    int q, k, v, h, pw, bytes;
 };
 __host__ __device__ inline SimtSmem simt_smem(int Dk, int C) {
     SimtSmem s;
-    s.Dp = (Dk + 7) / 8 * 8;
-    s.qs = s.Dp + 4;             // 4 mod 8 floats: rows 16 lanes read start in different banks
-    s.q = 0;
-    s.k = s.q + C * s.qs;
-    s.v = s.k + C * s.qs;
-    s.p = s.v + C * kVS;
-    s.h = s.p + C * (C + 4);
-    s.pw = s.h + s.Dp * kVS;
+    s.Dp = Dk <= 16 ? 16 : (Dk + 31) / 32 * 32;
+    s.mask = s.Dp == 16 ? 12 : 28;
+    s.q = 0;                                            // q, then P [C][C]
+    s.k = s.q + C * (s.Dp > C ? s.Dp : C);
+    s.v = s.k + C * s.Dp;
+    s.h = s.v + C * kVT;
+    s.pw = s.h + s.Dp * kVT;
     s.bytes = (s.pw + C + 4) * 4;
     return s;
 }
+// Column c of row r, swizzled in fours: the rows that a warp reads at once (16 neighbours of k, 2 of q
+// and P) start in different banks.
+__device__ __forceinline__ int swz_k(int r, int c, int mask) { return c ^ ((r << 2) & mask); }
+__device__ __forceinline__ int swz_q(int r, int c) { return c ^ ((r & 1) << 2); }
 
 __device__ __forceinline__ void fma4(float4& a, float s, const float4& b) {
     a.x = fmaf(s, b.x, a.x); a.y = fmaf(s, b.y, a.y);
@@ -81,7 +86,7 @@ __device__ __forceinline__ void store4(T* p, const float (&o)[4], int left, bool
 }
 
 template <typename T, int C, bool kStateOnly>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 lin_simt_kernel(const __grid_constant__ LinParams p) {
     constexpr int RI = C / 16;      // rows a thread owns in the S and y products
     extern __shared__ __align__(16) float sm[];
@@ -101,13 +106,57 @@ lin_simt_kernel(const __grid_constant__ LinParams p) {
     if (kStateOnly && order == w.nseg - 1) return;    // nobody reads the last one's
 
     const SimtSmem L = simt_smem(j.Dk, C);
-    float *sq = sm + L.q, *sk = sm + L.k, *sv = sm + L.v, *sp = sm + L.p, *sh = sm + L.h, *pw = sm + L.pw;
+    float *sq = sm + L.q, *sk = sm + L.k, *sv = sm + L.v, *sp = sq, *sh = sm + L.h, *pw = sm + L.pw;
     const float g2 = p.log_decay[h] * 1.4426950408889634f;
     for (int i = tid; i <= C; i += kThreads) pw[i] = lin_pow(g2, static_cast<float>(i));
     const bool blank = kStateOnly || (order == 0 && !j.init);      // no state before this segment
-    for (int e = tid; e < L.Dp * kVT; e += kThreads) {
-        const int r = e / kVT, c = e % kVT;
-        sh[r * kVS + c] = blank || r >= j.Dk ? 0.f : lin_start_state(p, j, w, x, h, rt, tile, g2, r, c);
+    if (kStateOnly) sm100::grid_dep_launch_dependents();
+    else if (order > 0) sm100::grid_dep_wait();         // the segments' end states are there
+    if (blank) {
+        for (int e = tid; e < L.Dp * (kVT / 4); e += kThreads) reinterpret_cast<float4*>(sh)[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    } else {
+        // the given state and the segments before, decayed: eight float4 a thread and sweep
+        const int before = static_cast<int>(j.reverse ? (order == 0 ? 0 : w.len - (seg0 + p.seg_len)) : seg0);
+        const float fi = lin_pow(g2, static_cast<float>(j.reverse && before > 0 ? before - 1 : before));
+        const int64_t unit = static_cast<int64_t>(w.seq) * p.H + h;
+#pragma unroll 1
+        for (int e0 = tid; e0 < L.Dp * (kVT / 4); e0 += 8 * kThreads) {
+            float4 acc[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (j.init && fi != 0.f) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int e = e0 + i * kThreads, r = e / (kVT / 4), c = tile * kVT + e % (kVT / 4) * 4;
+                    if (r >= j.Dk) continue;
+                    const float* src = j.init + unit * j.Dk * j.Dv + r * j.init_k + c * j.init_v;
+                    if (c < j.Dv) acc[i].x = fi * src[0];
+                    if (c + 1 < j.Dv) acc[i].y = fi * src[j.init_v];
+                    if (c + 2 < j.Dv) acc[i].z = fi * src[2 * j.init_v];
+                    if (c + 3 < j.Dv) acc[i].w = fi * src[3 * j.init_v];
+                }
+            }
+#pragma unroll 1
+            for (int o = 0; o < order; ++o) {
+                const int sg = j.reverse ? w.nseg - 1 - o : o;
+                const int64_t gap = j.reverse ? static_cast<int64_t>(sg) * p.seg_len - (seg0 + p.seg_len)
+                                              : seg0 - static_cast<int64_t>(sg + 1) * p.seg_len;
+                const float f = lin_pow(g2, static_cast<float>(gap));
+                if (f == 0.f) continue;
+                const float4* src = reinterpret_cast<const float4*>(
+                    p.seg + ((static_cast<int64_t>(x - w.seg + sg) * p.H + h) * p.rtiles + rt) * p.seg_rows * kVT);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int e = e0 + i * kThreads;
+                    if (e < j.Dk * (kVT / 4)) fma4(acc[i], f, __ldcg(src + e));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int e = e0 + i * kThreads;
+                if (e < L.Dp * (kVT / 4)) reinterpret_cast<float4*>(sh)[e] = acc[i];
+            }
+        }
     }
     const T* q = static_cast<const T*>(j.q.p) + w.batch * j.q.batch + (h / j.q.ratio) * j.q.head + w.row0 * j.q.token;
     const T* k = static_cast<const T*>(j.k.p) + w.batch * j.k.batch + (h / j.k.ratio) * j.k.head + w.row0 * j.k.token;
@@ -124,7 +173,6 @@ lin_simt_kernel(const __grid_constant__ LinParams p) {
                      (4 * es - 1)) == 0;
     const int64_t ntok = seg_end - seg0;
     const int nchunks = static_cast<int>((ntok + C - 1) / C);
-    const int hrows = (L.Dp + 63) / 64;     // 64-row blocks of the state
     for (int cc = 0; cc < nchunks; ++cc) {
         const int c = j.reverse ? nchunks - 1 - cc : cc;
         const int64_t t0 = seg0 + static_cast<int64_t>(c) * C;
@@ -151,26 +199,32 @@ lin_simt_kernel(const __grid_constant__ LinParams p) {
             for (int a = 0; a < RI; ++a) {
                 const int r = ty + 16 * a;
                 if (c < L.Dp) {
-                    if (!kStateOnly) *reinterpret_cast<float4*>(sq + r * L.qs + c) = fq[a];
-                    *reinterpret_cast<float4*>(sk + r * L.qs + c) = fk[a];
+                    if (!kStateOnly) *reinterpret_cast<float4*>(sq + r * L.Dp + swz_q(r, c)) = fq[a];
+                    *reinterpret_cast<float4*>(sk + r * L.Dp + swz_k(r, c, L.mask)) = fk[a];
                 }
-                if (c < kVT) *reinterpret_cast<float4*>(sv + r * kVS + c) = fv[a];
+                if (c < kVT) *reinterpret_cast<float4*>(sv + r * kVT + c) = fv[a];
             }
         }
         __syncthreads();
         if (!kStateOnly) {
             float s[RI][RI];
+            float4 yh[RI];
 #pragma unroll
-            for (int a = 0; a < RI; ++a)
+            for (int a = 0; a < RI; ++a) {
+                yh[a] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int b = 0; b < RI; ++b) s[a][b] = 0.f;
+            }
+            const float *qr = sq + ty * L.Dp, *kr = sk + tx * L.Dp, *hr = sh + 4 * tx;
+            const bool fresh = blank && cc == 0;        // no state to read yet
+            const int xq = swz_q(ty, 0), xk = swz_k(tx, 0, L.mask);
 #pragma unroll 1
             for (int d = 0; d < L.Dp; d += 4) {
                 float4 qa[RI], kb[RI];
 #pragma unroll
-                for (int a = 0; a < RI; ++a) qa[a] = *reinterpret_cast<const float4*>(sq + (ty + 16 * a) * L.qs + d);
+                for (int a = 0; a < RI; ++a) qa[a] = *reinterpret_cast<const float4*>(qr + 16 * a * L.Dp + (d ^ xq));
 #pragma unroll
-                for (int b = 0; b < RI; ++b) kb[b] = *reinterpret_cast<const float4*>(sk + (tx + 16 * b) * L.qs + d);
+                for (int b = 0; b < RI; ++b) kb[b] = *reinterpret_cast<const float4*>(kr + 16 * b * L.Dp + (d ^ xk));
 #pragma unroll
                 for (int a = 0; a < RI; ++a)
 #pragma unroll
@@ -180,90 +234,96 @@ lin_simt_kernel(const __grid_constant__ LinParams p) {
                         s[a][b] = fmaf(qa[a].z, kb[b].z, s[a][b]);
                         s[a][b] = fmaf(qa[a].w, kb[b].w, s[a][b]);
                     }
+                if (fresh) continue;
+                float4 hh[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) hh[u] = *reinterpret_cast<const float4*>(hr + (d + u) * kVT);
+#pragma unroll
+                for (int a = 0; a < RI; ++a) {
+                    fma4(yh[a], qa[a].x, hh[0]); fma4(yh[a], qa[a].y, hh[1]);
+                    fma4(yh[a], qa[a].z, hh[2]); fma4(yh[a], qa[a].w, hh[3]);
+                }
             }
+            __syncthreads();        // q has been read: P takes its place
 #pragma unroll
             for (int a = 0; a < RI; ++a)
 #pragma unroll
                 for (int b = 0; b < RI; ++b) {
                     const int i = ty + 16 * a, jj = tx + 16 * b;
                     const int d = j.reverse ? jj - i : i - jj;
-                    sp[i * (C + 4) + jj] = (d >= 0 && jj < n) ? s[a][b] * (j.p_scale * pw[d]) : 0.f;
+                    sp[i * C + swz_q(i, jj)] = (d >= 0 && jj < n) ? s[a][b] * (j.p_scale * pw[d]) : 0.f;
                 }
             __syncthreads();
-            // columns of P that hold tokens; no state yet (a fresh sequence's first chunk): nothing to read
-            const int nr = (n + 3) & ~3, hd4 = (cc == 0 && blank) ? 0 : L.Dp;
-            float4 yi[RI], yh[RI];
 #pragma unroll
-            for (int a = 0; a < RI; ++a) yi[a] = yh[a] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int a = 0; a < RI; ++a) {
+                const float f = j.o_scale * pw[max((j.reverse ? n - (ty + 16 * a) : ty + 16 * a + 1) - off, 0)];
+                yh[a].x *= f; yh[a].y *= f; yh[a].z *= f; yh[a].w *= f;
+            }
+            const float *pr = sp + ty * C, *vr = sv + 4 * tx;
+            const int nr = (n + 3) & ~3;        // columns of P that hold tokens
 #pragma unroll 2
             for (int jj = 0; jj < nr; jj += 4) {
                 float4 vv[4];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) vv[u] = *reinterpret_cast<const float4*>(sv + (jj + u) * kVS + 4 * tx);
+                for (int u = 0; u < 4; ++u) vv[u] = *reinterpret_cast<const float4*>(vr + (jj + u) * kVT);
 #pragma unroll
                 for (int a = 0; a < RI; ++a) {
-                    const float4 pp = *reinterpret_cast<const float4*>(sp + (ty + 16 * a) * (C + 4) + jj);
-                    fma4(yi[a], pp.x, vv[0]); fma4(yi[a], pp.y, vv[1]);
-                    fma4(yi[a], pp.z, vv[2]); fma4(yi[a], pp.w, vv[3]);
-                }
-            }
-#pragma unroll 1
-            for (int d = 0; d < hd4; d += 4) {
-                float4 hh[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) hh[u] = *reinterpret_cast<const float4*>(sh + (d + u) * kVS + 4 * tx);
-#pragma unroll
-                for (int a = 0; a < RI; ++a) {
-                    const float4 qq = *reinterpret_cast<const float4*>(sq + (ty + 16 * a) * L.qs + d);
-                    fma4(yh[a], qq.x, hh[0]); fma4(yh[a], qq.y, hh[1]);
-                    fma4(yh[a], qq.z, hh[2]); fma4(yh[a], qq.w, hh[3]);
+                    const float4 pp = *reinterpret_cast<const float4*>(pr + 16 * a * C + (jj ^ xq));
+                    fma4(yh[a], pp.x, vv[0]); fma4(yh[a], pp.y, vv[1]);
+                    fma4(yh[a], pp.z, vv[2]); fma4(yh[a], pp.w, vv[3]);
                 }
             }
 #pragma unroll
             for (int a = 0; a < RI; ++a) {
                 const int i = ty + 16 * a;
                 if (i >= n) continue;
-                const float f = j.o_scale * pw[(j.reverse ? n - i : i + 1) - off];
-                const float o[4] = {fmaf(f, yh[a].x, yi[a].x), fmaf(f, yh[a].y, yi[a].y),
-                                    fmaf(f, yh[a].z, yi[a].z), fmaf(f, yh[a].w, yi[a].w)};
+                const float o[4] = {yh[a].x, yh[a].y, yh[a].z, yh[a].w};
                 const int64_t at = y0 + (t0 + i) * j.y_token + 4 * tx;
                 if (j.y_f32) store4(static_cast<float*>(j.y) + at, o, vdim - 4 * tx, yv);
                 else store4(static_cast<T*>(j.y) + at, o, vdim - 4 * tx, yv);
             }
-            __syncthreads();     // the state has been read
         }
         // the last chunk's update only for a state that somebody wants
         if (!kStateOnly && cc + 1 == nchunks && !(j.final_state && order == w.nseg - 1)) break;
         const float hd = pw[n - off];
-        for (int b = 0; b < hrows; ++b) {
-            const int k0 = 64 * b + 4 * ty;
-            if (k0 >= L.Dp) continue;
-            float4 acc[4];
+#pragma unroll 1
+        for (int k0 = 4 * ty; k0 < L.Dp; k0 += 128) {       // two blocks of 64 rows at a time
+            const bool two = k0 + 64 < L.Dp;
+            float4 acc[8];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int u = 0; u < 8; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
             for (int i = 0; i < n; ++i) {
-                const float wt = pw[j.reverse ? i : n - 1 - i];
-                const float4 kk = *reinterpret_cast<const float4*>(sk + i * L.qs + k0);
-                float4 vv = *reinterpret_cast<const float4*>(sv + i * kVS + 4 * tx);
+                const float wt = j.x_scale * pw[j.reverse ? i : n - 1 - i];
+                const float* kr = sk + i * L.Dp;
+                const float4 ka = *reinterpret_cast<const float4*>(kr + swz_k(i, k0, L.mask));
+                float4 vv = *reinterpret_cast<const float4*>(sv + i * kVT + 4 * tx);
                 vv.x *= wt; vv.y *= wt; vv.z *= wt; vv.w *= wt;
-                fma4(acc[0], kk.x, vv); fma4(acc[1], kk.y, vv);
-                fma4(acc[2], kk.z, vv); fma4(acc[3], kk.w, vv);
+                fma4(acc[0], ka.x, vv); fma4(acc[1], ka.y, vv);
+                fma4(acc[2], ka.z, vv); fma4(acc[3], ka.w, vv);
+                if (two) {
+                    const float4 kb = *reinterpret_cast<const float4*>(kr + swz_k(i, k0 + 64, L.mask));
+                    fma4(acc[4], kb.x, vv); fma4(acc[5], kb.y, vv);
+                    fma4(acc[6], kb.z, vv); fma4(acc[7], kb.w, vv);
+                }
             }
+            // (every thread owns its rows' columns, and what read the state is behind the last barrier)
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                float4* at = reinterpret_cast<float4*>(sh + (k0 + u) * kVS + 4 * tx);
+            for (int u = 0; u < 8; ++u) {
+                if (u >= 4 && !two) break;
+                float4* at = reinterpret_cast<float4*>(sh + (k0 + (u & 3) + (u >= 4 ? 64 : 0)) * kVT + 4 * tx);
                 float4 hv = *at;
-                hv.x = fmaf(hd, hv.x, j.x_scale * acc[u].x); hv.y = fmaf(hd, hv.y, j.x_scale * acc[u].y);
-                hv.z = fmaf(hd, hv.z, j.x_scale * acc[u].z); hv.w = fmaf(hd, hv.w, j.x_scale * acc[u].w);
+                hv.x = fmaf(hd, hv.x, acc[u].x); hv.y = fmaf(hd, hv.y, acc[u].y);
+                hv.z = fmaf(hd, hv.z, acc[u].z); hv.w = fmaf(hd, hv.w, acc[u].w);
                 *at = hv;
             }
         }
     }
+    if (!kStateOnly && tid == 0) sm100::grid_dep_wait();    // no CTA ends before the launch before it
     __syncthreads();
     if (kStateOnly) {
         float* e = p.seg + ((static_cast<int64_t>(x) * p.H + h) * p.rtiles + rt) * p.seg_rows * kVT;
-        for (int i = tid; i < j.Dk * kVT; i += kThreads) e[i] = sh[(i / kVT) * kVS + i % kVT];
+        for (int i = tid; i < j.Dk * kVT; i += kThreads) e[i] = sh[i];
         return;
     }
     if (j.final_state && order == w.nseg - 1) {
@@ -272,38 +332,37 @@ lin_simt_kernel(const __grid_constant__ LinParams p) {
         const float f = (j.reverse && w.len > 0) ? pw[1] : 1.f;
         for (int i = tid; i < j.Dk * kVT; i += kThreads) {
             const int r = i / kVT, c = i % kVT;
-            if (c < vdim) dst[static_cast<int64_t>(r) * j.Dv + c] = f * sh[r * kVS + c];
+            if (c < vdim) dst[static_cast<int64_t>(r) * j.Dv + c] = f * sh[i];
         }
     }
 }
 
-template <typename T, int C, bool kStateOnly>
-cudaError_t launch_one(const LinParams& p, int Dk, cudaStream_t s) {
-    static std::atomic<uint64_t> done{0};
-    auto k = lin_simt_kernel<T, C, kStateOnly>;
-    const cudaError_t e = allow_smem(k, simt_smem(C == 64 ? 128 : 256, C).bytes, done);
-    if (e != cudaSuccess) return e;
-    k<<<static_cast<unsigned>(p.blocks_x * p.H * p.rtiles), kThreads, simt_smem(Dk, C).bytes, s>>>(p);
-    return cudaGetLastError();
-}
-
 template <typename T, int C>
 cudaError_t launch_t(const LinParams& p, int Dk, bool cut, cudaStream_t s) {
-    if (cut) {
-        const cudaError_t e = launch_one<T, C, true>(p, Dk, s);
-        if (e != cudaSuccess) return e;
+    static std::atomic<uint64_t> done_state{0}, done{0};
+    const int most = simt_smem(C == 64 ? 128 : 256, C).bytes, bytes = simt_smem(Dk, C).bytes;
+    const unsigned grid = static_cast<unsigned>(p.blocks_x * p.H * p.rtiles);
+    cudaError_t e = allow_smem(lin_simt_kernel<T, C, false>, most, done);
+    if (e != cudaSuccess) return e;
+    if (!cut) {
+        lin_simt_kernel<T, C, false><<<grid, kThreads, bytes, s>>>(p);
+        return cudaGetLastError();
     }
-    return launch_one<T, C, false>(p, Dk, s);
+    if ((e = allow_smem(lin_simt_kernel<T, C, true>, most, done_state)) != cudaSuccess) return e;
+    lin_simt_kernel<T, C, true><<<grid, kThreads, bytes, s>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    // may start while the end states' kernel runs; whoever reads them waits for it
+    return launch_after_rms(lin_simt_kernel<T, C, false>, grid, kThreads, bytes, s, p);
 }
 
 }  // namespace
 
-int lin_simt_slots() { return device_sm_count(); }
+LinForm lin_simt_form() { return LinForm{2 * device_sm_count(), 64, 1}; }
 
 cudaError_t launch_lin_simt(const LinParams& p, bool bf16, bool cut, cudaStream_t s) {
     int Dk = 1;
     for (int i = 0; i < p.njobs; ++i) Dk = p.job[i].Dk > Dk ? p.job[i].Dk : Dk;
-    // 64-token chunks need 222 KB at Dk = 256; there chunks of 32
+    // 64-token chunks need 208 KB at Dk = 256; there chunks of 32 (136 KB)
     if (Dk <= 128) return bf16 ? launch_t<__nv_bfloat16, 64>(p, Dk, cut, s) : launch_t<float, 64>(p, Dk, cut, s);
     return bf16 ? launch_t<__nv_bfloat16, 32>(p, Dk, cut, s) : launch_t<float, 32>(p, Dk, cut, s);
 }

@@ -682,7 +682,8 @@ bool mappable(const LinTensor& t, int64_t L) {
 
 }  // namespace
 
-int lin_tc_slots() { return device_sm_count(); }
+// a shorter segment's set-up costs as much as its chunks
+LinForm lin_tc_form() { return LinForm{device_sm_count(), kC, 2}; }
 
 bool lin_tc_supported(const LinParams& p) {
     for (int i = 0; i < p.njobs; ++i) {

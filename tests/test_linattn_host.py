@@ -239,7 +239,7 @@ def test_workspace_grows_with_the_cut(lib, n, L, per):
     sequences need one 64-column end state per segment and tile."""
     d = ldims(nseq=n, seqlen=L, nheads=per, qheads=1, kheads=1, vheads=1, kdim=128, vdim=64)
     need = lib.m3_linattn_workspace_bytes(ctypes.byref(d), 0)
-    assert (need > 0) == (L >= 512 and n * per < 148)
+    assert (need > 0) == (L >= 128 and n * per < 148)
     if need:
         assert need >= 2 * n * per * 128 * 64 * 4
 
