@@ -7,8 +7,10 @@
 //     H <- a^n H + sum_j x_scale a^{w(j)} k_j v_j^T,
 // as register-tiled products of 256 threads (4 x 4 outputs a thread, operands read as float4; q k^T
 // and q H share one sweep over q). With C = 64 a token and head cost 2 (64 Dk + 64 64 + 2 Dk 64)
-// flops, so a chunk is bound by the FMA pipe and by shared-memory reads, not by DRAM. Rows are not
-// padded but swizzled, and P takes q's place, so that two CTAs of Dk = 128 fit an SM (112 KB each).
+// flops, so a chunk is bound by instruction issue, not by DRAM: the products are packed pairs of FMAs,
+// and blocks above the mask's diagonal are left out. In reverse a chunk's tokens are staged last to
+// first, which makes it a forward one. Rows are not padded but swizzled, and P takes q's place, so
+// that two CTAs of Dk = 128 fit an SM (112 KB each).
 #include "m3_common.cuh"
 #include "m3_internal.h"
 #include "m3_linattn.h"
@@ -40,6 +42,21 @@ __host__ __device__ inline SimtSmem simt_smem(int Dk, int C) {
 // and P) start in different banks.
 __device__ __forceinline__ int swz_k(int r, int c, int mask) { return c ^ ((r << 2) & mask); }
 __device__ __forceinline__ int swz_q(int r, int c) { return c ^ ((r & 1) << 2); }
+
+// pairs of products: c += a b in one instruction
+__device__ __forceinline__ void fma2(float2& c, const float2& a, const float2& b) { c = __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 lo2(const float4& v) { return make_float2(v.x, v.y); }
+__device__ __forceinline__ float2 hi2(const float4& v) { return make_float2(v.z, v.w); }
+__device__ __forceinline__ float2 dup(float v) { return make_float2(v, v); }
+// four columns as two pairs += s times four columns
+struct Four {
+    float2 a, b;
+    __device__ __forceinline__ void add(float s, const float4& v) {
+        const float2 d = dup(s);
+        fma2(a, d, lo2(v));
+        fma2(b, d, hi2(v));
+    }
+};
 
 __device__ __forceinline__ void fma4(float4& a, float s, const float4& b) {
     a.x = fmaf(s, b.x, a.x); a.y = fmaf(s, b.y, a.y);
@@ -188,11 +205,12 @@ lin_simt_kernel(const __grid_constant__ LinParams p) {
 #pragma unroll
             for (int a = 0; a < RI; ++a) {
                 const int r = ty + 16 * a;
+                const int64_t t = t0 + (j.reverse ? n - 1 - r : r);
                 fq[a] = fk[a] = fv[a] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (r < n) {
-                    if (!kStateOnly && c < j.Dk) fq[a] = fetch4(q + (t0 + r) * j.q.token, c, j.Dk, vq);
-                    if (c < j.Dk) fk[a] = fetch4(k + (t0 + r) * j.k.token, c, j.Dk, vk);
-                    if (c < vdim) fv[a] = fetch4(v + (t0 + r) * j.v.token, c, vdim, vv4);
+                    if (!kStateOnly && c < j.Dk) fq[a] = fetch4(q + t * j.q.token, c, j.Dk, vq);
+                    if (c < j.Dk) fk[a] = fetch4(k + t * j.k.token, c, j.Dk, vk);
+                    if (c < vdim) fv[a] = fetch4(v + t * j.v.token, c, vdim, vv4);
                 }
             }
 #pragma unroll
@@ -207,13 +225,14 @@ lin_simt_kernel(const __grid_constant__ LinParams p) {
         }
         __syncthreads();
         if (!kStateOnly) {
-            float s[RI][RI];
-            float4 yh[RI];
+            // s[a][b]: rows ty + 16 a, columns tx + 16 b, the sums of even and odd d apart; b > a is masked
+            float2 s[RI][RI];
+            Four yh[RI];
 #pragma unroll
             for (int a = 0; a < RI; ++a) {
-                yh[a] = make_float4(0.f, 0.f, 0.f, 0.f);
+                yh[a].a = yh[a].b = dup(0.f);
 #pragma unroll
-                for (int b = 0; b < RI; ++b) s[a][b] = 0.f;
+                for (int b = 0; b < RI; ++b) s[a][b] = dup(0.f);
             }
             const float *qr = sq + ty * L.Dp, *kr = sk + tx * L.Dp, *hr = sh + 4 * tx;
             const bool fresh = blank && cc == 0;        // no state to read yet
@@ -228,11 +247,9 @@ lin_simt_kernel(const __grid_constant__ LinParams p) {
 #pragma unroll
                 for (int a = 0; a < RI; ++a)
 #pragma unroll
-                    for (int b = 0; b < RI; ++b) {
-                        s[a][b] = fmaf(qa[a].x, kb[b].x, s[a][b]);
-                        s[a][b] = fmaf(qa[a].y, kb[b].y, s[a][b]);
-                        s[a][b] = fmaf(qa[a].z, kb[b].z, s[a][b]);
-                        s[a][b] = fmaf(qa[a].w, kb[b].w, s[a][b]);
+                    for (int b = 0; b <= a; ++b) {
+                        fma2(s[a][b], lo2(qa[a]), lo2(kb[b]));
+                        fma2(s[a][b], hi2(qa[a]), hi2(kb[b]));
                     }
                 if (fresh) continue;
                 float4 hh[4];
@@ -240,45 +257,50 @@ lin_simt_kernel(const __grid_constant__ LinParams p) {
                 for (int u = 0; u < 4; ++u) hh[u] = *reinterpret_cast<const float4*>(hr + (d + u) * kVT);
 #pragma unroll
                 for (int a = 0; a < RI; ++a) {
-                    fma4(yh[a], qa[a].x, hh[0]); fma4(yh[a], qa[a].y, hh[1]);
-                    fma4(yh[a], qa[a].z, hh[2]); fma4(yh[a], qa[a].w, hh[3]);
+                    yh[a].add(qa[a].x, hh[0]); yh[a].add(qa[a].y, hh[1]);
+                    yh[a].add(qa[a].z, hh[2]); yh[a].add(qa[a].w, hh[3]);
                 }
             }
             __syncthreads();        // q has been read: P takes its place
 #pragma unroll
             for (int a = 0; a < RI; ++a)
 #pragma unroll
-                for (int b = 0; b < RI; ++b) {
-                    const int i = ty + 16 * a, jj = tx + 16 * b;
-                    const int d = j.reverse ? jj - i : i - jj;
-                    sp[i * C + swz_q(i, jj)] = (d >= 0 && jj < n) ? s[a][b] * (j.p_scale * pw[d]) : 0.f;
+                for (int b = 0; b <= a; ++b) {
+                    // (rows behind the last token are zeros)
+                    const int i = ty + 16 * a, jj = tx + 16 * b, d = i - jj;
+                    sp[i * C + swz_q(i, jj)] = d >= 0 ? (s[a][b].x + s[a][b].y) * (j.p_scale * pw[d]) : 0.f;
                 }
             __syncthreads();
 #pragma unroll
             for (int a = 0; a < RI; ++a) {
-                const float f = j.o_scale * pw[max((j.reverse ? n - (ty + 16 * a) : ty + 16 * a + 1) - off, 0)];
-                yh[a].x *= f; yh[a].y *= f; yh[a].z *= f; yh[a].w *= f;
+                const float2 f = dup(j.o_scale * pw[ty + 16 * a + 1 - off]);
+                yh[a].a = __fmul2_rn(yh[a].a, f);
+                yh[a].b = __fmul2_rn(yh[a].b, f);
             }
             const float *pr = sp + ty * C, *vr = sv + 4 * tx;
-            const int nr = (n + 3) & ~3;        // columns of P that hold tokens
-#pragma unroll 2
-            for (int jj = 0; jj < nr; jj += 4) {
-                float4 vv[4];
+            // columns [16 b, 16 b + 16) reach rows from 16 b on
 #pragma unroll
-                for (int u = 0; u < 4; ++u) vv[u] = *reinterpret_cast<const float4*>(vr + (jj + u) * kVT);
+            for (int b = 0; b < RI; ++b) {
+                if (16 * b >= n) break;
+#pragma unroll 1
+                for (int jj = 16 * b; jj < 16 * b + 16; jj += 4) {
+                    float4 vv[4];
 #pragma unroll
-                for (int a = 0; a < RI; ++a) {
-                    const float4 pp = *reinterpret_cast<const float4*>(pr + 16 * a * C + (jj ^ xq));
-                    fma4(yh[a], pp.x, vv[0]); fma4(yh[a], pp.y, vv[1]);
-                    fma4(yh[a], pp.z, vv[2]); fma4(yh[a], pp.w, vv[3]);
+                    for (int u = 0; u < 4; ++u) vv[u] = *reinterpret_cast<const float4*>(vr + (jj + u) * kVT);
+#pragma unroll
+                    for (int a = b; a < RI; ++a) {
+                        const float4 pp = *reinterpret_cast<const float4*>(pr + 16 * a * C + (jj ^ xq));
+                        yh[a].add(pp.x, vv[0]); yh[a].add(pp.y, vv[1]);
+                        yh[a].add(pp.z, vv[2]); yh[a].add(pp.w, vv[3]);
+                    }
                 }
             }
 #pragma unroll
             for (int a = 0; a < RI; ++a) {
                 const int i = ty + 16 * a;
                 if (i >= n) continue;
-                const float o[4] = {yh[a].x, yh[a].y, yh[a].z, yh[a].w};
-                const int64_t at = y0 + (t0 + i) * j.y_token + 4 * tx;
+                const float o[4] = {yh[a].a.x, yh[a].a.y, yh[a].b.x, yh[a].b.y};
+                const int64_t at = y0 + (t0 + (j.reverse ? n - 1 - i : i)) * j.y_token + 4 * tx;
                 if (j.y_f32) store4(static_cast<float*>(j.y) + at, o, vdim - 4 * tx, yv);
                 else store4(static_cast<T*>(j.y) + at, o, vdim - 4 * tx, yv);
             }
@@ -289,22 +311,31 @@ lin_simt_kernel(const __grid_constant__ LinParams p) {
 #pragma unroll 1
         for (int k0 = 4 * ty; k0 < L.Dp; k0 += 128) {       // two blocks of 64 rows at a time
             const bool two = k0 + 64 < L.Dp;
-            float4 acc[8];
+            // acc[u][c]: rows k0 + 2 u, 2 u + 1 (from u = 2 on those of the other block) of column 4 tx + c
+            float2 acc[4][4];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) acc[u][c] = dup(0.f);
+#pragma unroll 2
             for (int i = 0; i < n; ++i) {
-                const float wt = j.x_scale * pw[j.reverse ? i : n - 1 - i];
+                const float wt = j.x_scale * pw[n - 1 - i];
                 const float* kr = sk + i * L.Dp;
                 const float4 ka = *reinterpret_cast<const float4*>(kr + swz_k(i, k0, L.mask));
-                float4 vv = *reinterpret_cast<const float4*>(sv + i * kVT + 4 * tx);
-                vv.x *= wt; vv.y *= wt; vv.z *= wt; vv.w *= wt;
-                fma4(acc[0], ka.x, vv); fma4(acc[1], ka.y, vv);
-                fma4(acc[2], ka.z, vv); fma4(acc[3], ka.w, vv);
+                const float4 vv = *reinterpret_cast<const float4*>(sv + i * kVT + 4 * tx);
+                const float2 w[4] = {dup(vv.x * wt), dup(vv.y * wt), dup(vv.z * wt), dup(vv.w * wt)};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    fma2(acc[0][c], lo2(ka), w[c]);
+                    fma2(acc[1][c], hi2(ka), w[c]);
+                }
                 if (two) {
                     const float4 kb = *reinterpret_cast<const float4*>(kr + swz_k(i, k0 + 64, L.mask));
-                    fma4(acc[4], kb.x, vv); fma4(acc[5], kb.y, vv);
-                    fma4(acc[6], kb.z, vv); fma4(acc[7], kb.w, vv);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        fma2(acc[2][c], lo2(kb), w[c]);
+                        fma2(acc[3][c], hi2(kb), w[c]);
+                    }
                 }
             }
             // (every thread owns its rows' columns, and what read the state is behind the last barrier)
@@ -313,8 +344,10 @@ lin_simt_kernel(const __grid_constant__ LinParams p) {
                 if (u >= 4 && !two) break;
                 float4* at = reinterpret_cast<float4*>(sh + (k0 + (u & 3) + (u >= 4 ? 64 : 0)) * kVT + 4 * tx);
                 float4 hv = *at;
-                hv.x = fmaf(hd, hv.x, acc[u].x); hv.y = fmaf(hd, hv.y, acc[u].y);
-                hv.z = fmaf(hd, hv.z, acc[u].z); hv.w = fmaf(hd, hv.w, acc[u].w);
+                const float2* r = acc[u >> 1];
+                const bool odd = u & 1;
+                hv.x = fmaf(hd, hv.x, odd ? r[0].y : r[0].x); hv.y = fmaf(hd, hv.y, odd ? r[1].y : r[1].x);
+                hv.z = fmaf(hd, hv.z, odd ? r[2].y : r[2].x); hv.w = fmaf(hd, hv.w, odd ? r[3].y : r[3].x);
                 *at = hv;
             }
         }
