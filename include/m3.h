@@ -424,7 +424,7 @@ M3_API m3_status m3_group_norm_fwd(const m3_group_norm_dims* dims, const m3_view
                                    const m3_view* z, const float* weight, const float* bias,
                                    const m3_view* out, void* stream);
 
-/* Workspace bytes of m3_group_norm_bwd, 0 for invalid dims. Any content. */
+/* Workspace bytes of m3_group_norm_bwd, 0 where none is needed or the dims are invalid. Any content. */
 M3_API size_t m3_group_norm_bwd_workspace_bytes(const m3_group_norm_dims* dims);
 
 /* Gradients of sum(out * dout): dx, dz (in_dtype; dz required with z, else not used), dweight and

@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_kernel(const GnParams p, int 
             if (kGate) Vec<T>::store(dz + k.col(i), z[i]);
         }
     }
-    if (!p.part) return;
+    if (!p.dw && !p.db) return;
     // the CTA's rows are added group row by group row
     const int width = gx * p.D;
     float* sw = s_part;
@@ -301,11 +301,12 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_kernel(const GnParams p, int 
         }
         __syncthreads();
     }
-    float* part = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.C;
     const int col0 = blockIdx.y * width;
+    float* part = p.shares > 1 ? p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.C : nullptr;
+    float *ow = part ? part : p.dw, *ob = part ? part + p.C : p.db;     // a single share is the sum
     for (int c = threadIdx.x; c < width && col0 + c < p.C; c += kThreads) {
-        part[col0 + c] = sw[c];
-        part[p.C + col0 + c] = sb[c];
+        if (ow) ow[col0 + c] = sw[c];
+        if (ob) ob[col0 + c] = sb[c];
     }
 }
 
@@ -376,9 +377,14 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_any_kernel(const GnParams p) 
     const int group = static_cast<int>(blockIdx.x - share * p.G), c0 = group * p.D;
     const uint32_t r0 = share * p.share_rows;
     const uint32_t r1 = min(r0 + p.share_rows, p.rows);
-    float* part = p.part ? p.part + static_cast<int64_t>(share) * 2 * p.C + c0 : nullptr;
-    if (part)
-        for (int d = threadIdx.x; d < p.D; d += kThreads) part[d] = part[p.C + d] = 0.f;
+    float* part = p.shares > 1 ? p.part + static_cast<int64_t>(share) * 2 * p.C : nullptr;
+    float *ow = part ? part : p.dw, *ob = part ? part + p.C : p.db;     // a single share is the sum
+    if (ow) ow += c0;
+    if (ob) ob += c0;
+    for (int d = threadIdx.x; d < p.D; d += kThreads) {
+        if (ow) ow[d] = 0.f;
+        if (ob) ob[d] = 0.f;
+    }
     for (uint32_t row = r0; row < r1; ++row) {
         const T* x = at<const T>(p.x, p, row, group);
         const T* dout = at<const T>(p.dout, p, row, group);
@@ -406,10 +412,8 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_any_kernel(const GnParams p) 
                 if (pass == 0) {
                     s1 = fmaf(g, xh, s1);
                     s2 += g;
-                    if (part) {
-                        part[d] = fmaf(dy, xh, part[d]);
-                        part[p.C + d] += dy;
-                    }
+                    if (ow) ow[d] = fmaf(dy, xh, ow[d]);
+                    if (ob) ob[d] += dy;
                 } else {
                     // this thread alone reads and writes element d from here on: dx may be x or dout
                     dx[d] = from_f<T>(r * (g - xh * s1 - s2));
@@ -471,8 +475,10 @@ int vector_count(const GnParams& p) {
     return ok ? p.D / N : 0;
 }
 
-// Shares of the rows: as many as give every SM `per_sm` CTAs, at most one per (CTA's) row.
+// Shares of the rows: as many as give every SM `per_sm` CTAs, at most one per (CTA's) row; of up to
+// four rows one (a second launch to add up shares costs more than the rows).
 int64_t share_count(int64_t rows, int64_t per_row_ctas, int per_sm) {
+    if (rows <= 4) return 1;
     const int64_t want = (per_sm * static_cast<int64_t>(device_sm_count()) + per_row_ctas - 1) / per_row_ctas;
     return rows < want ? (rows > 0 ? rows : 1) : want;
 }
@@ -544,7 +550,7 @@ cudaError_t launch_bwd(GnParams p, uint32_t flags, cudaStream_t s) {
         });
     });
     cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || !p.part) return e;
+    if (e != cudaSuccess || p.shares == 1 || (!p.dw && !p.db)) return e;
     return launch_after_rms(gn_shares_kernel, static_cast<unsigned>((2 * static_cast<int64_t>(p.C) + 31) / 32), 1024, 0, s, p);
 }
 
@@ -645,7 +651,8 @@ m3_status m3_group_norm_fwd(const m3_group_norm_dims* dims, const m3_view* x, co
 
 size_t m3_group_norm_bwd_workspace_bytes(const m3_group_norm_dims* dims) {
     if (check(dims) != M3_OK) return 0;
-    const size_t n = static_cast<size_t>(max_shares(dims->batch * dims->rows)) * 2 * static_cast<size_t>(dims->channels) * 4;
+    const int64_t shares = max_shares(dims->batch * dims->rows);
+    const size_t n = shares > 1 ? static_cast<size_t>(shares) * 2 * static_cast<size_t>(dims->channels) * 4 : 0;
     return (n + 255) / 256 * 256;
 }
 
@@ -673,7 +680,7 @@ m3_status m3_group_norm_bwd(const m3_group_norm_dims* dims, const m3_view* x, co
     }
     if ((st = check_out(dx, dims, "dx")) != M3_OK || (gate && (st = check_out(dz, dims, "dz")) != M3_OK)) return st;
     const size_t need = m3_group_norm_bwd_workspace_bytes(dims);
-    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || ws_bytes < need)
+    if (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || ws_bytes < need))
         return err(M3_ERR_INVALID_ARG, "workspace: NULL, misaligned or below %zu bytes", need);
     GnParams p = make_params(dims, x, z, weight, bias);
     p.dout = tensor(dout);
@@ -681,7 +688,7 @@ m3_status m3_group_norm_bwd(const m3_group_norm_dims* dims, const m3_view* x, co
     p.dz = gate ? tensor(dz) : GnTensor{};
     p.dw = dweight;
     p.db = dbias;
-    p.part = (dweight || dbias) ? static_cast<float*>(workspace) : nullptr;
+    p.part = static_cast<float*>(workspace);
     const cudaError_t e = bf16 ? launch_bwd<__nv_bfloat16>(p, dims->flags, s) : launch_bwd<float>(p, dims->flags, s);
     return e == cudaSuccess ? M3_OK : err(M3_ERR_CUDA, "group norm backward launch: %s", cudaGetErrorString(e));
 }

@@ -430,7 +430,7 @@ m3_status m3_linattn_step(const m3_linattn_dims* dims, const m3_linattn_inputs* 
     if ((st = check_state(state_in, "state_in")) != M3_OK || (st = check_state(state_out, "state_out")) != M3_OK ||
         (st = check_view(o, "o", dims->in_dtype == M3_BF16 ? 2 : 4, any)) != M3_OK)
         return st;
-    if (dims->nseq * dims->nheads > kMaxGrid / 4) return err(M3_ERR_UNSUPPORTED, "nseq * nheads exceeds the grid limit");
+    if (dims->nseq * dims->nheads > kMaxGrid / 16) return err(M3_ERR_UNSUPPORTED, "nseq * nheads exceeds the grid limit");
     if (!any) return M3_OK;
     LinStep p{};
     p.q = tensor(dims, in->q, dims->qheads, false);

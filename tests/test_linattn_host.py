@@ -273,7 +273,7 @@ def test_group_norm_refuses_dims(lib, kw, code):
 
 
 def test_group_norm_refuses_pointers(lib):
-    d = gdims()
+    d = gdims(rows=40)
     fwd = lambda x=gview(), z=None, w=None, b=None, o=gview(): lib.m3_group_norm_fwd(  # noqa: E731
         ctypes.byref(d), x, z, w, b, o, None)
     for kw in (dict(x=None), dict(x=gview(None)), dict(x=gview(FAKE + 1)), dict(z=gview(FAKE + 1)),
