@@ -108,9 +108,10 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-
+__device__ __forceinline__ uint32_t pack2(const float2& v) { return pack2(v.x, v.y); }
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
 // The products and commits below run in convergent code of one warp, predicated on its first lane
 // (`el`), so that descriptors stay in uniform registers: inside a branch of one lane each product
 // took some 200 cycles to issue.
@@ -286,7 +287,9 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
                         const float f = ahead > 0 ? ps * pw[sgn * (32 * b - t) - (rev ? 0 : 31)] : ps;
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) pk[i] = pack2(v[2 * i] * f * m[2 * i], v[2 * i + 1] * f * m[2 * i + 1]);
+                        for (int i = 0; i < 16; ++i)
+                            pk[i] = pack2(__fmul2_rn(__fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), make_float2(f, f)),
+                                                     make_float2(m[2 * i], m[2 * i + 1])));
                     }
                     // block b of P lies over S's block b / 2, which has been read
                     tmem_st_32x32b_x16(ls + 16u * b, pk);
@@ -307,7 +310,11 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
                     tmem_ld_32x32b_x32(ls + T_O2 + 32u * q, o);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = fmaf(f1, a[i], o[i]);
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 y2 = __ffma2_rn(make_float2(f1, f1), make_float2(a[i], a[i + 1]), make_float2(o[i], o[i + 1]));
+                        o[i] = y2.x;
+                        o[i + 1] = y2.y;
+                    }
                     const int left = t < n ? cols - 32 * q : 0;
                     if (j.y_f32) {
 #pragma unroll
@@ -422,7 +429,12 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
                     tmem_ld_32x32b_x16(lb + 64u * part + 16u * q, d);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) hv[16 * q + i] = fmaf(dc, hv[16 * q + i], d[i]);
+                    for (int i = 0; i < 16; i += 2) {
+                        float* at = hv + 16 * q + i;
+                        const float2 h2 = __ffma2_rn(make_float2(dc, dc), make_float2(at[0], at[1]), make_float2(d[i], d[i + 1]));
+                        at[0] = h2.x;
+                        at[1] = h2.y;
+                    }
                 }
             }
             fence_before_sync();
@@ -506,11 +518,11 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
             if (lane == 0) mbar_arrive(&bars[B_VFREE + st]);
 #pragma unroll
             for (int u = 0; u < 16; ++u) {
-                const float a = wt * lo_f(p0[u]), b = wt * hi_f(p0[u]);
-                p0[u] = pack2(a, b);
-                const float a1 = a - lo_f(p0[u]), b1 = b - hi_f(p0[u]);
-                p1[u] = pack2(a1, b1);
-                p2[u] = pack2(a1 - lo_f(p1[u]), b1 - hi_f(p1[u]));
+                const float2 ab = __fmul2_rn(make_float2(wt, wt), unpack2(p0[u])), minus = make_float2(-1.f, -1.f);
+                p0[u] = pack2(ab);
+                const float2 ab1 = __ffma2_rn(unpack2(p0[u]), minus, ab);       // exact
+                p1[u] = pack2(ab1);
+                p2[u] = pack2(__ffma2_rn(unpack2(p1[u]), minus, ab1));
             }
             if (c > 0 && !lwait_warp(&bars[B_DH], c - 1, &s_abort)) break;
 #pragma unroll
