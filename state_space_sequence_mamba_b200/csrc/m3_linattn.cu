@@ -11,20 +11,35 @@
 namespace m3 {
 
 // Segments trade work for parallelism: every cut sequence reads its k and v a second time (for the
-// segments' end states), so sequences are cut only while their number leaves CTA slots empty.
+// segments' end states) and sums its predecessors' states, but the CTAs fill the device's slots more
+// evenly. A batch takes the number of segments with the least estimated time (waves of CTAs, of both
+// launches, times a CTA's chunks), more of them only for a tenth less: they read more of k and v
+// again. (b1 H64 L65536: 2 segments, one wave of 256 chunks on 128 SMs, 0.98 ms; 9 segments, 4 waves of
+// 57 on all 148, 1.02.)
 LinPlan lin_plan(int64_t nseq, int64_t L, bool packed, int64_t per_x, const LinForm& form) {
     LinPlan pl{};
     const int64_t chunks = (L + form.chunk - 1) / form.chunk;
     if (!packed) {
-        int64_t want = form.slots / (nseq * per_x);
-        if (want > chunks / form.min_chunks) want = chunks / form.min_chunks;
-        if (want > kLinMaxSegs) want = kLinMaxSegs;
-        if (want < 1) want = 1;
-        const int64_t seg = chunks > 0 ? (chunks + want - 1) / want : 1;    // chunks of a segment
+        const int64_t units = nseq * per_x, slots = form.slots;
+        int64_t best = 1;
+        float least = 0.f;
+        for (int64_t n = 1; n <= kLinMaxSegs && (n == 1 || n * form.min_chunks <= chunks); ++n) {
+            const int64_t seg = (chunks + n - 1) / n;
+            if (n > 1 && (chunks + seg - 1) / seg != n) continue;   // the same cut as a smaller n
+            float cost = static_cast<float>((units * n + slots - 1) / slots) * (seg + form.setup);
+            if (n > 1)
+                cost += static_cast<float>((units * (n - 1) + slots - 1) / slots) * (form.state_chunk * seg + form.setup) +
+                        form.predecessor * (n - 1);
+            if (n == 1 || cost < 0.9f * least) {
+                best = n;
+                least = cost;
+            }
+        }
+        const int64_t seg = chunks > 0 ? (chunks + best - 1) / best : 1;    // chunks of a segment
         pl.seg_len = static_cast<int>(seg * form.chunk);
-        pl.nseg = static_cast<int>(chunks > 0 ? (chunks + seg - 1) / seg : 1);
-        pl.blocks_x = nseq * pl.nseg;
-        pl.cut = pl.nseg > 1;
+        pl.nseg = static_cast<int>(best);
+        pl.blocks_x = nseq * best;
+        pl.cut = best > 1;
         return pl;
     }
     // the rows' share of one slot, whichever sequences they belong to

@@ -66,6 +66,9 @@ struct LinPlan {
 };
 struct LinForm {
     int slots, chunk, min_chunks;
+    // costs in chunks of the full pass: a CTA's set-up, a chunk of the state-only pass, the sum of one
+    // predecessor's end state
+    float setup, state_chunk, predecessor;
 };
 LinPlan lin_plan(int64_t nseq, int64_t L, bool packed, int64_t per_x, const LinForm& form);
 

@@ -390,7 +390,7 @@ cudaError_t launch_t(const LinParams& p, int Dk, bool cut, cudaStream_t s) {
 
 }  // namespace
 
-LinForm lin_simt_form() { return LinForm{2 * device_sm_count(), 64, 1}; }
+LinForm lin_simt_form() { return LinForm{2 * device_sm_count(), 64, 1, 0.5f, 0.4f, 0.05f}; }
 
 cudaError_t launch_lin_simt(const LinParams& p, bool bf16, bool cut, cudaStream_t s) {
     int Dk = 1;

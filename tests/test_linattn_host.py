@@ -233,13 +233,14 @@ def test_linattn_step_refusals(lib):
     assert step(slots=FAKE + 2, n=5) == bd.M3_ERR_INVALID_ARG
 
 
-@pytest.mark.parametrize("n,L,per", [(1, 1, 1), (1, 128, 1), (1, 4096, 1), (2, 65536, 64), (300, 129, 4)])
-def test_workspace_grows_with_the_cut(lib, n, L, per):
+@pytest.mark.parametrize("n,L,per,cut", [(1, 1, 1, False), (1, 64, 1, False), (1, 4096, 1, True),
+                                         (1, 65536, 64, True), (300, 129, 4, False), (4, 2048, 148, False)])
+def test_workspace_grows_with_the_cut(lib, n, L, per, cut):
     """A call that fills the device's CTA slots with whole sequences needs no workspace; few long
     sequences need one 64-column end state per segment and tile."""
     d = ldims(nseq=n, seqlen=L, nheads=per, qheads=1, kheads=1, vheads=1, kdim=128, vdim=64)
     need = lib.m3_linattn_workspace_bytes(ctypes.byref(d), 0)
-    assert (need > 0) == (L >= 128 and n * per < 148)
+    assert (need > 0) == cut
     if need:
         assert need >= 2 * n * per * 128 * 64 * 4
 
