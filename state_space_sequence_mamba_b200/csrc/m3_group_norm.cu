@@ -49,40 +49,43 @@ __device__ __forceinline__ T* at(const GnTensor& t, const GnParams& p, uint32_t 
 
 constexpr int kThreads = 256;
 
+// 16 bytes of T as pairs of floats (two elements are worked on in one instruction)
 template <typename T>
-struct Vec;   // 16 bytes of T as floats
+struct Vec;
 template <>
 struct Vec<float> {
-    static constexpr int N = 4;
-    static __device__ __forceinline__ void unpack(const uint4& v, float* f) {
-        f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y);
-        f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
+    static constexpr int N = 2;
+    static __device__ __forceinline__ void unpack(const uint4& v, float2* f) {
+        f[0] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+        f[1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
     }
-    static __device__ __forceinline__ void store(float* p, const float* f) {
-        *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    static __device__ __forceinline__ void store(float* p, const float2* f) {
+        *reinterpret_cast<float4*>(p) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
     }
 };
 template <>
 struct Vec<__nv_bfloat16> {
-    static constexpr int N = 8;
-    static __device__ __forceinline__ void unpack(const uint4& v, float* f) {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ void unpack(const uint4& v, float2* f) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
+        for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
     }
-    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* f) {
+    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float2* f) {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            const __nv_bfloat162 v = __floats2bfloat162_rn(f[i].x, f[i].y);
             w[i] = *reinterpret_cast<const uint32_t*>(&v);
         }
         *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 };
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 mul2(const float2& a, const float2& b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add2(const float2& a, const float2& b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(const float2& a, const float2& b, const float2& c) { return __ffma2_rn(a, b, c); }
 
 // 1 / (1 + e^-v); e^-v = inf gives 0. The approximate divide is within 2 units in the last place.
 __device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
@@ -96,6 +99,26 @@ __device__ __forceinline__ void act_slope(float v, float* a, float* da) {
     *a = v * s;
     *da = s * fmaf(v, 1.f - s, 1.f);
 }
+// The same for two elements, with the hardware's 2^x and 1 / x (1 + 2^x lies in [1, inf], so that
+// denormals need no care).
+__device__ __forceinline__ float2 sigmoid2(const float2& v) {
+    float2 e = mul2(v, both(-1.4426950408889634f));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+    e = add2(e, both(1.f));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+    return e;
+}
+template <bool kSilu>
+__device__ __forceinline__ float2 act2(const float2& v) { return kSilu ? mul2(v, sigmoid2(v)) : v; }
+template <bool kSilu>
+__device__ __forceinline__ void act_slope2(const float2& v, float2* a, float2* da) {
+    if (!kSilu) { *a = v; *da = both(1.f); return; }
+    const float2 s = sigmoid2(v);
+    *a = mul2(v, s);
+    *da = fma2(*a, fma2(s, both(-1.f), both(1.f)), s);      // s (1 + v (1 - s))
+}
 
 // the sum over the LPG lanes that hold a group
 template <int LPG>
@@ -105,32 +128,30 @@ __device__ __forceinline__ float group_sum(float v) {
     return v;
 }
 
-// mean (0 without centring) and 1 / sqrt(var + eps) of the group in v[NV][N]; lanes beyond the
-// group's end hold zeros and cnt[i] = 0
+// v becomes the group's deviations from the mean (or stays, without centring); returns
+// 1 / sqrt(var + eps). Vectors beyond the group's end hold zeros and keep them.
 template <int LPG, int NV, int N, bool kCenter>
-__device__ __forceinline__ void stats(float (&v)[NV][N], const bool (&in)[NV], float inv, float eps, float* r) {
+__device__ __forceinline__ float stats(float2 (&v)[NV][N], const bool (&in)[NV], float inv, float eps) {
     if (kCenter) {
-        float s = 0.f;
+        float2 s = both(0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int e = 0; e < N; ++e) s += v[i][e];
-        const float m = group_sum<LPG>(s) * inv;
+            for (int e = 0; e < N; ++e) s = add2(s, v[i][e]);
+        const float m = group_sum<LPG>(s.x + s.y) * inv;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int i = 0; i < NV; ++i) {
+            const float2 mi = both(in[i] ? -m : 0.f);
 #pragma unroll
-            for (int e = 0; e < N; ++e) v[i][e] = in[i] ? v[i][e] - m : 0.f;
+            for (int e = 0; e < N; ++e) v[i][e] = add2(v[i][e], mi);
+        }
     }
-    float q = 0.f;
+    float2 q = both(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int e = 0; e < N; ++e) q = fmaf(v[i][e], v[i][e], q);
-    *r = rsqrtf(fmaf(group_sum<LPG>(q), inv, eps));
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int e = 0; e < N; ++e) v[i][e] *= *r;
+        for (int e = 0; e < N; ++e) q = fma2(v[i][e], v[i][e], q);
+    return rsqrtf(fmaf(group_sum<LPG>(q.x + q.y), inv, eps));
 }
 
 // The row walk of both directions. A CTA's threads lie side by side over gx whole groups and, where
@@ -139,7 +160,7 @@ __device__ __forceinline__ void stats(float (&v)[NV][N], const bool (&in)[NV], f
 // measured the same: 45.3 against 43.8 us forward, 82.0 against 84.4 backward, on 8192 x 4096).
 template <typename T, int LPG, int NV>
 struct Walk {
-    static constexpr int N = Vec<T>::N;
+    static constexpr int N = 2 * Vec<T>::N;     // elements of a vector
     int lane, ry, nry, group, c0;
     uint32_t row, r1, turns;
     bool col_ok, in[NV];
@@ -167,11 +188,14 @@ struct Walk {
         for (int i = 0; i < NV; ++i)
             raw[i] = live && in[i] ? __ldcs(reinterpret_cast<const uint4*>(src + col(i))) : make_uint4(0u, 0u, 0u, 0u);
     }
-    __device__ __forceinline__ void weights(const float* src, float other, float (&w)[NV][N]) const {
+    __device__ __forceinline__ void weights(const float* src, float other, float2 (&w)[NV][N / 2]) const {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int e = 0; e < N; ++e) w[i][e] = src && in[i] ? __ldg(src + c0 + col(i) + e) : other;
+            for (int e = 0; e < N / 2; ++e) {
+                const float* at = src + c0 + col(i) + 2 * e;
+                w[i][e] = src && in[i] ? make_float2(__ldg(at), __ldg(at + 1)) : both(other);
+            }
     }
 };
 
@@ -182,33 +206,30 @@ __global__ void __launch_bounds__(kThreads) gn_fwd_kernel(const GnParams p, int 
     uint4 rx[NV], rz[NV];
     k.fetch(p, p.x, k.row, rx);
     if (kGate) k.fetch(p, p.z, k.row, rz);
-    float w[NV][N], b[NV][N];
+    float2 w[NV][N], b[NV][N];
     k.weights(p.w, 1.f, w);
     k.weights(p.b, 0.f, b);
     const float inv = 1.f / p.D;
     for (uint32_t t = 0; t < k.turns; ++t, k.row += k.nry) {
-        float v[NV][N], g[NV][N];
-        bool on[NV];
+        float2 v[NV][N], g[NV][N];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            on[i] = k.in[i] && k.row < k.r1;
             Vec<T>::unpack(rx[i], v[i]);
             if (kGate) Vec<T>::unpack(rz[i], g[i]);
         }
         k.fetch(p, p.x, k.row + k.nry, rx);
         if (kGate) k.fetch(p, p.z, k.row + k.nry, rz);
-        float r;
-        stats<LPG, NV, N, kCenter>(v, on, inv, p.eps, &r);
+        const float r = stats<LPG, NV, N, kCenter>(v, k.in, inv, p.eps);
         if (!(k.col_ok && k.row < k.r1)) continue;
         T* out = at<T>(p.out, p, k.row, k.group);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if (!on[i]) continue;
-            float o[N];
+            if (!k.in[i]) continue;
+            float2 o[N];
 #pragma unroll
             for (int e = 0; e < N; ++e) {
-                const float y = fmaf(v[i][e], w[i][e], b[i][e]);
-                o[e] = kGate ? y * act<kSilu>(g[i][e]) : act<kSilu>(y);
+                const float2 y = fma2(mul2(v[i][e], both(r)), w[i][e], b[i][e]);
+                o[e] = kGate ? mul2(y, act2<kSilu>(g[i][e])) : act2<kSilu>(y);
             }
             Vec<T>::store(out + k.col(i), o);
         }
@@ -225,58 +246,60 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_kernel(const GnParams p, int 
     k.fetch(p, p.x, k.row, rx);
     k.fetch(p, p.dout, k.row, rd);
     if (kGate) k.fetch(p, p.z, k.row, rz);
-    float w[NV][N], b[NV][N], dw[NV][N], db[NV][N];
+    float2 w[NV][N], b[NV][N], dw[NV][N], db[NV][N];
     k.weights(p.w, 1.f, w);
     k.weights(p.b, 0.f, b);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int e = 0; e < N; ++e) dw[i][e] = db[i][e] = 0.f;
+        for (int e = 0; e < N; ++e) dw[i][e] = db[i][e] = both(0.f);
     const float inv = 1.f / p.D;
     for (uint32_t t = 0; t < k.turns; ++t, k.row += k.nry) {
-        float v[NV][N], dy[NV][N], z[NV][N];
-        bool on[NV];
+        float2 v[NV][N], dy[NV][N], z[NV][N];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            on[i] = k.in[i] && k.row < k.r1;
             Vec<T>::unpack(rx[i], v[i]);
             Vec<T>::unpack(rd[i], dy[i]);
             if (kGate) Vec<T>::unpack(rz[i], z[i]);
         }
         const uint32_t row = k.row;
+        const bool live = k.col_ok && row < k.r1;
         k.fetch(p, p.x, row + k.nry, rx);
         k.fetch(p, p.dout, row + k.nry, rd);
         if (kGate) k.fetch(p, p.z, row + k.nry, rz);
-        float r;
-        stats<LPG, NV, N, kCenter>(v, on, inv, p.eps, &r);
-        float s1 = 0.f, s2 = 0.f;
+        float r = stats<LPG, NV, N, kCenter>(v, k.in, inv, p.eps);
+        r = live ? r : 0.f;         // with eps = 0 an absent row's would be infinite
+        float2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
 #pragma unroll
             for (int e = 0; e < N; ++e) {
-                const float y = fmaf(v[i][e], w[i][e], b[i][e]);
-                float a, da;
-                act_slope<kSilu>(kGate ? z[i][e] : y, &a, &da);
-                const float d = dy[i][e];
-                if (kGate) z[i][e] = d * y * da;      // dz
-                const float g = on[i] ? (kGate ? d * a : d * da) : 0.f;
-                dw[i][e] = fmaf(g, v[i][e], dw[i][e]);
-                db[i][e] += g;
-                dy[i][e] = g * w[i][e];
-                s1 = fmaf(dy[i][e], v[i][e], s1);
-                s2 += dy[i][e];
+                v[i][e] = mul2(v[i][e], both(r));
+                const float2 y = fma2(v[i][e], w[i][e], b[i][e]), d = dy[i][e];
+                float2 a, da;
+                act_slope2<kSilu>(kGate ? z[i][e] : y, &a, &da);
+                if (kGate) z[i][e] = mul2(mul2(d, y), da);      // dz
+                const float2 g = mul2(d, kGate ? a : da);       // (absent elements have dout = 0)
+                dw[i][e] = fma2(g, v[i][e], dw[i][e]);
+                db[i][e] = add2(db[i][e], g);
+                dy[i][e] = mul2(g, w[i][e]);
+                s1 = fma2(dy[i][e], v[i][e], s1);
+                s2 = add2(s2, dy[i][e]);
             }
         }
-        s1 = group_sum<LPG>(s1) * inv;
-        s2 = kCenter ? group_sum<LPG>(s2) * inv : 0.f;
-        if (!(k.col_ok && row < k.r1)) continue;
+        const float m1 = -group_sum<LPG>(s1.x + s1.y) * inv, m2 = kCenter ? -group_sum<LPG>(s2.x + s2.y) * inv : 0.f;
+        if (!live) continue;
         T* dx = at<T>(p.dx, p, row, k.group);
         T* dz = kGate ? at<T>(p.dz, p, row, k.group) : nullptr;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if (!on[i]) continue;
+            if (!k.in[i]) continue;
 #pragma unroll
-            for (int e = 0; e < N; ++e) dy[i][e] = r * (dy[i][e] - v[i][e] * s1 - s2);
+            for (int e = 0; e < N; ++e) {
+                float2 g = fma2(v[i][e], both(m1), dy[i][e]);
+                if (kCenter) g = add2(g, both(m2));
+                dy[i][e] = mul2(g, both(r));
+            }
             Vec<T>::store(dx + k.col(i), dy[i]);
             if (kGate) Vec<T>::store(dz + k.col(i), z[i]);
         }
@@ -294,8 +317,9 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_kernel(const GnParams p, int 
                 const int c = (k.group - blockIdx.y * gx) * p.D + k.col(i);
 #pragma unroll
                 for (int e = 0; e < N; ++e) {
-                    sw[c + e] = y ? sw[c + e] + dw[i][e] : dw[i][e];
-                    sb[c + e] = y ? sb[c + e] + db[i][e] : db[i][e];
+                    float2 *tw = reinterpret_cast<float2*>(sw + c) + e, *tb = reinterpret_cast<float2*>(sb + c) + e;
+                    *tw = y ? add2(*tw, dw[i][e]) : dw[i][e];
+                    *tb = y ? add2(*tb, db[i][e]) : db[i][e];
                 }
             }
         }
@@ -469,7 +493,7 @@ bool ok16(const GnTensor& t, int es) {
 // 16-byte vectors of a group, or 0 where the vector form does not apply
 template <typename T>
 int vector_count(const GnParams& p) {
-    constexpr int N = Vec<T>::N, es = sizeof(T);
+    constexpr int N = 2 * Vec<T>::N, es = sizeof(T);
     if (p.D % N != 0 || p.D / N > 128) return 0;
     const bool ok = ok16(p.x, es) && ok16(p.z, es) && ok16(p.out, es) && ok16(p.dout, es) && ok16(p.dx, es) && ok16(p.dz, es);
     return ok ? p.D / N : 0;

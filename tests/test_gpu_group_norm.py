@@ -177,3 +177,11 @@ def test_refusals(cuda_dev):
         m3.group_norm_fwd(d["x"], 4, out=d["x"][:1].expand(6, 64))
     with pytest.raises(ValueError):
         m3.group_norm_bwd(d["dout"][:5], d["x"], 4)
+
+
+def test_gradients_with_eps_zero(cuda_dev):
+    """eps = 0 is allowed: rows and groups that a launch's threads stand on without any (41 rows, 5
+    groups of 24 channels) leave nothing behind, infinite deviations of theirs included."""
+    for T in (3, 41, 700):
+        check(cuda_dev, T, 120, 5, F32, eps=0.0)
+        check(cuda_dev, T, 120, 5, BF, eps=0.0, center=False)
