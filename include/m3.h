@@ -314,7 +314,8 @@ M3_API m3_status m3_scan_fwd_noalloc(const m3_dims* dims, const m3_inputs* in,
  * Packed sequences: with cu_seqlens (device, int32, nseq + 1 values, ascending from >= 0), the
  * tensors hold seqlen rows in all and sequence i is rows [cu_seqlens[i], cu_seqlens[i + 1]).
  * Rows outside every sequence are not read as tokens and their outputs are left as they were.
- * Values outside [0, seqlen] are clamped to it and a descending pair is an empty sequence.
+ * Values outside [0, seqlen] are clamped to it and a descending pair is an empty sequence (rows
+ * around one may then be left out of the gradients of shared heads).
  * Sequences of length 0 and 1 are allowed: the state after an empty one is its initial state. */
 
 /* A tensor of rows [nseq][seqlen][heads][dim] by its strides, in elements; the last dimension is
@@ -355,9 +356,9 @@ M3_API size_t m3_linattn_bwd_workspace_bytes(const m3_linattn_dims* dims, int pa
 /* Prompts. init, final: fp32 [nseq, H, K, V], or NULL for zero / not wanted; final may be init.
  * o: the output [nseq][seqlen][H][V] by its view, in_dtype. workspace: 256-byte aligned, at least
  * m3_linattn_workspace_bytes (NULL where that is 0). bf16 tensors whose pointers and strides are
- * multiples of 16 bytes run on the tensor cores for K <= 128 (chunks of 128 tokens; products of
- * bf16 operands with fp32 accumulators, the state exact to fp32); every other call runs in fp32
- * on the CUDA cores. Asynchronous on `stream`. */
+ * multiples of 16 bytes, with K and V multiples of 8 and K <= 128, run on the tensor cores (chunks
+ * of 128 tokens; products of bf16 operands with fp32 accumulators, the state exact to fp32); every
+ * other call runs in fp32 on the CUDA cores. Asynchronous on `stream`. */
 M3_API m3_status m3_linattn_fwd(const m3_linattn_dims* dims, const m3_linattn_inputs* in,
                                 const float* init, float* final_state, const m3_view* o,
                                 void* workspace, size_t ws_bytes, void* stream);

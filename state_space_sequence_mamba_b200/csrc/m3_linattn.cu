@@ -193,7 +193,15 @@ __global__ void __launch_bounds__(256) fold_heads_kernel(const __grid_constant__
         const int64_t rh = e / per;
         const int g = static_cast<int>(rh % f.heads);
         const int64_t row = rh / f.heads;
-        if (p.cu && (row < p.cu[0] || row >= p.cu[p.nseq])) continue;   // rows of no sequence are left alone
+        if (p.cu) {     // rows of no sequence are left alone: the last sequence that starts by this row
+            int lo = 0, hi = p.nseq - 1;
+            while (lo < hi) {
+                const int m = (lo + hi + 1) >> 1;
+                if (p.cu[m] <= row) lo = m;
+                else hi = m - 1;
+            }
+            if (row < p.cu[lo] || row >= p.cu[lo + 1]) continue;
+        }
         const int64_t b = p.cu ? 0 : row / p.L, t = p.cu ? row : row % p.L;
         const float* src = f.part + (row * f.heads + g) * static_cast<int64_t>(f.ratio) * f.dim + c;
         T* out = static_cast<T*>(f.out) + b * f.batch + t * f.token + g * f.head + c;

@@ -29,6 +29,8 @@
 // registers, half a row a thread), 16-23 v', 24 TMA loads, 25 issues S and O2, 26 O1, 27 k^T v'.
 // Hand-offs are mbarriers. All waits are bounded: one that gives up marks the library's timeout word,
 // and every role leaves its loop at its next wait.
+#include <cstdlib>
+
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -84,6 +86,9 @@ struct LinTcParams {
     int head_ratio[3][3];       // head coordinate = h / ratio
     int batched[3][3];          // batch coordinate = sequence (0: one entry for all)
     int parts[3];               // bf16 parts of v'
+    // Test hook: > 0 makes CTA 0 skip the load of that chunk's v, so that its bounded waits run out and
+    // the timeout path is exercised. Set only from the M3_TEST_LINATTN_SKIP_LOAD environment variable.
+    int test_skip;
 };
 
 // Waits for the phase of `bar` with the given parity, giving up after kMaxPolls polls (the thread is
@@ -225,6 +230,7 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
             (void)mbar_wait(&bars[B_QK + st], (c >> 1) & 1, kDrainCycles);
             return false;
         }
+        if (blockIdx.x == 0 && c > 0 && c == tp.test_skip) return true;     // (test hook)
         mbar_arrive_expect_tx(&bars[B_V + st], kSlab);
         tma_load_4d(sm + S_V + st * kSlab, &maps.m[tp.map[ji][2]], &bars[B_V + st], tile * kVT, hv, at, bv);
         return true;
@@ -714,6 +720,8 @@ cudaError_t launch_lin_tc(const LinParams& p, bool cut, cudaStream_t s) {
     LinTcParams tp;
     LinMaps maps;
     tp.p = p;
+    const char* skip = std::getenv("M3_TEST_LINATTN_SKIP_LOAD");
+    tp.test_skip = skip ? std::atoi(skip) : 0;
     int used = 0;
     LinTensor seen[kMaps];
     int seen_dim[kMaps];

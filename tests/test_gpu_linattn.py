@@ -439,3 +439,119 @@ def test_refusals(cuda_dev):
         m3.linattn_bwd(**args, do=d["do"][:, :5])
     with pytest.raises(ValueError):
         m3.linattn_bwd(**args, do=d["do"], grads=(d["q"], d["k"].float(), d["v"]))
+
+
+def test_timeout_is_reported(cuda_dev):
+    """The test hook makes CTA 0 skip one load, so that its bounded waits run out (a few seconds): the
+    CTA drains what it started, releases its tensor memory and marks the timeout, which
+    linattn_check reports once; the other CTAs' results and the next call are right."""
+    import os
+    t, d, cu, s = draw(cuda_dev, 2, 700, 2, 2, 2, 2, 64, 64, seed=12)
+    args = (d["q"], d["k"], d["v"], d["log_decay"])
+    o, S = m3.linattn_fwd(*args, scale=s, init=d["init"])
+    os.environ["M3_TEST_LINATTN_SKIP_LOAD"] = "1"
+    try:
+        o2, S2 = m3.linattn_fwd(*args, scale=s, init=d["init"])
+        torch.cuda.synchronize()
+    finally:
+        del os.environ["M3_TEST_LINATTN_SKIP_LOAD"]
+    with pytest.raises(m3.M3Error) as ei:
+        m3.linattn_check()
+    assert ei.value.status == m3.M3_ERR_TIMEOUT
+    m3.linattn_check()                                  # the mark is gone
+    assert torch.equal(o2[1], o[1]) and torch.equal(S2[1], S[1])
+    o3, S3 = m3.linattn_fwd(*args, scale=s, init=d["init"])
+    torch.cuda.synchronize()
+    m3.linattn_check()
+    assert torch.equal(o3, o) and torch.equal(S3, S)
+
+
+def test_first_calls_inside_a_capture(cuda_dev):
+    """A process whose first calls are captured into a graph (nothing warmed up)."""
+    import subprocess
+    import sys
+    code = """
+import torch
+from state_space_sequence_mamba_b200 import binding as m3
+torch.manual_seed(0)
+q, k, v = (torch.randn(1, 2000, 2, 64, device='cuda', dtype=torch.bfloat16) for _ in range(3))
+g = torch.tensor([-0.1, -0.01], device='cuda')
+st = torch.zeros(1, 2, 64, 64, device='cuda')
+torch.cuda.synchronize()
+cg = torch.cuda.CUDAGraph()
+with torch.cuda.graph(cg):
+    o, S = m3.linattn_fwd(q, k, v, g)
+    r = m3.linattn_bwd(q, k, v, g, o)
+    f, _ = m3.linattn_fwd(q[:, :70].float(), k[:, :70].float(), v[:, :70].float(), g)
+    t, _ = m3.linattn_step(q[:, 0], k[:, 0], v[:, 0], g, st, state_out=torch.empty_like(st))
+    n = m3.group_norm_fwd(o.flatten(-2), 2)
+    b = m3.group_norm_bwd(n, o.flatten(-2), 2)
+cg.replay()
+torch.cuda.synchronize()
+o2, S2 = m3.linattn_fwd(q, k, v, g)
+r2 = m3.linattn_bwd(q, k, v, g, o2)
+assert torch.equal(o, o2) and torch.equal(S, S2) and all(torch.equal(r[x], r2[x]) for x in r)
+assert torch.equal(f, m3.linattn_fwd(q[:, :70].float(), k[:, :70].float(), v[:, :70].float(), g)[0])
+assert torch.equal(n, m3.group_norm_fwd(o2.flatten(-2), 2))
+print('captured')
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    p = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0 and "captured" in p.stdout, p.stderr[-2000:]
+
+
+def test_calls_on_two_streams_at_once(cuda_dev):
+    """Interleaved calls on two streams, each with its own workspaces, equal the calls alone."""
+    sets = [draw(cuda_dev, 1, 3000, 2, 2, 2, 2, 64, 64, seed=20 + i) for i in range(2)]
+    alone = [m3.linattn_fwd(d["q"], d["k"], d["v"], d["log_decay"], scale=s, init=d["init"]) for _, d, _, s in sets]
+    galone = [m3.linattn_bwd(d["q"], d["k"], d["v"], d["log_decay"], d["do"], scale=s, init=d["init"]) for _, d, _, s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[] for _ in sets]
+    for _ in range(5):
+        for i, (_, d, _, s) in enumerate(sets):
+            a = (d["q"], d["k"], d["v"], d["log_decay"])
+            got[i].append((m3.linattn_fwd(*a, scale=s, init=d["init"], stream=streams[i]),
+                           m3.linattn_bwd(*a, d["do"], scale=s, init=d["init"], stream=streams[i])))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for (o, S), g in got[i]:
+            assert torch.equal(o, alone[i][0]) and torch.equal(S, alone[i][1])
+            assert all(torch.equal(g[n], galone[i][n]) for n in g)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_shared_heads_and_padding_left_alone(cuda_dev, dtype):
+    """Gradients of heads shared by 8, written into slices of wider rows: the sums of the separate
+    heads' gradients, and nothing beside the slices."""
+    b, L, H, K, V = 2, 90, 8, 40, 24
+    t, d, _, s = draw(cuda_dev, b, L, H, 1, 2, 4, K, V, dtype=dtype)
+    wide = torch.full((b, L, 7, 64), 7.0, dtype=dtype, device=cuda_dev)
+    grads = wide[:, :, :1, 8:8 + K], wide[:, :, 1:3, 16:16 + K], wide[:, :, 3:, 24:24 + V]
+    m3.linattn_bwd(d["q"], d["k"], d["v"], d["log_decay"], d["do"], scale=s, init=d["init"], dfinal=d["dfinal"],
+                   grads=grads)
+    torch.cuda.synchronize()
+    ref = ol.gradients(t["q"], t["k"], t["v"], t["log_decay"], t["do"], s, t["init"], t["dfinal"])
+    for x, r in zip(grads, ref):
+        assert err(x, r) <= tol(dtype, K, V)
+        x.fill_(7.0)
+    assert bool((wide == 7.0).all())
+
+
+def test_many_short_sequences(cuda_dev):
+    """More packed sequences than one warp locates at a time, empty ones among them."""
+    g = torch.Generator().manual_seed(1)
+    lens = torch.randint(0, 9, (300,), generator=g).tolist()
+    t, d, cu, s = draw(cuda_dev, 1, 0, 2, 2, 1, 1, 16, 32, lens=lens, extra=1, seed=31)
+    total = sum(lens)
+    t = {n: x[:, :total] if n in ("q", "k", "v", "do") else x for n, x in t.items()}
+    o, S = m3.linattn_fwd(d["q"], d["k"], d["v"], d["log_decay"], scale=s, init=d["init"], cu_seqlens=cu)
+    gr = m3.linattn_bwd(d["q"], d["k"], d["v"], d["log_decay"], d["do"], scale=s, init=d["init"], cu_seqlens=cu)
+    torch.cuda.synchronize()
+    ro, rS = ol.forward(t["q"], t["k"], t["v"], t["log_decay"], s, t["init"], lens)
+    assert err(o[:, :total], ro) <= tol(BF, 16, 32) and err(S, rS) <= STATE_TOL
+    ref = ol.gradients(t["q"], t["k"], t["v"], t["log_decay"], t["do"], s, t["init"], None, lens)
+    for n, r in zip(("dq", "dk", "dv"), ref):
+        assert err(gr[n][:, :total], r) <= tol(BF, 16, 32) and bool((gr[n][:, total:] == 0).all())
+    assert err(gr["dinit"], ref[3]) <= STATE_TOL
