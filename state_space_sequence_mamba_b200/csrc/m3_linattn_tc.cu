@@ -146,8 +146,8 @@ __device__ __forceinline__ void commit_el(uint32_t el, uint64_t* bar) {
 
 // The 72 registers a thread that 28 warps leave are dealt out again by what the roles hold. Spills are
 // what to avoid: beside 227 KB of shared memory the L1 cache is too small to hold them.
-constexpr int kRegsLaunch = 72, kRegsRow = 96, kRegsState = 64, kRegsIssue = 40;
-static_assert(2 * kRegsRow + 2 * kRegsState + 2 * kRegsLaunch + kRegsIssue == 7 * kRegsLaunch,
+constexpr int kRegsLaunch = 72, kRegsRow = 88, kRegsState = 64, kRegsPart = 80, kRegsIssue = 40;
+static_assert(2 * kRegsRow + 2 * kRegsState + 2 * kRegsPart + kRegsIssue == 7 * kRegsLaunch,
               "an increase beyond what the block was launched with would wait for ever");
 template <int N>
 __device__ __forceinline__ void regs_inc() {
@@ -208,23 +208,19 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
     auto chunk_n = [&](int c) { const int n = seg_end - chunk_t0(c); return n < kC ? n : kC; };
 
     // ---------------- set-up ----------------
-    if (tid == 32 * kOutWarp) {     // the maps on their way while the barriers are set up
-        for (int a = 0; a < 3; ++a)
-            asm volatile("prefetch.tensormap [%0];" :: "l"(&maps.m[tp.map[ji][a]]) : "memory");
-        s_abort = 0;
-    }
-    // what the first loads need, before anything else: they are issued ahead of the block's barrier
+    // The load warp needs nothing but its barriers: its first loads are issued ahead of the block's
+    // barrier, while other warps allocate TMEM and fill the tables.
+    const int nloads = kStateOnly ? nupdates : nchunks;
+    int hq = 0, hk = 0, hv_ = 0, bq = 0, bk = 0, bv = 0;
+    const void *mq = nullptr, *mk = nullptr, *mv = nullptr;
     auto load = [&](int c) {
         const int st = c & 1, at = w.row0 + chunk_t0(c);
-        const int hq = h / tp.head_ratio[ji][0], hk = h / tp.head_ratio[ji][1], hv = h / tp.head_ratio[ji][2];
-        const int bq = tp.batched[ji][0] ? w.batch : 0, bk = tp.batched[ji][1] ? w.batch : 0, bv = tp.batched[ji][2] ? w.batch : 0;
         if (c > 1 && !lwait(&bars[B_QKFREE + st], (c >> 1) - 1, &s_abort)) return false;
         mbar_arrive_expect_tx(&bars[B_QK + st], (kStateOnly ? 1 : 2) * slabs * kSlab);
 #pragma unroll 1
         for (int s = 0; s < slabs; ++s) {
-            tma_load_4d(sm + S_K + (2 * st + s) * kSlab, &maps.m[tp.map[ji][1]], &bars[B_QK + st], 64 * s, hk, at, bk);
-            if (!kStateOnly)
-                tma_load_4d(sm + S_Q + (2 * st + s) * kSlab, &maps.m[tp.map[ji][0]], &bars[B_QK + st], 64 * s, hq, at, bq);
+            tma_load_4d(sm + S_K + (2 * st + s) * kSlab, mk, &bars[B_QK + st], 64 * s, hk, at, bk);
+            if (!kStateOnly) tma_load_4d(sm + S_Q + (2 * st + s) * kSlab, mq, &bars[B_QK + st], 64 * s, hq, at, bq);
         }
         if (c > 1 && !lwait(&bars[B_VFREE + st], (c >> 1) - 1, &s_abort)) {
             (void)mbar_wait(&bars[B_QK + st], (c >> 1) & 1, kDrainCycles);
@@ -232,19 +228,31 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
         }
         if (blockIdx.x == 0 && c > 0 && c == tp.test_skip) return true;     // (test hook)
         mbar_arrive_expect_tx(&bars[B_V + st], kSlab);
-        tma_load_4d(sm + S_V + st * kSlab, &maps.m[tp.map[ji][2]], &bars[B_V + st], tile * kVT, hv, at, bv);
+        tma_load_4d(sm + S_V + st * kSlab, mv, &bars[B_V + st], tile * kVT, hv_, at, bv);
         return true;
     };
-    const int nloads = kStateOnly ? nupdates : nchunks;
     if (warp == kLoadWarp) {
         if (lane == 0) {
+            mq = &maps.m[tp.map[ji][0]];
+            mk = &maps.m[tp.map[ji][1]];
+            mv = &maps.m[tp.map[ji][2]];
+            asm volatile("prefetch.tensormap [%0];" :: "l"(mk) : "memory");
+            if (!kStateOnly) asm volatile("prefetch.tensormap [%0];" :: "l"(mq) : "memory");
+            asm volatile("prefetch.tensormap [%0];" :: "l"(mv) : "memory");
             for (int i = 0; i < kNumBars; ++i) mbar_init(&bars[i], bar_count(i));
             fence_mbar_init();
             fence_proxy_async();
-#pragma unroll 1
-            for (int c = 0; c < 2 && c < nloads; ++c) load(c);
+            hq = h / tp.head_ratio[ji][0];
+            hk = h / tp.head_ratio[ji][1];
+            hv_ = h / tp.head_ratio[ji][2];
+            bq = tp.batched[ji][0] ? w.batch : 0;
+            bk = tp.batched[ji][1] ? w.batch : 0;
+            bv = tp.batched[ji][2] ? w.batch : 0;
+            if (nloads > 0) load(0);
         }
         __syncwarp();
+    } else if (warp == kOutWarp) {
+        if (lane == 0) s_abort = 0;
         tmem_alloc(&tslot, kTmemCols);
     }
     if (tid <= kC) pw[tid] = lin_pow(g2, static_cast<float>(tid));
@@ -363,71 +371,64 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
         float hv[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) hv[i] = 0.f;
+        // the state as the next chunk's bf16 operand
+        auto publish = [&]() {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<uint4*>(sm + S_H + swz128(r, c0 + 8 * i)) =
+                    make_uint4(pack2(hv[8 * i], hv[8 * i + 1]), pack2(hv[8 * i + 2], hv[8 * i + 3]),
+                               pack2(hv[8 * i + 4], hv[8 * i + 5]), pack2(hv[8 * i + 6], hv[8 * i + 7]));
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[B_H0]);
+        };
         if (!kStateOnly) {
-            // the state before this segment (the given one and the segments before, decayed), sixteen
-            // columns at a time into the accumulator, from where it is taken like a chunk's products
+            // the state before this segment: the given one and the segments before, decayed
             const int before = rev ? (order == 0 ? 0 : w.len - (seg0 + p.seg_len)) : seg0;
             const float fi = lin_pow(g2, static_cast<float>(rev && before > 0 ? before - 1 : before));
-            const bool live = r < j.Dk, given = j.init && live && fi != 0.f;
-            if (order > 0) grid_dep_wait();     // the segments' end states are there
-            const float* src = given ? j.init + (static_cast<int64_t>(w.seq) * p.H + h) * j.Dk * j.Dv + r * j.init_k +
-                                           (tile * kVT + c0) * j.init_v
-                                     : nullptr;
-#pragma unroll 1
-            for (int c = 0; c < 32; c += 16) {
-                float v[16];
+            const bool live = r < j.Dk;
+            if (j.init && live && fi != 0.f) {
+                const float* src = j.init + (static_cast<int64_t>(w.seq) * p.H + h) * j.Dk * j.Dv + r * j.init_k +
+                                   (tile * kVT + c0) * j.init_v;
+                if (j.init_v == 1) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = 0.f;
-                if (given && c < cols) {
-                    if (j.init_v == 1) {        // Dv is a multiple of 8
+                    for (int i = 0; i < 32; i += 4)
+                        if (i < cols) {         // Dv is a multiple of 8
+                            const float4 v4 = *reinterpret_cast<const float4*>(src + i);
+                            hv[i] = fi * v4.x; hv[i + 1] = fi * v4.y; hv[i + 2] = fi * v4.z; hv[i + 3] = fi * v4.w;
+                        }
+                } else {
 #pragma unroll
-                        for (int i = 0; i < 16; i += 4)
-                            if (c + i < cols) {
-                                const float4 v4 = *reinterpret_cast<const float4*>(src + c + i);
-                                v[i] = fi * v4.x; v[i + 1] = fi * v4.y; v[i + 2] = fi * v4.z; v[i + 3] = fi * v4.w;
-                            }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (c + i < cols) v[i] = fi * src[(c + i) * j.init_v];
-                    }
+                    for (int i = 0; i < 32; ++i)
+                        if (i < cols) hv[i] = fi * src[i * j.init_v];
                 }
-#pragma unroll 1
-                for (int o = 0; o < order && live; ++o) {
-                    const int sg = rev ? w.nseg - 1 - o : o;
-                    const int gap = rev ? sg * p.seg_len - (seg0 + p.seg_len) : seg0 - (sg + 1) * p.seg_len;
-                    const float f = lin_pow(g2, static_cast<float>(gap));
-                    if (f == 0.f) continue;
-                    const float* e = p.seg + (((static_cast<int64_t>(x - w.seg + sg) * p.H + h) * p.rtiles + rt) * p.seg_rows + r) *
-                                                 kVT + c0 + c;
-#pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const float4 v4 = *reinterpret_cast<const float4*>(e + i);
-                        v[i] = fmaf(f, v4.x, v[i]); v[i + 1] = fmaf(f, v4.y, v[i + 1]);
-                        v[i + 2] = fmaf(f, v4.z, v[i + 2]); v[i + 3] = fmaf(f, v4.w, v[i + 3]);
-                    }
-                }
-                __syncwarp();
-                uint32_t u[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(v[i]);
-                tmem_st_32x32b_x16(lb + c, u);
             }
-            tmem_wait_st();
+            if (order > 0) grid_dep_wait();     // the segments' end states are there
+#pragma unroll 1
+            for (int o = 0; o < order && live; ++o) {
+                const int sg = rev ? w.nseg - 1 - o : o;
+                const int gap = rev ? sg * p.seg_len - (seg0 + p.seg_len) : seg0 - (sg + 1) * p.seg_len;
+                const float f = lin_pow(g2, static_cast<float>(gap));
+                if (f == 0.f) continue;
+                const float* e = p.seg + (((static_cast<int64_t>(x - w.seg + sg) * p.H + h) * p.rtiles + rt) * p.seg_rows + r) * kVT + c0;
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                    const float4 v4 = *reinterpret_cast<const float4*>(e + i);
+                    hv[i] = fmaf(f, v4.x, hv[i]); hv[i + 1] = fmaf(f, v4.y, hv[i + 1]);
+                    hv[i + 2] = fmaf(f, v4.z, hv[i + 2]); hv[i + 3] = fmaf(f, v4.w, hv[i + 3]);
+                }
+            }
+            __syncwarp();
+            if (nchunks > 0) publish();
         }
         bool good = true;
-        // chunk -1 takes up the state before the segment
 #pragma unroll 1
-        for (int c = kStateOnly ? 0 : -1; c < nupdates; ++c) {
-            float decay = 0.f;
-            if (c >= 0) {
-                decay = pw[chunk_n(c) - ((rev && order == 0 && c == 0) ? 1 : 0)];
-                if (!lwait_warp(&bars[B_DH], c, &s_abort)) { good = false; break; }
-                fence_after_sync();
-            }
-            const int np = c < 0 ? 1 : parts;
+        for (int c = 0; c < nupdates; ++c) {
+            const float decay = pw[chunk_n(c) - ((rev && order == 0 && c == 0) ? 1 : 0)];
+            if (!lwait_warp(&bars[B_DH], c, &s_abort)) { good = false; break; }
+            fence_after_sync();
 #pragma unroll 1
-            for (int part = 0; part < np; ++part) {
+            for (int part = 0; part < parts; ++part) {
                 const float dc = part == 0 ? decay : 1.f;
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
@@ -447,16 +448,9 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[B_HFREE]);
             if (kStateOnly || c + 1 >= nchunks) continue;
-            // the state as the next chunk's bf16 operand, once O1 has read this chunk's
-            if (c >= 0 && !lwait_warp(&bars[B_O1 + (c & 1)], c >> 1, &s_abort)) { good = false; break; }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<uint4*>(sm + S_H + swz128(r, c0 + 8 * i)) =
-                    make_uint4(pack2(hv[8 * i], hv[8 * i + 1]), pack2(hv[8 * i + 2], hv[8 * i + 3]),
-                               pack2(hv[8 * i + 4], hv[8 * i + 5]), pack2(hv[8 * i + 6], hv[8 * i + 7]));
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[B_H0]);
+            // the next chunk's operand, once O1 has read this chunk's
+            if (!lwait_warp(&bars[B_O1 + (c & 1)], c >> 1, &s_abort)) { good = false; break; }
+            publish();
         }
         if (good && (kStateOnly || want_final)) {
             // through the accumulator once more, so that the copy out is a short loop
@@ -487,6 +481,7 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
         }
     } else if (warp < kLoadWarp) {
         // ================= v', the weighted v in bf16 parts =================
+        if constexpr (!kStateOnly) regs_inc<kRegsPart>();
         // Half of token r's columns a thread. The parts are formed in registers while the product of
         // the chunk before still reads theirs.
         const int r = 32 * (warp & 3) + lane, half = (warp - kPartWarp0) >> 2;
@@ -548,7 +543,7 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
         if (warp == kLoadWarp) {
             // ================= TMA loads (one lane) =================
             if (lane == 0) {
-                int done = nloads < 2 ? nloads : 2;
+                int done = nloads < 1 ? nloads : 1;
 #pragma unroll 1
                 for (int c = done; c < nloads; ++c) {
                     if (!load(c)) break;
@@ -645,10 +640,8 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
 #pragma unroll 1
                 for (int c = 0; c < nupdates; ++c) {
                     const int st = c & 1, steps = (chunk_n(c) + 15) / 16;
-                    // before the first product the accumulator held the state before the segment
-                    const int freed = kStateOnly ? c - 1 : c;
                     if (!lwait_warp(&bars[B_QK + st], c >> 1, &s_abort) || !lwait_warp(&bars[B_VP], c, &s_abort) ||
-                        (freed >= 0 && !lwait_warp(&bars[B_HFREE], freed, &s_abort)))
+                        (c > 0 && !lwait_warp(&bars[B_HFREE], c - 1, &s_abort)))
                         break;
                     fence_after_sync();
                     issued = true;
@@ -682,7 +675,7 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
     __syncthreads();
     fence_after_sync();
     if (s_abort && tid == 0) atomicExch(&g_lin_timeout, 1);
-    if (warp == kLoadWarp) tmem_dealloc(tmem, kTmemCols);
+    if (warp == kOutWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
 bool aligned(const LinTensor& t) {
