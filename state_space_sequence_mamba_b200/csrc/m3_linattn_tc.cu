@@ -120,22 +120,44 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
 // The products and commits below run in convergent code of one warp, predicated on its first lane
 // (`el`), so that descriptors stay in uniform registers: inside a branch of one lane each product
 // took some 200 cycles to issue.
-__device__ __forceinline__ void mma_el(uint32_t el, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// Four K steps of one product: descriptors given by their low words (the high word is the layout's),
+// which advance by kA and kB a step; the first step accumulates if acc.
+template <uint32_t kA, uint32_t kB>
+__device__ __forceinline__ void mma4_el(uint32_t el, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+    constexpr uint32_t hi = desc_hi_sw128(1024);
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n"
-        :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(el));
+        "{\n\t.reg .pred p, q, t;\n\t.reg .b64 x, y;\n\t.reg .b32 u, v;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "mov.b64 x, {%1, %6};\n\tmov.b64 y, {%2, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t"
+        "add.u32 u, %1, %7;\n\tadd.u32 v, %2, %8;\n\tmov.b64 x, {u, %6};\n\tmov.b64 y, {v, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+        "add.u32 u, %1, %9;\n\tadd.u32 v, %2, %10;\n\tmov.b64 x, {u, %6};\n\tmov.b64 y, {v, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+        "add.u32 u, %1, %11;\n\tadd.u32 v, %2, %12;\n\tmov.b64 x, {u, %6};\n\tmov.b64 y, {v, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t}\n"
+        :: "r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(el), "r"(hi), "n"(kA), "n"(kB), "n"(2 * kA), "n"(2 * kB),
+           "n"(3 * kA), "n"(3 * kB));
 }
-__device__ __forceinline__ void mma_ts_el(uint32_t el, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// The same with the A operand in TMEM, eight columns a step.
+template <uint32_t kB>
+__device__ __forceinline__ void mma4_ts_el(uint32_t el, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+    constexpr uint32_t hi = desc_hi_sw128(1024);
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
-        :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(el));
+        "{\n\t.reg .pred p, q, t;\n\t.reg .b64 y;\n\t.reg .b32 u, v;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "mov.b64 y, {%2, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t"
+        "add.u32 u, %1, 8;\n\tadd.u32 v, %2, %7;\n\tmov.b64 y, {v, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %3, t;\n\t"
+        "add.u32 u, %1, 16;\n\tadd.u32 v, %2, %8;\n\tmov.b64 y, {v, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %3, t;\n\t"
+        "add.u32 u, %1, 24;\n\tadd.u32 v, %2, %9;\n\tmov.b64 y, {v, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %3, t;\n\t}\n"
+        :: "r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(el), "r"(hi), "n"(kB), "n"(2 * kB), "n"(3 * kB));
 }
+// Steps of the operands' low words: 16 columns of a row (K-major), 16 rows (MN-major)
+constexpr uint32_t kStepK = 2, kStepMN = 128, kNextSlab = kSlab >> 4;
 __device__ __forceinline__ void commit_el(uint32_t el, uint64_t* bar) {
     asm volatile(
         "{\n\t.reg .pred q;\n\t"
@@ -200,7 +222,7 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
     const bool want_final = !kStateOnly && j.final_state && last_seg;
     // chunks whose state product runs: the last one's only for a state that somebody wants
     const int nupdates = (kStateOnly || want_final) ? nchunks : nchunks - 1;
-    const int ksteps = (j.Dk + 15) / 16, slabs = j.Dk > 64 ? 2 : 1;
+    const int slabs = j.Dk > 64 ? 2 : 1;     // of 64 columns of q and k (zeros beyond Dk)
     const int parts = tp.parts[ji];
     const float g2 = p.log_decay[h] * 1.4426950408889634f;
     // token 0 and length of the c-th chunk in processing order
@@ -264,7 +286,6 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
     __syncthreads();
     fence_after_sync();
     const uint32_t tmem = tslot;
-    constexpr uint32_t hi = desc_hi_sw128(1024);
 
     if (warp < kRowWarps) {
         // ================= rows: S -> P, then y =================
@@ -286,9 +307,9 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
                 const int t0 = chunk_t0(c), n = chunk_n(c);
                 if (!lwait_warp(&bars[B_S + g], c >> 1, &s_abort)) break;
                 fence_after_sync();
-                // 32 columns at a time, as far as columns hold tokens (scores behind the last are zero)
+                // 32 columns at a time, as far as the product reads (scores behind the last token are zero)
 #pragma unroll 1
-                for (int b = 0; 32 * b < n; ++b) {
+                for (int b = 0; b < (n > 64 ? 4 : 2); ++b) {
                     uint32_t pk[16];
                     const int ahead = sgn * (b - rw);           // 0: the diagonal block
                     if (ahead < 0) {
@@ -576,22 +597,22 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
                         issued = true;
                         const uint32_t loQ = desc_lo(smem_u32(sm + S_Q + 2 * st * kSlab), 16);
                         const uint32_t loK = desc_lo(smem_u32(sm + S_K + 2 * st * kSlab), 16);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            if (k < ksteps) mma_el(el, tmem + T_S + 128u * st, desc_pack(loQ + (kmajor_off(k, kSlab) >> 4), hi),
-                                     desc_pack(loK + (kmajor_off(k, kSlab) >> 4), hi), id_s, k > 0);
+                        mma4_el<kStepK, kStepK>(el, tmem + T_S + 128u * st, loQ, loK, id_s, 0);
+                        if (slabs == 2)
+                            mma4_el<kStepK, kStepK>(el, tmem + T_S + 128u * st, loQ + kNextSlab, loK + kNextSlab, id_s, 1);
                         commit_el(el, &bars[B_S + st]);
                         if (c + 3 < nchunks) commit_el(el, &bars[B_QKFREE + st]);
                     }
                     if (c >= 0) {
-                        const int st = c & 1, ph = c >> 1, steps = (chunk_n(c) + 15) / 16;
+                        const int st = c & 1, ph = c >> 1;
+                        const bool far = chunk_n(c) > 64;       // tokens in the chunk's second half
                         if (!lwait_warp(&bars[B_P + st], ph, &s_abort) || !lwait_warp(&bars[B_V + st], ph, &s_abort)) break;
                         fence_after_sync();
                         const uint32_t loV = desc_lo(smem_u32(sm + S_V + st * kSlab), kSlab);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            if (k < steps) mma_ts_el(el, tmem + T_S + 128u * st + T_O2, tmem + T_S + 128u * st + 8u * k,
-                                        desc_pack(loV + (mnmajor_off(k) >> 4), hi), id_o, k > 0);
+                        mma4_ts_el<kStepMN>(el, tmem + T_S + 128u * st + T_O2, tmem + T_S + 128u * st, loV, id_o, 0);
+                        if (far)
+                            mma4_ts_el<kStepMN>(el, tmem + T_S + 128u * st + T_O2, tmem + T_S + 128u * st + 32u,
+                                                loV + 4 * kStepMN, id_o, 1);
                         commit_el(el, &bars[B_O2 + st]);
                         if (c + 2 < nchunks) commit_el(el, &bars[B_VFREE + st]);
                     }
@@ -617,11 +638,8 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
                     fence_after_sync();
                     issued = true;
                     const uint32_t loQ = desc_lo(smem_u32(sm + S_Q + 2 * st * kSlab), 16);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        if (k < ksteps)
-                            mma_el(el, tmem + T_O1, desc_pack(loQ + (kmajor_off(k, kSlab) >> 4), hi),
-                                     desc_pack(loH + (mnmajor_off(k) >> 4), hi), id_o, k > 0);
+                    mma4_el<kStepK, kStepMN>(el, tmem + T_O1, loQ, loH, id_o, 0);
+                    if (slabs == 2) mma4_el<kStepK, kStepMN>(el, tmem + T_O1, loQ + kNextSlab, loH + 4 * kStepMN, id_o, 1);
                     commit_el(el, &bars[B_O1 + st]);
                     if (c + 2 < nchunks) commit_el(el, &bars[B_QKFREE + st]);
                 }
@@ -639,18 +657,16 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
                 bool issued = false;
 #pragma unroll 1
                 for (int c = 0; c < nupdates; ++c) {
-                    const int st = c & 1, steps = (chunk_n(c) + 15) / 16;
+                    const int st = c & 1;
+                    const bool far = chunk_n(c) > 64;
                     if (!lwait_warp(&bars[B_QK + st], c >> 1, &s_abort) || !lwait_warp(&bars[B_VP], c, &s_abort) ||
                         (c > 0 && !lwait_warp(&bars[B_HFREE], c - 1, &s_abort)))
                         break;
                     fence_after_sync();
                     issued = true;
                     const uint32_t loK = desc_lo(smem_u32(sm + S_K + 2 * st * kSlab), kSlab);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        if (k < steps)
-                            mma_el(el, tmem + T_H, desc_pack(loK + (mnmajor_off(k) >> 4), hi),
-                                     desc_pack(loVP + (mnmajor_off(k) >> 4), hi), id_h, k > 0);
+                    mma4_el<kStepMN, kStepMN>(el, tmem + T_H, loK, loVP, id_h, 0);
+                    if (far) mma4_el<kStepMN, kStepMN>(el, tmem + T_H, loK + 4 * kStepMN, loVP + 4 * kStepMN, id_h, 1);
                     commit_el(el, &bars[B_DH]);
                     if (c + 2 < nchunks) {
                         commit_el(el, &bars[B_QKFREE + st]);
