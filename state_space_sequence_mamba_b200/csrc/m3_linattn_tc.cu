@@ -16,14 +16,19 @@
 // (2^-17) for a state that only feeds bf16 operands, three (2^-25) for one that is returned. The
 // parts lie side by side as one operand of 128 or 192 columns, so k is read once for all of them,
 // and their products are summed in registers: the tensor core's accumulator drops the bits below
-// its sum's last, and a state kept there would shrink by them at every step (1.5e-6 over a long
-// memory, against 7e-7 here).
+// its sum's last, and a state kept there would shrink by them at every step (relative to
+// the state after 4096 tokens with a = 0.9999: 1.5e-6, against 1.7e-7 here).
 //
-// What bounds it: the products read 1800 cycles of shared memory a chunk (S 64 KB, O1 48, k^T v' 80,
-// O2 16, at 128 bytes a cycle); per-head q, k, v and y of K 128, V 64 are 96 KB of HBM a chunk, some
-// 4200 cycles. Only H <- a^n H + ... is serial from chunk to chunk, so everything else runs ahead of
-// it: q, k and v are double-buffered, v' and its product do not wait for the state, and S and P of a
-// chunk do not wait for the outputs of the one before.
+// What bounds it: shared memory and the hand-offs of a chunk, about alike. The products read 1800 cycles
+// of shared memory a chunk (S 64 KB, O1 48, k^T v' 80, O2 16, at 128 bytes a cycle); the loads' writes, v',
+// its parts and the state's operand take it to some 2900. Measured are 3600 to 3900 cycles from chunk to
+// chunk, of which 96 KB of HBM (per-head q, k, v and y of K 128, V 64) would take 4200 if all 148 SMs asked
+// at once. Only H <- a^n H + ... is serial from chunk to chunk, so everything else runs ahead of it: q, k
+// and v are double-buffered, v' and its product do not wait for the state, and S and P of a chunk do not
+// wait for the outputs of the one before. A CTA's start (launch, TMEM, tables, first loads, the first
+// chunk's chain of products) is some 11 000 cycles until its first output: short sequences are bound by that.
+// Measured: 4 x 2048 tokens of 64 heads (K 128, V 64, q and k shared) 84 us, its three gradients with q and
+// k of every head 319 us (2.3 TB/s); 65 536 tokens of 64 heads 960 us (3.4 TB/s).
 //
 // Warps: 0-3 and 4-7 the rows of the even and of the odd chunks (S -> P, then y), 8-15 the state (in
 // registers, half a row a thread), 16-23 v', 24 TMA loads, 25 issues S and O2, 26 O1, 27 k^T v'.
