@@ -425,8 +425,8 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
                         }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (i < cols) hv[i] = fi * src[i * j.init_v];
+                    for (int i = 0; i < 32; ++i, src += j.init_v)
+                        if (i < cols) hv[i] = fi * *src;
                 }
             }
             if (order > 0) grid_dep_wait();     // the segments' end states are there
