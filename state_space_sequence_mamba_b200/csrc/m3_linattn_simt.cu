@@ -10,8 +10,8 @@
 // flops, so a chunk is bound by instruction issue, not by DRAM: the products are packed pairs of FMAs,
 // and blocks above the mask's diagonal are left out. In reverse a chunk's tokens are staged last to
 // first, which makes it a forward one. Rows are not padded but swizzled, and P takes q's place, so
-// that two CTAs of Dk = 128 fit an SM (112 KB each). 4096 tokens of 16 heads, K 128, V 64, fp32: 187 us,
-// 20 TFLOP/s, with an instruction issued in 64 % of the cycles and the FMA pipe busy in 37 %; the rest is
+// that two CTAs of Dk = 128 fit an SM (112 KB each). 4096 tokens of 16 heads, K 128, V 64, fp32: 179 us,
+// 21 TFLOP/s, with an instruction issued in 64 % of the cycles and the FMA pipe busy in 37 %; the rest is
 // waiting at the barriers between a chunk's products, which two CTAs an SM do not fill.
 #include "m3_common.cuh"
 #include "m3_internal.h"
@@ -284,7 +284,7 @@ lin_simt_kernel(const __grid_constant__ LinParams p) {
 #pragma unroll
             for (int b = 0; b < RI; ++b) {
                 if (16 * b >= n) break;
-#pragma unroll 1
+#pragma unroll 2
                 for (int jj = 16 * b; jj < 16 * b + 16; jj += 4) {
                     float4 vv[4];
 #pragma unroll
@@ -310,6 +310,43 @@ lin_simt_kernel(const __grid_constant__ LinParams p) {
         // the last chunk's update only for a state that somebody wants
         if (!kStateOnly && cc + 1 == nchunks && !(j.final_state && order == w.nseg - 1)) break;
         const float hd = pw[n - off];
+        if (C == 64 && L.Dp <= 32) {    // (P holds 64 rows of 64: parts x Dp)
+            // Rows for a part of the threads only: the others take parts of the chunk's tokens, whose sums
+            // meet in P's place and are added in order (one chunk of K 16: 11.8 -> 9.0 us a call).
+            const int rows = L.Dp / 4, part = ty / rows, parts = 16 / rows, r0 = 4 * (ty - part * rows);
+            float2 acc[2][4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[0][c] = acc[1][c] = dup(0.f);
+#pragma unroll 4
+            for (int i = part; i < n; i += parts) {
+                const float wt = j.x_scale * pw[n - 1 - i];
+                const float4 ka = *reinterpret_cast<const float4*>(sk + i * L.Dp + swz_k(i, r0, L.mask));
+                const float4 vv = *reinterpret_cast<const float4*>(sv + i * kVT + 4 * tx);
+                const float2 w[4] = {dup(vv.x * wt), dup(vv.y * wt), dup(vv.z * wt), dup(vv.w * wt)};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    fma2(acc[0][c], lo2(ka), w[c]);
+                    fma2(acc[1][c], hi2(ka), w[c]);
+                }
+            }
+            __syncthreads();        // P has been read
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float2* r = acc[u >> 1];
+                const bool odd = u & 1;
+                *reinterpret_cast<float4*>(sp + (part * L.Dp + r0 + u) * kVT + 4 * tx) =
+                    make_float4(odd ? r[0].y : r[0].x, odd ? r[1].y : r[1].x, odd ? r[2].y : r[2].x, odd ? r[3].y : r[3].x);
+            }
+            __syncthreads();
+            for (int e = tid; e < L.Dp * (kVT / 4); e += kThreads) {
+                float4* at = reinterpret_cast<float4*>(sh) + e;
+                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int a = 0; a < parts; ++a) fma4(sum, 1.f, reinterpret_cast<const float4*>(sp)[a * L.Dp * (kVT / 4) + e]);
+                fma4(sum, hd, *at);
+                *at = sum;
+            }
+            continue;
+        }
 #pragma unroll 1
         for (int k0 = 4 * ty; k0 < L.Dp; k0 += 128) {       // two blocks of 64 rows at a time
             const bool two = k0 + 64 < L.Dp;
@@ -319,7 +356,7 @@ lin_simt_kernel(const __grid_constant__ LinParams p) {
             for (int u = 0; u < 4; ++u)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) acc[u][c] = dup(0.f);
-#pragma unroll 2
+#pragma unroll 4
             for (int i = 0; i < n; ++i) {
                 const float wt = j.x_scale * pw[n - 1 - i];
                 const float* kr = sk + i * L.Dp;
