@@ -22,13 +22,13 @@
 // What bounds it: shared memory and the hand-offs of a chunk, about alike. The products read 1800 cycles
 // of shared memory a chunk (S 64 KB, O1 48, k^T v' 80, O2 16, at 128 bytes a cycle); the loads' writes, v',
 // its parts and the state's operand take it to some 2900. Measured are 3600 to 3900 cycles from chunk to
-// chunk, of which 96 KB of HBM (per-head q, k, v and y of K 128, V 64) would take 4200 if all 148 SMs asked
+// chunk, with the data pipe in front of shared memory and TMEM busy for 78 % of a launch; 96 KB of HBM (per-head q, k, v and y of K 128, V 64) would take 4200 if all 148 SMs asked
 // at once. Only H <- a^n H + ... is serial from chunk to chunk, so everything else runs ahead of it: q, k
 // and v are double-buffered, v' and its product do not wait for the state, and S and P of a chunk do not
 // wait for the outputs of the one before. A CTA's start (launch, TMEM, tables, first loads, the first
 // chunk's chain of products) is some 11 000 cycles until its first output: short sequences are bound by that.
-// Measured: 4 x 2048 tokens of 64 heads (K 128, V 64, q and k shared) 84 us, its three gradients with q and
-// k of every head 319 us (2.3 TB/s); 65 536 tokens of 64 heads 960 us (3.4 TB/s).
+// Measured: 4 x 2048 tokens of 64 heads (K 128, V 64, q and k shared) 83 us, its three gradients with q and
+// k of every head 315 us (2.4 TB/s); 65 536 tokens of 64 heads 955 us (3.4 TB/s).
 //
 // Warps: 0-3 and 4-7 the rows of the even and of the odd chunks (S -> P, then y), 8-15 the state (in
 // registers, half a row a thread), 16-23 v', 24 TMA loads, 25 issues S and O2, 26 O1, 27 k^T v'.
@@ -201,8 +201,9 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
     __shared__ __align__(8) uint64_t bars[kNumBars];
     __shared__ __align__(16) float pw[kC + 4];
     // a^{31 - k} (reverse: a^{k - 31}), zero where the exponent is negative: entries 31 - r + i are row r
-    // of the mask's diagonal blocks, a^{31 - i} (a^i) the columns' factors of the others
+    // of the mask's diagonal blocks; and the columns' factors of the other blocks, a^{31 - i} (a^i)
     __shared__ float mask[64];
+    __shared__ __align__(16) float colw[32];
     __shared__ uint32_t tslot;
     __shared__ volatile int s_abort;
 
@@ -285,7 +286,9 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
     if (tid <= kC) pw[tid] = lin_pow(g2, static_cast<float>(tid));
     if (tid >= 256 && tid < 320) {
         const int d = rev ? tid - 287 : 287 - tid;
-        mask[tid - 256] = d >= 0 ? lin_pow(g2, static_cast<float>(d)) : 0.f;
+        const float m = d >= 0 ? lin_pow(g2, static_cast<float>(d)) : 0.f;
+        mask[tid - 256] = m;
+        if (rev ? tid >= 287 && tid < 319 : tid < 288) colw[rev ? tid - 287 : tid - 256] = m;
     }
     fence_before_sync();
     __syncthreads();
@@ -323,13 +326,25 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
                     } else {
                         float v[32];
                         tmem_ld_32x32b_x32(ls + 32u * b, v);
-                        const float* m = mask + (ahead > 0 ? (rev ? 31 : 0) : 31 - lane);
-                        const float f = ahead > 0 ? ps * pw[sgn * (32 * b - t) - (rev ? 0 : 31)] : ps;
-                        tmem_wait_ld();
+                        if (ahead > 0) {
+                            const float f = ps * pw[sgn * (32 * b - t) - (rev ? 0 : 31)];
+                            const float2 f2 = make_float2(f, f);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            pk[i] = pack2(__fmul2_rn(__fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), make_float2(f, f)),
-                                                     make_float2(m[2 * i], m[2 * i + 1])));
+                            for (int i = 0; i < 8; ++i) {
+                                const float4 m = reinterpret_cast<const float4*>(colw)[i];
+                                pk[2 * i] = pack2(__fmul2_rn(__fmul2_rn(make_float2(v[4 * i], v[4 * i + 1]), f2), make_float2(m.x, m.y)));
+                                pk[2 * i + 1] = pack2(__fmul2_rn(__fmul2_rn(make_float2(v[4 * i + 2], v[4 * i + 3]), f2), make_float2(m.z, m.w)));
+                            }
+                        } else {
+                            const float* m = mask + 31 - lane;
+                            const float2 f2 = make_float2(ps, ps);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                pk[i] = pack2(__fmul2_rn(__fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), f2),
+                                                         make_float2(m[2 * i], m[2 * i + 1])));
+                        }
                     }
                     // block b of P lies over S's block b / 2, which has been read
                     tmem_st_32x32b_x16(ls + 16u * b, pk);
