@@ -320,7 +320,8 @@ M3_API m3_status m3_scan_fwd_noalloc(const m3_dims* dims, const m3_inputs* in,
 
 /* A tensor of rows [nseq][seqlen][heads][dim] by its strides, in elements; the last dimension is
  * contiguous. With cu_seqlens the batch stride is not used. Any element-aligned pointer and any
- * strides (0 for an input, to broadcast); outputs must not overlap one another or an input. */
+ * strides (0 for an input, to broadcast); outputs must not overlap one another or an input (one
+ * that begins at another tensor's address is refused). */
 typedef struct {
     void* data;
     int64_t batch, token, head;
@@ -381,7 +382,7 @@ M3_API m3_status m3_linattn_step(const m3_linattn_dims* dims, const m3_linattn_i
  *     R_t = a R_{t+1} + scale q_t d_o_t^T   (R_T such that a R_T = dfinal)
  * d_o: [nseq][seqlen][H][V]. dq, dk, dv: in_dtype, laid out by their views with the heads of q,
  * k and v. dfinal, dinit: fp32 [nseq, H, K, V], or NULL for zero / not wanted; dinit may be
- * dfinal. The same tensor-core condition as m3_linattn_fwd, with K, V <= 128. Results do not
+ * dfinal, not init. The same tensor-core condition as m3_linattn_fwd, with K, V <= 128. Results do not
  * depend on the order of execution. */
 typedef struct {
     m3_view dq, dk, dv;

@@ -633,6 +633,16 @@ m3_status check_out(const m3_view* v, const m3_group_norm_dims* d, const char* n
     return M3_OK;
 }
 
+// An output that begins where another tensor does: allowed for the ones named, by the same strides.
+m3_status check_shared(const m3_view* out, const m3_view* t, const m3_group_norm_dims* d, bool allowed,
+                       const char* name, const char* other) {
+    if (!out || !t || !out->data || out->data != t->data) return M3_OK;
+    const bool same = (d->batch == 1 || out->batch == t->batch) && (d->rows == 1 || out->token == t->token) &&
+                      (d->groups == 1 || out->head == t->head);
+    if (allowed && same) return M3_OK;
+    return err(M3_ERR_INVALID_ARG, allowed ? "%s is %s by other strides" : "%s is %s", name, other);
+}
+
 GnParams make_params(const m3_group_norm_dims* d, const m3_view* x, const m3_view* z, const float* w, const float* b) {
     GnParams p{};
     p.rows = static_cast<uint32_t>(d->batch * d->rows);
@@ -668,7 +678,9 @@ m3_status m3_group_norm_fwd(const m3_group_norm_dims* dims, const m3_view* x, co
         (st = check_view(out, es, "out", any)) != M3_OK)
         return st;
     if (!any) return M3_OK;
-    if ((st = check_out(out, dims, "out")) != M3_OK) return st;
+    if ((st = check_out(out, dims, "out")) != M3_OK || (st = check_shared(out, x, dims, true, "out", "x")) != M3_OK ||
+        (st = check_shared(out, z, dims, true, "out", "z")) != M3_OK)
+        return st;
     GnParams p = make_params(dims, x, z, weight, bias);
     p.out = tensor(out);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -706,6 +718,15 @@ m3_status m3_group_norm_bwd(const m3_group_norm_dims* dims, const m3_view* x, co
         return e == cudaSuccess ? M3_OK : err(M3_ERR_CUDA, "empty gradient: %s", cudaGetErrorString(e));
     }
     if ((st = check_out(dx, dims, "dx")) != M3_OK || (gate && (st = check_out(dz, dims, "dz")) != M3_OK)) return st;
+    if ((st = check_shared(dx, x, dims, true, "dx", "x")) != M3_OK ||
+        (st = check_shared(dx, dout, dims, true, "dx", "dout")) != M3_OK ||
+        (st = check_shared(dx, z, dims, false, "dx", "z")) != M3_OK)
+        return st;
+    if (gate && ((st = check_shared(dz, z, dims, true, "dz", "z")) != M3_OK ||
+                 (st = check_shared(dz, x, dims, false, "dz", "x")) != M3_OK ||
+                 (st = check_shared(dz, dout, dims, false, "dz", "dout")) != M3_OK ||
+                 (st = check_shared(dz, dx, dims, false, "dz", "dx")) != M3_OK))
+        return st;
     const size_t need = m3_group_norm_bwd_workspace_bytes(dims);
     if (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || ws_bytes < need))
         return err(M3_ERR_INVALID_ARG, "workspace: NULL, misaligned or below %zu bytes", need);

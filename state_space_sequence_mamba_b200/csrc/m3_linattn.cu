@@ -116,6 +116,21 @@ m3_status check_inputs(const m3_linattn_dims* d, const m3_linattn_inputs* in, bo
     return M3_OK;
 }
 
+// An output that begins where an input or another output does would be written while it is read (or
+// written twice); overlaps further in are the caller's to avoid.
+m3_status check_apart(const m3_linattn_inputs* in, const m3_view* d_o, const m3_view* const* outs,
+                      const char* const* names, int n) {
+    const void* ins[] = {in->q.data, in->k.data, in->v.data, d_o ? d_o->data : nullptr};
+    const char* in_names[] = {"q", "k", "v", "d_o"};
+    for (int i = 0; i < n; ++i) {
+        for (int a = 0; a < 4; ++a)
+            if (outs[i]->data == ins[a]) return err(M3_ERR_INVALID_ARG, "%s is %s", names[i], in_names[a]);
+        for (int a = 0; a < i; ++a)
+            if (outs[i]->data == outs[a]->data) return err(M3_ERR_INVALID_ARG, "%s is %s", names[i], names[a]);
+    }
+    return M3_OK;
+}
+
 // A dimension of one entry has stride 0, whatever the caller's says.
 LinTensor tensor(const m3_linattn_dims* d, const m3_view& v, int64_t heads, bool packed) {
     return LinTensor{v.data, packed || d->nseq == 1 ? 0 : v.batch, d->seqlen == 1 ? 0 : v.token,
@@ -336,6 +351,8 @@ m3_status m3_linattn_fwd(const m3_linattn_dims* dims, const m3_linattn_inputs* i
     if ((st = check_workspace(workspace, ws_bytes, need)) != M3_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (!any) return pass_state(dims, init, final_state, s);
+    const char* const out_names[] = {"o"};
+    if ((st = check_apart(in, nullptr, &o, out_names, 1)) != M3_OK) return st;
     LinParams p = make_params(dims, in);
     const bool packed = in->cu_seqlens != nullptr;
     LinJob& j = p.job[0];
@@ -380,6 +397,7 @@ m3_status m3_linattn_bwd(const m3_linattn_dims* dims, const m3_linattn_inputs* i
     const size_t need = m3_linattn_bwd_workspace_bytes(dims, packed);
     if ((st = check_workspace(workspace, ws_bytes, need)) != M3_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (dinit && dinit == init) return err(M3_ERR_INVALID_ARG, "dinit is init");
     if (!any) return pass_state(dims, dfinal, dinit, s);
 
     LinParams p = make_params(dims, in);
@@ -390,7 +408,9 @@ m3_status m3_linattn_bwd(const m3_linattn_dims* dims, const m3_linattn_inputs* i
     char* ws = static_cast<char*>(workspace);
     char* seg = ws;
     ws += seg_bytes(dims, packed, bwd_tiles(dims), bwd_rows(dims));
-    const m3_view* outs[3] = {&grads->dq, &grads->dk, &grads->dv};
+    const m3_view* const outs[3] = {&grads->dq, &grads->dk, &grads->dv};
+    const char* const out_names[] = {"dq", "dk", "dv"};
+    if ((st = check_apart(in, d_o, outs, out_names, 3)) != M3_OK) return st;
     float* part[3];
     for (int i = 0; i < 3; ++i) {
         const size_t n = shared_bytes(dims, i, packed);
@@ -455,6 +475,8 @@ m3_status m3_linattn_step(const m3_linattn_dims* dims, const m3_linattn_inputs* 
         return st;
     if (dims->nseq * dims->nheads > kMaxGrid / 16) return err(M3_ERR_UNSUPPORTED, "nseq * nheads exceeds the grid limit");
     if (!any) return M3_OK;
+    const char* const out_names[] = {"o"};
+    if ((st = check_apart(in, nullptr, &o, out_names, 1)) != M3_OK) return st;
     LinStep p{};
     p.q = tensor(dims, in->q, dims->qheads, false);
     p.k = tensor(dims, in->k, dims->kheads, false);

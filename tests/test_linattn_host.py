@@ -287,3 +287,53 @@ def test_group_norm_refuses_pointers(lib):
     for kw in (dict(z=gview()), dict(ws=None), dict(ws=FAKE + 8), dict(n=need - 1), dict(dx=None),
                dict(dx=gview(FAKE, 0)), dict(z=gview(), dz=gview(FAKE, 4))):
         assert bwd(**kw) == bd.M3_ERR_INVALID_ARG, kw
+
+
+def test_linattn_refuses_outputs_on_inputs(lib):
+    """An output at the address of an input (or of another output) would be written while it is read."""
+    far = [FAKE + 4096 * n for n in range(1, 8)]
+    i = bd.LinattnInputs(*(bd.View(far[n], 64, 8, 8) for n in range(3)), FAKE, None)
+    d, d1 = ldims(), ldims(seqlen=1)
+    vw = lambda a: bd.View(a, 64, 8, 8)  # noqa: E731
+    need = lib.m3_linattn_bwd_workspace_bytes(ctypes.byref(d), 0)
+    for n, name in enumerate((b"q", b"k", b"v")):
+        o = vw(far[n])
+        assert lib.m3_linattn_fwd(ctypes.byref(d), ctypes.byref(i), None, None, ctypes.byref(o), None, 0,
+                                  None) == bd.M3_ERR_INVALID_ARG
+        assert lib.m3_last_error() == b"o is " + name
+        assert lib.m3_linattn_step(ctypes.byref(d1), ctypes.byref(i), FAKE, FAKE, 2, None, ctypes.byref(o),
+                                   None) == bd.M3_ERR_INVALID_ARG
+        assert lib.m3_last_error() == b"o is " + name
+
+    def bwd(dq, dk, dv, init=None, dinit=None):
+        g = bd.LinattnGrads(vw(dq), vw(dk), vw(dv))
+        do = vw(far[3])
+        return lib.m3_linattn_bwd(ctypes.byref(d), ctypes.byref(i), init, ctypes.byref(do), None, ctypes.byref(g),
+                                  dinit, FAKE, need, None)
+    for grads, msg in (((far[0], far[5], far[6]), b"dq is q"), ((far[4], far[3], far[6]), b"dk is d_o"),
+                       ((far[4], far[5], far[1]), b"dv is k"), ((far[4], far[4], far[6]), b"dk is dq"),
+                       ((far[4], far[5], far[4]), b"dv is dq")):
+        assert bwd(*grads) == bd.M3_ERR_INVALID_ARG and lib.m3_last_error() == msg
+    assert bwd(far[4], far[5], far[6], init=FAKE + 64, dinit=FAKE + 64) == bd.M3_ERR_INVALID_ARG
+    assert lib.m3_last_error() == b"dinit is init"
+
+
+def test_group_norm_refuses_outputs_on_inputs(lib):
+    d = gdims(rows=40)
+    x, z, dout, dx, dz = (FAKE + 65536 * n for n in range(1, 6))
+    assert lib.m3_group_norm_fwd(ctypes.byref(d), gview(x), gview(z), None, None, gview(x, 128),
+                                 None) == bd.M3_ERR_INVALID_ARG
+    assert lib.m3_last_error() == b"out is x by other strides"
+    assert lib.m3_group_norm_fwd(ctypes.byref(d), gview(x), gview(z), None, None, gview(z, 64, 18),
+                                 None) == bd.M3_ERR_INVALID_ARG
+    assert lib.m3_last_error() == b"out is z by other strides"
+    need = lib.m3_group_norm_bwd_workspace_bytes(ctypes.byref(d))
+
+    def bwd(dx, dz):
+        return lib.m3_group_norm_bwd(ctypes.byref(d), gview(x), gview(z), None, None, gview(dout), dx, dz, None, None,
+                                     FAKE, need, None)
+    for a, b, msg in ((gview(z), gview(dz), b"dx is z"), (gview(dx), gview(x), b"dz is x"),
+                      (gview(dx), gview(dout), b"dz is dout"), (gview(dx), gview(dx), b"dz is dx"),
+                      (gview(x, 128), gview(dz), b"dx is x by other strides"),
+                      (gview(dx), gview(z, 128), b"dz is z by other strides")):
+        assert bwd(a, b) == bd.M3_ERR_INVALID_ARG and lib.m3_last_error() == msg, msg
