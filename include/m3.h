@@ -359,7 +359,8 @@ M3_API size_t m3_linattn_bwd_workspace_bytes(const m3_linattn_dims* dims, int pa
  * m3_linattn_workspace_bytes (NULL where that is 0). bf16 tensors whose pointers and strides are
  * multiples of 16 bytes, with K and V multiples of 8 and K <= 128, run on the tensor cores (chunks
  * of 128 tokens; products of bf16 operands with fp32 accumulators, the state exact to fp32); every
- * other call runs in fp32 on the CUDA cores. Asynchronous on `stream`. */
+ * other call, and sequences of up to 8 tokens that are not packed, run in fp32 on the CUDA cores.
+ * Asynchronous on `stream`. */
 M3_API m3_status m3_linattn_fwd(const m3_linattn_dims* dims, const m3_linattn_inputs* in,
                                 const float* init, float* final_state, const m3_view* o,
                                 void* workspace, size_t ws_bytes, void* stream);

@@ -81,6 +81,7 @@ bool lin_tc_supported(const LinParams& p);
 cudaError_t launch_lin_tc(const LinParams& p, bool cut, cudaStream_t s);
 cudaError_t lin_tc_timeout(int* flag);   // reads and clears the timeout mark (blocks)
 
+constexpr int kLinShort = 8;        // tokens of the longest prompt that runs as steps
 struct LinStep {
     LinTensor q, k, v;
     const float* log_decay;
@@ -89,9 +90,9 @@ struct LinStep {
     int64_t nstates;
     const int32_t* slots;
     void* o;
-    int64_t o_batch, o_head;
+    int64_t o_batch, o_token, o_head;
     int64_t nseq;
-    int H, K, V;
+    int H, K, V, L;                 // L tokens of each, from 2 on without slots and for V % 4 == 0
     float scale;
 };
 cudaError_t launch_lin_step(const LinStep& p, bool bf16, cudaStream_t s);

@@ -555,3 +555,51 @@ def test_many_short_sequences(cuda_dev):
     for n, r in zip(("dq", "dk", "dv"), ref):
         assert err(gr[n][:, :total], r) <= tol(BF, 16, 32) and bool((gr[n][:, total:] == 0).all())
     assert err(gr["dinit"], ref[3]) <= STATE_TOL
+
+
+SHORT = [  # b, L, H, hq, hk, hv, K, V
+    (1, 2, 1, 1, 1, 1, 1, 4), (3, 2, 6, 2, 3, 6, 33, 20), (2, 3, 4, 1, 1, 4, 128, 64), (1, 4, 2, 2, 2, 2, 256, 256),
+    (2, 5, 3, 3, 1, 1, 96, 200), (1, 7, 8, 8, 2, 2, 64, 68), (5, 8, 40, 40, 40, 40, 48, 128), (2, 8, 2, 2, 2, 2, 255, 12),
+    (70, 8, 5, 5, 5, 5, 72, 252), (2, 6, 3, 3, 3, 3, 40, 6), (4, 1, 3, 1, 3, 3, 40, 6), (300, 1, 2, 2, 2, 2, 64, 96),
+]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("shape", SHORT)
+def test_short_prompts(cuda_dev, shape, dtype):
+    """Prompts of a few tokens, with and without a state before and after, on strided tensors and in place.
+    Products are exact and sums fp32: bf16 outputs are off by their own rounding, 2^-8 at most."""
+    b, L, H, hq, hk, hv, K, V = shape
+    t, d, _, s = draw(cuda_dev, *shape, dtype=dtype, seed=11)
+    bound = (2.0 ** -8 if dtype == BF else 0.0) + tol(F32, K, V)
+    zero = torch.zeros(b, H, K, V)
+    pad = {n: torch.nn.functional.pad(d[n], (3, 2, 0, 1, 1, 0)) for n in "qkv"}
+    at = {n: pad[n][:, 1:, :-1, 3:-2] for n in "qkv"}
+    for init in (d["init"], None):
+        ro, rS = ol.forward(t["q"], t["k"], t["v"], t["log_decay"], s, t["init"] if init is not None else zero)
+        for x in (d, at):
+            o, S = m3.linattn_fwd(x["q"], x["k"], x["v"], d["log_decay"], scale=s, init=init)
+            assert err(o, ro) <= bound and err(S, rS) <= STATE_TOL
+        wide = torch.full((b, L, H + 1, V + 3), 7.0, dtype=dtype, device=cuda_dev)
+        none = m3.linattn_fwd(d["q"], d["k"], d["v"], d["log_decay"], scale=s, init=init, final=False,
+                              o=wide[:, :, :H, :V])[1]
+        assert none is None and torch.equal(wide[:, :, :H, :V], o)
+        assert bool((wide[:, :, H] == 7).all()) and bool((wide[..., V:] == 7).all())
+    state = d["init"].clone()
+    m3.linattn_fwd(d["q"], d["k"], d["v"], d["log_decay"], scale=s, init=state, final=state)
+    assert torch.equal(state, m3.linattn_fwd(d["q"], d["k"], d["v"], d["log_decay"], scale=s, init=d["init"])[1])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_short_prompts_leave_nan_behind(cuda_dev, dtype):
+    """A token's NaN reaches its own and later outputs, not those before it or of other sequences."""
+    t, d, _, s = draw(cuda_dev, 3, 6, 2, 2, 2, 2, 64, 64, dtype=dtype, seed=3)
+    clean, _ = m3.linattn_fwd(d["q"], d["k"], d["v"], d["log_decay"], scale=s, init=d["init"])
+    d["k"][1, 3, 0, 5] = float("nan")
+    d["v"][1, 4, 1, 7] = float("inf")
+    o, S = m3.linattn_fwd(d["q"], d["k"], d["v"], d["log_decay"], scale=s, init=d["init"])
+    assert torch.equal(o[0], clean[0]) and torch.equal(o[2], clean[2])
+    assert torch.equal(o[1, :3], clean[1, :3]) and torch.equal(o[1, 3, 1], clean[1, 3, 1])
+    assert bool(torch.isnan(o[1, 3:, 0]).all()) and bool(torch.isfinite(S[0]).all())
+    keep = [c for c in range(64) if c != 7]
+    assert torch.equal(o[1, 4:, 1][:, keep], clean[1, 4:, 1][:, keep])
