@@ -511,9 +511,13 @@ int64_t share_count(int64_t rows, int64_t per_row_ctas, int per_sm) {
 }
 // One wave of CTAs: what the registers let an SM hold (62 and 96 a thread at groups of 64). More, shorter
 // shares were slower: 46.1 us with 16 CTAs an SM forward, 90.8 with 4 backward.
-constexpr int kFwdPerSm = 4, kBwdPerSm = 2;
+// The backward in fp32 holds 64: four an SM (8192 x 4096 gated 147 -> 115 us, 2000 x 2048 22.4 -> 19.4), but
+// not for shares of fewer than six rows, whose sums then cost more (777 x 1920: 8.8 against 9.5 us).
+constexpr int kFwdPerSm = 4, kBwdPerSm = 2, kBwdPerSmF32 = 4, kBwdRowsF32 = 6;
+template <typename T, int NV>
+constexpr int bwd_per_sm() { return sizeof(T) == 4 && NV == 1 ? kBwdPerSmF32 : kBwdPerSm; }
 // the most shares any form of the backward takes
-int64_t max_shares(int64_t rows) { return share_count(rows, 1, kBwdPerSm); }
+int64_t max_shares(int64_t rows, bool bf16) { return share_count(rows, 1, bf16 ? kBwdPerSm : kBwdPerSmF32); }
 
 // Groups side by side in a CTA: as many as its threads and 32 KB of column sums hold, the row's groups
 // spread evenly over the slabs.
@@ -523,11 +527,16 @@ int groups_per_cta(const GnParams& p, int per) {
     return (p.G + slabs - 1) / slabs;
 }
 
-// The walk's grid: fills in the shares.
-dim3 walk_grid(GnParams& p, int gx, int per, int per_sm) {
+// The walk's grid (per_sm CTAs an SM, or down to `least` where shares get short): fills in the shares.
+dim3 walk_grid(GnParams& p, int gx, int per, int per_sm, int least) {
     const int nry = per / gx;
     const unsigned slabs = static_cast<unsigned>((p.G + gx - 1) / gx);
-    const int64_t turns = (p.rows + nry - 1) / nry, n = share_count(turns, slabs, per_sm);
+    const int64_t turns = (p.rows + nry - 1) / nry;
+    int64_t n = share_count(turns, slabs, per_sm);
+    if (least < per_sm && n > turns / kBwdRowsF32) {
+        const int64_t few = share_count(turns, slabs, least);
+        n = few > turns / kBwdRowsF32 ? few : turns / kBwdRowsF32;
+    }
     p.share_rows = static_cast<uint32_t>((turns + n - 1) / n * nry);
     p.shares = static_cast<int>((p.rows + p.share_rows - 1) / p.share_rows);
     return dim3(static_cast<unsigned>(p.shares), slabs);
@@ -546,7 +555,7 @@ cudaError_t launch_fwd(GnParams p, uint32_t flags, cudaStream_t s) {
             using S = decltype(sh);
             constexpr int per = kThreads / S::LPG;
             const int gx = groups_per_cta(p, per);
-            const dim3 grid = walk_grid(p, gx, per, kFwdPerSm);
+            const dim3 grid = walk_grid(p, gx, per, kFwdPerSm, kFwdPerSm);
             gn_fwd_kernel<T, S::LPG, S::NV, F::C, F::S, F::Z><<<grid, kThreads, 0, s>>>(p, gx);
             return 0;
         });
@@ -570,7 +579,7 @@ cudaError_t launch_bwd(GnParams p, uint32_t flags, cudaStream_t s) {
             using S = decltype(sh);
             constexpr int per = kThreads / S::LPG;
             const int gx = groups_per_cta(p, per);
-            const dim3 grid = walk_grid(p, gx, per, kBwdPerSm);
+            const dim3 grid = walk_grid(p, gx, per, bwd_per_sm<T, S::NV>(), kBwdPerSm);
             const size_t smem = static_cast<size_t>(gx) * p.D * 2 * sizeof(float);
             gn_bwd_kernel<T, S::LPG, S::NV, F::C, F::S, F::Z><<<grid, kThreads, smem, s>>>(p, gx);
             return 0;
@@ -690,7 +699,7 @@ m3_status m3_group_norm_fwd(const m3_group_norm_dims* dims, const m3_view* x, co
 
 size_t m3_group_norm_bwd_workspace_bytes(const m3_group_norm_dims* dims) {
     if (check(dims) != M3_OK) return 0;
-    const int64_t shares = max_shares(dims->batch * dims->rows);
+    const int64_t shares = max_shares(dims->batch * dims->rows, dims->in_dtype == M3_BF16);
     const size_t n = shares > 1 ? static_cast<size_t>(shares) * 2 * static_cast<size_t>(dims->channels) * 4 : 0;
     return (n + 255) / 256 * 256;
 }
