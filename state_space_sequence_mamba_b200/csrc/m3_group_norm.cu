@@ -511,13 +511,14 @@ int64_t share_count(int64_t rows, int64_t per_row_ctas, int per_sm) {
 }
 // One wave of CTAs: what the registers let an SM hold (62 and 96 a thread at groups of 64). More, shorter
 // shares were slower: 46.1 us with 16 CTAs an SM forward, 90.8 with 4 backward.
-// The backward in fp32 holds 64: four an SM (8192 x 4096 gated 147 -> 115 us, 2000 x 2048 22.4 -> 19.4), but
+// The backward without a gate holds 72 to 80: three (8192 x 4096 in groups of 64: 68.6 -> 58.7 us). In fp32
+// it holds 64: four (8192 x 4096 gated 147 -> 115 us, 2000 x 2048 22.4 -> 19.4), but
 // not for shares of fewer than six rows, whose sums then cost more (777 x 1920: 8.8 against 9.5 us).
-constexpr int kFwdPerSm = 4, kBwdPerSm = 2, kBwdPerSmF32 = 4, kBwdRowsF32 = 6;
-template <typename T, int NV>
-constexpr int bwd_per_sm() { return sizeof(T) == 4 && NV == 1 ? kBwdPerSmF32 : kBwdPerSm; }
+constexpr int kFwdPerSm = 4, kBwdPerSm = 2, kBwdPerSmF32 = 4, kBwdPerSmPlain = 3, kBwdRowsF32 = 6;
+template <typename T, int NV, bool kGate>
+constexpr int bwd_per_sm() { return NV > 1 ? kBwdPerSm : sizeof(T) == 4 ? kBwdPerSmF32 : kGate ? kBwdPerSm : kBwdPerSmPlain; }
 // the most shares any form of the backward takes
-int64_t max_shares(int64_t rows, bool bf16) { return share_count(rows, 1, bf16 ? kBwdPerSm : kBwdPerSmF32); }
+int64_t max_shares(int64_t rows, bool bf16) { return share_count(rows, 1, bf16 ? kBwdPerSmPlain : kBwdPerSmF32); }
 
 // Groups side by side in a CTA: as many as its threads and 32 KB of column sums hold, the row's groups
 // spread evenly over the slabs.
@@ -579,7 +580,7 @@ cudaError_t launch_bwd(GnParams p, uint32_t flags, cudaStream_t s) {
             using S = decltype(sh);
             constexpr int per = kThreads / S::LPG;
             const int gx = groups_per_cta(p, per);
-            const dim3 grid = walk_grid(p, gx, per, bwd_per_sm<T, S::NV>(), kBwdPerSm);
+            const dim3 grid = walk_grid(p, gx, per, bwd_per_sm<T, S::NV, F::Z>(), kBwdPerSm);
             const size_t smem = static_cast<size_t>(gx) * p.D * 2 * sizeof(float);
             gn_bwd_kernel<T, S::LPG, S::NV, F::C, F::S, F::Z><<<grid, kThreads, smem, s>>>(p, gx);
             return 0;
