@@ -314,8 +314,9 @@ M3_API m3_status m3_scan_fwd_noalloc(const m3_dims* dims, const m3_inputs* in,
  * Packed sequences: with cu_seqlens (device, int32, nseq + 1 values, ascending from >= 0), the
  * tensors hold seqlen rows in all and sequence i is rows [cu_seqlens[i], cu_seqlens[i + 1]).
  * Rows outside every sequence are not read as tokens and their outputs are left as they were.
- * Values outside [0, seqlen] are clamped to it and a descending pair is an empty sequence (rows
- * around one may then be left out of the gradients of shared heads).
+ * Values outside [0, seqlen] are clamped to it and a descending pair is an empty sequence. Sequences
+ * behind one may overlap others: each has states of its own, the rows that they share hold the values
+ * of one of them, and rows around the pair may be left out of the gradients of shared heads.
  * Sequences of length 0 and 1 are allowed: the state after an empty one is its initial state. */
 
 /* A tensor of rows [nseq][seqlen][heads][dim] by its strides, in elements; the last dimension is

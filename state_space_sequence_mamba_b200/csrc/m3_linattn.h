@@ -121,7 +121,10 @@ struct LinWhere {
 };
 
 // Sequence and segment of block x. Packed: the running count of segments, 32 sequences at a
-// time (all lanes of a warp call this together).
+// time (all lanes of a warp call this together). The plan reserves a block for each sequence and
+// L / seg_len more, which is all that ascending offsets can ask for. Descending ones may overlap and
+// ask for any number: the sequence that would go beyond the reserve, and every long one behind it, is
+// one segment, however long. So no segment has an index at or above blocks_x, and every sequence runs.
 __device__ __forceinline__ LinWhere lin_locate(const LinParams& p, unsigned x) {
     LinWhere w{};
     if (!p.cu) {
@@ -134,36 +137,48 @@ __device__ __forceinline__ LinWhere lin_locate(const LinParams& p, unsigned x) {
         return w;
     }
     const int lane = threadIdx.x & 31, L = static_cast<int>(p.L);
-    int64_t before = 0;         // offsets that overlap may add up to anything
+    const int64_t reserve = p.blocks_x - p.nseq;
+    int64_t before = 0, asked = 0;      // blocks of the sequences before; segments beyond the first they ask for
 #pragma unroll 1
     for (int base = 0; base < p.nseq; base += 32) {
-        const int i = base + lane;
-        int s = 0, e = 0, n = 0;
+        const int i = base + lane, here = min(p.nseq - base, 32);
+        int s = 0, e = 0, more = 0;
         if (i < p.nseq) {
             s = min(max(p.cu[i], 0), L);
             e = min(max(p.cu[i + 1], s), L);
-            n = max((e - s + p.seg_len - 1) / p.seg_len, 1);
+            more = max((e - s + p.seg_len - 1) / p.seg_len, 1) - 1;
         }
-        int incl = n;           // at most 32 (2^30 / 128 + 1)
+        int incl = more;        // at most 32 * 2^30 / 64
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int up = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += up;
         }
-        const unsigned hit = __ballot_sync(0xffffffffu, before + incl > static_cast<int64_t>(x));
+        // the lanes within the reserve come first: incl ascends
+        const unsigned fits = __ballot_sync(0xffffffffu, asked + incl <= reserve);
+        const int most = __shfl_sync(0xffffffffu, incl, fits ? 31 - __clz(fits) : 0), cap = fits ? most : 0;
+        const int upto = min(lane + 1, here) + min(incl, cap);      // blocks up to and with this lane's sequence
+        const unsigned hit = __ballot_sync(0xffffffffu, before + upto > static_cast<int64_t>(x));
         if (hit) {
-            const int src = __ffs(hit) - 1;
+            const int src = __ffs(hit) - 1, n = (fits >> lane & 1) ? more + 1 : 1;
             w.seq = base + src;
-            w.seg = static_cast<int>(x - before) - __shfl_sync(0xffffffffu, incl - n, src);
+            w.seg = static_cast<int>(x - before) - __shfl_sync(0xffffffffu, upto - n, src);
             w.nseg = __shfl_sync(0xffffffffu, n, src);
             w.row0 = __shfl_sync(0xffffffffu, s, src);
             w.len = __shfl_sync(0xffffffffu, e - s, src);
             w.valid = true;
             return w;
         }
-        before += __shfl_sync(0xffffffffu, incl, 31);
+        before += __shfl_sync(0xffffffffu, upto, 31);
+        asked += __shfl_sync(0xffffffffu, incl, 31);
     }
     return w;
+}
+
+// The end of a segment that starts at token seg0: the only one of a sequence reaches its end.
+__device__ __forceinline__ int64_t lin_seg_end(const LinParams& p, const LinWhere& w, int64_t seg0) {
+    const int64_t end = seg0 + p.seg_len;
+    return w.nseg == 1 || end > w.len ? w.len : end;
 }
 
 // a^n from log2(a): exact at n = 0 whatever a is (a = 0 included).

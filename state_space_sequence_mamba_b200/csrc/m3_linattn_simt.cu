@@ -120,7 +120,7 @@ lin_simt_kernel(const __grid_constant__ LinParams p) {
     const LinWhere w = lin_locate(p, x);
     if (!w.valid) return;
     const int64_t seg0 = static_cast<int64_t>(w.seg) * p.seg_len;
-    const int64_t seg_end = seg0 + p.seg_len < w.len ? seg0 + p.seg_len : w.len;
+    const int64_t seg_end = lin_seg_end(p, w, seg0);
     const int order = j.reverse ? w.nseg - 1 - w.seg : w.seg;
     if (kStateOnly && order == w.nseg - 1) return;    // nobody reads the last one's
 

@@ -223,7 +223,7 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
     const bool last_seg = order == w.nseg - 1;
     if (kStateOnly && last_seg) return;              // nobody reads the last one's
     const int seg0 = w.seg * p.seg_len;
-    const int seg_end = min(seg0 + p.seg_len, w.len);
+    const int seg_end = static_cast<int>(lin_seg_end(p, w, seg0));
     const int nchunks = (seg_end - seg0 + kC - 1) / kC;
     const bool want_final = !kStateOnly && j.final_state && last_seg;
     // chunks whose state product runs: the last one's only for a state that somebody wants
