@@ -805,7 +805,9 @@ cudaError_t launch_lin_tc(const LinParams& p, bool cut, cudaStream_t s) {
 }
 
 cudaError_t lin_tc_timeout(int* flag) {
-    cudaError_t e = cudaMemcpyFromSymbol(flag, g_lin_timeout, sizeof(int));
+    // the copy below waits for the default stream alone, not for streams that do not block on it
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e == cudaSuccess) e = cudaMemcpyFromSymbol(flag, g_lin_timeout, sizeof(int));
     if (e != cudaSuccess || *flag == 0) return e;
     const int zero = 0;
     return cudaMemcpyToSymbol(g_lin_timeout, &zero, sizeof(int));

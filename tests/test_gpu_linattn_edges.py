@@ -45,3 +45,27 @@ def test_overlapping_offsets_of_cut_sequences(cuda_dev, cu, spans, dtype):
             assert err(r["dv"][:, lo:hi][:, alone.to(cuda_dev)], ref[2][:, alone]) <= tol(dtype, K, V)
     for x in (o, *grads):
         assert bool((x[:, L:] == 7.0).all())
+
+
+def test_check_waits_for_a_call_on_another_stream(cuda_dev):
+    """linattn_check directly behind a call on a stream of its own (torch's do not wait for the default
+    one) finds that call's timed-out wait, and not a later caller."""
+    import os
+    t, d, _, s = draw(cuda_dev, 2, 700, 2, 2, 2, 2, 64, 64, seed=12)
+    args = (d["q"], d["k"], d["v"], d["log_decay"])
+    o, S = m3.linattn_fwd(*args, scale=s, init=d["init"])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    m3.linattn_check()
+    os.environ["M3_TEST_LINATTN_SKIP_LOAD"] = "1"
+    try:
+        m3.linattn_fwd(*args, scale=s, init=d["init"], stream=side)
+    finally:
+        del os.environ["M3_TEST_LINATTN_SKIP_LOAD"]
+    try:
+        with pytest.raises(m3.M3Error) as ei:
+            m3.linattn_check()
+        assert ei.value.status == m3.M3_ERR_TIMEOUT
+    finally:
+        torch.cuda.synchronize()
+    m3.linattn_check()
