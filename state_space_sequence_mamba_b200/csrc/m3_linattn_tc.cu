@@ -192,6 +192,62 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
                  : "memory");
 }
 
+// 8 and 1 columns of 32 lanes (thread i of the warp gets lane base + i)
+__device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, float (&v)[8]) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]) : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ uint32_t tmem_ld_x1(uint32_t taddr) {
+    uint32_t r;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+    return r;
+}
+
+// The outputs of a warp's 32 rows from P (lp) and O1 (lo) in TMEM and v in global memory, row t over the
+// tokens up to its own alone. v: the chunk's first token; y: this thread's row.
+__device__ __noinline__ void sum_rows(const LinJob& j, const __nv_bfloat16* v, uint8_t* y, uint32_t lp, uint32_t lo, int t,
+                                      int n, int cols, float f1) {
+#pragma unroll 1
+    for (int c = 0; c < kVT && c < cols; c += 8) {
+        float o[8], a[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = 0.f;
+#pragma unroll 1
+        for (int s = 0; s < n; ++s) {
+            const uint32_t p2 = tmem_ld_x1(lp + (s >> 1));
+            tmem_wait_ld();
+            const uint4 raw = *reinterpret_cast<const uint4*>(v + s * j.v.token + c);
+            // (selects, not a branch: the loads from TMEM need the whole warp)
+            const uint32_t on = (j.reverse ? s >= t : s <= t) ? 0xFFFFFFFFu : 0u;
+            const float pr = __uint_as_float((s & 1 ? p2 & 0xFFFF0000u : p2 << 16) & on);
+            const uint32_t u[4] = {raw.x & on, raw.y & on, raw.z & on, raw.w & on};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = unpack2(u[i]);
+                o[2 * i] = fmaf(pr, f.x, o[2 * i]);
+                o[2 * i + 1] = fmaf(pr, f.y, o[2 * i + 1]);
+            }
+        }
+        tmem_ld_x8(lo + c, a);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = fmaf(f1, a[i], o[i]);
+        if (t >= n) {
+            // (no token)
+        } else if (j.y_f32) {
+            float4* at = reinterpret_cast<float4*>(y + 4 * c);
+            at[0] = make_float4(o[0], o[1], o[2], o[3]);
+            at[1] = make_float4(o[4], o[5], o[6], o[7]);
+        } else {
+            *reinterpret_cast<uint4*>(y + 2 * c) = make_uint4(pack2(o[0], o[1]), pack2(o[2], o[3]), pack2(o[4], o[5]), pack2(o[6], o[7]));
+        }
+        __syncwarp();
+    }
+}
+
 template <bool kStateOnly>
 __global__ void __launch_bounds__(kThreads, 1)
 lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ LinMaps maps) {
@@ -310,98 +366,134 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
                              (w.batch * j.y_batch + w.row0 * j.y_token + h * j.y_head + tile * kVT) * es;
             // whether every row's pieces are whole 32-byte sectors
             const bool wide = ((reinterpret_cast<uintptr_t>(ybase) | static_cast<uintptr_t>(j.y_token * es)) & 31u) == 0;
+            // what the output adds to P v: the state's share of row t
+            auto state_factor = [&](int c) {
+                const int e = (rev ? chunk_n(c) - t : t + 1) - ((rev && order == 0 && c == 0) ? 1 : 0);
+                return j.o_scale * pw[e < 0 ? 0 : e];
+            };
+            int c = g;
+            // P v runs over all of the chunk's tokens, and zero times what is not finite is NaN: a later token's
+            // would reach the rows before it (and a growing decay's overflow, from tokens that are not there).
+            // A warp that finds such sums leaves the loop, sums its rows again over the tokens up to theirs,
+            // and comes back: inside the loop the sums' 64 registers would be spilled around that.
+            bool again;
 #pragma unroll 1
-            for (int c = g; c < nchunks; c += 2) {
-                const int t0 = chunk_t0(c), n = chunk_n(c);
-                if (!lwait_warp(&bars[B_S + g], c >> 1, &s_abort)) break;
-                fence_after_sync();
-                // 32 columns at a time, as far as the product reads (scores behind the last token are zero)
+            do {
+                again = false;
 #pragma unroll 1
-                for (int b = 0; b < (n > 64 ? 4 : 2); ++b) {
-                    uint32_t pk[16];
-                    const int ahead = sgn * (b - rw);           // 0: the diagonal block
-                    if (ahead < 0) {
+                for (; c < nchunks; c += 2) {
+                    const int t0 = chunk_t0(c), n = chunk_n(c);
+                    if (!lwait_warp(&bars[B_S + g], c >> 1, &s_abort)) break;
+                    fence_after_sync();
+                    // 32 columns at a time, as far as the product reads (scores behind the last token are zero)
+#pragma unroll 1
+                    for (int b = 0; b < (n > 64 ? 4 : 2); ++b) {
+                        uint32_t pk[16];
+                        const int ahead = sgn * (b - rw);           // 0: the diagonal block
+                        if (ahead < 0) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) pk[i] = 0u;
-                    } else {
-                        float v[32];
-                        tmem_ld_32x32b_x32(ls + 32u * b, v);
-                        if (ahead > 0) {
-                            const float f = ps * pw[sgn * (32 * b - t) - (rev ? 0 : 31)];
-                            const float2 f2 = make_float2(f, f);
-                            tmem_wait_ld();
+                            for (int i = 0; i < 16; ++i) pk[i] = 0u;
+                        } else {
+                            float v[32];
+                            tmem_ld_32x32b_x32(ls + 32u * b, v);
+                            if (ahead > 0) {
+                                const float f = ps * pw[sgn * (32 * b - t) - (rev ? 0 : 31)];
+                                const float2 f2 = make_float2(f, f);
+                                tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float4 m = reinterpret_cast<const float4*>(colw)[i];
-                                pk[2 * i] = pack2(__fmul2_rn(__fmul2_rn(make_float2(v[4 * i], v[4 * i + 1]), f2), make_float2(m.x, m.y)));
-                                pk[2 * i + 1] = pack2(__fmul2_rn(__fmul2_rn(make_float2(v[4 * i + 2], v[4 * i + 3]), f2), make_float2(m.z, m.w)));
+                                for (int i = 0; i < 8; ++i) {
+                                    const float4 m = reinterpret_cast<const float4*>(colw)[i];
+                                    pk[2 * i] = pack2(__fmul2_rn(__fmul2_rn(make_float2(v[4 * i], v[4 * i + 1]), f2), make_float2(m.x, m.y)));
+                                    pk[2 * i + 1] = pack2(__fmul2_rn(__fmul2_rn(make_float2(v[4 * i + 2], v[4 * i + 3]), f2), make_float2(m.z, m.w)));
+                                }
+                            } else {
+                                const float* m = mask + 31 - lane;
+                                const float2 f2 = make_float2(ps, ps);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    pk[i] = pack2(__fmul2_rn(__fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), f2),
+                                                             make_float2(m[2 * i], m[2 * i + 1])));
+                            }
+                        }
+                        // block b of P lies over S's block b / 2, which has been read
+                        tmem_st_32x32b_x16(ls + 16u * b, pk);
+                    }
+                    tmem_wait_st();
+                    fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[B_P + g]);
+                    const float f1 = state_factor(c);
+                    uint8_t* y = ybase + static_cast<int64_t>(t0 + t) * j.y_token * es;
+                    if (!lwait_warp(&bars[B_O1 + g], c >> 1, &s_abort) || !lwait_warp(&bars[B_O2 + g], c >> 1, &s_abort)) break;
+                    fence_after_sync();
+                    float2 odd = make_float2(0.f, 0.f);     // stays zero while the sums of O2 are finite
+#pragma unroll 1
+                    for (int q = 0; q < 2; ++q) {
+                        float a[32], o[32];
+                        tmem_ld_32x32b_x32(lo + 32u * q, a);
+                        tmem_ld_32x32b_x32(ls + T_O2 + 32u * q, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) odd = __ffma2_rn(make_float2(o[i], o[i + 1]), make_float2(0.f, 0.f), odd);
+                        if (q == 1) {
+                            again = __any_sync(0xffffffffu, odd.x + odd.y != 0.f);
+                            if (again) break;
+                            // O1, O2 and P have been read
+                            fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) {
+                                mbar_arrive(&bars[B_OFREE]);
+                                mbar_arrive(&bars[B_SFREE + g]);
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const float2 y2 = __ffma2_rn(make_float2(f1, f1), make_float2(a[i], a[i + 1]), make_float2(o[i], o[i + 1]));
+                            o[i] = y2.x;
+                            o[i + 1] = y2.y;
+                        }
+                        const int left = t < n ? cols - 32 * q : 0;
+                        if (j.y_f32) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                uint32_t u[8];
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) u[k] = __float_as_uint(o[8 * i + k]);
+                                if (8 * i < left) store32(y + 128 * q + 32 * i, u);     // always whole sectors
                             }
                         } else {
-                            const float* m = mask + 31 - lane;
-                            const float2 f2 = make_float2(ps, ps);
-                            tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                pk[i] = pack2(__fmul2_rn(__fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), f2),
-                                                         make_float2(m[2 * i], m[2 * i + 1])));
-                        }
-                    }
-                    // block b of P lies over S's block b / 2, which has been read
-                    tmem_st_32x32b_x16(ls + 16u * b, pk);
-                }
-                tmem_wait_st();
-                fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[B_P + g]);
-                const int e = (rev ? n - t : t + 1) - ((rev && order == 0 && c == 0) ? 1 : 0);
-                const float f1 = j.o_scale * pw[e < 0 ? 0 : e];
-                uint8_t* y = ybase + static_cast<int64_t>(t0 + t) * j.y_token * es;
-                if (!lwait_warp(&bars[B_O1 + g], c >> 1, &s_abort) || !lwait_warp(&bars[B_O2 + g], c >> 1, &s_abort)) break;
-                fence_after_sync();
-#pragma unroll 1
-                for (int q = 0; q < 2; ++q) {
-                    float a[32], o[32];
-                    tmem_ld_32x32b_x32(lo + 32u * q, a);
-                    tmem_ld_32x32b_x32(ls + T_O2 + 32u * q, o);
-                    tmem_wait_ld();
+                            for (int i = 0; i < 2; ++i) {
+                                uint32_t u[8];
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        const float2 y2 = __ffma2_rn(make_float2(f1, f1), make_float2(a[i], a[i + 1]), make_float2(o[i], o[i + 1]));
-                        o[i] = y2.x;
-                        o[i + 1] = y2.y;
-                    }
-                    const int left = t < n ? cols - 32 * q : 0;
-                    if (j.y_f32) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t u[8];
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) u[k] = __float_as_uint(o[8 * i + k]);
-                            if (8 * i < left) store32(y + 128 * q + 32 * i, u);     // always whole sectors
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            uint32_t u[8];
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) u[k] = pack2(o[16 * i + 2 * k], o[16 * i + 2 * k + 1]);
-                            uint8_t* at = y + 64 * q + 32 * i;
-                            if (wide && left >= 16 * i + 16) {
-                                store32(at, u);
-                            } else {
-                                if (left > 16 * i) *reinterpret_cast<uint4*>(at) = make_uint4(u[0], u[1], u[2], u[3]);
-                                if (left > 16 * i + 8) *reinterpret_cast<uint4*>(at + 16) = make_uint4(u[4], u[5], u[6], u[7]);
+                                for (int k = 0; k < 8; ++k) u[k] = pack2(o[16 * i + 2 * k], o[16 * i + 2 * k + 1]);
+                                uint8_t* at = y + 64 * q + 32 * i;
+                                if (wide && left >= 16 * i + 16) {
+                                    store32(at, u);
+                                } else {
+                                    if (left > 16 * i) *reinterpret_cast<uint4*>(at) = make_uint4(u[0], u[1], u[2], u[3]);
+                                    if (left > 16 * i + 8) *reinterpret_cast<uint4*>(at + 16) = make_uint4(u[4], u[5], u[6], u[7]);
+                                }
                             }
                         }
                     }
+                    if (again) break;
                 }
-                fence_before_sync();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&bars[B_OFREE]);
-                    mbar_arrive(&bars[B_SFREE + g]);
+                if (again) {
+                    const int t0 = chunk_t0(c), n = chunk_n(c);
+                    sum_rows(j, static_cast<const __nv_bfloat16*>(j.v.p) + w.batch * j.v.batch + (w.row0 + t0) * j.v.token +
+                                    (h / j.v.ratio) * j.v.head + tile * kVT,
+                             ybase + static_cast<int64_t>(t0 + t) * j.y_token * es, ls, lo, t, n, cols, state_factor(c));
+                    fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&bars[B_OFREE]);
+                        mbar_arrive(&bars[B_SFREE + g]);
+                    }
+                    c += 2;
                 }
-            }
+            } while (again);
         }
     } else if (warp < kPartWarp0) {
         // ================= the state: half of row r (32 columns) in a thread's registers =================

@@ -69,3 +69,83 @@ def test_check_waits_for_a_call_on_another_stream(cuda_dev):
     finally:
         torch.cuda.synchronize()
     m3.linattn_check()
+
+
+def agrees(got, ref, bound):
+    """Finite exactly where the recurrence is, and equal to it there."""
+    got = got.detach().double().cpu()
+    fin = torch.isfinite(ref)
+    assert torch.equal(torch.isfinite(got), fin), (int((torch.isfinite(got) != fin).sum()), ref.numel())
+    e = err(got[fin], ref[fin])
+    assert e <= bound, e
+
+
+POISON = [("k", float("nan")), ("v", float("nan")), ("v", float("inf")), ("k", -float("inf")),
+          ("q", float("nan")), ("do", float("inf"))]
+
+
+@pytest.mark.parametrize("dtype,K,V", [(BF, 64, 64), (BF, 128, 72)])
+@pytest.mark.parametrize("L", [9, 40, 300])
+@pytest.mark.parametrize("name,value", POISON)
+def test_a_token_that_is_not_finite_stays_out_of_earlier_ones(cuda_dev, name, value, L, dtype, K, V):
+    """One element of one token of one head: outputs and gradients are finite exactly where the recurrence's
+    are (o before the token, dk and dv behind it, other heads, other columns), whatever the chunk."""
+    t, d, _, s = draw(cuda_dev, 2, L, 2, 2, 2, 2, K, V, dtype=dtype, seed=51, decay=[-0.01, -0.05])
+    for at in (L // 2, L - 2) if L < 300 else (170, 290):
+        u, e = dict(t), dict(d)
+        u[name], e[name] = t[name].clone(), d[name].clone()
+        u[name][1, at, 0, 5] = value
+        e[name][1, at, 0, 5] = value
+        a = (e["q"], e["k"], e["v"], e["log_decay"])
+        o, S = m3.linattn_fwd(*a, scale=s, init=e["init"])
+        g = m3.linattn_bwd(*a, e["do"], scale=s, init=e["init"], dfinal=e["dfinal"])
+        torch.cuda.synchronize()
+        m3.linattn_check()
+        ro, rS = ol.forward(u["q"], u["k"], u["v"], u["log_decay"], s, u["init"])
+        ref = ol.gradients(u["q"], u["k"], u["v"], u["log_decay"], u["do"], s, u["init"], u["dfinal"])
+        agrees(o, ro, tol(dtype, K, V))
+        agrees(S, rS, STATE_TOL)
+        for n, r in zip(("dq", "dk", "dv", "dinit"), ref):
+            agrees(g[n], r, STATE_TOL if n == "dinit" else tol(dtype, K, V))
+
+
+@pytest.mark.parametrize("lens", [[130, 40, 100], [5, 260, 3]])
+def test_packed_tokens_that_are_not_finite(cuda_dev, lens):
+    """The same in packed sequences, with heads shared: the last token of one sequence is the neighbour of
+    the next one's first."""
+    t, d, cu, s = draw(cuda_dev, 1, 0, 4, 4, 2, 2, 64, 64, lens=lens, seed=52, decay=[-0.01, -0.05])
+    at = lens[0] + lens[1] - 1
+    for n, c in (("k", 3), ("v", 9), ("do", 7)):
+        t[n][0, at, 1, c] = float("nan")
+        d[n][0, at, 1, c] = float("nan")
+    a = (d["q"], d["k"], d["v"], d["log_decay"])
+    o, S = m3.linattn_fwd(*a, scale=s, init=d["init"], cu_seqlens=cu)
+    g = m3.linattn_bwd(*a, d["do"], scale=s, init=d["init"], dfinal=d["dfinal"], cu_seqlens=cu)
+    torch.cuda.synchronize()
+    m3.linattn_check()
+    ro, rS = ol.forward(t["q"], t["k"], t["v"], t["log_decay"], s, t["init"], lens)
+    ref = ol.gradients(t["q"], t["k"], t["v"], t["log_decay"], t["do"], s, t["init"], t["dfinal"], lens)
+    agrees(o, ro, tol(BF, 64, 64))
+    agrees(S, rS, STATE_TOL)
+    for n, r in zip(("dq", "dk", "dv", "dinit"), ref):
+        agrees(g[n], r, STATE_TOL if n == "dinit" else tol(BF, 64, 64))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("L,grow", [(9, 1.0), (65, 1.0), (80, 1.0), (20, 3.0), (27, 3.0)])
+def test_growing_decay_in_a_part_of_a_chunk(cuda_dev, L, grow, dtype):
+    """e^1 or e^3 a token: the sequence's own factors stay inside fp32's range (e^81 = 2e35), those of the
+    chunk's absent rows (e^127) do not."""
+    t, d, cu, s = draw(cuda_dev, 1, L, 2, 2, 2, 2, 64, 64, dtype=dtype, seed=53, decay=[grow, -0.01])
+    o, S = m3.linattn_fwd(d["q"], d["k"], d["v"], d["log_decay"], scale=s, init=d["init"])
+    g = m3.linattn_bwd(d["q"], d["k"], d["v"], d["log_decay"], d["do"], scale=s, init=d["init"], dfinal=d["dfinal"])
+    torch.cuda.synchronize()
+    ro, rS = ol.forward(t["q"], t["k"], t["v"], t["log_decay"], s, t["init"])
+    ref = ol.gradients(t["q"], t["k"], t["v"], t["log_decay"], t["do"], s, t["init"], t["dfinal"])
+    # the factor e^n is 2^x of a product rounded twice at 2^-24 of x = n log2(a) <= 117: 2^-17 together
+    more = 2.0 ** -16
+    for h in range(2):      # one head at a time: the growing one is all of a common norm
+        assert err(o[:, :, h], ro[:, :, h]) <= tol(dtype, 64, 64) + more
+        for n, r in zip(("dq", "dk", "dv"), ref):
+            assert err(g[n][:, :, h], r[:, :, h]) <= tol(dtype, 64, 64) + more, n
+        assert err(S[:, h], rS[:, h]) <= STATE_TOL + more and err(g["dinit"][:, h], ref[3][:, h]) <= STATE_TOL + more
