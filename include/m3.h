@@ -317,7 +317,11 @@ M3_API m3_status m3_scan_fwd_noalloc(const m3_dims* dims, const m3_inputs* in,
  * Values outside [0, seqlen] are clamped to it and a descending pair is an empty sequence. Sequences
  * behind one may overlap others: each has states of its own, the rows that they share hold the values
  * of one of them, and rows around the pair may be left out of the gradients of shared heads.
- * Sequences of length 0 and 1 are allowed: the state after an empty one is its initial state. */
+ * Sequences of length 0 and 1 are allowed: the state after an empty one is its initial state.
+ *
+ * Values that are not finite reach what the formulas say: a NaN or infinity in k or v the state and the
+ * outputs from its token on (never earlier ones), in q its own output, as NaN or infinity; the gradients
+ * likewise. Where a power of the decay underflows, it may end them. */
 
 /* A tensor of rows [nseq][seqlen][heads][dim] by its strides, in elements; the last dimension is
  * contiguous. With cu_seqlens the batch stride is not used. Any element-aligned pointer and any

@@ -109,6 +109,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 lin_simt_kernel(const __grid_constant__ LinParams p) {
     constexpr int RI = C / 16;      // rows a thread owns in the S and y products
     extern __shared__ __align__(16) float sm[];
+    __shared__ volatile int odd_chunk;      // 1 + the last chunk whose v is not all finite
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const unsigned per_x = static_cast<unsigned>(p.H) * p.rtiles;
     const unsigned x = blockIdx.x / per_x;
@@ -127,6 +128,7 @@ lin_simt_kernel(const __grid_constant__ LinParams p) {
     const SimtSmem L = simt_smem(j.Dk, C);
     float *sq = sm + L.q, *sk = sm + L.k, *sv = sm + L.v, *sp = sq, *sh = sm + L.h, *pw = sm + L.pw;
     const float g2 = p.log_decay[h] * 1.4426950408889634f;
+    if (tid == 0) odd_chunk = 0;
     for (int i = tid; i <= C; i += kThreads) pw[i] = lin_pow(g2, static_cast<float>(i));
     const bool blank = kStateOnly || (order == 0 && !j.init);      // no state before this segment
     if (kStateOnly) sm100::grid_dep_launch_dependents();
@@ -201,6 +203,7 @@ lin_simt_kernel(const __grid_constant__ LinParams p) {
         __syncthreads();
         // q, k and v rows as fp32, zeros behind the last token and column: 16 threads side by side, four
         // elements each, every load of a sweep issued before the first is stored
+        float odd = 0.f;            // stays zero while v is finite
 #pragma unroll 1
         for (int c = 4 * tx; c < L.Dp || c < kVT; c += 64) {
             float4 fq[RI], fk[RI], fv[RI];
@@ -222,9 +225,13 @@ lin_simt_kernel(const __grid_constant__ LinParams p) {
                     if (!kStateOnly) *reinterpret_cast<float4*>(sq + r * L.Dp + swz_q(r, c)) = fq[a];
                     *reinterpret_cast<float4*>(sk + r * L.Dp + swz_k(r, c, L.mask)) = fk[a];
                 }
-                if (c < kVT) *reinterpret_cast<float4*>(sv + r * kVT + c) = fv[a];
+                if (c < kVT) {
+                    *reinterpret_cast<float4*>(sv + r * kVT + c) = fv[a];
+                    if (!kStateOnly) odd = fmaf(0.f, (fv[a].x + fv[a].y) + (fv[a].z + fv[a].w), odd);
+                }
             }
         }
+        if (!kStateOnly && odd != 0.f) odd_chunk = cc + 1;
         __syncthreads();
         if (!kStateOnly) {
             // s[a][b]: rows ty + 16 a, columns tx + 16 b, the sums of even and odd d apart; b > a is masked
@@ -280,10 +287,21 @@ lin_simt_kernel(const __grid_constant__ LinParams p) {
                 yh[a].b = __fmul2_rn(yh[a].b, f);
             }
             const float *pr = sp + ty * C, *vr = sv + 4 * tx;
+            const bool all_finite = odd_chunk != cc + 1;
+            if (!all_finite) {
+                // zero times what is not finite is NaN: every row over the tokens up to its own alone
+#pragma unroll 1
+                for (int jj = 0; jj < n; ++jj) {
+                    const float4 vv = *reinterpret_cast<const float4*>(vr + jj * kVT);
+#pragma unroll
+                    for (int a = 0; a < RI; ++a)
+                        if (jj <= ty + 16 * a) yh[a].add(pr[16 * a * C + (jj ^ xq)], vv);
+                }
+            }
             // columns [16 b, 16 b + 16) reach rows from 16 b on
 #pragma unroll
             for (int b = 0; b < RI; ++b) {
-                if (16 * b >= n) break;
+                if (16 * b >= n || !all_finite) break;
 #pragma unroll 2
                 for (int jj = 16 * b; jj < 16 * b + 16; jj += 4) {
                     float4 vv[4];

@@ -84,7 +84,7 @@ POISON = [("k", float("nan")), ("v", float("nan")), ("v", float("inf")), ("k", -
           ("q", float("nan")), ("do", float("inf"))]
 
 
-@pytest.mark.parametrize("dtype,K,V", [(BF, 64, 64), (BF, 128, 72)])
+@pytest.mark.parametrize("dtype,K,V", [(BF, 64, 64), (BF, 128, 72), (F32, 64, 64), (F32, 16, 40), (BF, 33, 64), (F32, 160, 16)])
 @pytest.mark.parametrize("L", [9, 40, 300])
 @pytest.mark.parametrize("name,value", POISON)
 def test_a_token_that_is_not_finite_stays_out_of_earlier_ones(cuda_dev, name, value, L, dtype, K, V):
