@@ -427,7 +427,7 @@ typedef struct {
 /* Tensors [batch][rows][G][C / G] by their strides (m3_view: batch, token = row, head = group), so
  * that linear attention's output is read as it lies and slices of wider rows are taken too.
  * x; z: the gate, or data NULL for none; out may be x or z (the same view), and outputs must not
- * overlap themselves or other tensors otherwise. weight, bias: fp32 [C], or NULL for one / zero. */
+ * overlap themselves or other tensors otherwise (one that begins at another's address is refused). weight, bias: fp32 [C], or NULL for one / zero. */
 M3_API m3_status m3_group_norm_fwd(const m3_group_norm_dims* dims, const m3_view* x,
                                    const m3_view* z, const float* weight, const float* bias,
                                    const m3_view* out, void* stream);

@@ -653,6 +653,18 @@ m3_status check_shared(const m3_view* out, const m3_view* t, const m3_group_norm
     return err(M3_ERR_INVALID_ARG, allowed ? "%s is %s by other strides" : "%s is %s", name, other);
 }
 
+// The gradients of weight and bias, and any output, begin at no other tensor's address.
+struct Named {
+    const void* p;
+    const char* name;
+};
+template <int I>
+m3_status check_apart(const Named& out, const Named (&others)[I]) {
+    for (const Named& o : others)
+        if (out.p && out.p == o.p) return err(M3_ERR_INVALID_ARG, "%s is %s", out.name, o.name);
+    return M3_OK;
+}
+
 GnParams make_params(const m3_group_norm_dims* d, const m3_view* x, const m3_view* z, const float* w, const float* b) {
     GnParams p{};
     p.rows = static_cast<uint32_t>(d->batch * d->rows);
@@ -689,7 +701,8 @@ m3_status m3_group_norm_fwd(const m3_group_norm_dims* dims, const m3_view* x, co
         return st;
     if (!any) return M3_OK;
     if ((st = check_out(out, dims, "out")) != M3_OK || (st = check_shared(out, x, dims, true, "out", "x")) != M3_OK ||
-        (st = check_shared(out, z, dims, true, "out", "z")) != M3_OK)
+        (st = check_shared(out, z, dims, true, "out", "z")) != M3_OK ||
+        (st = check_apart({out->data, "out"}, {{weight, "weight"}, {bias, "bias"}})) != M3_OK)
         return st;
     GnParams p = make_params(dims, x, z, weight, bias);
     p.out = tensor(out);
@@ -736,6 +749,14 @@ m3_status m3_group_norm_bwd(const m3_group_norm_dims* dims, const m3_view* x, co
                  (st = check_shared(dz, x, dims, false, "dz", "x")) != M3_OK ||
                  (st = check_shared(dz, dout, dims, false, "dz", "dout")) != M3_OK ||
                  (st = check_shared(dz, dx, dims, false, "dz", "dx")) != M3_OK))
+        return st;
+    const void *pz = gate ? z->data : nullptr, *pdz = gate ? dz->data : nullptr;
+    const Named params[] = {{weight, "weight"}, {bias, "bias"}};
+    const Named all[] = {{x->data, "x"}, {pz, "z"}, {dout->data, "dout"}, {weight, "weight"}, {bias, "bias"},
+                         {dx->data, "dx"}, {pdz, "dz"}};
+    if ((st = check_apart({dx->data, "dx"}, params)) != M3_OK || (st = check_apart({pdz, "dz"}, params)) != M3_OK ||
+        (st = check_apart({dweight, "dweight"}, all)) != M3_OK || (st = check_apart({dbias, "dbias"}, all)) != M3_OK ||
+        (st = check_apart({dbias, "dbias"}, {{dweight, "dweight"}})) != M3_OK)
         return st;
     const size_t need = m3_group_norm_bwd_workspace_bytes(dims);
     if (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || ws_bytes < need))

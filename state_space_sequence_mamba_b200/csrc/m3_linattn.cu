@@ -117,16 +117,21 @@ m3_status check_inputs(const m3_linattn_dims* d, const m3_linattn_inputs* in, bo
 }
 
 // An output that begins where an input or another output does would be written while it is read (or
-// written twice); overlaps further in are the caller's to avoid.
-m3_status check_apart(const m3_linattn_inputs* in, const m3_view* d_o, const m3_view* const* outs,
-                      const char* const* names, int n) {
-    const void* ins[] = {in->q.data, in->k.data, in->v.data, d_o ? d_o->data : nullptr};
-    const char* in_names[] = {"q", "k", "v", "d_o"};
-    for (int i = 0; i < n; ++i) {
-        for (int a = 0; a < 4; ++a)
-            if (outs[i]->data == ins[a]) return err(M3_ERR_INVALID_ARG, "%s is %s", names[i], in_names[a]);
+// written twice); overlaps further in are the caller's to avoid. The last output is a state, which may be
+// the last input: the state that it follows.
+struct Named {
+    const void* p;
+    const char* name;
+};
+template <int I, int O>
+m3_status check_apart(const Named (&ins)[I], const Named (&outs)[O]) {
+    for (int i = 0; i < O; ++i) {
+        if (!outs[i].p) continue;
+        for (int a = 0; a < I; ++a)
+            if (outs[i].p == ins[a].p && !(i == O - 1 && a == I - 1))
+                return err(M3_ERR_INVALID_ARG, "%s is %s", outs[i].name, ins[a].name);
         for (int a = 0; a < i; ++a)
-            if (outs[i]->data == outs[a]->data) return err(M3_ERR_INVALID_ARG, "%s is %s", names[i], names[a]);
+            if (outs[i].p == outs[a].p) return err(M3_ERR_INVALID_ARG, "%s is %s", outs[i].name, outs[a].name);
     }
     return M3_OK;
 }
@@ -375,8 +380,10 @@ m3_status m3_linattn_fwd(const m3_linattn_dims* dims, const m3_linattn_inputs* i
     if ((st = check_workspace(workspace, ws_bytes, need)) != M3_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (!any) return pass_state(dims, init, final_state, s);
-    const char* const out_names[] = {"o"};
-    if ((st = check_apart(in, nullptr, &o, out_names, 1)) != M3_OK) return st;
+    const Named ins[] = {{in->q.data, "q"}, {in->k.data, "k"}, {in->v.data, "v"}, {in->log_decay, "log_decay"},
+                         {in->cu_seqlens, "cu_seqlens"}, {init, "init"}};
+    const Named outs[] = {{o->data, "o"}, {final_state, "final_state"}};
+    if ((st = check_apart(ins, outs)) != M3_OK) return st;
     const bool packed = in->cu_seqlens != nullptr;
     if (!packed && dims->seqlen <= kLinShort && (dims->seqlen == 1 || dims->vdim % 4 == 0) &&
         dims->nseq * dims->nheads <= kMaxStepUnits) {
@@ -442,8 +449,10 @@ m3_status m3_linattn_bwd(const m3_linattn_dims* dims, const m3_linattn_inputs* i
     char* seg = ws;
     ws += seg_bytes(dims, packed, bwd_tiles(dims), bwd_rows(dims));
     const m3_view* const outs[3] = {&grads->dq, &grads->dk, &grads->dv};
-    const char* const out_names[] = {"dq", "dk", "dv"};
-    if ((st = check_apart(in, d_o, outs, out_names, 3)) != M3_OK) return st;
+    const Named ins[] = {{in->q.data, "q"}, {in->k.data, "k"}, {in->v.data, "v"}, {d_o->data, "d_o"},
+                         {in->log_decay, "log_decay"}, {in->cu_seqlens, "cu_seqlens"}, {init, "init"}, {dfinal, "dfinal"}};
+    const Named named[] = {{grads->dq.data, "dq"}, {grads->dk.data, "dk"}, {grads->dv.data, "dv"}, {dinit, "dinit"}};
+    if ((st = check_apart(ins, named)) != M3_OK) return st;
     float* part[3];
     for (int i = 0; i < 3; ++i) {
         const size_t n = shared_bytes(dims, i, packed);
@@ -508,8 +517,10 @@ m3_status m3_linattn_step(const m3_linattn_dims* dims, const m3_linattn_inputs* 
         return st;
     if (dims->nseq * dims->nheads > kMaxStepUnits) return err(M3_ERR_UNSUPPORTED, "nseq * nheads exceeds the grid limit");
     if (!any) return M3_OK;
-    const char* const out_names[] = {"o"};
-    if ((st = check_apart(in, nullptr, &o, out_names, 1)) != M3_OK) return st;
+    const Named ins[] = {{in->q.data, "q"}, {in->k.data, "k"}, {in->v.data, "v"}, {in->log_decay, "log_decay"},
+                         {slots, "slots"}, {state_in, "state_in"}};
+    const Named outs[] = {{o->data, "o"}, {state_out, "state_out"}};
+    if ((st = check_apart(ins, outs)) != M3_OK) return st;
     const LinStep p = make_step(dims, in, state_in, state_out, nstates, slots, o);
     const cudaError_t e = launch_lin_step(p, dims->in_dtype == M3_BF16, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? M3_OK : cuda_err(e, "linear attention step launch");

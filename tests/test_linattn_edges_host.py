@@ -109,3 +109,75 @@ def test_restated_plan_is_the_librarys(lib, L, nseq, H):
     need = max(plan(L, nseq, H, *form)[1] if L > plan(L, nseq, H, *form)[0] else 0
                for form in ((148, 128, 2), (296, 64, 1)))
     assert lib.m3_linattn_workspace_bytes(ctypes.byref(d), 1) == need * H * 128 * 64 * 4 + state
+
+
+# ---------------------------------------------------------------- outputs at other tensors' addresses
+
+def far(n):
+    return 0x10000 + 65536 * n
+
+
+def test_linattn_refuses_outputs_on_states_and_parameters(lib):
+    """An output that begins where a state, the decays, the offsets, the slots or another output does is
+    refused; the states that may be updated in place are not (their calls get as far as the next refusal)."""
+    vw = lambda a: bd.View(a, 64, 8, 8)  # noqa: E731
+    d = bd.LinattnDims(2, 300, 4, 4, 2, 1, 32, 48, bd.M3_BF16, 1.0)
+    d1 = bd.LinattnDims(2, 1, 4, 4, 2, 1, 32, 48, bd.M3_BF16, 1.0)
+    q, k, v, decay, cu, init, final, o, do, dfinal, dinit, dq, dk, dv, slots = (far(n) for n in range(1, 16))
+    packed = bd.LinattnInputs(vw(q), vw(k), vw(v), decay, cu)
+    plain = bd.LinattnInputs(vw(q), vw(k), vw(v), decay, None)
+    need = lib.m3_linattn_workspace_bytes(ctypes.byref(d), 1)
+    bneed = lib.m3_linattn_bwd_workspace_bytes(ctypes.byref(d), 1)
+
+    def refused(rc, msg):
+        assert rc == bd.M3_ERR_INVALID_ARG and lib.m3_last_error() == msg, lib.m3_last_error()
+
+    def fwd(o=o, final=final, i=packed):
+        return lib.m3_linattn_fwd(ctypes.byref(d), ctypes.byref(i), init, final, ctypes.byref(vw(o)), far(40), need, None)
+    refused(fwd(o=decay), b"o is log_decay")
+    refused(fwd(o=cu), b"o is cu_seqlens")
+    refused(fwd(o=init), b"o is init")
+    for at, name in ((q, b"q"), (k, b"k"), (v, b"v"), (decay, b"log_decay"), (cu, b"cu_seqlens"), (o, b"o")):
+        refused(fwd(final=at), b"final_state is " + name)
+
+    def bwd(dq=dq, dk=dk, dv=dv, dinit=dinit):
+        g = bd.LinattnGrads(vw(dq), vw(dk), vw(dv))
+        return lib.m3_linattn_bwd(ctypes.byref(d), ctypes.byref(packed), init, ctypes.byref(vw(do)), dfinal, ctypes.byref(g),
+                                  dinit, far(40), bneed, None)
+    refused(bwd(dq=init), b"dq is init")
+    refused(bwd(dk=dfinal), b"dk is dfinal")
+    refused(bwd(dv=decay), b"dv is log_decay")
+    refused(bwd(dv=dinit), b"dinit is dv")
+    for at, name in ((q, b"q"), (v, b"v"), (do, b"d_o"), (decay, b"log_decay"), (init, b"init"), (dq, b"dq")):
+        refused(bwd(dinit=at), b"dinit is " + name)
+    refused(bwd(dq=q, dinit=dfinal), b"dq is q")
+
+    def step(o=o, out=final, sl=slots):
+        return lib.m3_linattn_step(ctypes.byref(d1), ctypes.byref(plain), init, out, 5, sl, ctypes.byref(vw(o)), None)
+    refused(step(o=init), b"o is state_in")
+    refused(step(o=slots), b"o is slots")
+    refused(step(out=o), b"state_out is o")
+    for at, name in ((q, b"q"), (k, b"k"), (decay, b"log_decay"), (slots, b"slots")):
+        refused(step(out=at), b"state_out is " + name)
+    refused(step(o=v, out=init), b"o is v")
+
+
+def test_group_norm_refuses_outputs_on_parameters(lib):
+    d = bd.GroupNormDims(1, 40, 64, 4, bd.M3_BF16, 1e-5, 3)
+    vw = lambda a: ctypes.byref(bd.View(a, 0, 64, 16))  # noqa: E731
+    x, z, w, b, dout, dx, dz, dw, db, out = (far(n) for n in range(1, 11))
+    need = lib.m3_group_norm_bwd_workspace_bytes(ctypes.byref(d))
+
+    def refused(rc, msg):
+        assert rc == bd.M3_ERR_INVALID_ARG and lib.m3_last_error() == msg, lib.m3_last_error()
+    for at, name in ((w, b"weight"), (b, b"bias")):
+        refused(lib.m3_group_norm_fwd(ctypes.byref(d), vw(x), vw(z), w, b, vw(at), None), b"out is " + name)
+
+    def bwd(dx=dx, dz=dz, dw=dw, db=db):
+        return lib.m3_group_norm_bwd(ctypes.byref(d), vw(x), vw(z), w, b, vw(dout), vw(dx), vw(dz), dw, db, far(40), need, None)
+    refused(bwd(dx=w), b"dx is weight")
+    refused(bwd(dz=b), b"dz is bias")
+    for at, name in ((x, b"x"), (z, b"z"), (dout, b"dout"), (w, b"weight"), (b, b"bias"), (dx, b"dx"), (dz, b"dz")):
+        refused(bwd(dw=at), b"dweight is " + name)
+        refused(bwd(db=at), b"dbias is " + name)
+    refused(bwd(db=dw), b"dbias is dweight")
