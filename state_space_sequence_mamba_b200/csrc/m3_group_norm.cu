@@ -172,10 +172,10 @@ struct Walk {
         const int grp = threadIdx.x / LPG;
         nry = (kThreads / LPG) / gx;
         ry = grp / gx;
-        group = blockIdx.y * gx + grp % gx;
+        group = blockIdx.x * gx + grp % gx;
         col_ok = group < p.G && ry < nry;
         c0 = group * p.D;
-        const uint32_t r0 = blockIdx.x * p.share_rows;
+        const uint32_t r0 = blockIdx.y * p.share_rows;
         r1 = min(r0 + p.share_rows, p.rows);
         row = r0 + ry;
         turns = (r1 - r0 + nry - 1) / nry;      // the same for every thread: the shuffles need whole warps
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_kernel(const GnParams p, int 
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 if (!k.in[i]) continue;
-                const int c = (k.group - blockIdx.y * gx) * p.D + k.col(i);
+                const int c = (k.group - blockIdx.x * gx) * p.D + k.col(i);
 #pragma unroll
                 for (int e = 0; e < N; ++e) {
                     float2 *tw = reinterpret_cast<float2*>(sw + c) + e, *tb = reinterpret_cast<float2*>(sb + c) + e;
@@ -328,8 +328,8 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_kernel(const GnParams p, int 
         }
         __syncthreads();
     }
-    const int col0 = blockIdx.y * width;
-    float* part = p.shares > 1 ? p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.C : nullptr;
+    const int col0 = blockIdx.x * width;
+    float* part = p.shares > 1 ? p.part + static_cast<int64_t>(blockIdx.y) * 2 * p.C : nullptr;
     float *ow = part ? part : p.dw, *ob = part ? part + p.C : p.db;     // a single share is the sum
     for (int c = threadIdx.x; c < width && col0 + c < p.C; c += kThreads) {
         if (ow) ow[col0 + c] = sw[c];
@@ -540,7 +540,7 @@ dim3 walk_grid(GnParams& p, int gx, int per, int per_sm, int least) {
     }
     p.share_rows = static_cast<uint32_t>((turns + n - 1) / n * nry);
     p.shares = static_cast<int>((p.rows + p.share_rows - 1) / p.share_rows);
-    return dim3(static_cast<unsigned>(p.shares), slabs);
+    return dim3(slabs, static_cast<unsigned>(p.shares));    // up to 2^16 slabs: more than gridDim.y holds
 }
 
 template <typename T>
