@@ -502,10 +502,10 @@ int vector_count(const GnParams& p) {
     return ok ? p.D / N : 0;
 }
 
-// Shares of the rows: as many as give every SM `per_sm` CTAs, at most one per (CTA's) row; of up to
-// four rows one (a second launch to add up shares costs more than the rows).
-int64_t share_count(int64_t rows, int64_t per_row_ctas, int per_sm) {
-    if (rows <= 4) return 1;
+// Shares of the rows: as many as give every SM `per_sm` CTAs, at most one per (CTA's) row. Where shares are
+// added up afterwards, one of up to four rows (a second launch costs more than the rows).
+int64_t share_count(int64_t rows, int64_t per_row_ctas, int per_sm, bool added) {
+    if (added && rows <= 4) return 1;
     const int64_t want = (per_sm * static_cast<int64_t>(device_sm_count()) + per_row_ctas - 1) / per_row_ctas;
     return rows < want ? (rows > 0 ? rows : 1) : want;
 }
@@ -518,7 +518,7 @@ constexpr int kFwdPerSm = 4, kBwdPerSm = 2, kBwdPerSmF32 = 4, kBwdPerSmPlain = 3
 template <typename T, int NV, bool kGate>
 constexpr int bwd_per_sm() { return NV > 1 ? kBwdPerSm : sizeof(T) == 4 ? kBwdPerSmF32 : kGate ? kBwdPerSm : kBwdPerSmPlain; }
 // the most shares any form of the backward takes
-int64_t max_shares(int64_t rows, bool bf16) { return share_count(rows, 1, bf16 ? kBwdPerSmPlain : kBwdPerSmF32); }
+int64_t max_shares(int64_t rows, bool bf16) { return share_count(rows, 1, bf16 ? kBwdPerSmPlain : kBwdPerSmF32, true); }
 
 // Groups side by side in a CTA: as many as its threads and 32 KB of column sums hold, the row's groups
 // spread evenly over the slabs.
@@ -529,13 +529,13 @@ int groups_per_cta(const GnParams& p, int per) {
 }
 
 // The walk's grid (per_sm CTAs an SM, or down to `least` where shares get short): fills in the shares.
-dim3 walk_grid(GnParams& p, int gx, int per, int per_sm, int least) {
+dim3 walk_grid(GnParams& p, int gx, int per, int per_sm, int least, bool added) {
     const int nry = per / gx;
     const unsigned slabs = static_cast<unsigned>((p.G + gx - 1) / gx);
     const int64_t turns = (p.rows + nry - 1) / nry;
-    int64_t n = share_count(turns, slabs, per_sm);
+    int64_t n = share_count(turns, slabs, per_sm, added);
     if (least < per_sm && n > turns / kBwdRowsF32) {
-        const int64_t few = share_count(turns, slabs, least);
+        const int64_t few = share_count(turns, slabs, least, added);
         n = few > turns / kBwdRowsF32 ? few : turns / kBwdRowsF32;
     }
     p.share_rows = static_cast<uint32_t>((turns + n - 1) / n * nry);
@@ -556,7 +556,7 @@ cudaError_t launch_fwd(GnParams p, uint32_t flags, cudaStream_t s) {
             using S = decltype(sh);
             constexpr int per = kThreads / S::LPG;
             const int gx = groups_per_cta(p, per);
-            const dim3 grid = walk_grid(p, gx, per, kFwdPerSm, kFwdPerSm);
+            const dim3 grid = walk_grid(p, gx, per, kFwdPerSm, kFwdPerSm, false);
             gn_fwd_kernel<T, S::LPG, S::NV, F::C, F::S, F::Z><<<grid, kThreads, 0, s>>>(p, gx);
             return 0;
         });
@@ -570,7 +570,7 @@ cudaError_t launch_bwd(GnParams p, uint32_t flags, cudaStream_t s) {
     with_flags(flags, p.z.p != nullptr, [&](auto f) {
         using F = decltype(f);
         if (vecs == 0) {
-            const int64_t n = share_count(p.rows, p.G, kBwdPerSm);
+            const int64_t n = share_count(p.rows, p.G, kBwdPerSm, true);
             p.share_rows = static_cast<uint32_t>((p.rows + n - 1) / n);
             p.shares = static_cast<int>((p.rows + p.share_rows - 1) / p.share_rows);
             gn_bwd_any_kernel<T, F::C, F::S, F::Z><<<static_cast<unsigned>(p.shares * static_cast<int64_t>(p.G)), kThreads, 0, s>>>(p);
@@ -580,7 +580,7 @@ cudaError_t launch_bwd(GnParams p, uint32_t flags, cudaStream_t s) {
             using S = decltype(sh);
             constexpr int per = kThreads / S::LPG;
             const int gx = groups_per_cta(p, per);
-            const dim3 grid = walk_grid(p, gx, per, bwd_per_sm<T, S::NV, F::Z>(), kBwdPerSm);
+            const dim3 grid = walk_grid(p, gx, per, bwd_per_sm<T, S::NV, F::Z>(), kBwdPerSm, true);
             const size_t smem = static_cast<size_t>(gx) * p.D * 2 * sizeof(float);
             gn_bwd_kernel<T, S::LPG, S::NV, F::C, F::S, F::Z><<<grid, kThreads, smem, s>>>(p, gx);
             return 0;

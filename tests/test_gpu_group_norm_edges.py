@@ -35,3 +35,10 @@ def test_widest_rows_of_the_smallest_groups(cuda_dev):
         dx, _, dw, db = ol.group_norm_gradients(d[:, part].cpu(), *args)
         assert err(r["dweight"][part], dw) <= bound(F32, T) and err(r["dbias"][part], db) <= bound(F32, T)
         assert err(r["dx"][:, part], dx) <= 4 * bound(F32, 4)
+@pytest.mark.parametrize("rows", [1, 2, 3, 4, 5, 6, 9])
+def test_few_rows(cuda_dev, rows):
+    for C, G in ((4096, 64), (96, 3)):
+        check(cuda_dev, rows, C, G, BF)
+        check(cuda_dev, rows, C, G, F32, affine=False, gate=False)
+
+
