@@ -509,21 +509,33 @@ int64_t share_count(int64_t rows, int64_t per_row_ctas, int per_sm, bool added) 
     const int64_t want = (per_sm * static_cast<int64_t>(device_sm_count()) + per_row_ctas - 1) / per_row_ctas;
     return rows < want ? (rows > 0 ? rows : 1) : want;
 }
-// One wave of CTAs: what the registers let an SM hold (62 and 96 a thread at groups of 64). More, shorter
-// shares were slower: 46.1 us with 16 CTAs an SM forward, 90.8 with 4 backward.
-// The backward without a gate holds 72 to 80: three (8192 x 4096 in groups of 64: 68.6 -> 58.7 us). In fp32
-// it holds 64: four (8192 x 4096 gated 147 -> 115 us, 2000 x 2048 22.4 -> 19.4), but
-// not for shares of fewer than six rows, whose sums then cost more (777 x 1920: 8.8 against 9.5 us).
-constexpr int kFwdPerSm = 4, kBwdPerSm = 2, kBwdPerSmF32 = 4, kBwdPerSmPlain = 3, kBwdRowsF32 = 6;
-template <typename T, int NV, bool kGate>
-constexpr int bwd_per_sm() { return NV > 1 ? kBwdPerSm : sizeof(T) == 4 ? kBwdPerSmF32 : kGate ? kBwdPerSm : kBwdPerSmPlain; }
+// One wave of CTAs: what the registers let an SM hold of this kernel, asked of the runtime once, up to the
+// most that pays (16 an SM forward: 46.1 us against 40.1 for 8192 x 4096 bf16 in groups of 64) and, in the
+// backward, that the workspace is laid out for. 8192 x 4096, gated / not, where the count was another:
+// four where one fits (bf16 forward, groups of 1024) 52.3 / 46.1 us against 43.0 / 37.0, two where one fits
+// (bf16 backward, groups of 512) 88.8 / 76.7 against 84.3 / 72.1, one where two fit (fp32 backward, groups of
+// 256, gated) 139 against 112. The exception is the gated bf16 backward of groups of 1024, which spills: two
+// where one fits 114, one 120.
+// Above kBwdPerSm CTAs an SM, shares of the backward keep kShareRows rows or more: shorter ones cost more in
+// their sums (two rows each against six: 777 x 1920 fp32 gated 12.3 against 11.9 us, bf16 ungated 12.3
+// against 11.1; 4000 x 512 fp32 gated 14.5 against 13.2, bf16 ungated 12.4 against 11.5; 300 x 1920 fp32 8.3 against 8.7).
+constexpr int kFwdPerSm = 4, kBwdPerSm = 2, kBwdMostF32 = 4, kBwdMostBf16 = 3, kShareRows = 6;
+template <typename T>
+constexpr int bwd_most() { return sizeof(T) == 4 ? kBwdMostF32 : kBwdMostBf16; }
+template <typename K>
+int resident_ctas(K* kernel, size_t smem, int most) {
+    int n = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, smem) != cudaSuccess || n < 1) n = 1;
+    return n < most ? n : most;
+}
 // the most shares any form of the backward takes
-int64_t max_shares(int64_t rows, bool bf16) { return share_count(rows, 1, bf16 ? kBwdPerSmPlain : kBwdPerSmF32, true); }
+int64_t max_shares(int64_t rows, bool bf16) { return share_count(rows, 1, bf16 ? kBwdMostBf16 : kBwdMostF32, true); }
 
-// Groups side by side in a CTA: as many as its threads and 32 KB of column sums hold, the row's groups
+constexpr int kMostSums = 32768;        // bytes of a CTA's column sums
+// Groups side by side in a CTA: as many as its threads and their column sums' room hold, the row's groups
 // spread evenly over the slabs.
 int groups_per_cta(const GnParams& p, int per) {
-    const int most = per < 4096 / p.D ? per : 4096 / p.D;
+    const int columns = kMostSums / (2 * sizeof(float)), most = per < columns / p.D ? per : columns / p.D;
     const int slabs = (p.G + most - 1) / most;
     return (p.G + slabs - 1) / slabs;
 }
@@ -534,9 +546,9 @@ dim3 walk_grid(GnParams& p, int gx, int per, int per_sm, int least, bool added) 
     const unsigned slabs = static_cast<unsigned>((p.G + gx - 1) / gx);
     const int64_t turns = (p.rows + nry - 1) / nry;
     int64_t n = share_count(turns, slabs, per_sm, added);
-    if (least < per_sm && n > turns / kBwdRowsF32) {
+    if (least < per_sm && n > turns / kShareRows) {
         const int64_t few = share_count(turns, slabs, least, added);
-        n = few > turns / kBwdRowsF32 ? few : turns / kBwdRowsF32;
+        n = few > turns / kShareRows ? few : turns / kShareRows;
     }
     p.share_rows = static_cast<uint32_t>((turns + n - 1) / n * nry);
     p.shares = static_cast<int>((p.rows + p.share_rows - 1) / p.share_rows);
@@ -556,8 +568,10 @@ cudaError_t launch_fwd(GnParams p, uint32_t flags, cudaStream_t s) {
             using S = decltype(sh);
             constexpr int per = kThreads / S::LPG;
             const int gx = groups_per_cta(p, per);
-            const dim3 grid = walk_grid(p, gx, per, kFwdPerSm, kFwdPerSm, false);
-            gn_fwd_kernel<T, S::LPG, S::NV, F::C, F::S, F::Z><<<grid, kThreads, 0, s>>>(p, gx);
+            auto* const kernel = gn_fwd_kernel<T, S::LPG, S::NV, F::C, F::S, F::Z>;
+            static const int per_sm = resident_ctas(kernel, 0, kFwdPerSm);
+            const dim3 grid = walk_grid(p, gx, per, per_sm, per_sm, false);
+            kernel<<<grid, kThreads, 0, s>>>(p, gx);
             return 0;
         });
     });
@@ -580,9 +594,11 @@ cudaError_t launch_bwd(GnParams p, uint32_t flags, cudaStream_t s) {
             using S = decltype(sh);
             constexpr int per = kThreads / S::LPG;
             const int gx = groups_per_cta(p, per);
-            const dim3 grid = walk_grid(p, gx, per, bwd_per_sm<T, S::NV, F::Z>(), kBwdPerSm, true);
+            auto* const kernel = gn_bwd_kernel<T, S::LPG, S::NV, F::C, F::S, F::Z>;
+            static const int per_sm = resident_ctas(kernel, kMostSums, bwd_most<T>());
+            const dim3 grid = walk_grid(p, gx, per, per_sm, kBwdPerSm, true);
             const size_t smem = static_cast<size_t>(gx) * p.D * 2 * sizeof(float);
-            gn_bwd_kernel<T, S::LPG, S::NV, F::C, F::S, F::Z><<<grid, kThreads, smem, s>>>(p, gx);
+            kernel<<<grid, kThreads, smem, s>>>(p, gx);
             return 0;
         });
     });
