@@ -26,9 +26,10 @@ LinPlan lin_plan(int64_t nseq, int64_t L, bool packed, int64_t per_x, const LinF
         for (int64_t n = 1; n <= kLinMaxSegs && (n == 1 || n * form.min_chunks <= chunks); ++n) {
             const int64_t seg = (chunks + n - 1) / n;
             if (n > 1 && (chunks + seg - 1) / seg != n) continue;   // the same cut as a smaller n
-            float cost = static_cast<float>((units * n + slots - 1) / slots) * (seg + form.setup);
+            const auto waves = [&](int64_t segs) { return std::ceil(static_cast<float>(units * segs) * form.unit / slots); };
+            float cost = waves(n) * (seg + form.setup);
             if (n > 1)
-                cost += static_cast<float>((units * (n - 1) + slots - 1) / slots) * (form.state_chunk * seg + form.setup) +
+                cost += waves(n - 1) * (form.state_chunk * seg + form.setup) +
                         form.predecessor * (n - 1);
             if (n == 1 || cost < 0.9f * least) {
                 best = n;
@@ -191,14 +192,26 @@ int fwd_tiles(const m3_linattn_dims* d) { return tiles_of(d->vdim); }
 int bwd_tiles(const m3_linattn_dims* d) { return 2 * tiles_of(d->kdim) + tiles_of(d->vdim); }
 int bwd_rows(const m3_linattn_dims* d) { return static_cast<int>(d->kdim > d->vdim ? d->kdim : d->vdim); }
 
+// The fp32 form's plan. A backward's units have states of V and of K rows: a chunk of 32 tokens of Dk costs
+// 32 (16 Dk + 16 64 + 2 Dk 64) products. (Counted as if all took as long as the longest: gradients of
+// 2048 tokens of 16 heads, K 256, V 64, bf16 1534 us, of 300 tokens of 4 heads 104; so 1132 and 62.)
+LinForm simt_form(const m3_linattn_dims* d, bool backward) {
+    if (!backward) return lin_simt_form(static_cast<int>(d->kdim), 1.f);
+    const auto cost = [](int64_t Dk) { return 144.f * Dk + 1024.f; };
+    const float k = cost(d->kdim), v = cost(d->vdim), most = k > v ? k : v;
+    const int tk = tiles_of(d->kdim), tv = tiles_of(d->vdim);
+    return lin_simt_form(bwd_rows(d), (2 * tk * v + tv * k) / ((2 * tk + tv) * most));
+}
+
 size_t seg_bytes(const m3_linattn_dims* d, bool packed, int rtiles, int rows, const LinForm& form) {
     if (d->nseq == 0 || d->seqlen == 0) return 0;
     const LinPlan pl = lin_plan(d->nseq, d->seqlen, packed, d->nheads * rtiles, form);
     return pl.cut ? static_cast<size_t>(pl.blocks_x) * d->nheads * rtiles * rows * kLinTile * 4 : 0;
 }
 // the larger of what the two forms take (which one runs depends on the tensors' alignment)
-size_t seg_bytes(const m3_linattn_dims* d, bool packed, int rtiles, int rows) {
-    const size_t a = seg_bytes(d, packed, rtiles, rows, lin_simt_form());
+size_t seg_bytes(const m3_linattn_dims* d, bool packed, bool backward) {
+    const int rtiles = backward ? bwd_tiles(d) : fwd_tiles(d), rows = backward ? bwd_rows(d) : static_cast<int>(d->kdim);
+    const size_t a = seg_bytes(d, packed, rtiles, rows, simt_form(d, backward));
     const size_t b = seg_bytes(d, packed, rtiles, rows < 128 ? 128 : rows, lin_tc_form());
     return ((a > b ? a : b) + 255) / 256 * 256;
 }
@@ -308,7 +321,7 @@ m3_status run_jobs(LinParams& p, const m3_linattn_dims* d, int state_rows, char*
     const bool bf16 = d->in_dtype == M3_BF16, packed = p.cu != nullptr;
     const bool tc = bf16 && lin_tc_supported(p);
     const LinPlan pl = lin_plan(d->nseq, d->seqlen, packed, d->nheads * p.rtiles,
-                                tc ? lin_tc_form() : lin_simt_form());
+                                tc ? lin_tc_form() : simt_form(d, p.njobs > 1));
     p.seg_len = pl.seg_len;
     p.nseg = pl.nseg;
     p.blocks_x = pl.blocks_x;
@@ -354,13 +367,13 @@ extern "C" {
 
 size_t m3_linattn_workspace_bytes(const m3_linattn_dims* dims, int packed) {
     if (check_dims(dims) != M3_OK) return 0;
-    const size_t n = seg_bytes(dims, packed != 0, fwd_tiles(dims), static_cast<int>(dims->kdim));
+    const size_t n = seg_bytes(dims, packed != 0, false);
     return n ? n + state_bytes(dims) : 0;
 }
 
 size_t m3_linattn_bwd_workspace_bytes(const m3_linattn_dims* dims, int packed) {
     if (check_dims(dims) != M3_OK) return 0;
-    size_t n = seg_bytes(dims, packed != 0, bwd_tiles(dims), bwd_rows(dims));
+    size_t n = seg_bytes(dims, packed != 0, true);
     for (int i = 0; i < 3; ++i) n += shared_bytes(dims, i, packed != 0);
     return n + state_bytes(dims);
 }
@@ -447,7 +460,7 @@ m3_status m3_linattn_bwd(const m3_linattn_dims* dims, const m3_linattn_inputs* i
                     v = tensor(dims, in->v, dims->vheads, packed), g = tensor(dims, *d_o, H, packed);
     char* ws = static_cast<char*>(workspace);
     char* seg = ws;
-    ws += seg_bytes(dims, packed, bwd_tiles(dims), bwd_rows(dims));
+    ws += seg_bytes(dims, packed, true);
     const m3_view* const outs[3] = {&grads->dq, &grads->dk, &grads->dv};
     const Named ins[] = {{in->q.data, "q"}, {in->k.data, "k"}, {in->v.data, "v"}, {d_o->data, "d_o"},
                          {in->log_decay, "log_decay"}, {in->cu_seqlens, "cu_seqlens"}, {init, "init"}, {dfinal, "dfinal"}};

@@ -69,11 +69,12 @@ struct LinForm {
     // costs in chunks of the full pass: a CTA's set-up, a chunk of the state-only pass, the sum of one
     // predecessor's end state
     float setup, state_chunk, predecessor;
+    float unit;                     // a unit's time on average, as a part of the longest one's
 };
 LinPlan lin_plan(int64_t nseq, int64_t L, bool packed, int64_t per_x, const LinForm& form);
 
-// fp32 on the CUDA cores, any dims and strides.
-LinForm lin_simt_form();
+// fp32 on the CUDA cores, any dims and strides. Dk: the largest of the jobs; unit: as in LinForm.
+LinForm lin_simt_form(int Dk, float unit);
 cudaError_t launch_lin_simt(const LinParams& p, bool bf16, bool cut, cudaStream_t s);
 // bf16 on the tensor cores: Dk <= 128, 16-byte aligned tensors.
 LinForm lin_tc_form();

@@ -822,7 +822,7 @@ bool mappable(const LinTensor& t, int64_t L) {
 }  // namespace
 
 // a shorter segment's set-up costs as much as its chunks
-LinForm lin_tc_form() { return LinForm{device_sm_count(), kC, 2, 2.f, 0.6f, 0.2f}; }
+LinForm lin_tc_form() { return LinForm{device_sm_count(), kC, 2, 2.f, 0.6f, 0.2f, 1.f}; }
 
 bool lin_tc_supported(const LinParams& p) {
     for (int i = 0; i < p.njobs; ++i) {

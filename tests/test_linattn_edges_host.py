@@ -102,13 +102,18 @@ def test_overlapping_offsets_beyond_the_reserve():
     assert check_blocks(cu, 4096, seg_len, blocks_x) == [11, 1, 1]
 
 
+# K, and the fp32 form's CTA slots, chunk and least chunks for it: two CTAs of its shared memory an SM, or one
+SIMT = [(128, (296, 64, 1)), (192, (296, 32, 1)), (256, (148, 32, 1))]
+
+
 @pytest.mark.parametrize("L,nseq,H", [(4096, 3, 4), (20000, 70, 2), (700, 2, 1)])
-def test_restated_plan_is_the_librarys(lib, L, nseq, H):
-    d = bd.LinattnDims(nseq, L, H, H, H, H, 128, 64, bd.M3_BF16, 1.0)
-    state = -(-nseq * H * 128 * 64 * 4 // 256) * 256
+@pytest.mark.parametrize("K,simt", SIMT)
+def test_restated_plan_is_the_librarys(lib, L, nseq, H, K, simt):
+    d = bd.LinattnDims(nseq, L, H, H, H, H, K, 64, bd.M3_BF16, 1.0)
+    state = -(-nseq * H * K * 64 * 4 // 256) * 256
     need = max(plan(L, nseq, H, *form)[1] if L > plan(L, nseq, H, *form)[0] else 0
-               for form in ((148, 128, 2), (296, 64, 1)))
-    assert lib.m3_linattn_workspace_bytes(ctypes.byref(d), 1) == need * H * 128 * 64 * 4 + state
+               for form in ((148, 128, 2), simt))
+    assert lib.m3_linattn_workspace_bytes(ctypes.byref(d), 1) == need * H * K * 64 * 4 + state
 
 
 # ---------------------------------------------------------------- outputs at other tensors' addresses
