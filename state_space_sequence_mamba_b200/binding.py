@@ -406,7 +406,9 @@ def scan_bwd(x, B, C, theta, dt, A, lam, dy, B_bias=None, C_bias=None, init: Sta
 # ---- linear attention with a decay for each head, and the grouped norm behind it ----
 # Marshalled in C++ (csrc/m3_torch.cpp), since these calls' kernels may be as short as the
 # marshalling. They run on the tensors' device and, unless a stream is given, on its current
-# stream; what they allocate is allocated on the stream they run on. Wrong shapes, types, strides
+# stream; what they allocate is allocated on the stream they run on. They are no autograd functions:
+# results are detached from inputs that require a gradient, whose gradients linattn_bwd and
+# group_norm_bwd compute; tensors given to be written count as changed. Wrong shapes, types, strides
 # and devices raise ValueError, the library's own refusals M3Error.
 
 _native = None

@@ -105,6 +105,12 @@ Tensor workspace(const Tensor* given, size_t need, const Tensor& ref) {
 void* data(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 size_t bytes(const Tensor& t) { return t.defined() ? t.nbytes() : 0; }
 
+// What a call wrote into a tensor of the caller's counts as a change of it, so that autograd refuses to use a
+// saved one unseen. (Inference tensors have no version.)
+void wrote(PyObject* given, const Tensor& t) {
+    if (THPVariable_Check(given) && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 void* stream_of(const Tensor& t) { return c10::cuda::getCurrentCUDAStream(t.device().index()).stream(); }
 
 PyObject* wrap(const Tensor& t) {
@@ -196,6 +202,8 @@ PyObject* linattn_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int rc = api.linattn_fwd(&d, &r.in, f32(init, "init", states), f32(fin.defined() ? &fin : nullptr, "final", states),
                                    &ov, data(ws), bytes(ws), stream_of(q));
     if (rc != M3_OK) return PyLong_FromLong(rc);
+    wrote(a[7], o);
+    wrote(a[6], fin);
     return tuple({o, fin});
     END_HANDLE_TH_ERRORS
 }
@@ -222,6 +230,8 @@ PyObject* linattn_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int rc = api.linattn_step(&d, &r.in, f32(&state, "state", states), f32(&out, "state_out", states), states[0],
                                     i32(slots, "slots", d.nseq), &ov, stream_of(q));
     if (rc != M3_OK) return PyLong_FromLong(rc);
+    wrote(a[8], o);
+    wrote(a[6] == Py_None ? a[5] : a[6], out);
     return tuple({o, out});
     END_HANDLE_TH_ERRORS
 }
@@ -260,6 +270,8 @@ PyObject* linattn_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int rc = api.linattn_bwd(&d, &r.in, f32(init, "init", states), &dv, f32(dfinal, "dfinal", states), &gc,
                                    f32(dinit.defined() ? &dinit : nullptr, "dinit", states), data(ws), bytes(ws), stream_of(q));
     if (rc != M3_OK) return PyLong_FromLong(rc);
+    for (int i = 0; i < 3; ++i) wrote(a[9 + i], g[i]);
+    wrote(a[12], dinit);
     return tuple({g[0], g[1], g[2], dinit});
     END_HANDLE_TH_ERRORS
 }
@@ -349,6 +361,7 @@ PyObject* group_norm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int rc = api.group_norm_fwd(&d, &v[0], &v[1], f32(w, "weight", {d.channels}), f32(b, "bias", {d.channels}), &v[2],
                                       stream_of(x));
     if (rc != M3_OK) return PyLong_FromLong(rc);
+    wrote(a[8], out);
     return wrap(out);
     END_HANDLE_TH_ERRORS
 }
@@ -377,6 +390,8 @@ PyObject* group_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                       static_cast<float*>(data(dw)), static_cast<float*>(data(db)), data(ws), bytes(ws),
                                       stream_of(x));
     if (rc != M3_OK) return PyLong_FromLong(rc);
+    wrote(a[9], dx);
+    if (z) wrote(a[10], dz);
     return tuple({dx, dz, dw, db});
     END_HANDLE_TH_ERRORS
 }

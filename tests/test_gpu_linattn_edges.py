@@ -149,3 +149,36 @@ def test_growing_decay_in_a_part_of_a_chunk(cuda_dev, L, grow, dtype):
         for n, r in zip(("dq", "dk", "dv"), ref):
             assert err(g[n][:, :, h], r[:, :, h]) <= tol(dtype, 64, 64) + more, n
         assert err(S[:, h], rS[:, h]) <= STATE_TOL + more and err(g["dinit"][:, h], ref[3][:, h]) <= STATE_TOL + more
+
+
+def test_outputs_given_by_the_caller_count_as_changed(cuda_dev):
+    """What a call writes into a tensor of the caller's raises its version, so that autograd refuses to use
+    a saved one that changed; tensors that are only read keep theirs."""
+    t, d, _, s = draw(cuda_dev, 2, 20, 2, 2, 2, 2, 16, 16, seed=54)
+    a = (d["q"], d["k"], d["v"], d["log_decay"])
+    o, S = torch.empty_like(d["do"]), torch.empty_like(d["init"])
+    grads, di = tuple(torch.empty_like(d[n]) for n in "qkv"), torch.empty_like(d["init"])
+    state, ot = d["init"].clone(), torch.empty_like(d["do"][:, 0])
+    x = d["do"].flatten(-2).contiguous()
+    out, dx, dz = (torch.empty_like(x) for _ in range(3))
+
+    def versions(*ts):
+        return [y._version for y in ts]
+    reads = (*a, d["do"], d["init"], d["dfinal"], x)
+    writes = (o, S, *grads, di, state, ot, out, dx, dz)
+    r0, w0 = versions(*reads), versions(*writes)
+    m3.linattn_fwd(*a, scale=s, init=d["init"], o=o, final=S)
+    m3.linattn_bwd(*a, d["do"], scale=s, init=d["init"], dfinal=d["dfinal"], grads=grads, want_init=di)
+    m3.linattn_step(*(y[:, 0] for y in a[:3]), a[3], state, scale=s, o=ot)
+    m3.group_norm_fwd(x, 2, z=x, out=out)
+    m3.group_norm_bwd(x, x, 2, z=x, dx=dx, dz=dz)
+    assert versions(*reads) == r0 and versions(*writes) == [v + 1 for v in w0]
+    p = torch.ones_like(x, requires_grad=True)
+    y = (p * x).sum()
+    m3.group_norm_fwd(x, 2, out=x)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    with torch.inference_mode():
+        w = torch.ones(3, 32, device=cuda_dev)
+    assert m3.group_norm_fwd(x.float(), 2)._version == 0
+    m3.group_norm_fwd(w.clone(), 2, out=w)      # (no version to raise)
