@@ -419,10 +419,13 @@ def _ext():
     global _native
     if _native is None:
         lib = load_library()
+        from .build import TORCH_EXT, ext_target
         try:
             from . import _m3torch
+            if _m3torch.built_for != ext_target():
+                raise ImportError(f"built for {_m3torch.built_for}")
         except ImportError as e:
-            raise ImportError(f"{os.path.join(_HERE, '_m3torch.so')} does not load: build it with "
+            raise ImportError(f"{TORCH_EXT} does not load under {ext_target()}: build it with "
                               "`python -m state_space_sequence_mamba_b200.build`") from e
         _m3torch.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
             "m3_linattn_workspace_bytes", "m3_linattn_bwd_workspace_bytes", "m3_linattn_fwd",

@@ -419,4 +419,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_m3torch", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__m3torch(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__m3torch(void) {
+    PyObject* m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "built_for", M3_BUILT_FOR) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}

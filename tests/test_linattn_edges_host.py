@@ -186,3 +186,33 @@ def test_group_norm_refuses_outputs_on_parameters(lib):
         refused(bwd(dw=at), b"dweight is " + name)
         refused(bwd(db=at), b"dbias is " + name)
     refused(bwd(db=dw), b"dbias is dweight")
+
+
+# ---------------------------------------------------------------- the torch binding's build
+
+def test_torch_binding_is_built_again_for_another_torch(lib, monkeypatch):
+    from state_space_sequence_mamba_b200 import build as b
+    assert not b._ext_stale()
+    monkeypatch.setattr(b, "ext_target", lambda: "torch 1.2.3, Python 3.0.0")
+    assert b._ext_stale()
+    monkeypatch.setattr(bd, "_native", None)
+    with pytest.raises(ImportError, match="built for|does not load under torch 1.2.3"):
+        bd._ext()
+
+
+@pytest.mark.parametrize("error", [FileNotFoundError("g++"), ImportError("torch")])
+def test_library_is_built_without_the_torch_binding(monkeypatch, error):
+    """No compiler or headers for the binding: the library is still built, and the error says so; without
+    the binding nothing of it is asked for."""
+    from state_space_sequence_mamba_b200 import build as b
+    done = []
+
+    def missing(*_):
+        raise error
+    monkeypatch.setattr(b, "_ext_stale", lambda: True)
+    monkeypatch.setattr(b, "_start_ext", missing)
+    monkeypatch.setattr(b, "_build_lib", lambda *a: done.append(a))
+    with pytest.raises(RuntimeError, match="libm3.so is built"):
+        b.build()
+    assert len(done) == 1
+    assert b.build(ext=False) == b.LIB and len(done) == 2
