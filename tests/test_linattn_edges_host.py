@@ -216,3 +216,11 @@ def test_library_is_built_without_the_torch_binding(monkeypatch, error):
         b.build()
     assert len(done) == 1
     assert b.build(ext=False) == b.LIB and len(done) == 2
+
+
+def test_package_exports():
+    """Every Python entry point of the operators, the check of a timeout among them, is the package's too."""
+    import state_space_sequence_mamba_b200 as m3
+    for name in ("linattn_fwd", "linattn_step", "linattn_bwd", "linattn_check", "linattn_workspace_bytes",
+                 "group_norm_fwd", "group_norm_bwd"):
+        assert getattr(m3, name) is getattr(bd, name)
