@@ -58,6 +58,50 @@ LinPlan lin_plan(int64_t nseq, int64_t L, bool packed, int64_t per_x, const LinF
 
 namespace {
 
+// One CTA walks down the sequences, 1024 at a time: starts[i + 1] = i + 1 + the segments beyond their first of
+// the sequences up to i, of those before the reserve runs out.
+constexpr int kStartThreads = 1024;
+__global__ void __launch_bounds__(kStartThreads) lin_starts_kernel(const LinParams p, int32_t* starts) {
+    __shared__ int s_sum[32];
+    __shared__ int s_cap;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int reserve = static_cast<int>(p.blocks_x - p.nseq);      // at most kLinMaxSegs
+    int asked = 0, cap = 0;         // what the sequences before ask for, and what of it fits
+    if (tid == 0) {
+        starts[0] = 0;
+        s_cap = 0;
+    }
+    for (int base = 0; base < p.nseq; base += kStartThreads) {
+        const int i = base + tid;
+        // (more than the reserve is as good as one more than it: the sums stay small)
+        int incl = i < p.nseq ? min(lin_span(p, i).more, reserve + 1) : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
+        }
+        if (lane == 31) s_sum[warp] = incl;
+        __syncthreads();
+        if (warp == 0) {
+            int sum = s_sum[lane];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += up;
+            }
+            s_sum[lane] = sum;
+        }
+        __syncthreads();
+        incl += asked + (warp > 0 ? s_sum[warp - 1] : 0);
+        if (incl <= reserve) atomicMax(&s_cap, incl);       // ascends: the last that fits
+        asked = min(asked + s_sum[31], reserve + 1);
+        __syncthreads();
+        cap = s_cap;
+        if (i < p.nseq) starts[i + 1] = i + 1 + min(incl, cap);
+        __syncthreads();
+    }
+}
+
 m3_status err(m3_status st, const char* fmt, ...) {
     char msg[256];
     va_list ap;
@@ -209,6 +253,11 @@ size_t seg_bytes(const m3_linattn_dims* d, bool packed, int rtiles, int rows, co
     return pl.cut ? static_cast<size_t>(pl.blocks_x) * d->nheads * rtiles * rows * kLinTile * 4 : 0;
 }
 // the larger of what the two forms take (which one runs depends on the tensors' alignment)
+size_t table_bytes(const m3_linattn_dims* d, bool packed) {
+    if (!packed || d->nseq <= kLinScanned || d->seqlen == 0) return 0;
+    return ((static_cast<size_t>(d->nseq) + 1) * 4 + 255) / 256 * 256;
+}
+
 size_t seg_bytes(const m3_linattn_dims* d, bool packed, bool backward) {
     const int rtiles = backward ? bwd_tiles(d) : fwd_tiles(d), rows = backward ? bwd_rows(d) : static_cast<int>(d->kdim);
     const size_t a = seg_bytes(d, packed, rtiles, rows, simt_form(d, backward));
@@ -316,8 +365,8 @@ cudaError_t fold_heads(const m3_linattn_dims* d, float* const (&part)[3], const 
     return cudaGetLastError();
 }
 
-// Plans and launches the jobs of p in the form that takes them.
-m3_status run_jobs(LinParams& p, const m3_linattn_dims* d, int state_rows, char* ws, cudaStream_t s) {
+// Plans and launches the jobs of p in the form that takes them. table: table_bytes of the workspace.
+m3_status run_jobs(LinParams& p, const m3_linattn_dims* d, int state_rows, char* ws, char* table, cudaStream_t s) {
     const bool bf16 = d->in_dtype == M3_BF16, packed = p.cu != nullptr;
     const bool tc = bf16 && lin_tc_supported(p);
     const LinPlan pl = lin_plan(d->nseq, d->seqlen, packed, d->nheads * p.rtiles,
@@ -329,7 +378,14 @@ m3_status run_jobs(LinParams& p, const m3_linattn_dims* d, int state_rows, char*
     p.seg_rows = tc && state_rows < 128 ? 128 : state_rows;
     if (p.blocks_x > kMaxGrid / (d->nheads * p.rtiles))
         return err(M3_ERR_UNSUPPORTED, "sequences * heads * column tiles exceed the grid limit");
-    const cudaError_t e = tc ? launch_lin_tc(p, pl.cut, s) : launch_lin_simt(p, bf16, pl.cut, s);
+    cudaError_t e = cudaSuccess;
+    if (table_bytes(d, packed) > 0) {
+        int32_t* starts = reinterpret_cast<int32_t*>(table);
+        lin_starts_kernel<<<1, kStartThreads, 0, s>>>(p, starts);
+        if ((e = cudaGetLastError()) != cudaSuccess) return cuda_err(e, "linear attention table launch");
+        p.starts = starts;
+    }
+    e = tc ? launch_lin_tc(p, pl.cut, s) : launch_lin_simt(p, bf16, pl.cut, s);
     return e == cudaSuccess ? M3_OK : cuda_err(e, "linear attention launch");
 }
 
@@ -368,14 +424,14 @@ extern "C" {
 size_t m3_linattn_workspace_bytes(const m3_linattn_dims* dims, int packed) {
     if (check_dims(dims) != M3_OK) return 0;
     const size_t n = seg_bytes(dims, packed != 0, false);
-    return n ? n + state_bytes(dims) : 0;
+    return (n ? n + state_bytes(dims) : 0) + table_bytes(dims, packed != 0);
 }
 
 size_t m3_linattn_bwd_workspace_bytes(const m3_linattn_dims* dims, int packed) {
     if (check_dims(dims) != M3_OK) return 0;
     size_t n = seg_bytes(dims, packed != 0, true);
     for (int i = 0; i < 3; ++i) n += shared_bytes(dims, i, packed != 0);
-    return n + state_bytes(dims);
+    return n + state_bytes(dims) + table_bytes(dims, packed != 0);
 }
 
 m3_status m3_linattn_fwd(const m3_linattn_dims* dims, const m3_linattn_inputs* in, const float* init,
@@ -424,12 +480,14 @@ m3_status m3_linattn_fwd(const m3_linattn_dims* dims, const m3_linattn_inputs* i
     j.final_state = final_state;
     p.njobs = 1;
     p.rtiles = j.tiles;
-    if (init && init == final_state && need > 0) {  // cut: later segments read it while the last writes
-        char* copy = static_cast<char*>(workspace) + need - state_bytes(dims);
+    const size_t seg = seg_bytes(dims, packed, false);
+    char* const ws = static_cast<char*>(workspace);
+    if (init && init == final_state && seg > 0) {   // cut: later segments read it while the last writes
+        char* copy = ws + seg;
         if ((st = keep_state(dims, init, copy, s)) != M3_OK) return st;
         j.init = reinterpret_cast<const float*>(copy);
     }
-    return run_jobs(p, dims, j.Dk, static_cast<char*>(workspace), s);
+    return run_jobs(p, dims, j.Dk, ws, ws + need - table_bytes(dims, packed), s);
 }
 
 m3_status m3_linattn_bwd(const m3_linattn_dims* dims, const m3_linattn_inputs* in, const float* init,
@@ -505,7 +563,8 @@ m3_status m3_linattn_bwd(const m3_linattn_dims* dims, const m3_linattn_inputs* i
         if ((st = keep_state(dims, dfinal, ws, s)) != M3_OK) return st;
         p.job[1].init = p.job[2].init = reinterpret_cast<const float*>(ws);
     }
-    if ((st = run_jobs(p, dims, bwd_rows(dims), seg, s)) != M3_OK) return st;
+    char* const table = static_cast<char*>(workspace) + need - table_bytes(dims, packed);
+    if ((st = run_jobs(p, dims, bwd_rows(dims), seg, table, s)) != M3_OK) return st;
     const cudaError_t e = fold_heads(dims, part, outs, in->cu_seqlens, s);
     if (e != cudaSuccess) return cuda_err(e, "gradient sum launch");
     return M3_OK;

@@ -46,6 +46,7 @@ struct LinJob {
 struct LinParams {
     const float* log_decay;
     const int32_t* cu;              // packed sequences, or null
+    const int32_t* starts;          // many packed sequences: [nseq + 1], the first block of each, or null
     int nseq, H;
     int64_t L;                      // tokens of each sequence, or rows in all
     int seg_len;                    // tokens of a segment (a multiple of the form's chunk)
@@ -72,6 +73,11 @@ struct LinForm {
     float unit;                     // a unit's time on average, as a part of the longest one's
 };
 LinPlan lin_plan(int64_t nseq, int64_t L, bool packed, int64_t per_x, const LinForm& form);
+
+// Packed sequences up to which each CTA counts blocks itself, which grows with their square; for more a launch
+// before it makes the table of first blocks. (Sequences of 4 tokens, 4 heads, counted against table: 64 26 us
+// against 31, 192 70 both, 256 91 against 82, 4096 7544 against 1089, 16 384 123 ms against 4.5.)
+constexpr int kLinScanned = 256;
 
 // fp32 on the CUDA cores, any dims and strides. Dk: the largest of the jobs; unit: as in LinForm.
 LinForm lin_simt_form(int Dk, float unit);
@@ -121,35 +127,35 @@ struct LinWhere {
     bool valid;
 };
 
+// A packed sequence's rows, and the segments beyond its first that it asks for.
+struct LinSpan {
+    int s, e, more;
+};
+__device__ __forceinline__ LinSpan lin_span(const LinParams& p, int i) {
+    const int L = static_cast<int>(p.L);
+    LinSpan r;
+    r.s = min(max(p.cu[i], 0), L);
+    r.e = min(max(p.cu[i + 1], r.s), L);
+    r.more = max((r.e - r.s + p.seg_len - 1) / p.seg_len, 1) - 1;
+    return r;
+}
+
 // Sequence and segment of block x. Packed: the running count of segments, 32 sequences at a
-// time (all lanes of a warp call this together). The plan reserves a block for each sequence and
-// L / seg_len more, which is all that ascending offsets can ask for. Descending ones may overlap and
+// time (all lanes of a warp call this together), or by halves in the table. The plan reserves a block for each
+// sequence and L / seg_len more, which is all that ascending offsets can ask for. Descending ones may overlap and
 // ask for any number: the sequence that would go beyond the reserve, and every long one behind it, is
 // one segment, however long. So no segment has an index at or above blocks_x, and every sequence runs.
-__device__ __forceinline__ LinWhere lin_locate(const LinParams& p, unsigned x) {
-    LinWhere w{};
-    if (!p.cu) {
-        const unsigned nseg = static_cast<unsigned>(p.nseg), seq = x / nseg;
-        w.seq = w.batch = static_cast<int>(seq);
-        w.seg = static_cast<int>(x - seq * nseg);
-        w.nseg = p.nseg;
-        w.len = static_cast<int>(p.L);
-        w.valid = w.seq < p.nseq;
-        return w;
-    }
-    const int lane = threadIdx.x & 31, L = static_cast<int>(p.L);
+// This is that count in full:
+__device__ __forceinline__ void lin_locate_any(const LinParams& p, unsigned x, LinWhere& w) {
+    const int lane = threadIdx.x & 31;
     const int64_t reserve = p.blocks_x - p.nseq;
     int64_t before = 0, asked = 0;      // blocks of the sequences before; segments beyond the first they ask for
 #pragma unroll 1
     for (int base = 0; base < p.nseq; base += 32) {
         const int i = base + lane, here = min(p.nseq - base, 32);
-        int s = 0, e = 0, more = 0;
-        if (i < p.nseq) {
-            s = min(max(p.cu[i], 0), L);
-            e = min(max(p.cu[i + 1], s), L);
-            more = max((e - s + p.seg_len - 1) / p.seg_len, 1) - 1;
-        }
-        int incl = more;        // at most 32 * 2^30 / 64
+        LinSpan r{};
+        if (i < p.nseq) r = lin_span(p, i);
+        int incl = r.more;      // at most 32 * 2^30 / 64
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int up = __shfl_up_sync(0xffffffffu, incl, o);
@@ -161,17 +167,82 @@ __device__ __forceinline__ LinWhere lin_locate(const LinParams& p, unsigned x) {
         const int upto = min(lane + 1, here) + min(incl, cap);      // blocks up to and with this lane's sequence
         const unsigned hit = __ballot_sync(0xffffffffu, before + upto > static_cast<int64_t>(x));
         if (hit) {
-            const int src = __ffs(hit) - 1, n = (fits >> lane & 1) ? more + 1 : 1;
+            const int src = __ffs(hit) - 1, n = (fits >> lane & 1) ? r.more + 1 : 1;
             w.seq = base + src;
             w.seg = static_cast<int>(x - before) - __shfl_sync(0xffffffffu, upto - n, src);
             w.nseg = __shfl_sync(0xffffffffu, n, src);
-            w.row0 = __shfl_sync(0xffffffffu, s, src);
-            w.len = __shfl_sync(0xffffffffu, e - s, src);
+            w.row0 = __shfl_sync(0xffffffffu, r.s, src);
+            w.len = __shfl_sync(0xffffffffu, r.e - r.s, src);
             w.valid = true;
-            return w;
+            return;
         }
         before += __shfl_sync(0xffffffffu, upto, 31);
         asked += __shfl_sync(0xffffffffu, incl, 31);
+    }
+}
+// and this the one without the bound, which finds the same for a sequence whose segments are within the reserve
+// (those before it then are too).
+__device__ __forceinline__ LinWhere lin_locate(const LinParams& p, unsigned x) {
+    LinWhere w{};
+    if (!p.cu) {
+        const unsigned nseg = static_cast<unsigned>(p.nseg), seq = x / nseg;
+        w.seq = w.batch = static_cast<int>(seq);
+        w.seg = static_cast<int>(x - seq * nseg);
+        w.nseg = p.nseg;
+        w.len = static_cast<int>(p.L);
+        w.valid = w.seq < p.nseq;
+        return w;
+    }
+    if (p.starts) {
+        const int at = static_cast<int>(x);         // (the grid has fewer than 2^31 blocks)
+        if (at >= __ldg(p.starts + p.nseq)) return w;
+        int lo = 0, hi = p.nseq;                    // starts[lo] <= at < starts[hi]
+        while (hi - lo > 1) {
+            const int m = (lo + hi) >> 1;
+            if (__ldg(p.starts + m) <= at) lo = m;
+            else hi = m;
+        }
+        const LinSpan r = lin_span(p, lo);
+        w.seq = lo;
+        w.seg = at - __ldg(p.starts + lo);
+        w.nseg = __ldg(p.starts + lo + 1) - __ldg(p.starts + lo);
+        w.row0 = r.s;
+        w.len = r.e - r.s;
+        w.valid = true;
+        return w;
+    }
+    const int lane = threadIdx.x & 31;
+    int64_t before = 0;
+#pragma unroll 1
+    for (int base = 0; base < p.nseq; base += 32) {
+        const int i = base + lane;
+        LinSpan r{};
+        if (i < p.nseq) r = lin_span(p, i);
+        const int n = i < p.nseq ? r.more + 1 : 0;
+        int incl = n;           // at most 32 (2^30 / 64 + 1)
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, before + incl > static_cast<int64_t>(x));
+        if (hit) {
+            const int src = __ffs(hit) - 1;
+            w.seq = base + src;
+            w.nseg = __shfl_sync(0xffffffffu, n, src);
+            const int64_t end = before + __shfl_sync(0xffffffffu, incl, src);
+            if (end - w.seq - 1 > p.blocks_x - p.nseq) {
+                LinWhere any{};
+                lin_locate_any(p, x, any);
+                return any;
+            }
+            w.seg = static_cast<int>(x - (end - w.nseg));
+            w.row0 = __shfl_sync(0xffffffffu, r.s, src);
+            w.len = __shfl_sync(0xffffffffu, r.e - r.s, src);
+            w.valid = true;
+            return w;
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
     }
     return w;
 }

@@ -182,3 +182,48 @@ def test_outputs_given_by_the_caller_count_as_changed(cuda_dev):
         w = torch.ones(3, 32, device=cuda_dev)
     assert m3.group_norm_fwd(x.float(), 2)._version == 0
     m3.group_norm_fwd(w.clone(), 2, out=w)      # (no version to raise)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("lens", [[1, 0, 3, 2] * 130, [2000] + [1, 0, 3] * 120 + [900, 5], [3] * 255, [3] * 256, [3] * 257,
+                                  [0] * 1030 + [700], [0] * 300])
+def test_many_packed_sequences(cuda_dev, lens, dtype):
+    """Below and above the number whose blocks are found in a table, long (cut) ones among them."""
+    t, d, cu, s = draw(cuda_dev, 1, 0, 2, 2, 2, 1, 32, 40, dtype=dtype, lens=lens, extra=2, seed=61)
+    total = sum(lens)
+    t = {n: x[:, :total] if n in ("q", "k", "v", "do") else x for n, x in t.items()}
+    a = (d["q"], d["k"], d["v"], d["log_decay"])
+    o, S = m3.linattn_fwd(*a, scale=s, init=d["init"], cu_seqlens=cu)
+    in_place = d["init"].clone()
+    o2, _ = m3.linattn_fwd(*a, scale=s, init=in_place, final=in_place, cu_seqlens=cu)
+    g = m3.linattn_bwd(*a, d["do"], scale=s, init=d["init"], dfinal=d["dfinal"], cu_seqlens=cu)
+    torch.cuda.synchronize()
+    m3.linattn_check()
+    assert torch.equal(o, o2) and torch.equal(S, in_place)
+    ro, rS = ol.forward(t["q"], t["k"], t["v"], t["log_decay"], s, t["init"], lens)
+    ref = ol.gradients(t["q"], t["k"], t["v"], t["log_decay"], t["do"], s, t["init"], t["dfinal"], lens)
+    assert err(o[:, :total], ro) <= tol(dtype, 32, 40) and err(S, rS) <= STATE_TOL
+    for n, r in zip(("dq", "dk", "dv"), ref):
+        assert err(g[n][:, :total], r) <= tol(dtype, 32, 40) and bool((g[n][:, total:] == 0).all()), n
+    assert err(g["dinit"], ref[3]) <= STATE_TOL and bool((o[:, total:] == 0).all())
+
+
+def test_overlapping_offsets_among_many(cuda_dev):
+    """The bound on the segments of sequences that overlap, from the table."""
+    L, H = 4096, 4
+    t, d, _, s = draw(cuda_dev, 1, L, H, H, H, H, 64, 64, init=False, seed=62)
+    cu = [0, 4096, 0, 4096] + [4096, 4000] * 400
+    a = (d["q"], d["k"], d["v"], d["log_decay"])
+    _, S = m3.linattn_fwd(*a, scale=s, cu_seqlens=torch.tensor(cu, dtype=torch.int32, device=cuda_dev))
+    g = m3.linattn_bwd(*a, d["do"], scale=s, cu_seqlens=torch.tensor(cu, dtype=torch.int32, device=cuda_dev))
+    torch.cuda.synchronize()
+    m3.linattn_check()
+    for lo, at in ((0, (0, 2)), (4000, (4, 6, 802))):
+        p = [t[n][:, lo:] for n in ("q", "k", "v", "do")]
+        _, rS = ol.forward(*p[:3], t["log_decay"], s)
+        ref = ol.gradients(*p[:3], t["log_decay"], p[3], s)
+        for i in at:
+            if cu[i] == lo and cu[i + 1] == L:
+                assert err(S[i:i + 1], rS) <= STATE_TOL and err(g["dinit"][i:i + 1], ref[3]) <= STATE_TOL
+    empty = [i for i in range(len(cu) - 1) if cu[i + 1] <= cu[i]]
+    assert bool((S[empty] == 0).all()) and len(empty) > 300

@@ -224,3 +224,49 @@ def test_package_exports():
     for name in ("linattn_fwd", "linattn_step", "linattn_bwd", "linattn_check", "linattn_workspace_bytes",
                  "group_norm_fwd", "group_norm_bwd"):
         assert getattr(m3, name) is getattr(bd, name)
+
+
+# ---------------------------------------------------------------- many packed sequences
+
+def table(cu, L, seg_len, blocks_x, width=1024):
+    """The table of first blocks as its kernel makes it, `width` sequences at a time."""
+    nseq, reserve = len(cu) - 1, blocks_x - (len(cu) - 1)
+    more = [min(n - 1, reserve + 1) for n in asked(cu, L, seg_len)]
+    starts, claimed, cap = [0], 0, 0
+    for base in range(0, nseq, width):
+        part, incl = more[base:base + width], []
+        for m in part:
+            incl.append((incl[-1] if incl else claimed) + m)
+        cap = max([cap] + [v for v in incl if v <= reserve])
+        starts += [base + i + 1 + min(v, cap) for i, v in enumerate(incl)]
+        claimed = min(incl[-1], reserve + 1)
+    return starts
+
+
+def test_table_of_first_blocks_is_the_count():
+    """By halves in the table, a block finds what the count over all sequences finds."""
+    rng = random.Random(9)
+    for case in range(60):
+        nseq, L = rng.choice((1, 5, 40, 300)), rng.choice((1, 100, 700, 4096, 20000))
+        seg_len, blocks_x = plan(L, nseq, rng.choice((1, 4, 12, 64)), *rng.choice(((148, 128, 2), (296, 64, 1))))
+        assert blocks_x - nseq <= 64
+        cu = [rng.randint(-L // 4, L + L // 4) for _ in range(nseq + 1)]
+        if case % 3 == 0:
+            cu.sort()
+        starts = table(cu, L, seg_len, blocks_x, rng.choice((8, 64, 1024)))
+        for x in range(blocks_x + 2):
+            got = None
+            if x < starts[nseq]:
+                i = max(j for j in range(nseq) if starts[j] <= x)
+                got = i, x - starts[i], starts[i + 1] - starts[i]
+            assert got == locate(cu, L, seg_len, blocks_x, x)
+
+
+def test_many_sequences_need_the_tables_room(lib):
+    """Above 256 packed sequences the workspace holds the table too, cut or not."""
+    def need(n, f=lib.m3_linattn_workspace_bytes):
+        d = bd.LinattnDims(n, 1000, 4, 4, 4, 4, 64, 64, bd.M3_BF16, 1.0)
+        return f(ctypes.byref(d), 1)
+    for f in (lib.m3_linattn_workspace_bytes, lib.m3_linattn_bwd_workspace_bytes):
+        grow = [need(n, f) - need(n - 1, f) for n in (256, 258)]
+        assert need(257, f) - need(256, f) == grow[0] + 1280 and grow[0] >= 0 and grow[1] >= 0
