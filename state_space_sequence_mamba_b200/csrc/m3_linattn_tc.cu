@@ -192,18 +192,13 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
                  : "memory");
 }
 
-// 8 and 1 columns of 32 lanes (thread i of the warp gets lane base + i)
+// 32 lanes x 32 bits, 8 consecutive columns: thread i of the warp gets lane (base + i).
 __device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, float (&v)[8]) {
     uint32_t r[8];
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]) : "r"(taddr));
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ uint32_t tmem_ld_x1(uint32_t taddr) {
-    uint32_t r;
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
-    return r;
 }
 
 // The outputs of a warp's 32 rows from P (lp) and O1 (lo) in TMEM and v in global memory, row t over the
@@ -216,19 +211,24 @@ __device__ __noinline__ void sum_rows(const LinJob& j, const __nv_bfloat16* v, u
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] = 0.f;
 #pragma unroll 1
-        for (int s = 0; s < n; ++s) {
-            const uint32_t p2 = tmem_ld_x1(lp + (s >> 1));
+        for (int s0 = 0; s0 < n; s0 += 32) {
+            float p[16];        // 32 tokens' scores
+            tmem_ld_32x32b_x16(lp + (s0 >> 1), p);
             tmem_wait_ld();
-            const uint4 raw = *reinterpret_cast<const uint4*>(v + s * j.v.token + c);
-            // (selects, not a branch: the loads from TMEM need the whole warp)
-            const uint32_t on = (j.reverse ? s >= t : s <= t) ? 0xFFFFFFFFu : 0u;
-            const float pr = __uint_as_float((s & 1 ? p2 & 0xFFFF0000u : p2 << 16) & on);
-            const uint32_t u[4] = {raw.x & on, raw.y & on, raw.z & on, raw.w & on};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = unpack2(u[i]);
-                o[2 * i] = fmaf(pr, f.x, o[2 * i]);
-                o[2 * i + 1] = fmaf(pr, f.y, o[2 * i + 1]);
+            for (int k = 0; k < 32; ++k) {
+                const int s = s0 + k;
+                const uint4 raw = s < n ? *reinterpret_cast<const uint4*>(v + s * j.v.token + c) : make_uint4(0u, 0u, 0u, 0u);
+                // (selects, not a branch: the loads from TMEM need the whole warp)
+                const uint32_t on = (s < n && (j.reverse ? s >= t : s <= t)) ? 0xFFFFFFFFu : 0u, p2 = __float_as_uint(p[k >> 1]);
+                const float pr = __uint_as_float((k & 1 ? p2 & 0xFFFF0000u : p2 << 16) & on);
+                const uint32_t u[4] = {raw.x & on, raw.y & on, raw.z & on, raw.w & on};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = unpack2(u[i]);
+                    o[2 * i] = fmaf(pr, f.x, o[2 * i]);
+                    o[2 * i + 1] = fmaf(pr, f.y, o[2 * i + 1]);
+                }
             }
         }
         tmem_ld_x8(lo + c, a);
