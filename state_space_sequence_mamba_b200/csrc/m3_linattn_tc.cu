@@ -201,8 +201,10 @@ __device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, float (&v)[8]) {
     for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// The outputs of a warp's 32 rows from P (lp) and O1 (lo) in TMEM and v in global memory, row t over the
-// tokens up to its own alone. v: the chunk's first token; y: this thread's row.
+constexpr float kInf = __builtin_huge_valf();
+
+// The outputs of a warp's 32 rows from P, O2 (lp) and O1 (lo) in TMEM and v in global memory: where O2 is not
+// finite, row t's sum over the tokens up to its own alone. v: the chunk's first token; y: this thread's row.
 __device__ __noinline__ void sum_rows(const LinJob& j, const __nv_bfloat16* v, uint8_t* y, uint32_t lp, uint32_t lo, int t,
                                       int n, int cols, float f1) {
 #pragma unroll 1
@@ -231,6 +233,10 @@ __device__ __noinline__ void sum_rows(const LinJob& j, const __nv_bfloat16* v, u
                 }
             }
         }
+        tmem_ld_x8(lp + T_O2 + c, a);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = fabsf(a[i]) < kInf ? a[i] : o[i];
         tmem_ld_x8(lo + c, a);
         tmem_wait_ld();
 #pragma unroll
@@ -375,7 +381,10 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
             // P v runs over all of the chunk's tokens, and zero times what is not finite is NaN: a later token's
             // would reach the rows before it (and a growing decay's overflow, from tokens that are not there).
             // A warp that finds such sums leaves the loop, sums its rows again over the tokens up to theirs,
-            // and comes back: inside the loop the sums' 64 registers would be spilled around that.
+            // and comes back: inside the loop the sums' 64 registers would be spilled around that. The look costs
+            // nothing in the forward and 4 % in the gradients (315 -> 328 us for 4 x 2048 tokens of 64 heads),
+            // where it delays O1's release. Elsewhere it cost more: v looked through by the v' warps, which run
+            // behind P, 350 us; O2 read before O1 is there, 340 (spills).
             bool again;
 #pragma unroll 1
             do {
@@ -427,7 +436,7 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
                     uint8_t* y = ybase + static_cast<int64_t>(t0 + t) * j.y_token * es;
                     if (!lwait_warp(&bars[B_O1 + g], c >> 1, &s_abort) || !lwait_warp(&bars[B_O2 + g], c >> 1, &s_abort)) break;
                     fence_after_sync();
-                    float2 odd = make_float2(0.f, 0.f);     // stays zero while the sums of O2 are finite
+                    float most = 0.f;       // of the sums of O2, NaN if one is
 #pragma unroll 1
                     for (int q = 0; q < 2; ++q) {
                         float a[32], o[32];
@@ -435,9 +444,9 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
                         tmem_ld_32x32b_x32(ls + T_O2 + 32u * q, o);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) odd = __ffma2_rn(make_float2(o[i], o[i + 1]), make_float2(0.f, 0.f), odd);
+                        for (int i = 0; i < 32; i += 2) asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(most) : "f"(o[i]), "f"(o[i + 1]));
                         if (q == 1) {
-                            again = __any_sync(0xffffffffu, odd.x + odd.y != 0.f);
+                            again = __any_sync(0xffffffffu, !(most < kInf));
                             if (again) break;
                             // O1, O2 and P have been read
                             fence_before_sync();

@@ -227,3 +227,25 @@ def test_overlapping_offsets_among_many(cuda_dev):
                 assert err(S[i:i + 1], rS) <= STATE_TOL and err(g["dinit"][i:i + 1], ref[3]) <= STATE_TOL
     empty = [i for i in range(len(cu) - 1) if cu[i + 1] <= cu[i]]
     assert bool((S[empty] == 0).all()) and len(empty) > 300
+
+
+def test_neighbours_that_are_not_finite_change_no_bit(cuda_dev):
+    """Packed sequences beside one full of NaN and infinities give the bits that they give beside any other:
+    a chunk's rows behind its sequence's last token, which are the neighbour's, are looked at and not used."""
+    lens = [100, 130, 200, 3, 127, 40]
+    t, d, cu, s = draw(cuda_dev, 1, 0, 2, 2, 2, 2, 64, 64, lens=lens, seed=63)
+    run = lambda: (m3.linattn_fwd(d["q"], d["k"], d["v"], d["log_decay"], scale=s, init=d["init"], cu_seqlens=cu),  # noqa: E731
+                   m3.linattn_bwd(d["q"], d["k"], d["v"], d["log_decay"], d["do"], scale=s, init=d["init"],
+                                  dfinal=d["dfinal"], cu_seqlens=cu))
+    (o, S), g = run()
+    for i, (lo, hi) in enumerate(zip(cu.tolist(), cu.tolist()[1:])):
+        if i % 2:
+            for n, x in (("q", float("nan")), ("k", float("inf")), ("v", float("nan")), ("do", -float("inf"))):
+                d[n][:, lo:hi] = x
+    (o2, S2), g2 = run()
+    torch.cuda.synchronize()
+    m3.linattn_check()
+    for i, (lo, hi) in enumerate(zip(cu.tolist(), cu.tolist()[1:])):
+        if i % 2 == 0:
+            assert torch.equal(o[:, lo:hi], o2[:, lo:hi]) and torch.equal(S[i], S2[i]) and torch.equal(g["dinit"][i], g2["dinit"][i])
+            assert all(torch.equal(g[n][:, lo:hi], g2[n][:, lo:hi]) for n in ("dq", "dk", "dv"))
