@@ -326,16 +326,16 @@ M3_API m3_status m3_scan_fwd_noalloc(const m3_dims* dims, const m3_inputs* in,
 /* A tensor of rows [nseq][seqlen][heads][dim] by its strides, in elements; the last dimension is
  * contiguous. With cu_seqlens the batch stride is not used. Any element-aligned pointer and any
  * strides (0 for an input, to broadcast); outputs must not overlap one another or an input (one
- * that begins at another tensor's address is refused). */
+ * that begins at another tensor's address is refused; states may be updated in place as each call says). */
 typedef struct {
     void* data;
     int64_t batch, token, head;
 } m3_view;
 
 typedef struct {
-    int64_t nseq;      /* sequences, >= 0                                                  */
-    int64_t seqlen;    /* tokens of each, >= 0, or with cu_seqlens the rows of the tensors */
-    int64_t nheads;    /* H >= 1                                                           */
+    int64_t nseq;      /* sequences, 0 to 2^24                                             */
+    int64_t seqlen;    /* tokens of each, 0 to 2^30, or with cu_seqlens the rows in all    */
+    int64_t nheads;    /* H, 1 to 65536                                                    */
     int64_t qheads;    /* heads of q, k and v: each divides H                              */
     int64_t kheads;
     int64_t vheads;
@@ -359,12 +359,15 @@ typedef struct {
 M3_API size_t m3_linattn_workspace_bytes(const m3_linattn_dims* dims, int packed);
 M3_API size_t m3_linattn_bwd_workspace_bytes(const m3_linattn_dims* dims, int packed);
 
-/* Prompts. init, final: fp32 [nseq, H, K, V], or NULL for zero / not wanted; final may be init.
+/* Prompts. init, final: fp32 [nseq, H, K, V], 16-byte aligned, or NULL for zero / not wanted; final may be init.
  * o: the output [nseq][seqlen][H][V] by its view, in_dtype. workspace: 256-byte aligned, at least
  * m3_linattn_workspace_bytes (NULL where that is 0). bf16 tensors whose pointers and strides are
  * multiples of 16 bytes, with K and V multiples of 8 and K <= 128, run on the tensor cores (chunks
  * of 128 tokens; products of bf16 operands with fp32 accumulators, the state exact to fp32); every
- * other call, and sequences of up to 8 tokens that are not packed, run in fp32 on the CUDA cores.
+ * other call, and sequences of up to 8 tokens that are not packed, run in fp32 on the CUDA cores. On the
+ * tensor cores the masked scores and the state as an operand are rounded to bf16 once each: outputs and
+ * gradients are off by some 2.3e-3 in all, where the output's own rounding is 1.7e-3. A caller who needs
+ * products of fp32 operands passes fp32 tensors.
  * Asynchronous on `stream`. */
 M3_API m3_status m3_linattn_fwd(const m3_linattn_dims* dims, const m3_linattn_inputs* in,
                                 const float* init, float* final_state, const m3_view* o,
@@ -387,8 +390,8 @@ M3_API m3_status m3_linattn_step(const m3_linattn_dims* dims, const m3_linattn_i
  *     dq_t = scale S_t d_o_t,   dk_t = R_t v_t,   dv_t = R_t^T k_t,   dinit = a R_0,
  *     R_t = a R_{t+1} + scale q_t d_o_t^T   (R_T such that a R_T = dfinal)
  * d_o: [nseq][seqlen][H][V]. dq, dk, dv: in_dtype, laid out by their views with the heads of q,
- * k and v. dfinal, dinit: fp32 [nseq, H, K, V], or NULL for zero / not wanted; dinit may be
- * dfinal, not init. The same tensor-core condition as m3_linattn_fwd, with K, V <= 128. Results do not
+ * k and v. dfinal, dinit: fp32 [nseq, H, K, V], 16-byte aligned (init too), or NULL for zero / not wanted;
+ * dinit may be dfinal, not init. The same tensor-core condition as m3_linattn_fwd, with K, V <= 128. Results do not
  * depend on the order of execution. */
 typedef struct {
     m3_view dq, dk, dv;

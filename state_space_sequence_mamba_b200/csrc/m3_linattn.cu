@@ -14,8 +14,8 @@ namespace m3 {
 // segments' end states) and sums its predecessors' states, but the CTAs fill the device's slots more
 // evenly. A batch takes the number of segments with the least estimated time (waves of CTAs, of both
 // launches, times a CTA's chunks), more of them only for a tenth less: they read more of k and v
-// again. (b1 H64 L65536: 2 segments, one wave of 256 chunks on 128 SMs, 0.98 ms; 9 segments, 4 waves of
-// 57 on all 148, 1.02.)
+// again. (b1 H64 L65536: 2 segments, one wave of 256 chunks on 128 SMs, 0.96 ms; 9 segments, 4 waves of
+// 57 on all 148, 4 % more.)
 LinPlan lin_plan(int64_t nseq, int64_t L, bool packed, int64_t per_x, const LinForm& form) {
     LinPlan pl{};
     const int64_t chunks = (L + form.chunk - 1) / form.chunk;
@@ -133,7 +133,8 @@ m3_status check_dims(const m3_linattn_dims* d) {
     if (!std::isfinite(d->scale)) return err(M3_ERR_INVALID_ARG, "scale must be finite");
     if (d->kdim > 256 || d->vdim > 256)
         return err(M3_ERR_UNSUPPORTED, "kdim %lld or vdim %lld exceeds 256", (long long)d->kdim, (long long)d->vdim);
-    // token counts stay exact as fp32 exponents, indexes of one sequence fit 32 bits
+    // indexes of one sequence fit 32 bits. As fp32 exponents of the decay, token counts above 2^24 are rounded: by
+    // 2^-24 of the exponent, so of the power by 2^-24 of its logarithm.
     if (d->seqlen > (int64_t(1) << 30) || H > 65536 || d->nseq > (int64_t(1) << 24))
         return err(M3_ERR_UNSUPPORTED, "seqlen above 2^30, nheads above 65536 or nseq above 2^24");
     return M3_OK;
@@ -458,7 +459,8 @@ m3_status m3_linattn_fwd(const m3_linattn_dims* dims, const m3_linattn_inputs* i
         dims->nseq * dims->nheads <= kMaxStepUnits) {
         // Few tokens are steps on a state held in registers: exact products, and less time than a chunk with few
         // rows. bf16, K 128, V 64, 64 sequences of 64 heads: 42, 55, 155 us for 1, 2, 8 tokens against 218 to
-        // 221; 4 sequences: 5.5, 6.1, 12.2 against 16.5. One sequence of 4 heads (V 64): 3.0, 3.8, 7.4 against 6.4.
+        // 221; 4 sequences: 5.5, 6.1, 12.2 against 16.5. One sequence of 4 heads (V 64): 3.0, 3.8, 7.4 against 6.4, a
+        // microsecond more at 8 tokens, which is left so that the products are exact whatever the batch.
         const LinStep p = make_step(dims, in, init, final_state, dims->nseq, nullptr, o);
         const cudaError_t e = launch_lin_step(p, dims->in_dtype == M3_BF16, s);
         return e == cudaSuccess ? M3_OK : cuda_err(e, "linear attention launch");

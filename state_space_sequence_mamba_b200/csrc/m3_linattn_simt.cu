@@ -10,7 +10,7 @@
 // flops, so a chunk is bound by instruction issue, not by DRAM: the products are packed pairs of FMAs,
 // and blocks above the mask's diagonal are left out. In reverse a chunk's tokens are staged last to
 // first, which makes it a forward one. Rows are not padded but swizzled, and P takes q's place, so
-// that two CTAs of Dk = 128 fit an SM (112 KB each). 4096 tokens of 16 heads, K 128, V 64, fp32: 179 us,
+// that two CTAs of Dk = 128 fit an SM (112 KB each). 4096 tokens of 16 heads, K 128, V 64, fp32: 182 us,
 // 21 TFLOP/s, with an instruction issued in 64 % of the cycles and the FMA pipe busy in 37 %; the rest is
 // waiting at the barriers between a chunk's products, which two CTAs an SM do not fill.
 #include "m3_common.cuh"

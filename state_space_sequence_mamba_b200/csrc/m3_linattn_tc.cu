@@ -22,13 +22,15 @@
 // What bounds it: shared memory and the hand-offs of a chunk, about alike. The products read 1800 cycles
 // of shared memory a chunk (S 64 KB, O1 48, k^T v' 80, O2 16, at 128 bytes a cycle); the loads' writes, v',
 // its parts and the state's operand take it to some 2900. Measured are 3600 to 3900 cycles from chunk to
-// chunk, with the data pipe in front of shared memory and TMEM busy for 78 % of a launch; 96 KB of HBM (per-head q, k, v and y of K 128, V 64) would take 4200 if all 148 SMs asked
-// at once. Only H <- a^n H + ... is serial from chunk to chunk, so everything else runs ahead of it: q, k
+// chunk, with the data pipe in front of shared memory and TMEM busy for 78 % of a launch of the gradients (in the
+// forward the warps' share of it is 40 %, against 50); 96 KB of HBM (per-head q, k, v and y of K 128, V 64) would
+// take 4200 if all 148 SMs asked at once. Only H <- a^n H + ... is serial from chunk to chunk, so everything else runs ahead of it: q, k
 // and v are double-buffered, v' and its product do not wait for the state, and S and P of a chunk do not
 // wait for the outputs of the one before. A CTA's start (launch, TMEM, tables, first loads, the first
 // chunk's chain of products) is some 11 000 cycles until its first output: short sequences are bound by that.
-// Measured: 4 x 2048 tokens of 64 heads (K 128, V 64, q and k shared) 83 us, its three gradients with q and
-// k of every head 315 us (2.4 TB/s); 65 536 tokens of 64 heads 955 us (3.4 TB/s).
+// Measured: 4 x 2048 tokens of 64 heads (K 128, V 64, q and k shared) 84 us, its three gradients with q and
+// k of every head 330 us (2.3 TB/s); 65 536 tokens of 64 heads 965 us (3.3 TB/s). These are bursts of four calls;
+// for seconds, under the power cap, 90, 370 and 1077.
 //
 // Warps: 0-3 and 4-7 the rows of the even and of the odd chunks (S -> P, then y), 8-15 the state (in
 // registers, half a row a thread), 16-23 v', 24 TMA loads, 25 issues S and O2, 26 O1, 27 k^T v'.
@@ -382,9 +384,9 @@ lin_tc_kernel(const __grid_constant__ LinTcParams tp, const __grid_constant__ Li
             // would reach the rows before it (and a growing decay's overflow, from tokens that are not there).
             // A warp that finds such sums leaves the loop, sums its rows again over the tokens up to theirs,
             // and comes back: inside the loop the sums' 64 registers would be spilled around that. The look costs
-            // nothing in the forward and 4 % in the gradients (315 -> 328 us for 4 x 2048 tokens of 64 heads),
+            // nothing in the forward and 4 % in the gradients (316 -> 330 us for 4 x 2048 tokens of 64 heads),
             // where it delays O1's release. Elsewhere it cost more: v looked through by the v' warps, which run
-            // behind P, 350 us; O2 read before O1 is there, 340 (spills).
+            // behind P, 350 us; O2 read before O1 is there, 368.
             bool again;
 #pragma unroll 1
             do {
