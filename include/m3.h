@@ -364,7 +364,8 @@ M3_API size_t m3_linattn_bwd_workspace_bytes(const m3_linattn_dims* dims, int pa
  * m3_linattn_workspace_bytes (NULL where that is 0). bf16 tensors whose pointers and strides are
  * multiples of 16 bytes, with K and V multiples of 8 and K <= 128, run on the tensor cores (chunks
  * of 128 tokens; products of bf16 operands with fp32 accumulators, the state exact to fp32); every
- * other call, and sequences of up to 8 tokens that are not packed, run in fp32 on the CUDA cores. On the
+ * other call, sequences of up to 8 tokens that are not packed, and calls of up to 512 tokens times heads
+ * in all, run in fp32 on the CUDA cores. On the
  * tensor cores the masked scores and the state as an operand are rounded to bf16 once each: outputs and
  * gradients are off by some 2.3e-3 in all, where the output's own rounding is 1.7e-3. A caller who needs
  * products of fp32 operands passes fp32 tensors.

@@ -369,7 +369,8 @@ cudaError_t fold_heads(const m3_linattn_dims* d, float* const (&part)[3], const 
 // Plans and launches the jobs of p in the form that takes them. table: table_bytes of the workspace.
 m3_status run_jobs(LinParams& p, const m3_linattn_dims* d, int state_rows, char* ws, char* table, cudaStream_t s) {
     const bool bf16 = d->in_dtype == M3_BF16, packed = p.cu != nullptr;
-    const bool tc = bf16 && lin_tc_supported(p);
+    const bool few = (packed ? d->seqlen : d->nseq * d->seqlen) * d->nheads <= kLinFew;
+    const bool tc = bf16 && !few && lin_tc_supported(p);
     const LinPlan pl = lin_plan(d->nseq, d->seqlen, packed, d->nheads * p.rtiles,
                                 tc ? lin_tc_form() : simt_form(d, p.njobs > 1));
     p.seg_len = pl.seg_len;

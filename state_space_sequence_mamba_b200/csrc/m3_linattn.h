@@ -74,6 +74,11 @@ struct LinForm {
 };
 LinPlan lin_plan(int64_t nseq, int64_t L, bool packed, int64_t per_x, const LinForm& form);
 
+// (token, head) pairs of the largest bf16 call that the fp32 form takes though the tensor cores could. A score's
+// rounding to bf16 is the same for a whole row of the output, and in few rows such roundings do not average out:
+// up to 1.5 times the output's own error and more, where it is 1.4 in large calls. (Gradients of 1, 8, 32 tokens of 4 heads,
+// K 64, V 64: 11.6, 12.1, 14.7 us in fp32, 7.4, 7.8, 7.8 on the tensor cores; packed 8 x 8 of 4 heads 13.0 and 9.9.)
+constexpr int64_t kLinFew = 512;
 // Packed sequences up to which each CTA counts blocks itself, which grows with their square; for more a launch
 // before it makes the table of first blocks. (Sequences of 4 tokens, 4 heads, counted against table: 64 26 us
 // against 31, 192 70 both, 256 91 against 82, 4096 7544 against 1089, 16 384 123 ms against 4.5.)

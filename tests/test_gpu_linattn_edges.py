@@ -90,7 +90,9 @@ POISON = [("k", float("nan")), ("v", float("nan")), ("v", float("inf")), ("k", -
 def test_a_token_that_is_not_finite_stays_out_of_earlier_ones(cuda_dev, name, value, L, dtype, K, V):
     """One element of one token of one head: outputs and gradients are finite exactly where the recurrence's
     are (o before the token, dk and dv behind it, other heads, other columns), whatever the chunk."""
-    t, d, _, s = draw(cuda_dev, 2, L, 2, 2, 2, 2, K, V, dtype=dtype, seed=51, decay=[-0.01, -0.05])
+    # enough sequences for the tensor-core form, which takes bf16 calls of more than 512 (token, head) pairs
+    b = 2 if dtype == F32 or L == 300 else 40
+    t, d, _, s = draw(cuda_dev, b, L, 2, 2, 2, 2, K, V, dtype=dtype, seed=51, decay=[-0.01, -0.05])
     for at in (L // 2, L - 2) if L < 300 else (170, 290):
         u, e = dict(t), dict(d)
         u[name], e[name] = t[name].clone(), d[name].clone()
@@ -136,7 +138,8 @@ def test_packed_tokens_that_are_not_finite(cuda_dev, lens):
 def test_growing_decay_in_a_part_of_a_chunk(cuda_dev, L, grow, dtype):
     """e^1 or e^3 a token: the sequence's own factors stay inside fp32's range (e^81 = 2e35), those of the
     chunk's absent rows (e^127) do not."""
-    t, d, cu, s = draw(cuda_dev, 1, L, 2, 2, 2, 2, 64, 64, dtype=dtype, seed=53, decay=[grow, -0.01])
+    # (more than 512 (token, head) pairs: the tensor-core form)
+    t, d, cu, s = draw(cuda_dev, 1 if dtype == F32 else 40, L, 2, 2, 2, 2, 64, 64, dtype=dtype, seed=53, decay=[grow, -0.01])
     o, S = m3.linattn_fwd(d["q"], d["k"], d["v"], d["log_decay"], scale=s, init=d["init"])
     g = m3.linattn_bwd(d["q"], d["k"], d["v"], d["log_decay"], d["do"], scale=s, init=d["init"], dfinal=d["dfinal"])
     torch.cuda.synchronize()
@@ -249,3 +252,22 @@ def test_neighbours_that_are_not_finite_change_no_bit(cuda_dev):
         if i % 2 == 0:
             assert torch.equal(o[:, lo:hi], o2[:, lo:hi]) and torch.equal(S[i], S2[i]) and torch.equal(g["dinit"][i], g2["dinit"][i])
             assert all(torch.equal(g[n][:, lo:hi], g2[n][:, lo:hi]) for n in ("dq", "dk", "dv"))
+
+
+@pytest.mark.parametrize("seed", [1, 2, 3])
+@pytest.mark.parametrize("lens,H,K,V", [([3, 0, 1, 1, 0, 2], 24, 40, 32), ([1, 1, 1], 8, 64, 64), ([9], 8, 64, 64), ([1] * 16, 16, 128, 64)])
+def test_small_calls_are_off_by_their_own_rounding(cuda_dev, lens, H, K, V, seed):
+    """bf16 calls of few rows: products of fp32 operands, so that an output is off by one rounding, which is
+    spread evenly over half a step of at most 2^-8 of the value: 2^-8 / sqrt(3) in the mean square at most."""
+    t, d, cu, s = draw(cuda_dev, 1, 0, H, H, H, H, K, V, lens=lens, seed=70 + seed, decay=[-0.01, -0.4])
+    a = (d["q"], d["k"], d["v"], d["log_decay"])
+    o, S = m3.linattn_fwd(*a, scale=s, init=d["init"], cu_seqlens=cu)
+    g = m3.linattn_bwd(*a, d["do"], scale=s, init=d["init"], dfinal=d["dfinal"], cu_seqlens=cu)
+    o0, _ = m3.linattn_fwd(*a, scale=s, cu_seqlens=cu)
+    g0 = m3.linattn_bwd(*a, d["do"], scale=s, cu_seqlens=cu)
+    torch.cuda.synchronize()
+    for got, grads, init, dfinal in ((o, g, t["init"], t["dfinal"]), (o0, g0, torch.zeros_like(t["init"]), None)):
+        ro, _ = ol.forward(t["q"], t["k"], t["v"], t["log_decay"], s, init, lens)
+        ref = ol.gradients(t["q"], t["k"], t["v"], t["log_decay"], t["do"], s, init, dfinal, lens)
+        errs = [err(got, ro)] + [err(grads[n], r) for n, r in zip(("dq", "dk", "dv"), ref)]
+        assert max(errs) <= 2.0 ** -8 / 3 ** 0.5, errs
