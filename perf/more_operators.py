@@ -306,7 +306,7 @@ def _gs(s):
     # the adjoint of h_t, from the last token back
     before = torch.cat([torch.zeros_like(h[:, :1]), h[:, :-1]], 1)
     up = torch.cat([a[:, 1:], torch.zeros_like(a[:, :1])], 1)
-    d = s["dy"][:, :h.shape[1]].float()
+    d = s["dy"][:, :h.shape[1]].to(torch.float32, copy=True)
     if s["lens"] is None:
         if s["state"] is not None:
             before[:, 0] = s["state"]
