@@ -448,6 +448,161 @@ M3_API m3_status m3_group_norm_bwd(const m3_group_norm_dims* dims, const m3_view
                                    float* dweight, float* dbias, void* workspace, size_t ws_bytes,
                                    void* stream);
 
+/* ---- Gated linear recurrence of each channel ----
+ * Per sequence and channel, with a gate r_t, an input gate i_t (or none) and a decay parameter d:
+ *     a_t = exp(-power softplus(d) sigmoid(r_t)),  w_t = sqrt(1 - a_t^2)
+ *     a_t = sigmoid(r_t + d),                      w_t = 1 - a_t             (M3_GS_LERP)
+ *     h_t = a_t h_{t-1} + w_t sigmoid(i_t) x_t,    y_t = h_t                 (h_{-1} = init)
+ * The gates arrive as they leave their projections. The state is one value a channel: where linear
+ * attention keeps a K x V state for each head, this keeps the width of the layer. State and arithmetic are
+ * fp32, y is rounded once. Packed sequences lie as linear attention's do; offsets must not descend.
+ * Views: batch and token strides (head is not used), channels contiguous. A sigmoid ends at 2^-62 (arguments
+ * below -43), not at zero. */
+#define M3_GS_LERP 1u
+#define M3_GS_BLOCK 64      /* tokens between two marks */
+
+typedef struct {
+    int64_t nseq;      /* sequences, 0 to 2^24                                             */
+    int64_t seqlen;    /* tokens of each, 0 to 2^30, or with cu_seqlens the rows in all    */
+    int64_t channels;  /* C, 1 to 2^24                                                     */
+    int32_t in_dtype;  /* m3_dtype of x, r, i, y and their gradients                       */
+    float power;       /* finite, > 0 (not used with M3_GS_LERP)                           */
+    uint32_t flags;    /* M3_GS_LERP                                                       */
+} m3_gated_scan_dims;
+
+typedef struct {
+    m3_view x, r, i;            /* read only; i.data NULL: no input gate                   */
+    const float* decay;         /* d [C], or NULL with M3_GS_LERP for zero                 */
+    const int32_t* cu_seqlens;  /* [nseq + 1], or NULL: every sequence has seqlen tokens   */
+} m3_gated_scan_inputs;
+
+/* Prompts. init, final: fp32 [nseq, C], 16-byte aligned, or NULL for zero / not wanted; final may be
+ * init. y: [nseq][seqlen][C] by its view; rows of no sequence are left as they were. marks: fp32
+ * [nseq (packed: 1)][ceil(seqlen / M3_GS_BLOCK)][C], 16-byte aligned, or NULL: receives the state
+ * before every M3_GS_BLOCK-th token (packed: row), which saves the backward a pass. No workspace.
+ * Results do not depend on the order of execution. What is not finite stays in its channel and
+ * sequence, from its token on. */
+M3_API m3_status m3_gated_scan_fwd(const m3_gated_scan_dims* dims, const m3_gated_scan_inputs* in,
+                                   const float* init, float* final_state, const m3_view* y,
+                                   float* marks, void* stream);
+
+/* One token of every sequence: dims->seqlen must be 1, cu_seqlens NULL. state_in, state_out: fp32
+ * [nstates, C], 16-byte aligned; state_out may be state_in (in place) but must not overlap it otherwise.
+ * slots as in m3_linattn_step: a slot outside [0, nstates) skips that sequence (its y row is zero);
+ * of two sequences that share one, that state and both outputs are undefined. */
+M3_API m3_status m3_gated_scan_step(const m3_gated_scan_dims* dims, const m3_gated_scan_inputs* in,
+                                    const float* state_in, float* state_out, int64_t nstates,
+                                    const int32_t* slots, const m3_view* y, void* stream);
+
+/* Workspace bytes of m3_gated_scan_bwd for these dims (packed: whether cu_seqlens will be given; have_marks:
+ * whether marks will), 0 where none is needed or the dims are invalid. Depends on the current device's SM
+ * count. Any content; calls that may overlap need workspaces of their own. */
+M3_API size_t m3_gated_scan_bwd_workspace_bytes(const m3_gated_scan_dims* dims, int packed, int have_marks);
+
+/* Gradients of sum(y * dy) + <final state, dfinal> for the call of m3_gated_scan_fwd with the same
+ * dims, inputs and init. dx, dr, di (with i): in_dtype, by their views; rows of no sequence are left as they
+ * were. ddecay: fp32 [C], summed over tokens and sequences, or NULL. dfinal, dinit: fp32 [nseq, C], or
+ * NULL for zero / not wanted; dinit may be dfinal, not init. marks: that call's, or NULL (they are formed
+ * in the workspace by a pass over the inputs). fp32 pointers 16-byte aligned, workspace 256. */
+typedef struct {
+    m3_view dx, dr, di;
+} m3_gated_scan_grads;
+M3_API m3_status m3_gated_scan_bwd(const m3_gated_scan_dims* dims, const m3_gated_scan_inputs* in,
+                                   const float* init, const float* marks, const m3_view* dy,
+                                   const float* dfinal, const m3_gated_scan_grads* grads, float* ddecay,
+                                   float* dinit, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---- Rotary positions of queries and keys ----
+ * Pair j of the first rotdim dimensions of every head, (j, j + rotdim / 2) or with M3_ROT_INTERLEAVED
+ * (2 j, 2 j + 1), becomes scale times itself turned by the angle position * freq[j]:
+ *     (x, y) -> scale (x cos - y sin, y cos + x sin)
+ * (M3_ROT_INVERSE: turned back, which is the gradient); the other dimensions are copied. Linear
+ * attention with a constant decay knows positions by its decay alone; its layers turn q and k. The scan's
+ * own rotation is data-dependent and part of it. freq: fp64 [rotdim / 2], radians per position, finite
+ * (scaled as the layer was trained). The angle is exact to 2^-54 turns a position, sine and cosine to some
+ * 1e-7; fp32 arithmetic, one rounding. */
+#define M3_ROT_INTERLEAVED 1u
+#define M3_ROT_INVERSE 2u
+#define M3_ROT_POS64 4u         /* positions are int64, otherwise int32 */
+
+typedef struct {
+    int64_t nseq;      /* sequences                                                        */
+    int64_t seqlen;    /* tokens of each, or with cu_seqlens the rows in all               */
+    int64_t qheads;    /* >= 1                                                             */
+    int64_t kheads;    /* >= 0; 0: no k                                                    */
+    int64_t headdim;   /* 1 to 1024                                                        */
+    int64_t rotdim;    /* even, 0 to headdim                                               */
+    int64_t offset;    /* added to every position                                          */
+    int32_t in_dtype;  /* m3_dtype of q, k and the outputs                                 */
+    float scale;       /* finite                                                           */
+    uint32_t flags;
+} m3_rotary_dims;
+
+/* positions: element [sequence * pos_batch + token * pos_token] (packed: row * pos_token), or NULL: the
+ * token's index in its sequence. cu_seqlens [nseq + 1] or NULL, as linear attention's; rows of no
+ * sequence are left as they were. q_out may be q and k_out k (in place, the same strides); outputs must
+ * not overlap other tensors otherwise. */
+M3_API m3_status m3_rotary(const m3_rotary_dims* dims, const m3_view* q, const m3_view* k,
+                           const double* freq, const void* positions, int64_t pos_batch,
+                           int64_t pos_token, const int32_t* cu_seqlens, const m3_view* q_out,
+                           const m3_view* k_out, void* stream);
+
+/* ---- Norms around a block, with its gate and residual ----
+ * Per row of C channels, with the block's output y, the residual stream x and a gate z:
+ *     n = post(y),  h = x + alpha n act(z),  out = pre(h)
+ * post and pre: nothing, or (v - mean) / sqrt(var + eps) (_LAYER) or v / sqrt(mean(v^2) + eps) (_RMS), times
+ * weight plus bias (fp32 [C], or NULL for one / zero; post's also apply without its norm: a scale for each
+ * channel). act: sigmoid, SiLU or identity of z; no z: 1. pre is the norm before the next block. The residual
+ * stream may be fp32 beside bf16 blocks. h is not rounded before pre; fp32 arithmetic, one rounding for
+ * each output. */
+#define M3_BN_POST_RMS 1u
+#define M3_BN_POST_LAYER 2u
+#define M3_BN_PRE_RMS 4u
+#define M3_BN_PRE_LAYER 8u
+#define M3_BN_SIGMOID 16u
+#define M3_BN_SILU 32u
+
+typedef struct {
+    int64_t batch;      /* >= 0                                                    */
+    int64_t rows;       /* rows of each batch entry, >= 0                          */
+    int64_t channels;   /* C, 1 to 2^24                                            */
+    int32_t in_dtype;   /* m3_dtype of y, z, out and their gradients               */
+    int32_t res_dtype;  /* m3_dtype of residual, h and their gradients: M3_F32 or in_dtype */
+    float eps;          /* finite, >= 0                                            */
+    float alpha;        /* finite                                                  */
+    uint32_t flags;     /* at most one of each pair above                          */
+} m3_block_norm_dims;
+
+/* Views: batch and token (row) strides, channels contiguous (head is not used). */
+typedef struct {
+    m3_view y, residual, z;                 /* z.data NULL: no gate                 */
+    const float *post_weight, *post_bias;   /* fp32 [C] or NULL                     */
+    const float *pre_weight, *pre_bias;
+} m3_block_norm_inputs;
+
+/* h; out: only with a pre norm. h may be residual and out may be y (the same view); otherwise outputs must
+ * not overlap other tensors. */
+M3_API m3_status m3_block_norm_fwd(const m3_block_norm_dims* dims, const m3_block_norm_inputs* in,
+                                   const m3_view* h, const m3_view* out, void* stream);
+
+typedef struct {
+    m3_view dy, dresidual, dz;              /* dz with z                            */
+    float *dpost_weight, *dpost_bias;       /* fp32 [C], or NULL: not wanted        */
+    float *dpre_weight, *dpre_bias;
+} m3_block_norm_grads;
+
+/* Workspace bytes of m3_block_norm_bwd, 0 where the dims are invalid. Depends on the current device's SM
+ * count. Any content; calls that may overlap need workspaces of their own. */
+M3_API size_t m3_block_norm_bwd_workspace_bytes(const m3_block_norm_dims* dims);
+
+/* Gradients of sum(h * dh) + sum(out * dout) for the call of m3_block_norm_fwd with the same dims and inputs.
+ * dh may be NULL or its data NULL (zero); dout: with a pre norm. dresidual may be dh and dy may be dout (the
+ * same view). Sums over rows run in a fixed order. workspace: 256-byte aligned. */
+M3_API m3_status m3_block_norm_bwd(const m3_block_norm_dims* dims, const m3_block_norm_inputs* in,
+                                   const m3_view* dh, const m3_view* dout,
+                                   const m3_block_norm_grads* grads, void* workspace,
+                                   size_t ws_bytes, void* stream);
+
 /* Static description of a status code. */
 M3_API const char* m3_status_str(m3_status s);
 

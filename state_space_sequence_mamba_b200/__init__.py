@@ -12,7 +12,9 @@ from .inputs import Dims, Problem, make_problem, make_config, make_decode, CONFI
 def __getattr__(name):
     if name in ("scan_fwd", "decode_step", "scan_workspace_bytes", "M3Error", "load_library",
                 "State", "linattn_fwd", "linattn_step", "linattn_bwd", "linattn_check",
-                "linattn_workspace_bytes", "group_norm_fwd", "group_norm_bwd"):
+                "linattn_workspace_bytes", "group_norm_fwd", "group_norm_bwd", "gated_scan_fwd",
+                "gated_scan_step", "gated_scan_bwd", "rotary", "rotary_frequencies", "block_norm_fwd",
+                "block_norm_bwd"):
         from . import binding
         return getattr(binding, name)
     raise AttributeError(name)

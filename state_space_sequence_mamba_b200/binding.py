@@ -7,6 +7,7 @@ implementation.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -22,6 +23,12 @@ M3_DT_SOFTPLUS, M3_LAM_SIGMOID, M3_DISC_ZOH, M3_BWD_FP32 = 1, 2, 4, 8
 BWD_FP32 = M3_BWD_FP32
 # m3_group_norm_dims.flags
 M3_GN_CENTER, M3_GN_SILU = 1, 2
+# m3_gated_scan_dims.flags, and the tokens between two of its marks
+M3_GS_LERP, M3_GS_BLOCK = 1, 64
+# m3_rotary_dims.flags
+M3_ROT_INTERLEAVED, M3_ROT_INVERSE, M3_ROT_POS64 = 1, 2, 4
+# m3_block_norm_dims.flags
+M3_BN_POST_RMS, M3_BN_POST_LAYER, M3_BN_PRE_RMS, M3_BN_PRE_LAYER, M3_BN_SIGMOID, M3_BN_SILU = 1, 2, 4, 8, 16, 32
 
 
 class M3Error(RuntimeError):
@@ -81,6 +88,42 @@ class GroupNormDims(ctypes.Structure):
                 ("groups", ctypes.c_int64), ("in_dtype", ctypes.c_int32), ("eps", ctypes.c_float), ("flags", ctypes.c_uint32)]
 
 
+class GatedScanDims(ctypes.Structure):
+    _fields_ = [("nseq", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("channels", ctypes.c_int64),
+                ("in_dtype", ctypes.c_int32), ("power", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
+class GatedScanInputs(ctypes.Structure):
+    _fields_ = [("x", View), ("r", View), ("i", View), ("decay", ctypes.c_void_p),
+                ("cu_seqlens", ctypes.c_void_p)]
+
+
+class GatedScanGrads(ctypes.Structure):
+    _fields_ = [("dx", View), ("dr", View), ("di", View)]
+
+
+class RotaryDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("nseq", "seqlen", "qheads", "kheads", "headdim", "rotdim",
+                                              "offset")] + [
+                   ("in_dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
+class BlockNormDims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("rows", ctypes.c_int64), ("channels", ctypes.c_int64),
+                ("in_dtype", ctypes.c_int32), ("res_dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("alpha", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
+class BlockNormInputs(ctypes.Structure):
+    _fields_ = [("y", View), ("residual", View), ("z", View)] + [
+        (n, ctypes.c_void_p) for n in ("post_weight", "post_bias", "pre_weight", "pre_bias")]
+
+
+class BlockNormGrads(ctypes.Structure):
+    _fields_ = [("dy", View), ("dresidual", View), ("dz", View)] + [
+        (n, ctypes.c_void_p) for n in ("dpost_weight", "dpost_bias", "dpre_weight", "dpre_bias")]
+
+
 class Grads(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("dx", "dB", "dC", "dtheta", "ddt", "dA", "dlam",
                                                "dB_bias", "dC_bias", "ddt_bias")]
@@ -92,7 +135,10 @@ EXPORTS = ("m3_scan_workspace_bytes", "m3_scan_fwd", "m3_decode_step", "m3_scan_
            "m3_scan_state", "m3_state_combine", "m3_scan_bwd_workspace_bytes", "m3_scan_bwd",
            "m3_linattn_workspace_bytes", "m3_linattn_fwd", "m3_linattn_step",
            "m3_linattn_bwd_workspace_bytes", "m3_linattn_bwd", "m3_linattn_check",
-           "m3_group_norm_fwd", "m3_group_norm_bwd_workspace_bytes", "m3_group_norm_bwd")
+           "m3_group_norm_fwd", "m3_group_norm_bwd_workspace_bytes", "m3_group_norm_bwd",
+           "m3_gated_scan_fwd", "m3_gated_scan_step", "m3_gated_scan_bwd_workspace_bytes",
+           "m3_gated_scan_bwd", "m3_rotary", "m3_block_norm_fwd",
+           "m3_block_norm_bwd_workspace_bytes", "m3_block_norm_bwd")
 
 _lib = None
 
@@ -159,8 +205,21 @@ def _declare_linattn(lib):
     lib.m3_group_norm_bwd_workspace_bytes.restype = sz
     lib.m3_group_norm_fwd.argtypes = [G, V, V, vp, vp, V, vp]
     lib.m3_group_norm_bwd.argtypes = [G, V, V, vp, vp, V, V, V, vp, vp, vp, sz, vp]
+    S, SI = P(GatedScanDims), P(GatedScanInputs)
+    lib.m3_gated_scan_fwd.argtypes = [S, SI, vp, vp, V, vp, vp]
+    lib.m3_gated_scan_step.argtypes = [S, SI, vp, vp, i64, vp, V, vp]
+    lib.m3_gated_scan_bwd_workspace_bytes.argtypes = [S, ctypes.c_int, ctypes.c_int]
+    lib.m3_gated_scan_bwd_workspace_bytes.restype = sz
+    lib.m3_gated_scan_bwd.argtypes = [S, SI, vp, vp, V, vp, P(GatedScanGrads), vp, vp, vp, sz, vp]
+    lib.m3_rotary.argtypes = [P(RotaryDims), V, V, vp, vp, i64, i64, vp, V, V, vp]
+    B, BI = P(BlockNormDims), P(BlockNormInputs)
+    lib.m3_block_norm_bwd_workspace_bytes.argtypes = [B]
+    lib.m3_block_norm_bwd_workspace_bytes.restype = sz
+    lib.m3_block_norm_fwd.argtypes = [B, BI, V, V, vp]
+    lib.m3_block_norm_bwd.argtypes = [B, BI, V, V, P(BlockNormGrads), vp, sz, vp]
     for name in ("m3_linattn_fwd", "m3_linattn_step", "m3_linattn_bwd", "m3_linattn_check",
-                 "m3_group_norm_fwd", "m3_group_norm_bwd"):
+                 "m3_group_norm_fwd", "m3_group_norm_bwd", "m3_gated_scan_fwd", "m3_gated_scan_step",
+                 "m3_gated_scan_bwd", "m3_rotary", "m3_block_norm_fwd", "m3_block_norm_bwd"):
         getattr(lib, name).restype = ctypes.c_int
 
 
@@ -403,12 +462,13 @@ def scan_bwd(x, B, C, theta, dt, A, lam, dy, B_bias=None, C_bias=None, init: Sta
     return g
 
 
-# ---- linear attention with a decay for each head, and the grouped norm behind it ----
+# ---- linear attention with a decay for each head, the grouped norm behind it, the gated scan, rotary
+# positions and the norms around a block ----
 # Marshalled in C++ (csrc/m3_torch.cpp), since these calls' kernels may be as short as the
 # marshalling. They run on the tensors' device and, unless a stream is given, on its current
 # stream; what they allocate is allocated on the stream they run on. They are no autograd functions:
-# results are detached from inputs that require a gradient, whose gradients linattn_bwd and
-# group_norm_bwd compute; tensors given to be written count as changed. Wrong shapes, types, strides
+# results are detached from inputs that require a gradient, whose gradients the _bwd calls
+# (and rotary with ``inverse``) compute; tensors given to be written count as changed. Wrong shapes, types, strides
 # and devices raise ValueError, the library's own refusals M3Error.
 
 _native = None
@@ -430,7 +490,9 @@ def _ext():
         _m3torch.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
             "m3_linattn_workspace_bytes", "m3_linattn_bwd_workspace_bytes", "m3_linattn_fwd",
             "m3_linattn_step", "m3_linattn_bwd", "m3_group_norm_fwd",
-            "m3_group_norm_bwd_workspace_bytes", "m3_group_norm_bwd")))
+            "m3_group_norm_bwd_workspace_bytes", "m3_group_norm_bwd", "m3_gated_scan_fwd",
+            "m3_gated_scan_step", "m3_gated_scan_bwd_workspace_bytes", "m3_gated_scan_bwd", "m3_rotary",
+            "m3_block_norm_fwd", "m3_block_norm_bwd_workspace_bytes", "m3_block_norm_bwd")))
         _native = _m3torch
     return _native
 
@@ -513,3 +575,119 @@ def group_norm_bwd(dout, x, groups, weight=None, bias=None, z=None, center=True,
     r = _run("group_norm_bwd", stream, x, dout, x, groups, weight, bias, z, center, silu, eps, dx, dz,
              workspace)
     return dict(dx=r[0], dz=r[1], dweight=r[2], dbias=r[3])
+
+
+def gated_scan_fwd(x, r, i=None, decay=None, power=8.0, lerp=False, init=None, final=True, y=None,
+                   cu_seqlens=None, marks=False, stream=None):
+    """m3_gated_scan_fwd: the gated linear recurrence h_t = a_t h_{t-1} + w_t sigmoid(i_t) x_t of every
+    channel over prompts, with a_t = exp(-power softplus(decay) sigmoid(r_t)) and w_t = sqrt(1 - a_t^2), or with
+    ``lerp`` a_t = sigmoid(r_t + decay) and w_t = 1 - a_t.
+
+    x, r, i [b, L, C] (any strides, channels contiguous; no ``i``: no input gate), decay [C] fp32 (optional with
+    ``lerp``), init [b, C] fp32 or None. ``cu_seqlens`` [n + 1] int32, not descending: n sequences packed in
+    tensors of batch 1, states [n, C]. ``final=True`` allocates the final state, ``False``/None skips it, or
+    pass a tensor (it may be ``init``). ``y`` is allocated unless given (packed: zeroed, since rows of no sequence
+    are not written). ``marks=True`` allocates the states that spare gated_scan_bwd a pass, [b or 1,
+    ceil(L / 64), C] fp32, or pass a tensor. Returns (y, final state or None, marks or None)."""
+    return _run("gated_scan_fwd", stream, x, x, r, i, decay, power, lerp, init, final, y, cu_seqlens, marks)
+
+
+def gated_scan_step(x, r, state, i=None, decay=None, power=8.0, lerp=False, state_out=None, slots=None,
+                    y=None, stream=None):
+    """m3_gated_scan_step: one token of every sequence. x, r, i [b, C]; ``state`` [b, C] fp32, or with
+    ``slots`` [b] int32 a pool [n, C] of which sequence s has state slots[s] (outside [0, n): the sequence is
+    skipped and its y row is zero). ``state_out`` defaults to ``state`` (in place). Returns (y, state_out)."""
+    return _run("gated_scan_step", stream, x, x, r, i, decay, power, lerp, state, state_out, slots, y)
+
+
+def gated_scan_bwd(dy, x, r, i=None, decay=None, power=8.0, lerp=False, init=None, dfinal=None,
+                   cu_seqlens=None, marks=None, grads=None, want_init=True, workspace=None, stream=None):
+    """m3_gated_scan_bwd: gradients of sum(y * dy) + <final state, dfinal> for gated_scan_fwd on the same
+    arguments. ``marks``: that call's, or None (one more pass over the inputs). ``grads``: tensors (dx, dr, di) to
+    write (di None without ``i``; packed: allocated ones are zeroed). Returns a dict of dx, dr, di (None without
+    ``i``), ddecay ([C] fp32; None without ``decay``) and dinit ([n, C] fp32; None without ``want_init``;
+    pass a tensor to have it written there)."""
+    dx, dr, di = grads if grads is not None else (None, None, None)
+    g = _run("gated_scan_bwd", stream, x, x, r, i, decay, power, lerp, dy, init, dfinal, cu_seqlens, marks,
+             dx, dr, di, want_init, workspace)
+    return dict(dx=g[0], dr=g[1], di=g[2], ddecay=g[3], dinit=g[4])
+
+
+def rotary_frequencies(rotdim, base=10000.0, scaling=None, factor=1.0, trained=8192, fast=32.0, slow=1.0,
+                       device=None):
+    """The frequencies [rotdim / 2] (fp64, radians per position) for ``rotary``, and the scale that goes with them.
+
+    base^(-2 j / rotdim), reaching ``factor`` times beyond ``trained`` tokens by ``scaling``: None;
+    "linear" (all divided by the factor); "ntk" (base times factor^(rotdim / (rotdim - 2)), which divides the
+    slowest one by it); "yarn" (pairs that turn more than ``fast`` times in ``trained`` tokens stay, those
+    below ``slow`` turns are divided, a ramp over the pairs between; scale 0.1 ln(factor) + 1); "bands" (the
+    same with a ramp over the turns themselves, scale 1; use fast=4)."""
+    if rotdim < 0 or rotdim % 2:
+        raise ValueError(f"rotdim must be even and >= 0, not {rotdim}")
+    if scaling not in (None, "linear", "ntk", "yarn", "bands"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    if not (base > 1 and factor > 0 and trained > 0 and fast > slow > 0):
+        raise ValueError("base > 1, factor > 0, trained > 0 and fast > slow > 0 are needed")
+    n, scale = rotdim, 1.0
+    if scaling == "ntk" and n > 2:
+        base = base * factor ** (n / (n - 2))
+    j = torch.arange(n // 2, dtype=torch.float64)
+    f = base ** (-2 * j / max(n, 1))
+    keep = torch.ones_like(f)
+    if scaling == "linear":
+        keep = torch.zeros_like(f)
+    elif scaling == "yarn":
+        lo, hi = (n * math.log(trained / (t * 2 * math.pi)) / (2 * math.log(base)) for t in (fast, slow))
+        lo, hi = max(math.floor(lo), 0), min(math.ceil(hi), n - 1)
+        keep = 1 - ((j - lo) / max(hi - lo, 0.001)).clamp(0, 1)
+        scale = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+    elif scaling == "bands":
+        keep = ((trained * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
+    return (f / factor * (1 - keep) + f * keep).to(device), scale
+
+
+def rotary(q, k, freq, positions=None, offset=0, cu_seqlens=None, interleaved=False, inverse=False,
+           scale=1.0, q_out=None, k_out=None, stream=None):
+    """m3_rotary: q [b, L, Hq, D] (a step: [b, Hq, D]) and k (or None) with the first 2 len(freq) dimensions of
+    every head turned by position * freq, pairs (j, j + len(freq)) or with ``interleaved`` (2 j, 2 j + 1), times
+    ``scale``; the rest is copied. ``inverse`` turns back: the gradient. freq: fp64 (``rotary_frequencies``).
+    ``positions``: int32 or int64 [b, L] or [L] (a step: [b]), or None: the token's index in its sequence
+    (``cu_seqlens`` [n + 1] int32: n sequences packed in tensors of batch 1); ``offset`` is added. ``q_out``
+    and ``k_out`` are allocated unless given (packed: zeroed) and may be q and k. Returns (q_out, k_out)."""
+    return _run("rotary", stream, q, q, k, freq, positions, offset, cu_seqlens, interleaved, inverse, scale,
+                q_out, k_out)
+
+
+_POST = {None: 0, "rms": M3_BN_POST_RMS, "layer": M3_BN_POST_LAYER}
+_PRE = {None: 0, "rms": M3_BN_PRE_RMS, "layer": M3_BN_PRE_LAYER}
+_GATE = {None: 0, "sigmoid": M3_BN_SIGMOID, "silu": M3_BN_SILU}
+
+
+def _block_flags(post, pre, gate):
+    for name, value, known in (("post", post, _POST), ("pre", pre, _PRE), ("gate", gate, _GATE)):
+        if value not in known:
+            raise ValueError(f"{name} must be one of {tuple(known)}, not {value!r}")
+    return _POST[post] | _PRE[pre] | _GATE[gate]
+
+
+def block_norm_fwd(y, residual, z=None, gate=None, alpha=1.0, post=None, post_weight=None, post_bias=None,
+                   pre="rms", pre_weight=None, pre_bias=None, eps=1e-5, h=None, out=None, stream=None):
+    """m3_block_norm_fwd: what stands between two blocks, in one pass: h = residual + alpha post(y) act(z),
+    out = pre(h). y, z, out [..., C]; residual, h [..., C] of y's type or fp32. post and pre: None, "rms" or
+    "layer" (mean taken off), times weight plus bias (fp32 [C], optional; post's also without its norm). ``gate``:
+    None (z as it is), "sigmoid" or "silu". Rows may be slices of wider ones, z may be expanded over rows. h may
+    be residual, out may be y. Returns (h, out or None)."""
+    return _run("block_norm_fwd", stream, y, y, residual, z, post_weight, post_bias, pre_weight, pre_bias,
+                alpha, eps, _block_flags(post, pre, gate), h, out)
+
+
+def block_norm_bwd(dh, dout, y, residual, z=None, gate=None, alpha=1.0, post=None, post_weight=None,
+                   post_bias=None, pre="rms", pre_weight=None, pre_bias=None, eps=1e-5, dy=None,
+                   dresidual=None, dz=None, workspace=None, stream=None):
+    """m3_block_norm_bwd: gradients of sum(h * dh) + sum(out * dout) for block_norm_fwd on the same arguments;
+    dh None: zero, dout None: without a pre norm. dresidual may be dh, dy may be dout. Returns a dict of dy,
+    dresidual, dz (None without z; of z's full shape where it is expanded), and dpost_weight, dpost_bias,
+    dpre_weight, dpre_bias (fp32 [C]; None where the parameter is)."""
+    g = _run("block_norm_bwd", stream, y, y, residual, z, post_weight, post_bias, pre_weight, pre_bias, alpha,
+             eps, _block_flags(post, pre, gate), dh, dout, dy, dresidual, dz, workspace)
+    return dict(zip(("dy", "dresidual", "dz", "dpost_weight", "dpost_bias", "dpre_weight", "dpre_bias"), g))

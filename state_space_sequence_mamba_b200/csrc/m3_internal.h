@@ -122,6 +122,10 @@ cudaError_t launch_after_rms(void (*kernel)(KArgs...), unsigned grid, unsigned b
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
+// outs[o][c] = the sum over the shares of part[share][o][c] in a fixed order, for up to four outputs of C
+// columns (null ones are left out). May start while the kernel before it in the stream finishes.
+cudaError_t launch_sum_shares(const float* part, int shares, int64_t C, float* const* outs, int nouts,
+                              cudaStream_t s);
 // SM count of the calling thread's current device, looked up once per device (148, the
 // B200's count, when no device answers). Safe to call from several host threads.
 int device_sm_count();

@@ -1,5 +1,5 @@
-// Argument marshalling of linear attention and the grouped norm between torch tensors and the C ABI,
-// in C++: a decode step's kernels take a few microseconds, as long as a dozen attribute reads in
+// Argument marshalling of linear attention, the gated scan, rotary positions and the norms between torch
+// tensors and the C ABI, in C++: a decode step's kernels take a few microseconds, as long as a dozen attribute reads in
 // Python. Checks shapes, types and devices, allocates what the caller did not give, and calls the
 // library's entry points (whose addresses the Python side hands over, so that both use the library
 // that it loaded) on the tensors' device and its current stream. Computes nothing.
@@ -26,6 +26,14 @@ struct Api {
     decltype(&m3_group_norm_fwd) group_norm_fwd;
     decltype(&m3_group_norm_bwd_workspace_bytes) group_norm_bwd_workspace;
     decltype(&m3_group_norm_bwd) group_norm_bwd;
+    decltype(&m3_gated_scan_fwd) gated_scan_fwd;
+    decltype(&m3_gated_scan_step) gated_scan_step;
+    decltype(&m3_gated_scan_bwd_workspace_bytes) gated_scan_bwd_workspace;
+    decltype(&m3_gated_scan_bwd) gated_scan_bwd;
+    decltype(&m3_rotary) rotary;
+    decltype(&m3_block_norm_fwd) block_norm_fwd;
+    decltype(&m3_block_norm_bwd_workspace_bytes) block_norm_bwd_workspace;
+    decltype(&m3_block_norm_bwd) block_norm_bwd;
 } api;
 
 const Tensor& tensor(PyObject* o, const char* name) {
@@ -298,24 +306,20 @@ bool one_stride(const Tensor& t, int64_t lo, int64_t hi, int64_t* step) {
     return true;
 }
 
-// (batch, rows) and the views of tensors [..., C] of the first one's shape and type: their leading
-// dimensions cut where each part of every tensor's lies at one stride. Absent tensors are skipped.
+// (batch, rows) and the views of tensors [..., C] of the first one's shape and of the given types: their
+// leading dimensions cut where each part of every tensor's lies at one stride. Absent tensors are skipped.
 template <int N>
-void gn_views(m3_group_norm_dims& d, const Tensor* const (&ts)[N], const char* const (&names)[N], m3_view (&vs)[N]) {
+void row_views(const Tensor* const (&ts)[N], const char* const (&names)[N], const at::ScalarType (&types)[N], int64_t D,
+               int64_t* batch, int64_t* rows, m3_view (&vs)[N]) {
     const Tensor& x = *ts[0];
-    TORCH_CHECK_VALUE(x.is_cuda(), "tensors must be on a CUDA device");
-    TORCH_CHECK_VALUE(x.dim() >= 1 && x.size(-1) >= 1, "x needs a last dimension of channels");
     const int64_t lead = x.dim() - 1, C = x.size(lead);
-    d.channels = C;
-    d.in_dtype = dtype_code(x);
-    const int64_t D = d.groups > 0 ? C / d.groups : C;
     bool plain = true;
     for (int i = 0; i < N; ++i) {
         if (!ts[i]) continue;
         const Tensor& t = *ts[i];
         same_device(x, &t, names[i]);
         TORCH_CHECK_VALUE(t.sizes() == x.sizes(), names[i], " has shape ", t.sizes(), ", expected ", x.sizes());
-        TORCH_CHECK_VALUE(t.scalar_type() == x.scalar_type(), names[i], " is ", t.scalar_type(), ", expected ", x.scalar_type());
+        TORCH_CHECK_VALUE(t.scalar_type() == types[i], names[i], " is ", t.scalar_type(), ", expected ", types[i]);
         TORCH_CHECK_VALUE(t.stride(lead) == 1 || C == 1, names[i], ": the channels must be contiguous");
         plain = plain && t.is_contiguous();
     }
@@ -329,11 +333,24 @@ void gn_views(m3_group_norm_dims& d, const Tensor* const (&ts)[N], const char* c
             vs[i] = m3_view{ts[i]->data_ptr(), outer, inner, D};
         }
         if (!ok) continue;
-        d.batch = d.rows = 1;
-        for (int64_t i = 0; i < lead; ++i) (i < cut ? d.batch : d.rows) *= x.size(i);
+        *batch = *rows = 1;
+        for (int64_t i = 0; i < lead; ++i) *(i < cut ? batch : rows) *= x.size(i);
         return;
     }
     TORCH_CHECK_VALUE(false, "rows must lie at one stride, or at one in every batch entry");
+}
+
+// the same for tensors of the first one's type
+template <int N>
+void gn_views(m3_group_norm_dims& d, const Tensor* const (&ts)[N], const char* const (&names)[N], m3_view (&vs)[N]) {
+    const Tensor& x = *ts[0];
+    TORCH_CHECK_VALUE(x.is_cuda(), "tensors must be on a CUDA device");
+    TORCH_CHECK_VALUE(x.dim() >= 1 && x.size(-1) >= 1, "x needs a last dimension of channels");
+    d.channels = x.size(-1);
+    d.in_dtype = dtype_code(x);
+    at::ScalarType types[N];
+    for (at::ScalarType& t : types) t = x.scalar_type();
+    row_views<N>(ts, names, types, d.groups > 0 ? d.channels / d.groups : d.channels, &d.batch, &d.rows, vs);
 }
 
 m3_group_norm_dims gn_dims(PyObject* groups, PyObject* center, PyObject* silu, PyObject* eps) {
@@ -396,6 +413,358 @@ PyObject* group_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// ---- gated scan
+
+// a tensor [b, L, C], or a step's [b, C], by its strides
+m3_view rows_view(const Tensor& t, const char* name, at::IntArrayRef shape, at::ScalarType type, bool written = false) {
+    TORCH_CHECK_VALUE(t.sizes() == shape, name, " has shape ", t.sizes(), ", expected ", shape);
+    TORCH_CHECK_VALUE(t.scalar_type() == type, name, " is ", t.scalar_type(), ", expected ", type);
+    const int64_t n = t.dim();
+    TORCH_CHECK_VALUE(t.stride(n - 1) == 1 || shape[n - 1] <= 1, name, ": the channels must be contiguous");
+    for (int64_t i = 0; written && i < n; ++i)
+        TORCH_CHECK_VALUE(t.stride(i) != 0 || shape[i] <= 1, name, " is written and must not be expanded");
+    return m3_view{t.data_ptr(), t.stride(0), n == 3 ? t.stride(1) : 0, 0};
+}
+
+struct ScanArgs {
+    const Tensor *x, *r, *i, *decay, *cu;
+    m3_gated_scan_dims d;
+    m3_gated_scan_inputs in;
+};
+
+// x, r, i (or None), decay (or None), power, lerp
+ScanArgs scan_args(PyObject* const* a, PyObject* cu, int64_t nd) {
+    ScanArgs s{};
+    s.x = &tensor(a[0], "x");
+    s.r = &tensor(a[1], "r");
+    s.i = maybe(a[2], "i");
+    s.decay = maybe(a[3], "decay");
+    s.cu = maybe(cu, "cu_seqlens");
+    const Tensor& x = *s.x;
+    TORCH_CHECK_VALUE(x.is_cuda(), "tensors must be on a CUDA device");
+    TORCH_CHECK_VALUE(x.dim() == nd, "x must have ", nd, " dimensions");
+    same_device(x, s.r, "r");
+    same_device(x, s.i, "i");
+    same_device(x, s.decay, "decay");
+    same_device(x, s.cu, "cu_seqlens");
+    m3_gated_scan_dims& d = s.d;
+    d.nseq = x.size(0);
+    d.seqlen = nd == 3 ? x.size(1) : 1;
+    d.channels = x.size(nd - 1);
+    d.in_dtype = dtype_code(x);
+    d.power = static_cast<float>(number(a[4]));
+    d.flags = truth(a[5]) ? M3_GS_LERP : 0u;
+    const auto type = x.scalar_type();
+    s.in.x = rows_view(x, "x", x.sizes(), type);
+    s.in.r = rows_view(*s.r, "r", x.sizes(), type);
+    if (s.i) s.in.i = rows_view(*s.i, "i", x.sizes(), type);
+    s.in.decay = f32(s.decay, "decay", {d.channels});
+    TORCH_CHECK_VALUE(s.decay || (d.flags & M3_GS_LERP), "decay is needed without lerp");
+    s.in.cu_seqlens = i32(s.cu, "cu_seqlens", -1);
+    if (s.cu) {
+        TORCH_CHECK_VALUE(d.nseq == 1, "packed sequences lie in tensors of batch 1");
+        d.nseq = s.cu->size(0) - 1;
+        TORCH_CHECK_VALUE(d.nseq >= 0, "cu_seqlens needs at least one value");
+    }
+    return s;
+}
+
+// True: a new tensor of that shape; None or False: none; else the caller's
+Tensor wanted(PyObject* o, const char* name, const Tensor& ref, at::IntArrayRef shape) {
+    Tensor t;
+    if (o == Py_True) t = at::empty(shape, ref.options().dtype(at::kFloat));
+    else if (o != Py_None && o != Py_False) t = tensor(o, name);
+    if (t.defined()) same_device(ref, &t, name);
+    return t;
+}
+float* f32(const Tensor& t, const char* name, at::IntArrayRef shape) { return f32(t.defined() ? &t : nullptr, name, shape); }
+
+// the caller's output or a new one (packed: rows of no sequence are zero)
+Tensor output(PyObject* o, const char* name, const Tensor& like, bool packed) {
+    if (o != Py_None) {
+        const Tensor& t = tensor(o, name);
+        same_device(like, &t, name);
+        return t;
+    }
+    return packed ? at::zeros(like.sizes(), like.options()) : at::empty(like.sizes(), like.options());
+}
+
+// (x, r, i, decay, power, lerp, init, final, y, cu_seqlens, marks) -> (y, final, marks) or a status
+PyObject* gated_scan_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    TORCH_CHECK_TYPE(n == 11, "gated_scan_fwd takes 11 arguments");
+    const ScanArgs s = scan_args(a, a[9], 3);
+    const Tensor& x = *s.x;
+    const m3_gated_scan_dims& d = s.d;
+    const c10::cuda::CUDAGuard guard(x.device());
+    const Tensor* init = maybe(a[6], "init");
+    same_device(x, init, "init");
+    const int64_t states[2] = {d.nseq, d.channels};
+    const int64_t blocks[3] = {s.cu ? 1 : d.nseq, (d.seqlen + M3_GS_BLOCK - 1) / M3_GS_BLOCK, d.channels};
+    const Tensor fin = wanted(a[7], "final", x, states), marks = wanted(a[10], "marks", x, blocks);
+    const Tensor y = output(a[8], "y", x, s.cu != nullptr);
+    const m3_view yv = rows_view(y, "y", x.sizes(), x.scalar_type(), true);
+    const int rc = api.gated_scan_fwd(&d, &s.in, f32(init, "init", states), f32(fin, "final", states), &yv,
+                                      f32(marks, "marks", blocks), stream_of(x));
+    if (rc != M3_OK) return PyLong_FromLong(rc);
+    wrote(a[8], y);
+    wrote(a[7], fin);
+    wrote(a[10], marks);
+    return tuple({y, fin, marks});
+    END_HANDLE_TH_ERRORS
+}
+
+// (x, r, i, decay, power, lerp, state, state_out, slots, y) -> (y, state_out) or a status
+PyObject* gated_scan_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    TORCH_CHECK_TYPE(n == 10, "gated_scan_step takes 10 arguments");
+    const ScanArgs s = scan_args(a, Py_None, 2);
+    const Tensor& x = *s.x;
+    const m3_gated_scan_dims& d = s.d;
+    const c10::cuda::CUDAGuard guard(x.device());
+    const Tensor& state = tensor(a[6], "state");
+    const Tensor& out = a[7] == Py_None ? state : tensor(a[7], "state_out");
+    const Tensor* slots = maybe(a[8], "slots");
+    same_device(x, &state, "state");
+    same_device(x, &out, "state_out");
+    same_device(x, slots, "slots");
+    TORCH_CHECK_VALUE(state.dim() == 2, "state must have 2 dimensions");
+    const int64_t states[2] = {slots ? state.size(0) : d.nseq, d.channels};
+    const Tensor y = output(a[9], "y", x, false);
+    const m3_view yv = rows_view(y, "y", x.sizes(), x.scalar_type(), true);
+    const int rc = api.gated_scan_step(&d, &s.in, f32(&state, "state", states), f32(&out, "state_out", states), states[0],
+                                       i32(slots, "slots", d.nseq), &yv, stream_of(x));
+    if (rc != M3_OK) return PyLong_FromLong(rc);
+    wrote(a[9], y);
+    wrote(a[7] == Py_None ? a[6] : a[7], out);
+    return tuple({y, out});
+    END_HANDLE_TH_ERRORS
+}
+
+// (x, r, i, decay, power, lerp, dy, init, dfinal, cu_seqlens, marks, dx, dr, di, want_init, workspace)
+// -> (dx, dr, di, ddecay, dinit) or a status
+PyObject* gated_scan_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    TORCH_CHECK_TYPE(n == 16, "gated_scan_bwd takes 16 arguments");
+    const ScanArgs s = scan_args(a, a[9], 3);
+    const Tensor& x = *s.x;
+    const m3_gated_scan_dims& d = s.d;
+    const c10::cuda::CUDAGuard guard(x.device());
+    const Tensor& dy = tensor(a[6], "dy");
+    const Tensor *init = maybe(a[7], "init"), *dfinal = maybe(a[8], "dfinal"), *marks = maybe(a[10], "marks");
+    same_device(x, &dy, "dy");
+    same_device(x, init, "init");
+    same_device(x, dfinal, "dfinal");
+    same_device(x, marks, "marks");
+    const int64_t states[2] = {d.nseq, d.channels};
+    const int64_t blocks[3] = {s.cu ? 1 : d.nseq, (d.seqlen + M3_GS_BLOCK - 1) / M3_GS_BLOCK, d.channels};
+    const bool packed = s.cu != nullptr;
+    const Tensor dx = output(a[11], "dx", x, packed), dr = output(a[12], "dr", x, packed);
+    Tensor di, dd;
+    if (s.i) di = output(a[13], "di", x, packed);
+    if (s.decay) dd = at::empty({d.channels}, s.decay->options());
+    const Tensor dinit = wanted(a[14], "want_init", x, states);
+    const auto type = x.scalar_type();
+    const m3_view dyv = rows_view(dy, "dy", x.sizes(), type);
+    m3_gated_scan_grads g{};
+    g.dx = rows_view(dx, "dx", x.sizes(), type, true);
+    g.dr = rows_view(dr, "dr", x.sizes(), type, true);
+    if (s.i) g.di = rows_view(di, "di", x.sizes(), type, true);
+    const Tensor ws = workspace(maybe(a[15], "workspace"), api.gated_scan_bwd_workspace(&d, packed, marks != nullptr), x);
+    const int rc = api.gated_scan_bwd(&d, &s.in, f32(init, "init", states), f32(marks, "marks", blocks), &dyv,
+                                      f32(dfinal, "dfinal", states), &g, static_cast<float*>(data(dd)),
+                                      f32(dinit, "dinit", states), data(ws), bytes(ws), stream_of(x));
+    if (rc != M3_OK) return PyLong_FromLong(rc);
+    wrote(a[11], dx);
+    wrote(a[12], dr);
+    if (s.i) wrote(a[13], di);
+    wrote(a[14], dinit);
+    return tuple({dx, dr, di, dd, dinit});
+    END_HANDLE_TH_ERRORS
+}
+
+// ---- rotary positions
+
+// (q, k, freq, positions, offset, cu_seqlens, interleaved, inverse, scale, q_out, k_out) -> (q_out, k_out) or a status
+PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    TORCH_CHECK_TYPE(n == 11, "rotary takes 11 arguments");
+    const Tensor& q = tensor(a[0], "q");
+    const Tensor* k = maybe(a[1], "k");
+    const Tensor& freq = tensor(a[2], "freq");
+    const Tensor *pos = maybe(a[3], "positions"), *cu = maybe(a[5], "cu_seqlens");
+    TORCH_CHECK_VALUE(q.is_cuda(), "tensors must be on a CUDA device");
+    const c10::cuda::CUDAGuard guard(q.device());
+    const int64_t nd = q.dim();
+    TORCH_CHECK_VALUE(nd == 3 || nd == 4, "q must have 3 or 4 dimensions");
+    TORCH_CHECK_VALUE(!k || k->dim() == nd, "k must have q's dimensions");
+    same_device(q, k, "k");
+    same_device(q, &freq, "freq");
+    same_device(q, pos, "positions");
+    same_device(q, cu, "cu_seqlens");
+    const int64_t b = q.size(0), L = nd == 4 ? q.size(1) : 1;
+    m3_rotary_dims d{};
+    d.nseq = b;
+    d.seqlen = L;
+    d.qheads = q.size(nd - 2);
+    d.kheads = k ? k->size(nd - 2) : 0;
+    d.headdim = q.size(nd - 1);
+    d.offset = integer(a[4]);
+    d.in_dtype = dtype_code(q);
+    d.scale = static_cast<float>(number(a[8]));
+    d.flags = (truth(a[6]) ? M3_ROT_INTERLEAVED : 0u) | (truth(a[7]) ? M3_ROT_INVERSE : 0u);
+    TORCH_CHECK_VALUE(freq.dim() == 1 && freq.scalar_type() == at::kDouble && freq.is_contiguous(),
+                      "freq must be a contiguous float64 vector");
+    d.rotdim = 2 * freq.size(0);
+    if (cu) {
+        TORCH_CHECK_VALUE(nd == 4 && b == 1, "packed sequences lie in tensors [1, rows, heads, dim]");
+        TORCH_CHECK_VALUE(cu->dim() == 1 && cu->size(0) >= 1, "cu_seqlens needs at least one value");
+        d.nseq = cu->size(0) - 1;
+    }
+    int64_t pb = 0, pt = 0;
+    if (pos) {
+        const bool wide = pos->scalar_type() == at::kLong;
+        TORCH_CHECK_VALUE(wide || pos->scalar_type() == at::kInt, "positions must be int32 or int64");
+        if (wide) d.flags |= M3_ROT_POS64;
+        if (nd == 3) {
+            TORCH_CHECK_VALUE(pos->dim() == 1 && pos->size(0) == b, "positions has shape ", pos->sizes(), ", expected [", b, "]");
+            pb = pos->stride(0);
+        } else if (pos->dim() == 1) {
+            TORCH_CHECK_VALUE(pos->size(0) == L, "positions has shape ", pos->sizes(), ", expected [", L, "] or [", b, ", ", L, "]");
+            pt = pos->stride(0);
+        } else {
+            TORCH_CHECK_VALUE(pos->dim() == 2 && pos->size(0) == b && pos->size(1) == L, "positions has shape ", pos->sizes(),
+                              ", expected [", L, "] or [", b, ", ", L, "]");
+            pb = pos->stride(0);
+            pt = pos->stride(1);
+        }
+    }
+    const Tensor qo = output(a[9], "q_out", q, cu != nullptr);
+    Tensor ko;
+    if (k) ko = output(a[10], "k_out", *k, cu != nullptr);
+    const auto type = q.scalar_type();
+    const m3_view qv = view(q, "q", q.sizes(), type), qov = out_view(qo, "q_out", q.sizes(), type);
+    m3_view kv{}, kov{};
+    if (k) {
+        const int64_t s4[4] = {b, L, d.kheads, d.headdim}, s3[3] = {b, d.kheads, d.headdim};
+        const at::IntArrayRef shape = nd == 4 ? at::IntArrayRef(s4, 4) : at::IntArrayRef(s3, 3);
+        kv = view(*k, "k", shape, type);
+        kov = out_view(ko, "k_out", shape, type);
+    }
+    const int rc = api.rotary(&d, &qv, &kv, static_cast<const double*>(freq.data_ptr()), pos ? pos->data_ptr() : nullptr, pb, pt,
+                              i32(cu, "cu_seqlens", -1), &qov, &kov, stream_of(q));
+    if (rc != M3_OK) return PyLong_FromLong(rc);
+    wrote(a[9], qo);
+    if (k) wrote(a[10], ko);
+    return tuple({qo, ko});
+    END_HANDLE_TH_ERRORS
+}
+
+// ---- block norm
+
+struct BlockArgs {
+    const Tensor *y, *x, *z;
+    m3_block_norm_dims d;
+    m3_block_norm_inputs in;
+};
+
+// (y, residual, z, post_weight, post_bias, pre_weight, pre_bias, alpha, eps, flags)
+BlockArgs block_args(PyObject* const* a) {
+    BlockArgs s{};
+    s.y = &tensor(a[0], "y");
+    s.x = &tensor(a[1], "residual");
+    s.z = maybe(a[2], "z");
+    const Tensor& y = *s.y;
+    TORCH_CHECK_VALUE(y.is_cuda(), "tensors must be on a CUDA device");
+    TORCH_CHECK_VALUE(y.dim() >= 1 && y.size(-1) >= 1, "y needs a last dimension of channels");
+    m3_block_norm_dims& d = s.d;
+    d.channels = y.size(-1);
+    d.in_dtype = dtype_code(y);
+    d.res_dtype = dtype_code(*s.x);
+    d.alpha = static_cast<float>(number(a[7]));
+    d.eps = static_cast<float>(number(a[8]));
+    d.flags = static_cast<uint32_t>(integer(a[9]));
+    const char* const names[4] = {"post_weight", "post_bias", "pre_weight", "pre_bias"};
+    const float** const to[4] = {&s.in.post_weight, &s.in.post_bias, &s.in.pre_weight, &s.in.pre_bias};
+    for (int i = 0; i < 4; ++i) {
+        const Tensor* t = maybe(a[3 + i], names[i]);
+        same_device(y, t, names[i]);
+        *to[i] = f32(t, names[i], {d.channels});
+    }
+    return s;
+}
+
+// (block_args ..., h, out) -> (h, out) or a status
+PyObject* block_norm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    TORCH_CHECK_TYPE(n == 12, "block_norm_fwd takes 12 arguments");
+    BlockArgs s = block_args(a);
+    const Tensor &y = *s.y, &x = *s.x;
+    const c10::cuda::CUDAGuard guard(y.device());
+    const bool pre = s.d.flags & (M3_BN_PRE_RMS | M3_BN_PRE_LAYER);
+    same_device(y, &x, "residual");
+    const Tensor h = a[10] != Py_None ? tensor(a[10], "h") : at::empty(y.sizes(), x.options());
+    Tensor out;
+    if (pre) out = a[11] != Py_None ? tensor(a[11], "out") : at::empty(y.sizes(), y.options());
+    const auto ty = y.scalar_type(), tx = x.scalar_type();
+    m3_view v[5];
+    row_views<5>({&y, &x, s.z, &h, pre ? &out : nullptr}, {"y", "residual", "z", "h", "out"}, {ty, tx, ty, tx, ty}, 0,
+                 &s.d.batch, &s.d.rows, v);
+    s.in.y = v[0];
+    s.in.residual = v[1];
+    s.in.z = v[2];
+    const int rc = api.block_norm_fwd(&s.d, &s.in, &v[3], &v[4], stream_of(y));
+    if (rc != M3_OK) return PyLong_FromLong(rc);
+    wrote(a[10], h);
+    if (pre) wrote(a[11], out);
+    return tuple({h, out});
+    END_HANDLE_TH_ERRORS
+}
+
+// (block_args ..., dh, dout, dy, dresidual, dz, workspace)
+// -> (dy, dresidual, dz, dpost_weight, dpost_bias, dpre_weight, dpre_bias) or a status
+PyObject* block_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    TORCH_CHECK_TYPE(n == 16, "block_norm_bwd takes 16 arguments");
+    BlockArgs s = block_args(a);
+    const Tensor &y = *s.y, &x = *s.x;
+    const c10::cuda::CUDAGuard guard(y.device());
+    const bool pre = s.d.flags & (M3_BN_PRE_RMS | M3_BN_PRE_LAYER);
+    same_device(y, &x, "residual");
+    const Tensor *dh = maybe(a[10], "dh"), *dout = maybe(a[11], "dout");
+    TORCH_CHECK_VALUE(!pre == !dout, pre ? "dout is needed with a pre norm" : "dout without a pre norm");
+    const Tensor dy = a[12] != Py_None ? tensor(a[12], "dy") : at::empty(y.sizes(), y.options());
+    const Tensor dx = a[13] != Py_None ? tensor(a[13], "dresidual") : at::empty(y.sizes(), x.options());
+    Tensor dz, sums[4];
+    if (s.z) dz = a[14] != Py_None ? tensor(a[14], "dz") : at::empty(y.sizes(), y.options());
+    const auto ty = y.scalar_type(), tx = x.scalar_type();
+    m3_view v[8];
+    row_views<8>({&y, &x, s.z, dh, dout, &dy, &dx, s.z ? &dz : nullptr},
+                 {"y", "residual", "z", "dh", "dout", "dy", "dresidual", "dz"}, {ty, tx, ty, tx, ty, ty, tx, ty}, 0,
+                 &s.d.batch, &s.d.rows, v);
+    s.in.y = v[0];
+    s.in.residual = v[1];
+    s.in.z = v[2];
+    m3_block_norm_grads g{};
+    g.dy = v[5];
+    g.dresidual = v[6];
+    g.dz = v[7];
+    float** const to[4] = {&g.dpost_weight, &g.dpost_bias, &g.dpre_weight, &g.dpre_bias};
+    for (int i = 0; i < 4; ++i)
+        if (a[3 + i] != Py_None) {
+            sums[i] = at::empty({s.d.channels}, y.options().dtype(at::kFloat));
+            *to[i] = static_cast<float*>(sums[i].data_ptr());
+        }
+    const Tensor ws = workspace(maybe(a[15], "workspace"), api.block_norm_bwd_workspace(&s.d), y);
+    const int rc = api.block_norm_bwd(&s.d, &s.in, &v[3], &v[4], &g, data(ws), bytes(ws), stream_of(y));
+    if (rc != M3_OK) return PyLong_FromLong(rc);
+    wrote(a[12], dy);
+    wrote(a[13], dx);
+    if (s.z) wrote(a[14], dz);
+    return tuple({dy, dx, dz, sums[0], sums[1], sums[2], sums[3]});
+    END_HANDLE_TH_ERRORS
+}
+
 // bind(addresses of the entry points, in Api's order)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -414,6 +783,9 @@ PyMethodDef method(const char* name) {
 PyMethodDef methods[] = {method<bind>("bind"), method<linattn_fwd>("linattn_fwd"),
                          method<linattn_step>("linattn_step"), method<linattn_bwd>("linattn_bwd"),
                          method<group_norm_fwd>("group_norm_fwd"), method<group_norm_bwd>("group_norm_bwd"),
+                         method<gated_scan_fwd>("gated_scan_fwd"), method<gated_scan_step>("gated_scan_step"),
+                         method<gated_scan_bwd>("gated_scan_bwd"), method<rotary>("rotary"),
+                         method<block_norm_fwd>("block_norm_fwd"), method<block_norm_bwd>("block_norm_bwd"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_m3torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
