@@ -2,10 +2,10 @@
 //     n = post(y),  h = x + alpha n act(z),  out = pre(h)
 //
 // Bound by HBM: the forward reads y, x, z and writes h, out, the backward reads those inputs, dh and dout
-// and writes dy, dx, dz, each once. A row lies in the registers of a team of W warps (NV 16-byte vectors
-// a lane), so h goes from its residual into the second norm's statistics without a trip through memory, and the
+// and writes dy, dx, dz, each once. A row lies in the registers of a team of W warps (NV parts of four
+// channels a lane), so h goes from its residual into the second norm's statistics without a trip through memory, and the
 // deviations are squared from registers. Teams walk over rows, the next row's loads in flight. Rows too
-// wide, or not 16-byte aligned, take one CTA each with scalar loads.
+// wide, or not aligned to parts, take one CTA each with scalar loads.
 //
 // Backward, with yh = (y - mean) ry, hh = (h - mean) rh, n = yh w1 + b1 and go = dout w2:
 //     d  = dh + rh (go - hh mean(go hh) - mean(go) [layer]),     dx = d
@@ -17,6 +17,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <type_traits>
 
 #include "m3_common.cuh"
 #include "m3_internal.h"
@@ -31,8 +32,8 @@ struct BnTensor {
     void* p;
     int64_t batch, row;         // strides in elements
 };
-enum Norm { kNone = 0, kRms = 1, kLayer = 2 };
-enum Act { kIdentity = 0, kSigmoid = 1, kSilu = 2 };
+enum Norm { kNone = 0, kRms = 1, kLayerNorm = 2 };
+enum Act { kIdentity = 0, kSigmoid = 1, kSilu = 2, kNoGate = 3 };
 struct BnParams {
     uint32_t rows, inner;       // rows in all, and of each batch entry
     int C, post, pre, act;
@@ -50,42 +51,46 @@ __device__ __forceinline__ T* at(const BnTensor& t, const BnParams& p, uint32_t 
     return static_cast<T*>(t.p) + b * t.batch + static_cast<int64_t>(row - b * p.inner) * t.row;
 }
 
-// N elements of TR where a 16-byte vector of the block's type has N: as bits, and as pairs of floats
+// A thread's part of a row: the N channels of one 16-byte word of the block's type. A tensor of TR has U words of them.
+template <typename T>
+constexpr int channels() { return 16 / static_cast<int>(sizeof(T)); }
 template <typename TR, int N>
-struct Part {
-    static constexpr int Q = N * static_cast<int>(sizeof(TR)) / 16;     // 16-byte words
-    uint4 w[Q];
-    __device__ __forceinline__ void zero() {
+constexpr int words() { return N * static_cast<int>(sizeof(TR)) / 16; }
+template <typename TR, int N, int U>
+__device__ __forceinline__ void unpack(const uint4 (&w)[U], float2 (&f)[N / 2]) {
 #pragma unroll
-        for (int i = 0; i < Q; ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
-    }
-    __device__ __forceinline__ void load(const TR* p) {
-#pragma unroll
-        for (int i = 0; i < Q; ++i) w[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
-    }
-    __device__ __forceinline__ void unpack(float2 (&f)[N / 2]) const {
-#pragma unroll
-        for (int i = 0; i < Q; ++i) Vec<TR>::unpack(w[i], f + i * Vec<TR>::N);
-    }
-    static __device__ __forceinline__ void store(TR* p, const float2 (&f)[N / 2]) {
-#pragma unroll
-        for (int i = 0; i < Q; ++i) Vec<TR>::store(p + i * 2 * Vec<TR>::N, f + i * Vec<TR>::N);
-    }
-};
-
-__device__ __forceinline__ float2 act2(int act, const float2& z) {
-    if (act == kIdentity) return z;
-    const float2 s = sigmoid2(z);
-    return act == kSigmoid ? s : mul2(z, s);
+    for (int u = 0; u < U; ++u) Vec<TR>::unpack(w[u], f + u * Vec<TR>::N);
 }
-__device__ __forceinline__ void act_slope2(int act, const float2& z, float2* a, float2* da) {
-    if (act == kIdentity) {
+template <typename TR, int N>
+__device__ __forceinline__ void store(TR* p, const float2 (&f)[N / 2]) {
+    constexpr int U = words<TR, N>();
+#pragma unroll
+    for (int u = 0; u < U; ++u) Vec<TR>::store(p + u * 2 * Vec<TR>::N, f + u * Vec<TR>::N);
+}
+// 16 bytes from memory to this thread's place in shared memory, without waiting for them
+__device__ __forceinline__ void copy_async(uint4* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sm100::smem_u32(dst)), "l"(src) : "memory");
+}
+template <int keep>
+__device__ __forceinline__ void copies_left() { asm volatile("cp.async.wait_group %0;" ::"n"(keep) : "memory"); }
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// The gate and its slope. kNoGate: one, without z.
+template <int kAct>
+__device__ __forceinline__ float2 act2(const float2& z) {
+    if (kAct == kIdentity) return z;
+    const float2 s = sigmoid2(z);
+    return kAct == kSigmoid ? s : mul2(z, s);
+}
+template <int kAct>
+__device__ __forceinline__ void act_slope2(const float2& z, float2* a, float2* da) {
+    if (kAct == kIdentity) {
         *a = z;
         *da = both(1.f);
         return;
     }
     const float2 s = sigmoid2(z), t = fma2(s, both(-1.f), both(1.f));
-    if (act == kSigmoid) {
+    if (kAct == kSigmoid) {
         *a = s;
         *da = mul2(s, t);
     } else {
@@ -93,341 +98,594 @@ __device__ __forceinline__ void act_slope2(int act, const float2& z, float2* a, 
         *da = fma2(*a, t, s);       // s (1 + z (1 - s))
     }
 }
+template <int k>
+struct ActIs {
+    static constexpr int value = k;
+};
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F&& f) {
+    if (act == kSilu) f(ActIs<kSilu>{});
+    else if (act == kSigmoid) f(ActIs<kSigmoid>{});
+    else if (act == kIdentity) f(ActIs<kIdentity>{});
+    else f(ActIs<kNoGate>{});
+}
 
-// A team: W warps that hold one row. Its sums go through shared memory, in turn through one of two places, so
-// that one barrier a sum is enough.
+// A team: W warps that hold one row. K sums at once: a warp halves what each lane holds as it adds (K - 1 shuffles and
+// the rest of the tree, in place of 5 K), the warps' sums meet in shared memory behind one barrier, in two places in turn.
 template <int W, int kTeams>
 struct Team {
-    float2 (*s)[kTeams][W];
+    float (*s)[kTeams][W][16];
     int team, warp, lane, turn = 0;
-    __device__ __forceinline__ explicit Team(float2 (*places)[kTeams][W]) : s(places) {
-        team = threadIdx.x / (32 * W);
+    __device__ __forceinline__ explicit Team(float (*places)[kTeams][W][16]) : s(places) {
+        team = kTeams == 1 ? 0 : threadIdx.x / (32 * W);
         warp = (threadIdx.x / 32) % W;
         lane = threadIdx.x & 31;
     }
-    __device__ __forceinline__ float2 sum(float2 v) {
+    template <int K>        // a power of two
+    __device__ __forceinline__ void sum(float (&a)[K]) {
+        constexpr int per = 32 / K;     // lane per j + i ends with the sum of value j
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const float2 u = make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o));
-            v = add2(v, u);
+        for (int n = K / 2; n >= 1; n /= 2) {
+            const bool up = lane & (per * n);
+#pragma unroll
+            for (int k = 0; k < n; ++k) {
+                const float give = up ? a[k] : a[k + n], keep = up ? a[k + n] : a[k];
+                a[k] = keep + __shfl_xor_sync(0xffffffffu, give, per * n);
+            }
         }
-        if (W == 1) return v;
-        if (lane == 0) s[turn][team][warp] = v;
+        float t = a[0];
+#pragma unroll
+        for (int o = per / 2; o >= 1; o /= 2) t += __shfl_xor_sync(0xffffffffu, t, o);
+        if (W == 1) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) a[k] = __shfl_sync(0xffffffffu, t, per * k);
+            return;
+        }
+        if (lane % per == 0) s[turn][team][warp][lane / per] = t;
         asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(32 * W) : "memory");
-        v = s[turn][team][0];
+        // lane K w + j takes value j of warps w, w + per, ...
+        t = lane / K < W ? s[turn][team][lane / K][lane % K] : 0.f;
 #pragma unroll
-        for (int w = 1; w < W; ++w) v = add2(v, s[turn][team][w]);
+        for (int w = per; w < W; w += per) t += s[turn][team][w + lane / K][lane % K];
         turn ^= 1;
-        return v;
-    }
-    __device__ __forceinline__ float sum(float v) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (W == 1) return v;
-        if (lane == 0) s[turn][team][warp].x = v;
-        asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(32 * W) : "memory");
-        v = s[turn][team][0].x;
+        for (int o = K; o < K * W && o < 32; o *= 2) t += __shfl_xor_sync(0xffffffffu, t, o);
 #pragma unroll
-        for (int w = 1; w < W; ++w) v += s[turn][team][w].x;
-        turn ^= 1;
-        return v;
+        for (int k = 0; k < K; ++k) a[k] = __shfl_sync(0xffffffffu, t, k);
     }
 };
 
-// v becomes its deviations over the root of its variance (or v over its root mean square); returns the factor.
-// Elements beyond the row hold zeros and keep them.
-template <int NV, int H, typename T>
-__device__ __forceinline__ float normalise(T& team, float2 (&v)[NV][H], const bool (&in)[NV], int kind, float inv, float eps) {
-    if (kind == kNone) return 1.f;
-    if (kind == kLayer) {
-        float2 s = both(0.f);
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int e = 0; e < H; ++e) s = add2(s, v[i][e]);
-        const float m = team.sum(s.x + s.y) * inv;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const float2 mi = both(in[i] ? -m : 0.f);
-#pragma unroll
-            for (int e = 0; e < H; ++e) v[i][e] = add2(v[i][e], mi);
-        }
+// One tensor's rows in the order that a team walks through them.
+template <typename T>
+struct RowPtr {
+    T* q;
+    int64_t step;
+    __device__ __forceinline__ RowPtr(const BnTensor& t, const BnParams& p, uint32_t row, uint32_t by)
+        : q(t.p && row < p.rows ? at<T>(t, p, row) : nullptr), step(static_cast<int64_t>(by) * t.row) {}
+    // to the row `row`, `by` behind the last one
+    __device__ __forceinline__ void next(const BnTensor& t, const BnParams& p, uint32_t row) {
+        if (p.inner == p.rows) q += step;
+        else if (row < p.rows && t.p) q = at<T>(t, p, row);
     }
-    float2 q = both(0.f);
+};
+
+// The channels' parameters, in shared memory as the threads read them: word q of vector i of thread t lies beside the
+// other threads' (from the L1 they would be a wait each, and the rows push them out of it). Parts beyond the row hold zeros.
+struct Params {
+    const float4* w[4];         // w1, b1, w2, b2 of this thread, or null
+};
+template <int W, int NV, int N>
+__device__ __forceinline__ Params load_params(const BnParams& p, float4* room) {
+    constexpr int Q = N / 4, kPlanes = NV * Q;
+    const float* const from[4] = {p.w1, p.b1, p.w2, p.b2};
+    Params r{};
+    const int t = threadIdx.x % (32 * W);
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int k = 0; k < 4; ++k) {
+        if (!from[k]) continue;
+        r.w[k] = room + t;
+        if (threadIdx.x < 32 * W)
 #pragma unroll
-        for (int e = 0; e < H; ++e) q = fma2(v[i][e], v[i][e], q);
-    const float r = rsqrtf(fmaf(team.sum(q.x + q.y), inv, eps));
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int e = 0; e < H; ++e) v[i][e] = in[i] ? mul2(v[i][e], both(r)) : both(0.f);
+            for (int i = 0; i < kPlanes; ++i) {
+                const int c = ((i / Q) * 32 * W + t) * N + 4 * (i % Q);
+                room[i * 32 * W + t] = c < p.C ? make_float4(__ldg(from[k] + c), __ldg(from[k] + c + 1), __ldg(from[k] + c + 2), __ldg(from[k] + c + 3))
+                                               : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        room += kPlanes * 32 * W;
+    }
     return r;
 }
-
-// a channel's parameters, or `other` without any
-template <int H>
-__device__ __forceinline__ void params(const float* w, int c, bool in, float other, float2 (&f)[H]) {
+// v times a channel's weight plus its bias, where there are any
+template <int W, int N>
+__device__ __forceinline__ void scaled(const float4* w, const float4* b, int i, float2 (&v)[N / 2]) {
+    constexpr int Q = N / 4;
 #pragma unroll
-    for (int e = 0; e < H; ++e) f[e] = w && in ? make_float2(__ldg(w + c + 2 * e), __ldg(w + c + 2 * e + 1)) : both(other);
+    for (int q = 0; q < Q; ++q) {
+        if (w) {
+            const float4 f = w[(i * Q + q) * 32 * W];
+            v[2 * q] = mul2(v[2 * q], make_float2(f.x, f.y));
+            v[2 * q + 1] = mul2(v[2 * q + 1], make_float2(f.z, f.w));
+        }
+        if (b) {
+            const float4 f = b[(i * Q + q) * 32 * W];
+            v[2 * q] = add2(v[2 * q], make_float2(f.x, f.y));
+            v[2 * q + 1] = add2(v[2 * q + 1], make_float2(f.z, f.w));
+        }
+    }
 }
 
 template <int W>
 constexpr int block_threads() { return 32 * (W > 8 ? W : 8); }
 
-template <typename T, typename TR, int W, int NV>
-__global__ void __launch_bounds__(block_threads<W>()) bn_fwd_kernel(const __grid_constant__ BnParams p) {
-    constexpr int N = 16 / sizeof(T), H = N / 2, kTeams = block_threads<W>() / (32 * W);
-    __shared__ float2 s_sum[2][kTeams][W];
+// kLayer: one of the norms takes its mean off; without it, the sum of y^2 of the next row comes with h^2 of this one,
+// and a row has one meeting.
+template <typename T, typename TR, int W, int NV, bool kLayer>
+__global__ void __launch_bounds__(block_threads<W>(), 512 / block_threads<W>()) bn_fwd_kernel(const __grid_constant__ BnParams p) {
+    constexpr int kTeams = block_threads<W>() / (32 * W), N = channels<T>(), H = N / 2, U = words<TR, N>();
+    __shared__ float s_sum[2][kTeams][W][16];
+    extern __shared__ float4 s_dyn[];       // the parameters
     Team<W, kTeams> team(s_sum);
-    const int t = threadIdx.x % (32 * W);
-    int c[NV];
+    const Params w = load_params<W, NV, N>(p, s_dyn);
+    __syncthreads();
+    const int c0 = static_cast<int>(threadIdx.x % (32 * W)) * N;
+    constexpr int kStep = 32 * W * N;       // channels from part to part
     bool in[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        c[i] = (i * 32 * W + t) * N;
-        in[i] = c[i] < p.C;
-    }
+    for (int i = 0; i < NV; ++i) in[i] = c0 + i * kStep < p.C;
     const float inv = 1.f / p.C;
-    Part<T, N> ry[NV], rz[NV];
-    Part<TR, N> rx[NV];
-    const auto fetch = [&](uint32_t row) {
-        const bool live = row < p.rows;
-        const T* y = live ? at<const T>(p.y, p, row) : nullptr;
-        const T* z = live && p.z.p ? at<const T>(p.z, p, row) : nullptr;
-        const TR* x = live ? at<const TR>(p.x, p, row) : nullptr;
+    const uint32_t step = gridDim.x * kTeams;
+    uint32_t row = blockIdx.x * kTeams + team.team;
+    RowPtr<const T> y(p.y, p, row, step), z(p.z, p, row, step);
+    RowPtr<const TR> x(p.x, p, row, step);
+    RowPtr<T> out(p.out, p, row, step);
+    RowPtr<TR> h(p.h, p, row, step);
+    uint4 ry[NV][1] = {}, rz[NV][1] = {}, rx[NV][U] = {};
+    const auto fetch = [&](bool live) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            ry[i].zero();
-            rx[i].zero();
-            rz[i].zero();
             if (!live || !in[i]) continue;
-            ry[i].load(y + c[i]);
-            rx[i].load(x + c[i]);
-            if (z) rz[i].load(z + c[i]);
+            ry[i][0] = __ldcs(reinterpret_cast<const uint4*>(y.q + c0 + i * kStep));
+#pragma unroll
+            for (int u = 0; u < U; ++u) rx[i][u] = __ldcs(reinterpret_cast<const uint4*>(x.q + c0 + i * kStep) + u);
+            if (p.z.p) rz[i][0] = __ldcs(reinterpret_cast<const uint4*>(z.q + c0 + i * kStep));
+        }
+    };
+    // the mean of a row's values (zero beyond the row), and the sum of what deviates from it squared
+    const auto mean = [&](const float2 (&v)[NV][H]) {
+        float2 s = both(0.f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < H; ++e) s = add2(s, v[i][e]);
+        float a[1] = {s.x + s.y};
+        team.sum(a);
+        return a[0] * inv;
+    };
+    const auto squares = [&](const float2 (&v)[NV][H]) {
+        float2 s = both(0.f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < H; ++e) s = fma2(v[i][e], v[i][e], s);
+        return s.x + s.y;
+    };
+    const auto centre = [&](float2 (&v)[NV][H]) {
+        const float m = mean(v);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < H; ++e) v[i][e] = add2(v[i][e], both(in[i] ? -m : 0.f));
+    };
+    const auto spread = [&](float sum) { return rsqrtf(fmaf(sum, inv, p.eps)); };
+    fetch(row < p.rows);
+    float r1 = 1.f;
+    if (!kLayer && p.post != kNone) {
+        float2 v[NV][H];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) unpack<T, N>(ry[i], v[i]);
+        float a[1] = {squares(v)};
+        team.sum(a);
+        r1 = spread(a[0]);
+    }
+    for (; row < p.rows; row += step) {
+        float2 v[NV][H];
+        uint4 cx[NV][U], cz[NV][1];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            unpack<T, N>(ry[i], v[i]);
+            cz[i][0] = rz[i][0];
+#pragma unroll
+            for (int u = 0; u < U; ++u) cx[i][u] = rx[i][u];
+        }
+        y.next(p.y, p, row + step);
+        x.next(p.x, p, row + step);
+        z.next(p.z, p, row + step);
+        fetch(row + step < p.rows);
+        if (kLayer && p.post != kNone) {
+            if (p.post == kLayerNorm) centre(v);
+            float a[1] = {squares(v)};
+            team.sum(a);
+            r1 = spread(a[0]);
+        }
+        with_act(p.act, [&](auto act) {
+            constexpr int kAct = decltype(act)::value;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float2 u[H], g[H];
+#pragma unroll
+                for (int e = 0; e < H; ++e) v[i][e] = mul2(v[i][e], both(r1));
+                scaled<W, N>(w.w[0], w.w[1], i, v[i]);
+                unpack<TR, N>(cx[i], u);
+                if (kAct != kNoGate) unpack<T, N>(cz[i], g);
+#pragma unroll
+                for (int e = 0; e < H; ++e) {
+                    const float2 n = kAct != kNoGate ? mul2(v[i][e], act2<kAct>(g[e])) : v[i][e];
+                    v[i][e] = fma2(n, both(p.alpha), u[e]);
+                }
+                if (in[i]) store<TR, N>(h.q + c0 + i * kStep, v[i]);
+            }
+        });
+        h.next(p.h, p, row + step);
+        float r2 = 1.f;
+        if (kLayer) {
+            if (p.pre == kNone) continue;
+            if (p.pre == kLayerNorm) centre(v);
+            float a[1] = {squares(v)};
+            team.sum(a);
+            r2 = spread(a[0]);
+        } else {
+            if (p.pre == kNone && p.post == kNone) continue;
+            float2 n[NV][H];
+#pragma unroll
+            for (int i = 0; i < NV; ++i) unpack<T, N>(ry[i], n[i]);
+            float a[2] = {squares(v), squares(n)};
+            team.sum(a);
+            r2 = spread(a[0]);
+            if (p.post != kNone) r1 = spread(a[1]);
+            if (p.pre == kNone) continue;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+#pragma unroll
+            for (int e = 0; e < H; ++e) v[i][e] = mul2(v[i][e], both(r2));
+            scaled<W, N>(w.w[2], w.w[3], i, v[i]);
+            if (in[i]) store<T, N>(out.q + c0 + i * kStep, v[i]);
+        }
+        out.next(p.out, p, row + step);
+    }
+}
+
+// Backward. Every sum over a row is linear in what the other sums give, so that one meeting is enough (two with a mean):
+// with yh known, hc = h (less its mean), go = dout w2, e = alpha act(z) w1, t = e yh, and q = rh^3 (go.hc) / C,
+//     d = dh + rh go - q hc [- rh mean(go)],
+//     g.yh = t.dh + rh t.go - q t.hc [- rh mean(go) sum t],     sum g likewise with e for t
+// and the next row's y^2 comes with them. The second walk over the row then finds the three gradients. kStaged:
+// the rows' tensors go through shared memory, each thread's parts in its own places, the next row's while one is
+// worked on; rows too wide for that are read from memory in each walk. dw1 and dw2 are summed in registers, db1 and db2,
+// where wanted, in shared memory.
+template <typename T, typename TR, int W, int NV, bool kLayer, bool kStaged>
+__global__ void __launch_bounds__(block_threads<W>(), 512 / block_threads<W>()) bn_bwd_kernel(const __grid_constant__ BnParams p) {
+    constexpr int kAll = block_threads<W>(), kTeams = kAll / (32 * W);
+    constexpr int N = channels<T>(), H = N / 2, Q = N / 4, U = words<TR, N>();
+    constexpr int kRow = 3 + 2 * U;         // words of a part in all five tensors: y, z, dout, x, dh
+    __shared__ float s_sum[2][kTeams][W][16];
+    extern __shared__ float4 s_dyn[];       // the stages [2][NV][kRow][threads]; db1, db2 [NV][Q][threads] each; parameters
+    sm100::grid_dep_launch_dependents();
+    Team<W, kTeams> team(s_sum);
+    uint4* const stages = reinterpret_cast<uint4*>(s_dyn) + threadIdx.x;
+    float4* const biases = s_dyn + (kStaged ? 2 * NV * kRow * kAll : 0) + threadIdx.x;
+    const bool any_bias = p.sums & 10;
+    const Params w = load_params<W, NV, N>(p, biases - threadIdx.x + (any_bias ? 2 * NV * Q * kAll : 0));
+    const int t = threadIdx.x % (32 * W), c0 = t * N;
+    constexpr int kStep = 32 * W * N;       // channels from part to part
+    bool in[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) in[i] = c0 + i * kStep < p.C;
+    if (kStaged)            // (what is not fetched stays zero)
+        for (int i = 0; i < 2 * NV * kRow; ++i) stages[i * kAll] = make_uint4(0u, 0u, 0u, 0u);
+    if (any_bias)
+        for (int i = 0; i < 2 * NV * Q; ++i) biases[i * kAll] = make_float4(0.f, 0.f, 0.f, 0.f);
+    __syncthreads();
+    float2 sw[2][NV][H];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < H; ++e) sw[0][i][e] = sw[1][i][e] = both(0.f);
+    const auto add_bias = [&](int which, int i, const float2 (&v)[H]) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            float4& a = biases[((which * NV + i) * Q + q) * kAll];
+            a = make_float4(a.x + v[2 * q].x, a.y + v[2 * q].y, a.z + v[2 * q + 1].x, a.w + v[2 * q + 1].y);
         }
     };
     const uint32_t step = gridDim.x * kTeams;
     uint32_t row = blockIdx.x * kTeams + team.team;
-    fetch(row);
-    for (; row < p.rows; row += step) {
-        float2 v[NV][H], x[NV][H], z[NV][H];
+    RowPtr<const T> y(p.y, p, row, step), z(p.z, p, row, step), o(p.dout, p, row, step);
+    RowPtr<const TR> x(p.x, p, row, step), dh(p.dh, p, row, step);
+    RowPtr<T> dy(p.dy, p, row, step), dz(p.dz, p, row, step);
+    RowPtr<TR> dx(p.dx, p, row, step);
+    // a row into a stage, y first (its sums are wanted earlier); the pointers move on to the next one
+    const auto fetch = [&](uint32_t r, int s) {
+        if (!kStaged) return;
+        const auto place = [&](int i, int k) { return stages + ((s * NV + i) * kRow + k) * kAll; };
+        const bool live = r < p.rows;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (live && in[i]) copy_async(place(i, 0), y.q + c0 + i * kStep);
+        copies_end();
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            ry[i].unpack(v[i]);
-            rx[i].unpack(x[i]);
-            rz[i].unpack(z[i]);
+            if (!live || !in[i]) continue;
+            if (p.z.p) copy_async(place(i, 1), z.q + c0 + i * kStep);
+            if (p.dout.p) copy_async(place(i, 2), o.q + c0 + i * kStep);
+#pragma unroll
+            for (int u = 0; u < U; ++u) copy_async(place(i, 3 + u), reinterpret_cast<const uint4*>(x.q + c0 + i * kStep) + u);
+            if (p.dh.p)
+#pragma unroll
+                for (int u = 0; u < U; ++u) copy_async(place(i, 3 + U + u), reinterpret_cast<const uint4*>(dh.q + c0 + i * kStep) + u);
         }
-        fetch(row + step);
-        normalise(team, v, in, p.post, inv, p.eps);
-        TR* h = at<TR>(p.h, p, row);
+        copies_end();
+    };
+    const auto advance = [&](uint32_t r) {
+        y.next(p.y, p, r);
+        z.next(p.z, p, r);
+        o.next(p.dout, p, r);
+        x.next(p.x, p, r);
+        dh.next(p.dh, p, r);
+    };
+    // a part of one tensor: k and U words as staged, or `from` in memory
+    int stage = 0;
+    const auto part_t = [&](int s, int k, int i, const T* from, float2 (&f)[H]) {
+        uint4 v[1] = {};
+        if (kStaged) v[0] = stages[((s * NV + i) * kRow + k) * kAll];
+        else if (from && in[i]) v[0] = *reinterpret_cast<const uint4*>(from + c0 + i * kStep);
+        unpack<T, N>(v, f);
+    };
+    const auto part_r = [&](int s, int k, int i, const TR* from, float2 (&f)[H]) {
+        uint4 v[U] = {};
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (kStaged) v[u] = stages[((s * NV + i) * kRow + k + u) * kAll];
+            else if (from && in[i]) v[u] = reinterpret_cast<const uint4*>(from + c0 + i * kStep)[u];
+        }
+        unpack<TR, N>(v, f);
+    };
+    // sums over the row of y in a stage (or at `from`): of what deviates from m, squared, or (kSum) as it is
+    const auto y_sum = [&](int s, const T* from, float m, bool squared) {
+        float2 q = both(0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            float2 w[H], b[H];
-            params(p.w1, c[i], in[i], 1.f, w);
-            params(p.b1, c[i], in[i], 0.f, b);
+            float2 v[H];
+            part_t(s, 0, i, from, v);
+            const float2 mi = both(kLayer && in[i] ? -m : 0.f);
 #pragma unroll
             for (int e = 0; e < H; ++e) {
-                float2 n = mul2(fma2(v[i][e], w[e], b[e]), both(p.alpha));
-                if (p.z.p) n = mul2(n, act2(p.act, z[i][e]));
-                v[i][e] = add2(x[i][e], n);
+                const float2 u = kLayer ? add2(v[e], mi) : v[e];
+                q = squared ? fma2(u, u, q) : add2(q, u);
             }
-            if (in[i]) Part<TR, N>::store(h + c[i], v[i]);
         }
-        if (p.pre == kNone) continue;
-        normalise(team, v, in, p.pre, inv, p.eps);
-        T* out = at<T>(p.out, p, row);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            float2 w[H], b[H];
-            params(p.w2, c[i], in[i], 1.f, w);
-            params(p.b2, c[i], in[i], 0.f, b);
-#pragma unroll
-            for (int e = 0; e < H; ++e) v[i][e] = fma2(v[i][e], w[e], b[e]);
-            if (in[i]) Part<T, N>::store(out + c[i], v[i]);
-        }
-    }
-}
-
-// A thread's columns in a team's sums: vector i, quarter q (two pairs) of thread t of the team lie side by side
-// with the other threads'.
-template <int W, int NV, int Q>
-__device__ __forceinline__ float4* place(float* s, int sum, int i, int q, int t) {
-    return reinterpret_cast<float4*>(s) + ((sum * NV + i) * Q + q) * (32 * W) + t;
-}
-
-template <typename T, typename TR, int W, int NV>
-__global__ void __launch_bounds__(block_threads<W>()) bn_bwd_kernel(const __grid_constant__ BnParams p) {
-    constexpr int N = 16 / sizeof(T), H = N / 2, Q = N / 4, kTeams = block_threads<W>() / (32 * W);
-    __shared__ float2 s_sum[2][kTeams][W];
-    extern __shared__ float4 s_cols[];      // [teams][nsums][NV][Q][32 W]
-    sm100::grid_dep_launch_dependents();
-    Team<W, kTeams> team(s_sum);
-    const int t = threadIdx.x % (32 * W);
-    float* cols = reinterpret_cast<float*>(s_cols) + static_cast<size_t>(team.team) * p.nsums * NV * N * 32 * W;
-    for (int i = 0; i < p.nsums * NV * Q; ++i) reinterpret_cast<float4*>(cols)[i * 32 * W + t] = make_float4(0.f, 0.f, 0.f, 0.f);
-    int c[NV];
-    bool in[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        c[i] = (i * 32 * W + t) * N;
-        in[i] = c[i] < p.C;
-    }
-    // which of the wanted sums is which
-    const int i0 = 0, i1 = i0 + (p.sums & 1), i2 = i1 + (p.sums >> 1 & 1), i3 = i2 + (p.sums >> 2 & 1);
-    const auto add = [&](int sum, int i, const float2 (&v)[H]) {
-#pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            float4* a = place<W, NV, Q>(cols, sum, i, q, t);
-            float4 o = *a;
-            const float2 lo = add2(make_float2(o.x, o.y), v[2 * q]), hi = add2(make_float2(o.z, o.w), v[2 * q + 1]);
-            *a = make_float4(lo.x, lo.y, hi.x, hi.y);
-        }
+        return q.x + q.y;
     };
     const float inv = 1.f / p.C;
-    Part<T, N> ry[NV], rz[NV], ro[NV];
-    Part<TR, N> rx[NV], rd[NV];
-    const auto fetch = [&](uint32_t row) {
-        const bool live = row < p.rows;
-        const T* y = live ? at<const T>(p.y, p, row) : nullptr;
-        const T* z = live && p.z.p ? at<const T>(p.z, p, row) : nullptr;
-        const T* o = live && p.pre != kNone ? at<const T>(p.dout, p, row) : nullptr;
-        const TR* x = live ? at<const TR>(p.x, p, row) : nullptr;
-        const TR* d = live && p.dh.p ? at<const TR>(p.dh, p, row) : nullptr;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            ry[i].zero();
-            rx[i].zero();
-            rz[i].zero();
-            ro[i].zero();
-            rd[i].zero();
-            if (!live || !in[i]) continue;
-            ry[i].load(y + c[i]);
-            rx[i].load(x + c[i]);
-            if (z) rz[i].load(z + c[i]);
-            if (o) ro[i].load(o + c[i]);
-            if (d) rd[i].load(d + c[i]);
+    fetch(row, 0);
+    if (kStaged) copies_left<1>();
+    float r1 = 1.f, my = 0.f;
+    if (p.post != kNone && (kStaged || row < p.rows)) {
+        float a[1];
+        if (kLayer && p.post == kLayerNorm) {
+            a[0] = y_sum(0, y.q, 0.f, false);
+            team.sum(a);
+            my = a[0] * inv;
         }
-    };
-    const uint32_t step = gridDim.x * kTeams;
-    for (uint32_t row = blockIdx.x * kTeams + team.team; row < p.rows; row += step) {
-        fetch(row);
-        float2 v[NV][H], d[NV][H];
+        a[0] = y_sum(0, y.q, my, true);
+        team.sum(a);
+        r1 = rsqrtf(fmaf(a[0], inv, p.eps));
+    }
+    const T *py = y.q, *pz = z.q, *po = o.q;
+    const TR *px = x.q, *pd = dh.q;
+    for (; row < p.rows; row += step) {
+        py = y.q, pz = z.q, po = o.q, px = x.q, pd = dh.q;
+        advance(row + step);
+        fetch(row + step, stage ^ 1);
+        if (kStaged) copies_left<2>();      // all of this row
+        const bool more = kStaged || row + step < p.rows;
+        float2 h[NV][H];
+        // yh of a part
+        const auto yhat = [&](int i, float2 (&v)[H]) {
+            part_t(stage, 0, i, py, v);
+            const float2 mi = both(kLayer && in[i] ? -my : 0.f);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            ry[i].unpack(v[i]);
-            rd[i].unpack(d[i]);
+            for (int e = 0; e < H; ++e) v[e] = mul2(kLayer ? add2(v[e], mi) : v[e], both(r1));
+        };
+        float mh = 0.f, my1 = 0.f;
+        // h of a part and its yh, from e = alpha act(z)
+        const auto find_h = [&](int i, float2 (&v)[H], const float2 (&e)[H]) {
+            float2 u[H], n[H];
+            yhat(i, v);
+            part_r(stage, 3, i, px, u);
+#pragma unroll
+            for (int k = 0; k < H; ++k) n[k] = v[k];
+            scaled<W, N>(w.w[0], w.w[1], i, n);
+#pragma unroll
+            for (int k = 0; k < H; ++k) h[i][k] = fma2(n[k], e[k], u[k]);
+        };
+        if (kLayer) {       // the means first
+            float2 s = both(0.f);
+            with_act(p.act, [&](auto act) {
+                constexpr int kAct = decltype(act)::value;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    float2 v[H], e[H], g[H];
+                    if (kAct != kNoGate) part_t(stage, 1, i, pz, g);
+#pragma unroll
+                    for (int k = 0; k < H; ++k) e[k] = kAct != kNoGate ? mul2(act2<kAct>(g[k]), both(p.alpha)) : both(p.alpha);
+                    find_h(i, v, e);
+#pragma unroll
+                    for (int k = 0; k < H; ++k) s = add2(s, h[i][k]);
+                }
+            });
+            if (kStaged) copies_left<1>();
+            float a[2] = {s.x + s.y, p.post == kLayerNorm && more ? y_sum(stage ^ 1, y.q, 0.f, false) : 0.f};
+            team.sum(a);
+            if (p.pre == kLayerNorm) mh = a[0] * inv;
+            my1 = a[1] * inv;
         }
-        const float r1 = normalise(team, v, in, p.post, inv, p.eps);
-        if (p.pre != kNone) {
-            float2 h[NV][H];
+        float2 s0 = both(0.f), s1 = s0, s2 = s0, s3 = s0, s4 = s0, s5 = s0, s6 = s0, s7 = s0, s8 = s0, s9 = s0, s10 = s0;
+        with_act(p.act, [&](auto act) {
+            constexpr int kAct = decltype(act)::value;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                float2 w[H], b[H], x[H], z[H];
-                params(p.w1, c[i], in[i], 1.f, w);
-                params(p.b1, c[i], in[i], 0.f, b);
-                rx[i].unpack(x);
-                rz[i].unpack(z);
+                float2 v[H], e[H], g[H], d[H];
+                if (kAct != kNoGate) part_t(stage, 1, i, pz, g);
 #pragma unroll
-                for (int e = 0; e < H; ++e) {
-                    float2 n = mul2(fma2(v[i][e], w[e], b[e]), both(p.alpha));
-                    if (p.z.p) n = mul2(n, act2(p.act, z[e]));
-                    h[i][e] = add2(x[e], n);
+                for (int k = 0; k < H; ++k) e[k] = kAct != kNoGate ? mul2(act2<kAct>(g[k]), both(p.alpha)) : both(p.alpha);
+                find_h(i, v, e);
+                part_r(stage, 3 + U, i, pd, d);
+                part_t(stage, 2, i, po, g);
+                scaled<W, N>(w.w[2], nullptr, i, g);
+                scaled<W, N>(w.w[0], nullptr, i, e);
+                const float2 mi = both(kLayer && in[i] ? -mh : 0.f);
+#pragma unroll
+                for (int k = 0; k < H; ++k) {
+                    if (kLayer) h[i][k] = add2(h[i][k], mi);
+                    const float2 tk = mul2(v[k], e[k]);
+                    s0 = fma2(h[i][k], h[i][k], s0);
+                    s1 = fma2(g[k], h[i][k], s1);
+                    s2 = fma2(tk, d[k], s2);
+                    s3 = fma2(tk, g[k], s3);
+                    s4 = fma2(tk, h[i][k], s4);
+                    if (!kLayer || !in[i]) continue;
+                    s5 = add2(s5, g[k]);
+                    s6 = add2(s6, tk);
+                    s7 = fma2(e[k], d[k], s7);
+                    s8 = fma2(e[k], g[k], s8);
+                    s9 = fma2(e[k], h[i][k], s9);
+                    s10 = add2(s10, e[k]);
                 }
             }
-            const float r2 = normalise(team, h, in, p.pre, inv, p.eps);
-            float2 s1 = both(0.f), s2 = both(0.f);
+        });
+        if (kStaged) copies_left<1>();      // y of the next row
+        const float ysq = p.post != kNone && more ? y_sum(stage ^ 1, y.q, my1, true) : 0.f;
+        float r2 = 0.f, k2 = 0.f, m2 = 0.f, m1 = 0.f, n1 = 0.f, next;
+        const auto join = [](const float2& v) { return v.x + v.y; };
+        if (!kLayer) {
+            float a[8] = {join(s0), join(s1), join(s2), join(s3), join(s4), ysq, 0.f, 0.f};
+            team.sum(a);
+            if (p.pre != kNone) {
+                r2 = rsqrtf(fmaf(a[0], inv, p.eps));
+                k2 = -r2 * r2 * r2 * a[1] * inv;
+            }
+            if (p.post != kNone) m1 = -(a[2] + (p.pre != kNone ? fmaf(r2, a[3], k2 * a[4]) : 0.f)) * inv * r1;
+            next = a[5];
+        } else {
+            float a[16] = {join(s0), join(s1), join(s2), join(s3), join(s4), ysq, join(s5), join(s6), join(s7), join(s8),
+                           join(s9), join(s10), 0.f, 0.f, 0.f, 0.f};
+            team.sum(a);
+            if (p.pre != kNone) {
+                r2 = rsqrtf(fmaf(a[0], inv, p.eps));
+                k2 = -r2 * r2 * r2 * a[1] * inv;
+                if (p.pre == kLayerNorm) m2 = -r2 * a[6] * inv;
+            }
+            const bool pre = p.pre != kNone;
+            if (p.post != kNone) m1 = -(a[2] + (pre ? fmaf(r2, a[3], k2 * a[4]) + m2 * a[7] : 0.f)) * inv * r1;
+            if (p.post == kLayerNorm) n1 = -(a[8] + (pre ? fmaf(r2, a[9], k2 * a[10]) + m2 * a[11] : 0.f)) * inv * r1;
+            next = a[5];
+        }
+        with_act(p.act, [&](auto act) {
+            constexpr int kAct = decltype(act)::value;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                float2 w[H], o[H], u[H];
-                params(p.w2, c[i], in[i], 1.f, w);
-                ro[i].unpack(o);
+                if (!in[i]) continue;
+                float2 v[H], d[H], n[H], g[H];
+                yhat(i, v);
+                part_r(stage, 3 + U, i, pd, d);
+                if (p.pre != kNone) {
+                    part_t(stage, 2, i, po, g);
 #pragma unroll
-                for (int e = 0; e < H; ++e) {
-                    u[e] = mul2(o[e], h[i][e]);
-                    s1 = fma2(u[e], w[e], s1);
-                    s2 = fma2(o[e], w[e], s2);
+                    for (int k = 0; k < H; ++k) sw[1][i][k] = fma2(g[k], mul2(h[i][k], both(r2)), sw[1][i][k]);
+                    if (p.sums & 8) add_bias(1, i, g);
+                    scaled<W, N>(w.w[2], nullptr, i, g);
+#pragma unroll
+                    for (int k = 0; k < H; ++k) {
+                        d[k] = fma2(g[k], both(r2), fma2(h[i][k], both(k2), d[k]));
+                        if (kLayer) d[k] = add2(d[k], both(m2));
+                    }
                 }
-                if (in[i] && (p.sums & 4)) add(i2, i, u);
-                if (in[i] && (p.sums & 8)) add(i3, i, o);
-            }
-            const float2 s = team.sum(make_float2(s1.x + s1.y, s2.x + s2.y));
-            const float m1 = -s.x * inv, m2 = p.pre == kLayer ? -s.y * inv : 0.f;
+                store<TR, N>(dx.q + c0 + i * kStep, d);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                float2 w[H], o[H];
-                params(p.w2, c[i], in[i], 1.f, w);
-                ro[i].unpack(o);
+                for (int k = 0; k < H; ++k) d[k] = mul2(d[k], both(p.alpha));
+                if constexpr (kAct != kNoGate) {
 #pragma unroll
-                for (int e = 0; e < H; ++e)
-                    d[i][e] = fma2(fma2(o[e], w[e], fma2(h[i][e], both(m1), both(m2))), both(r2), d[i][e]);
-            }
-        }
-        TR* dx = at<TR>(p.dx, p, row);
-        T* dz = p.z.p ? at<T>(p.dz, p, row) : nullptr;
-        float2 s1 = both(0.f), s2 = both(0.f);
+                    for (int k = 0; k < H; ++k) n[k] = v[k];
+                    scaled<W, N>(w.w[0], w.w[1], i, n);
+                    part_t(stage, 1, i, pz, g);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (in[i]) Part<TR, N>::store(dx + c[i], d[i]);
-            float2 w[H], b[H], z[H], u[H];
-            params(p.w1, c[i], in[i], 1.f, w);
-            params(p.b1, c[i], in[i], 0.f, b);
-            rz[i].unpack(z);
-#pragma unroll
-            for (int e = 0; e < H; ++e) {
-                d[i][e] = mul2(d[i][e], both(p.alpha));
-                if (p.z.p) {
-                    float2 a, da;
-                    act_slope2(p.act, z[e], &a, &da);
-                    z[e] = mul2(mul2(d[i][e], fma2(v[i][e], w[e], b[e])), da);
-                    d[i][e] = mul2(d[i][e], a);
+                    for (int k = 0; k < H; ++k) {
+                        float2 a, da;
+                        act_slope2<kAct>(g[k], &a, &da);
+                        g[k] = mul2(mul2(d[k], n[k]), da);
+                        d[k] = mul2(d[k], a);
+                    }
+                    store<T, N>(dz.q + c0 + i * kStep, g);
                 }
-                u[e] = mul2(d[i][e], v[i][e]);
+#pragma unroll
+                for (int k = 0; k < H; ++k) sw[0][i][k] = fma2(d[k], v[k], sw[0][i][k]);
+                if (p.sums & 2) add_bias(0, i, d);
+                scaled<W, N>(w.w[0], nullptr, i, d);
+#pragma unroll
+                for (int k = 0; k < H; ++k) {
+                    d[k] = fma2(d[k], both(r1), mul2(v[k], both(m1)));
+                    if (kLayer) d[k] = add2(d[k], both(n1));
+                }
+                store<T, N>(dy.q + c0 + i * kStep, d);
             }
-            if (in[i] && dz) Part<T, N>::store(dz + c[i], z);
-            if (in[i] && (p.sums & 1)) add(i0, i, u);
-            if (in[i] && (p.sums & 2)) add(i1, i, d[i]);
-#pragma unroll
-            for (int e = 0; e < H; ++e) {
-                if (!in[i]) continue;       // (m2 reaches what lies beyond the row)
-                s1 = fma2(u[e], w[e], s1);
-                d[i][e] = mul2(d[i][e], w[e]);
-                s2 = add2(s2, d[i][e]);
-            }
-        }
-        float m1 = 0.f, m2 = 0.f;
-        if (p.post != kNone) {
-            const float2 s = team.sum(make_float2(s1.x + s1.y, s2.x + s2.y));
-            m1 = -s.x * inv;
-            m2 = p.post == kLayer ? -s.y * inv : 0.f;
-        }
-        T* dy = at<T>(p.dy, p, row);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (!in[i]) continue;
-#pragma unroll
-            for (int e = 0; e < H; ++e) d[i][e] = mul2(add2(d[i][e], fma2(v[i][e], both(m1), both(m2))), both(r1));
-            Part<T, N>::store(dy + c[i], d[i]);
-        }
+        });
+        if (p.post != kNone) r1 = rsqrtf(fmaf(next, inv, p.eps));
+        my = my1;
+        dx.next(p.dx, p, row + step);
+        dz.next(p.dz, p, row + step);
+        dy.next(p.dy, p, row + step);
+        stage ^= 1;
     }
     if (p.nsums == 0) return;
-    __syncthreads();
-    // the teams' sums, added in order, to the CTA's share
+    // the teams' sums, added in order, to the CTA's share (a sum at a time, through the dynamic shared memory)
     float* part = p.part + static_cast<int64_t>(blockIdx.x) * p.nsums * p.C;
-    constexpr int kCols = NV * N * 32 * W;
-    for (int sum = 0; sum < p.nsums; ++sum)
-        for (int k = threadIdx.x; k < kCols / 4; k += block_threads<W>()) {
-            const int tt = k % (32 * W), iq = k / (32 * W), q = iq % Q, i = iq / Q;
-            const int col = (i * 32 * W + tt) * N + 4 * q;
-            if (col >= p.C) continue;
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int u = 0; u < kTeams; ++u) {
-                const float4 o = *place<W, NV, Q>(reinterpret_cast<float*>(s_cols) + static_cast<size_t>(u) * p.nsums * kCols, sum, i, q, tt);
-                a = make_float4(a.x + o.x, a.y + o.y, a.z + o.z, a.w + o.w);
+    copies_left<0>();
+    float4 keep[2][NV * Q];
+    if (any_bias)
+#pragma unroll
+        for (int i = 0; i < 2 * NV * Q; ++i) keep[i / (NV * Q)][i % (NV * Q)] = biases[i * kAll];
+    float4* const sums = s_dyn;             // [NV][Q][threads]
+    for (int which = 0, n = 0; which < 4; ++which) {
+        if (!(p.sums >> which & 1)) continue;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                float4 v;
+                if (which == 1) v = keep[0][i * Q + q];
+                else if (which == 3) v = keep[1][i * Q + q];
+                else if (which == 0) v = make_float4(sw[0][i][2 * q].x, sw[0][i][2 * q].y, sw[0][i][2 * q + 1].x, sw[0][i][2 * q + 1].y);
+                else v = make_float4(sw[1][i][2 * q].x, sw[1][i][2 * q].y, sw[1][i][2 * q + 1].x, sw[1][i][2 * q + 1].y);
+                sums[(i * Q + q) * kAll + threadIdx.x] = v;
             }
-            *reinterpret_cast<float4*>(part + static_cast<int64_t>(sum) * p.C + col) = a;
-        }
+        __syncthreads();
+        if (team.team == 0)
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int q = 0; q < Q; ++q) {
+                    if (!in[i]) continue;
+                    float4 a = sums[(i * Q + q) * kAll + t];
+                    for (int u = 1; u < kTeams; ++u) {
+                        const float4 f = sums[(i * Q + q) * kAll + u * 32 * W + t];
+                        a = make_float4(a.x + f.x, a.y + f.y, a.z + f.z, a.w + f.w);
+                    }
+                    *reinterpret_cast<float4*>(part + static_cast<int64_t>(n) * p.C + c0 + i * kStep + 4 * q) = a;
+                }
+        ++n;
+    }
 }
 
 // ---- any width and alignment: one CTA a row, scalar loads, each pass over the row from memory
@@ -444,9 +702,12 @@ __device__ __forceinline__ float block_sum(float v, float* s) {
     return v;
 }
 
-__device__ __forceinline__ float act1(int act, float z) {
-    const float2 r = act2(act, both(z));
-    return r.x;
+__device__ __forceinline__ float2 act1(int act, float z) {
+    float2 a = both(1.f), da = both(0.f);
+    with_act(act, [&](auto k) {
+        if constexpr (decltype(k)::value != kNoGate) act_slope2<decltype(k)::value>(both(z), &a, &da);
+    });
+    return make_float2(a.x, da.x);
 }
 
 template <typename T, typename TR>
@@ -464,13 +725,13 @@ struct AnyRow {
     __device__ __forceinline__ float n(int c) const { return fmaf(yh(c), p.w1 ? p.w1[c] : 1.f, p.b1 ? p.b1[c] : 0.f); }
     __device__ __forceinline__ float h(int c) const {
         const float v = n(c) * p.alpha;
-        return to_f(x[c]) + (z ? v * act1(p.act, to_f(z[c])) : v);
+        return to_f(x[c]) + (z ? v * act1(p.act, to_f(z[c])).x : v);
     }
     template <typename F>
     __device__ __forceinline__ void stats(int kind, F&& v, float* m, float* r, float* s) {
         if (kind == kNone) return;
         float mean = 0.f, q = 0.f;
-        if (kind == kLayer) {
+        if (kind == kLayerNorm) {
             for (int c = threadIdx.x; c < p.C; c += kAny) mean += v(c);
             mean = block_sum(mean, s) / p.C;
         }
@@ -532,7 +793,7 @@ __global__ void __launch_bounds__(kAny) bn_bwd_any_kernel(const __grid_constant_
                 u2 += g;
             }
             u1 = block_sum(u1, s) / p.C;
-            u2 = p.pre == kLayer ? block_sum(u2, s) / p.C : 0.f;
+            u2 = p.pre == kLayerNorm ? block_sum(u2, s) / p.C : 0.f;
         }
         // d, the gradient of h
         const auto back = [&](int c, float hh) {
@@ -545,10 +806,9 @@ __global__ void __launch_bounds__(kAny) bn_bwd_any_kernel(const __grid_constant_
                 float e = d * p.alpha, slope = 0.f;
                 const float dn = e;
                 if (a.z) {
-                    float2 f, g;
-                    act_slope2(p.act, both(to_f(a.z[c])), &f, &g);
+                    const float2 f = act1(p.act, to_f(a.z[c]));
                     e *= f.x;
-                    slope = g.x;
+                    slope = f.y;
                 }
                 const float g = e * (p.w1 ? p.w1[c] : 1.f);
                 if (pass == 0) {
@@ -568,7 +828,7 @@ __global__ void __launch_bounds__(kAny) bn_bwd_any_kernel(const __grid_constant_
             }
             if (pass == 0) {
                 v1 = block_sum(v1, s) / p.C;
-                v2 = p.post == kLayer ? block_sum(v2, s) / p.C : 0.f;
+                v2 = p.post == kLayerNorm ? block_sum(v2, s) / p.C : 0.f;
             }
         }
         __syncthreads();
@@ -581,28 +841,33 @@ template <int w, int v>
 struct Shape {
     static constexpr int W = w, NV = v;
 };
-// Warps and vectors a lane for a row of `vecs` vectors: two vectors a lane from 32 lanes on.
-template <typename F>
-auto with_shape(int vecs, F&& f) {
-    if (vecs <= 32) return f(Shape<1, 1>{});
-    if (vecs <= 64) return f(Shape<1, 2>{});
-    if (vecs <= 128) return f(Shape<2, 2>{});
-    if (vecs <= 256) return f(Shape<4, 2>{});
-    if (vecs <= 512) return f(Shape<8, 2>{});
+// Warps and parts a lane for a row of `parts` parts: two a lane from 32 lanes on, which is what registers (and,
+// backward, the stages) hold for two rows an SM at 512 parts; wider rows have an SM each, up to kMostChannels, the most
+// whose parameters fit beside them.
+template <typename T, typename F>
+auto with_shape(int parts, F&& f) {
+    if (parts <= 32) return f(Shape<1, 1>{});
+    if (parts <= 64) return f(Shape<1, 2>{});
+    if (parts <= 128) return f(Shape<2, 2>{});
+    if (parts <= 256) return f(Shape<4, 2>{});
+    if (parts <= 512) return f(Shape<8, 2>{});
+    if constexpr (sizeof(T) == 4) {
+        if (parts > 1024) return f(Shape<16, 4>{});
+    }
     return f(Shape<16, 2>{});
 }
-constexpr int kMostVecs = 1024;
+constexpr int kMostChannels = 8192;
 
 bool ok16(const BnTensor& t, int es) {
     return !t.p || ((reinterpret_cast<uintptr_t>(t.p) | static_cast<uintptr_t>(t.batch * es) |
                      static_cast<uintptr_t>(t.row * es)) & 15u) == 0;
 }
 
-// 16-byte vectors of a row, or 0 where the vector form does not apply
+// 16-byte parts of a row, or 0 where that form does not apply
 template <typename T, typename TR>
-int vector_count(const BnParams& p) {
-    constexpr int N = 16 / sizeof(T);
-    if (p.C % N != 0 || p.C / N > kMostVecs) return 0;
+int part_count(const BnParams& p) {
+    constexpr int N = channels<T>();
+    if (p.C % N != 0 || p.C > kMostChannels) return 0;
     for (const BnTensor* t : {&p.y, &p.z, &p.out, &p.dout, &p.dy, &p.dz})
         if (!ok16(*t, sizeof(T))) return 0;
     for (const BnTensor* t : {&p.x, &p.h, &p.dh, &p.dx})
@@ -610,6 +875,14 @@ int vector_count(const BnParams& p) {
     return p.C / N;
 }
 
+// a kernel and its bytes of shared memory beside its sums
+template <auto k, int n>
+struct Kernel {
+    static constexpr auto f = k;
+    static constexpr int bytes = n;
+};
+
+constexpr int kRoom = 225 * 1024;       // dynamic shared memory of a CTA, beside its teams' places
 template <typename K>
 int resident(K* kernel, int threads, size_t smem) {
     int n = 0;
@@ -626,51 +899,81 @@ int64_t most_shares(int64_t rows) {
 
 template <typename T, typename TR>
 cudaError_t launch_fwd(const BnParams& p, cudaStream_t s) {
-    const int vecs = vector_count<T, TR>(p);
+    const int parts = part_count<T, TR>(p);
     const int64_t sms = device_sm_count();
-    if (vecs == 0) {
+    if (parts == 0) {
         const int64_t grid = p.rows < 16 * sms ? p.rows : 16 * sms;
         bn_fwd_any_kernel<T, TR><<<static_cast<unsigned>(grid), kAny, 0, s>>>(p);
         return cudaGetLastError();
     }
-    with_shape(vecs, [&](auto sh) {
+    cudaError_t e = cudaSuccess;
+    const bool layer = p.post == kLayerNorm || p.pre == kLayerNorm;
+    const int params = (p.w1 != nullptr) + (p.b1 != nullptr) + (p.w2 != nullptr) + (p.b2 != nullptr);
+    with_shape<T>(parts, [&](auto sh) {
         using S = decltype(sh);
         constexpr int threads = block_threads<S::W>(), teams = threads / (32 * S::W);
-        auto* const kernel = bn_fwd_kernel<T, TR, S::W, S::NV>;
-        static const int per_sm = resident(kernel, threads, 0);
-        const int64_t want = (p.rows + teams - 1) / teams, most = per_sm * sms;
-        kernel<<<static_cast<unsigned>(want < most ? want : most), threads, 0, s>>>(p);
+        constexpr int one = S::NV * 32 * S::W * channels<T>() * 4;     // bytes of one parameter: up to 32 KB
+        const auto go = [&](auto k) {
+            using K = decltype(k);
+            static std::atomic<uint64_t> done{0};
+            if ((e = allow_smem(K::f, 4 * one < kRoom ? K::bytes + 4 * one : kRoom, done)) != cudaSuccess) return;
+            static const int per_sm[5] = {resident(K::f, threads, 0), resident(K::f, threads, one), resident(K::f, threads, 2 * one),
+                                          resident(K::f, threads, 3 * one), resident(K::f, threads, 4 * one)};
+            const int64_t want = (p.rows + teams - 1) / teams, most = per_sm[params] * sms;
+            K::f<<<static_cast<unsigned>(want < most ? want : most), threads, params * one, s>>>(p);
+        };
+        if (layer) go(Kernel<bn_fwd_kernel<T, TR, S::W, S::NV, true>, 0>{});
+        else go(Kernel<bn_fwd_kernel<T, TR, S::W, S::NV, false>, 0>{});
         return 0;
     });
-    return cudaGetLastError();
+    return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 template <typename T, typename TR>
 cudaError_t launch_bwd(BnParams p, float* const (&outs)[4], cudaStream_t s) {
-    const int vecs = vector_count<T, TR>(p);
+    const int parts = part_count<T, TR>(p);
     int shares = 1;
     float* wanted[4] = {};
     for (int k = 0, n = 0; k < 4; ++k)
         if (p.sums >> k & 1) wanted[n++] = outs[k];
     cudaError_t e = cudaSuccess;
-    if (vecs > 0) with_shape(vecs, [&](auto sh) {
+    const bool layer = p.post == kLayerNorm || p.pre == kLayerNorm;
+    const int params = (p.w1 != nullptr) + (p.b1 != nullptr) + (p.w2 != nullptr) + (p.b2 != nullptr);
+    if (parts > 0) with_shape<T>(parts, [&](auto sh) {
         using S = decltype(sh);
-        constexpr int threads = block_threads<S::W>(), teams = threads / (32 * S::W);
-        constexpr int one = teams * S::NV * (16 / static_cast<int>(sizeof(T))) * 32 * S::W * 4;     // bytes of one sum: up to 32 KB
-        static_assert(one <= 32768, "a CTA's sums fit");
-        auto* const kernel = bn_bwd_kernel<T, TR, S::W, S::NV>;
-        static std::atomic<uint64_t> done{0};
-        if ((e = allow_smem(kernel, 4 * one, done)) != cudaSuccess) return 0;
-        static const int per_sm[5] = {resident(kernel, threads, 0), resident(kernel, threads, one), resident(kernel, threads, 2 * one),
-                                      resident(kernel, threads, 3 * one), resident(kernel, threads, 4 * one)};
-        const int64_t want = (p.rows + teams - 1) / teams;
-        int64_t most = static_cast<int64_t>(device_sm_count()) * (per_sm[p.nsums] < kMostPerSm ? per_sm[p.nsums] : kMostPerSm);
-        shares = static_cast<int>(want < most ? want : most);
-        kernel<<<static_cast<unsigned>(shares), threads, p.nsums * one, s>>>(p);
+        constexpr int threads = block_threads<S::W>(), teams = threads / (32 * S::W), N = channels<T>();
+        constexpr int one = S::NV * 32 * S::W * N * 4, staged = 2 * S::NV * threads * 16 * (3 + 2 * words<TR, N>());
+        const auto go = [&](auto k) {
+            using K = decltype(k);
+            // parameters, db1 and db2, and room for one sum at the end
+            int smem = K::bytes + params * one + (p.sums & 10 ? 2 * teams * one : 0);
+            if (smem < teams * one) smem = teams * one;
+            static std::atomic<uint64_t> done{0};
+            if ((e = allow_smem(K::f, kRoom, done)) != cudaSuccess) return;
+            static std::atomic<int> per_sm[5][2];       // looked up once (all devices are alike)
+            std::atomic<int>& known = per_sm[params][p.sums & 10 ? 1 : 0];
+            int fit = known.load(std::memory_order_relaxed);
+            if (fit == 0) known.store(fit = resident(K::f, threads, smem), std::memory_order_relaxed);
+            const int64_t want = (p.rows + teams - 1) / teams;
+            const int64_t all = device_sm_count() * static_cast<int64_t>(fit < kMostPerSm ? fit : kMostPerSm);
+            shares = static_cast<int>(want < all ? want : all);
+            K::f<<<static_cast<unsigned>(shares), threads, smem, s>>>(p);
+        };
+        if constexpr (staged <= kRoom) {
+            if (staged + params * one + (p.sums & 10 ? 2 * teams * one : 0) <= kRoom) {
+                if (layer) go(Kernel<bn_bwd_kernel<T, TR, S::W, S::NV, true, true>, staged>{});
+                else go(Kernel<bn_bwd_kernel<T, TR, S::W, S::NV, false, true>, staged>{});
+                return 0;
+            }
+        }
+        if constexpr (staged + 4 * one + 2 * teams * one > kRoom) {
+            if (layer) go(Kernel<bn_bwd_kernel<T, TR, S::W, S::NV, true, false>, 0>{});
+            else go(Kernel<bn_bwd_kernel<T, TR, S::W, S::NV, false, false>, 0>{});
+        }
         return 0;
     });
     if (e != cudaSuccess) return e;
-    if (vecs == 0) {
+    if (parts == 0) {
         shares = static_cast<int>(most_shares(p.rows));
         bn_bwd_any_kernel<T, TR><<<static_cast<unsigned>(shares), kAny, 0, s>>>(p);
     }
@@ -705,6 +1008,7 @@ m3_status check(const m3_block_norm_dims* d) {
     if (d->flags & ~(post | pre | act)) return err(M3_ERR_INVALID_ARG, "unknown bits in flags (0x%x)", (unsigned)d->flags);
     if (both_of(d->flags, post) || both_of(d->flags, pre) || both_of(d->flags, act))
         return err(M3_ERR_INVALID_ARG, "flags (0x%x) name both of a pair", (unsigned)d->flags);
+    // (rows are counted in 32 bits, up to two walks' steps beyond the last)
     if (d->channels > (int64_t(1) << 24) || (d->batch > 0 && d->rows > 0x7fffffffLL / d->batch))
         return err(M3_ERR_UNSUPPORTED, "more than 2^31 rows or 2^24 channels");
     return M3_OK;
@@ -770,9 +1074,9 @@ BnParams make_params(const m3_block_norm_dims* d, const m3_block_norm_inputs* in
     p.rows = static_cast<uint32_t>(d->batch * d->rows);
     p.inner = static_cast<uint32_t>(d->rows);
     p.C = static_cast<int>(d->channels);
-    p.post = d->flags & M3_BN_POST_LAYER ? kLayer : d->flags & M3_BN_POST_RMS ? kRms : kNone;
-    p.pre = d->flags & M3_BN_PRE_LAYER ? kLayer : d->flags & M3_BN_PRE_RMS ? kRms : kNone;
-    p.act = d->flags & M3_BN_SILU ? kSilu : d->flags & M3_BN_SIGMOID ? kSigmoid : kIdentity;
+    p.post = d->flags & M3_BN_POST_LAYER ? kLayerNorm : d->flags & M3_BN_POST_RMS ? kRms : kNone;
+    p.pre = d->flags & M3_BN_PRE_LAYER ? kLayerNorm : d->flags & M3_BN_PRE_RMS ? kRms : kNone;
+    p.act = !in->z.data ? kNoGate : d->flags & M3_BN_SILU ? kSilu : d->flags & M3_BN_SIGMOID ? kSigmoid : kIdentity;
     p.y = tensor(d, &in->y);
     p.x = tensor(d, &in->residual);
     p.z = tensor(d, &in->z);
