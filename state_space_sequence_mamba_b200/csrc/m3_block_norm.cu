@@ -177,7 +177,7 @@ struct Params {
 template <int W, int NV, int N>
 __device__ __forceinline__ Params load_params(const BnParams& p, float4* room) {
     constexpr int Q = N / 4, kPlanes = NV * Q;
-    const float* const from[4] = {p.w1, p.b1, p.w2, p.b2};
+    const float* const from[4] = {p.w1, p.b1, p.w2, p.b2};      // (the backward has no use for b2)
     Params r{};
     const int t = threadIdx.x % (32 * W);
 #pragma unroll
@@ -220,13 +220,11 @@ constexpr int block_threads() { return 32 * (W > 8 ? W : 8); }
 // kLayer: one of the norms takes its mean off; without it, the sum of y^2 of the next row comes with h^2 of this one,
 // and a row has one meeting.
 template <typename T, typename TR, int W, int NV, bool kLayer>
-__global__ void __launch_bounds__(block_threads<W>(), 512 / block_threads<W>()) bn_fwd_kernel(const __grid_constant__ BnParams p) {
+__global__ void __launch_bounds__(block_threads<W>(), 768 / block_threads<W>()) bn_fwd_kernel(const __grid_constant__ BnParams p) {
     constexpr int kTeams = block_threads<W>() / (32 * W), N = channels<T>(), H = N / 2, U = words<TR, N>();
     __shared__ float s_sum[2][kTeams][W][16];
     extern __shared__ float4 s_dyn[];       // the parameters
     Team<W, kTeams> team(s_sum);
-    const Params w = load_params<W, NV, N>(p, s_dyn);
-    __syncthreads();
     const int c0 = static_cast<int>(threadIdx.x % (32 * W)) * N;
     constexpr int kStep = 32 * W * N;       // channels from part to part
     bool in[NV];
@@ -278,6 +276,8 @@ __global__ void __launch_bounds__(block_threads<W>(), 512 / block_threads<W>()) 
     };
     const auto spread = [&](float sum) { return rsqrtf(fmaf(sum, inv, p.eps)); };
     fetch(row < p.rows);
+    const Params w = load_params<W, NV, N>(p, s_dyn);
+    __syncthreads();
     float r1 = 1.f;
     if (!kLayer && p.post != kNone) {
         float2 v[NV][H];
@@ -375,7 +375,6 @@ __global__ void __launch_bounds__(block_threads<W>(), 512 / block_threads<W>()) 
     uint4* const stages = reinterpret_cast<uint4*>(s_dyn) + threadIdx.x;
     float4* const biases = s_dyn + (kStaged ? 2 * NV * kRow * kAll : 0) + threadIdx.x;
     const bool any_bias = p.sums & 10;
-    const Params w = load_params<W, NV, N>(p, biases - threadIdx.x + (any_bias ? 2 * NV * Q * kAll : 0));
     const int t = threadIdx.x % (32 * W), c0 = t * N;
     constexpr int kStep = 32 * W * N;       // channels from part to part
     bool in[NV];
@@ -385,7 +384,6 @@ __global__ void __launch_bounds__(block_threads<W>(), 512 / block_threads<W>()) 
         for (int i = 0; i < 2 * NV * kRow; ++i) stages[i * kAll] = make_uint4(0u, 0u, 0u, 0u);
     if (any_bias)
         for (int i = 0; i < 2 * NV * Q; ++i) biases[i * kAll] = make_float4(0.f, 0.f, 0.f, 0.f);
-    __syncthreads();
     float2 sw[2][NV][H];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -468,6 +466,8 @@ __global__ void __launch_bounds__(block_threads<W>(), 512 / block_threads<W>()) 
     };
     const float inv = 1.f / p.C;
     fetch(row, 0);
+    const Params w = load_params<W, NV, N>(p, biases - threadIdx.x + (any_bias ? 2 * NV * Q * kAll : 0));
+    __syncthreads();
     if (kStaged) copies_left<1>();
     float r1 = 1.f, my = 0.f;
     if (p.post != kNone && (kStaged || row < p.rows)) {
@@ -938,7 +938,8 @@ cudaError_t launch_bwd(BnParams p, float* const (&outs)[4], cudaStream_t s) {
         if (p.sums >> k & 1) wanted[n++] = outs[k];
     cudaError_t e = cudaSuccess;
     const bool layer = p.post == kLayerNorm || p.pre == kLayerNorm;
-    const int params = (p.w1 != nullptr) + (p.b1 != nullptr) + (p.w2 != nullptr) + (p.b2 != nullptr);
+    p.b2 = nullptr;         // has no part in any gradient
+    const int params = (p.w1 != nullptr) + (p.b1 != nullptr) + (p.w2 != nullptr);
     if (parts > 0) with_shape<T>(parts, [&](auto sh) {
         using S = decltype(sh);
         constexpr int threads = block_threads<S::W>(), teams = threads / (32 * S::W), N = channels<T>();

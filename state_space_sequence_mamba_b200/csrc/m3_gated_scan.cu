@@ -24,9 +24,11 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <type_traits>
 
 #include "m3_common.cuh"
 #include "m3_internal.h"
+#include "m3_linattn.h"
 #include "m3_sm100.cuh"
 #include "m3_vec.cuh"
 
@@ -98,15 +100,20 @@ __device__ __forceinline__ V neg(const V& v) { return mul2(v, splat<V>(-1.f)); }
 __device__ __forceinline__ float hw_ex2(float v) { asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(v)); return v; }
 __device__ __forceinline__ float hw_rcp(float v) { asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(v)); return v; }
 __device__ __forceinline__ float hw_rsqrt(float v) { asm("rsqrt.approx.ftz.f32 %0, %0;" : "+f"(v)); return v; }
-__device__ __forceinline__ float at_most(float v, float b) { asm("min.NaN.f32 %0, %0, %1;" : "+f"(v) : "f"(b)); return v; }
 __device__ __forceinline__ float at_least(float v, float b) { asm("max.NaN.f32 %0, %0, %1;" : "+f"(v) : "f"(b)); return v; }
 
 constexpr float kLog2e = 1.4426950408889634f;
-// e^-v, at most 2^62, so that (1 + e)(1 + e') is finite: sigmoids end at 2^-62 instead of at zero
-template <typename V>
-__device__ __forceinline__ V exp_neg(const V& v) {
-    return each(mul2(v, splat<V>(-kLog2e)), [](float x) { return at_most(hw_ex2(x), 4.611686018427388e18f); });
+// A gate is taken to be at least -43 (NaN stays): then (1 + e^-r)(1 + e^-i) is finite, and a sigmoid ends at 2^-62
+// instead of at zero. For a pair of bf16 that is one instruction.
+constexpr float kLeast = -43.f;
+__device__ __forceinline__ float bounded(float, uint32_t w) { return at_least(__uint_as_float(w), kLeast); }
+__device__ __forceinline__ float2 bounded(const float2&, uint32_t w) {
+    uint32_t v;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(v) : "r"(w), "r"(0xc22cc22cu));       // bf16 -43 twice
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
 }
+template <typename V>
+__device__ __forceinline__ V exp_neg(const V& v) { return each(mul2(v, splat<V>(-kLog2e)), hw_ex2); }
 
 // 1 - e^l: the series' up to kSeries, the other beyond
 constexpr float kSeries = 0.35f;
@@ -124,20 +131,20 @@ struct Gates {
     V l, lw;        // power: log a and log a / w
 };
 
-// k: power: -power softplus(d), the largest |log a|; lerp: d. kSmall: |k| <= kSeries, the series of
-// 1 - e^l alone serves (it holds for |l| <= kSeries: the next term is 0.35^8 / 8! = 6e-9); otherwise e^l from the
-// hardware's 2^x where |l| is larger. 1 - a^2 = m (2 - m) with m = 1 - a: no digits are lost for a near 1.
-template <bool kLerp, bool kGate, bool kBack, typename V>
-__device__ __forceinline__ Gates<V> gates(const V& r, const V& i, const V& k, bool small) {
+// r, i: the gates' words. k: power: -power softplus(d), the largest |log a|; lerp: d. kSmall: |k| <= kSeries, the series
+// of 1 - e^l alone serves (it holds for |l| <= kSeries: the next term is 0.35^8 / 8! = 6e-9); otherwise e^l from the
+// hardware's 2^x where |l| is larger. 1 - a^2 = m (2 - m) with m = 1 - a: no digits are lost for a near 1. log a is
+// taken 1e-30 lower, so that w is not zero where sig(r) is.
+template <bool kLerp, bool kGate, bool kBack, bool kSmall, typename V>
+__device__ __forceinline__ Gates<V> gates(uint32_t rw, uint32_t iw, const V& k) {
     Gates<V> g{};
     const V one = splat<V>(1.f);
-    V er, R;
-    if (kLerp) er = exp_neg(add2(r, k));
-    else er = exp_neg(r);
-    V sr;
+    V er, sr;
+    if (kLerp) er = exp_neg(each(add2(bounded(k, rw), k), [](float v) { return at_least(v, kLeast); }));
+    else er = exp_neg(bounded(k, rw));
     if (kGate) {        // one reciprocal for both sigmoids
-        const V ei = exp_neg(i), pr = add2(er, one), pi = add2(ei, one);
-        R = each(mul2(pr, pi), hw_rcp);
+        const V ei = exp_neg(bounded(k, iw)), pr = add2(er, one), pi = add2(ei, one);
+        const V R = each(mul2(pr, pi), hw_rcp);
         sr = mul2(pi, R);
         g.si = mul2(pr, R);
         if (kBack) g.ci = mul2(ei, g.si);
@@ -150,22 +157,21 @@ __device__ __forceinline__ Gates<V> gates(const V& r, const V& i, const V& k, bo
         return g;
     }
     if (kBack) g.cr = mul2(er, sr);
-    const V l = mul2(k, sr);
-    // m = 1 - e^l = -l (1 + l/2 (1 + l/3 (1 + ... l/7)))
+    const V l = fma2(k, sr, splat<V>(-1e-30f));
+    // -m = e^l - 1 = l (1 + l/2 (1 + l/3 (1 + ... l/7)))
     V s = fma2(l, splat<V>(1.f / 5040.f), splat<V>(1.f / 720.f));
     s = fma2(l, s, splat<V>(1.f / 120.f));
     s = fma2(l, s, splat<V>(1.f / 24.f));
     s = fma2(l, s, splat<V>(1.f / 6.f));
     s = fma2(l, s, splat<V>(0.5f));
     s = fma2(l, s, one);
-    V m = neg(mul2(l, s));
-    if (!small) {
-        const V big = each(mul2(l, splat<V>(kLog2e)), [](float x) { return 1.f - hw_ex2(x); });
+    V m = mul2(l, s);
+    if (!kSmall) {
+        const V big = each(mul2(l, splat<V>(kLog2e)), [](float x) { return hw_ex2(x) - 1.f; });
         m = beyond(l, m, big);
     }
-    g.a = add2(one, neg(m));
-    const V q = each(mul2(m, add2(splat<V>(2.f), neg(m))), [](float v) { return at_least(v, 1e-37f); });
-    const V rs = each(q, hw_rsqrt);
+    g.a = add2(one, m);
+    const V q = mul2(neg(m), add2(splat<V>(2.f), m)), rs = each(q, hw_rsqrt);
     g.w = mul2(q, rs);
     if (kBack) {
         g.l = l;
@@ -295,56 +301,142 @@ struct Pair {
     V a, b;
 };
 
+// Tiles of the input tensors. kStaged (rows of whole 16-byte words): rows of 128 bytes in shared memory, brought by
+// asynchronous copies while other tiles are worked on; otherwise each thread's own words in its registers, a tile ahead.
+constexpr int kRowBytes = 128, kTileBytes = kTile * kRowBytes;
+template <typename T, bool kVec, bool kStaged, int kTensors>
+struct Tiles {
+    using Col = Column<T, kVec>;
+    const T* base[kTensors];        // kStaged: of the batch entry; otherwise of this thread's column
+    int64_t token[kTensors];
+    uint32_t at[kTensors];          // kStaged: this thread's first 16 bytes of a tile
+    uint32_t raw[kStaged ? 1 : kTensors][kStaged ? 1 : kTok];
+    uint8_t* room;
+    const Col& k;
+    int chunk_bytes, warp, lane;
+    __device__ __forceinline__ Tiles(const Col& col, int column, int C, uint8_t* smem) : room(smem), k(col) {
+        warp = threadIdx.x >> 5;
+        lane = threadIdx.x & 31;
+        const int c = column * 32 * Word<T>::E + static_cast<int>(threadIdx.x & 7) * (16 / static_cast<int>(sizeof(T)));
+        chunk_bytes = c < C ? 16 : 0;
+    }
+    __device__ __forceinline__ void set(int n, const GsTensor& t, int64_t b, int column) {
+        token[n] = t.token;
+        if (kStaged) {
+            const int c = column * 32 * Word<T>::E;
+            base[n] = static_cast<const T*>(t.p) + b * t.batch + c;
+            at[n] = (static_cast<uint32_t>(threadIdx.x >> 3) * static_cast<uint32_t>(t.token) +
+                     (chunk_bytes ? threadIdx.x & 7u : 0u) * static_cast<uint32_t>(16 / sizeof(T)));
+        } else {
+            base[n] = static_cast<const T*>(t.p) + b * t.batch + k.c;
+        }
+    }
+    // the rows of a tile, `rows` of which hold tokens, into a slot
+    __device__ __forceinline__ void fetch(int64_t tile, int rows, int slot) {
+        if constexpr (kStaged) {
+            const int r = threadIdx.x >> 3;
+#pragma unroll
+            for (int n = 0; n < kTensors; ++n) {
+                const T* src = base[n] + tile * kTile * token[n];
+                uint8_t* dst = room + (slot * kTensors + n) * kTileBytes + threadIdx.x * 16;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const bool live = r + 32 * half < rows;
+                    const T* from = live ? src + at[n] + static_cast<uint32_t>(half * 32) * static_cast<uint32_t>(token[n]) : base[n];
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sm100::smem_u32(dst + half * 4096)), "l"(from),
+                                 "r"(live ? chunk_bytes : 0) : "memory");
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        } else {
+#pragma unroll
+            for (int n = 0; n < kTensors; ++n) {
+                const T* src = base[n] + (tile * kTile + warp * kTok) * token[n];
+#pragma unroll
+                for (int j = 0; j < kTok; ++j) raw[n][j] = k.load(src + j * token[n], k.ok && warp * kTok + j < rows);
+            }
+        }
+    }
+    template <int keep>
+    __device__ __forceinline__ void wait() const {
+        if (kStaged) asm volatile("cp.async.wait_group %0;" ::"n"(keep) : "memory");
+    }
+    __device__ __forceinline__ uint32_t word(int slot, int n, int j) const {
+        if constexpr (kStaged)
+            return *reinterpret_cast<const uint32_t*>(room + (slot * kTensors + n) * kTileBytes + (warp * kTok + j) * kRowBytes + lane * 4);
+        else return raw[n][j];
+    }
+};
+
+// the eight rows of a warp that hold tokens: [lo, hi) of its eight
+struct Live {
+    int lo, hi;
+    __device__ __forceinline__ bool all() const { return lo <= 0 && hi >= kTok; }
+    __device__ __forceinline__ bool operator()(int j) const { return j >= lo && j < hi; }
+};
+__device__ __forceinline__ int clamp_tile(int64_t n) { return n < 0 ? 0 : n > kTile ? kTile : static_cast<int>(n); }
+
+template <bool k>
+struct Is {
+    static constexpr bool value = k;
+};
+template <typename F>
+__device__ __forceinline__ void branch(bool b, F&& f) {
+    if (b) f(Is<true>{});
+    else f(Is<false>{});
+}
+
 // ---- forward
 
-template <typename T, bool kLerp, bool kGate, bool kPacked, bool kVec, bool kCluster>
-__global__ void __launch_bounds__(kThreads, 2) gs_fwd_kernel(const __grid_constant__ GsParams p) {
+template <typename T, bool kLerp, bool kGate, bool kPacked, int kMode, bool kCluster>
+__global__ void __launch_bounds__(kThreads, kMode == 2 ? 3 : 2) gs_fwd_kernel(const __grid_constant__ GsParams p) {
+    constexpr bool kVec = kMode >= 1, kStaged = kMode == 2;
+    constexpr int kTensors = kGate ? 3 : 2, kSlots = 3;
     using Col = Column<T, kVec>;
     using V = typename Col::V;
     __shared__ Pair<V> s_warp[2][kWarps][32];
     __shared__ Pair<V> s_rank[kCluster ? 2 : 1][kCluster ? kMaxRanks : 1][32];
     __shared__ int s_reset[2][kMaxRanks];
     __shared__ Rows s_rows[kPacked ? 3 : 1];
+    extern __shared__ __align__(16) uint8_t s_tiles[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = kCluster ? static_cast<int>(blockIdx.x % p.ranks) : 0;
-    const int64_t unit = kCluster ? blockIdx.x / p.ranks : blockIdx.x;
+    const int ranks = kCluster ? p.ranks : 1;
+    const int rank = kCluster ? static_cast<int>(blockIdx.x % ranks) : 0;
+    const int64_t unit = kCluster ? blockIdx.x / ranks : blockIdx.x;
     const int64_t b = unit / p.cols;
-    const Col k(p, static_cast<int>(unit - b * p.cols));
+    const int column = static_cast<int>(unit - b * p.cols);
+    const Col k(p, column);
     int64_t first = 0, last = p.L;
     if (kPacked) packed_span(p, &first, &last);
     const int64_t tiles = (last + kTile - 1) / kTile;
-    const int64_t steps = (tiles + p.ranks - 1) / p.ranks;
+    const int64_t steps = (tiles + ranks - 1) / ranks;
+
+    Tiles<T, kVec, kStaged, kTensors> in(k, column, p.C, s_tiles);
+    in.set(0, p.x, b, column);
+    in.set(1, p.r, b, column);
+    if constexpr (kGate) in.set(2, p.i, b, column);
+    const auto fetch = [&](int64_t tile, int slot) { in.fetch(tile, clamp_tile(last - tile * kTile), slot); };
+    if (steps > 0) {
+        fetch(rank, 0);
+        if (kStaged) fetch(rank + ranks, 1);
+    }
 
     const V d = k.param(p.decay);
     const V kd = kLerp ? d : each(d, [&](float v) { return -p.power * softplus(v); });
     bool small = true;
     each(kd, [&](float v) { small = small && v >= -kSeries; return v; });
-    small = __all_sync(0xffffffffu, small);
+    small = kLerp || __all_sync(0xffffffffu, small);
     if (kPacked && p.final_state) empty_sequences(p, k, rank, p.init, p.final_state);
     V carry = splat<V>(0.f);
     if (!kPacked && p.init) carry = k.get(p.init + b * p.C);
+    if (kPacked && threadIdx.x < kTile) find_rows(p, s_rows[0], rank, last);
+    in.template wait<1>();
+    if (kStaged || kPacked) __syncthreads();
 
-    const T *px = at<const T>(p.x, b, k.c), *pr = at<const T>(p.r, b, k.c), *pi = kGate ? at<const T>(p.i, b, k.c) : nullptr;
-    T* py = p.y.p ? at<T>(p.y, b, k.c) : nullptr;
-    uint32_t rx[kTok], rr[kTok], ri[kTok];
-    const auto fetch = [&](int64_t tile) {
-        const int64_t t0 = tile * kTile + warp * kTok;
-#pragma unroll
-        for (int j = 0; j < kTok; ++j) {
-            const bool live = k.ok && t0 + j < last;
-            rx[j] = k.load(px + (t0 + j) * p.x.token, live);
-            rr[j] = k.load(pr + (t0 + j) * p.r.token, live);
-            if (kGate) ri[j] = k.load(pi + (t0 + j) * p.i.token, live);
-        }
-    };
-    fetch(rank);
-    if (kPacked) {
-        if (threadIdx.x < kTile) find_rows(p, s_rows[0], rank, last);
-        __syncthreads();
-    }
-    int rb = 0;
+    T* py = p.y.p ? static_cast<T*>(p.y.p) + b * p.y.batch + k.c : nullptr;
+    int rb = 0, slot = 0;
     for (int64_t step = 0; step < steps; ++step) {
-        const int64_t tile = step * p.ranks + rank, t0 = tile * kTile + warp * kTok;
+        const int64_t tile = step * ranks + rank, t0 = tile * kTile + warp * kTok;
         const int buf = static_cast<int>(step & 1);
         Rows& rows = s_rows[kPacked ? rb : 0];
         uint32_t st = 0;
@@ -353,19 +445,23 @@ __global__ void __launch_bounds__(kThreads, 2) gs_fwd_kernel(const __grid_consta
             st = mine(rows.start, warp);
             rb = rb == 2 ? 0 : rb + 1;
         }
+        // (the slot of the tile before, which every thread has read)
+        const int next = slot == 2 ? 0 : slot + 1;
+        if (kStaged) fetch(tile + 2 * ranks, next == 2 ? 0 : next + 1);
+        branch(small, [&](auto is_small) {
 #pragma unroll
-        for (int j = 0; j < kTok; ++j) {
-            const V x = Word<T>::unpack(rx[j]);
-            const Gates<V> g = gates<kLerp, kGate, false>(Word<T>::unpack(rr[j]), Word<T>::unpack(kGate ? ri[j] : 0u), kd, small);
-            a[j] = g.a;
-            h[j] = mul2(g.w, kGate ? mul2(g.si, x) : x);
-        }
-        fetch(tile + p.ranks);
-        if (kPacked && st) {
+            for (int j = 0; j < kTok; ++j) {
+                const V x = Word<T>::unpack(in.word(slot, 0, j));
+                const Gates<V> g = gates<kLerp, kGate, false, decltype(is_small)::value>(in.word(slot, 1, j), kGate ? in.word(slot, kTensors - 1, j) : 0u, kd);
+                a[j] = g.a;
+                h[j] = mul2(g.w, kGate ? mul2(g.si, x) : x);
+            }
+        });
+        if (!kStaged) fetch(tile + ranks, 0);
+        if (kPacked && st && p.init) {
 #pragma unroll
             for (int j = 0; j < kTok; ++j)
-                if (st >> j & 1)
-                    if (p.init) h[j] = fma2(a[j], k.get(p.init + static_cast<int64_t>(rows.seq[warp * kTok + j]) * p.C), h[j]);
+                if (st >> j & 1) h[j] = fma2(a[j], k.get(p.init + static_cast<int64_t>(rows.seq[warp * kTok + j]) * p.C), h[j]);
         }
         // a[j] becomes the product of the decays, h[j] the state from zero, both from the thread's first
         // token (or from the last one up to j that begins a sequence)
@@ -377,14 +473,15 @@ __global__ void __launch_bounds__(kThreads, 2) gs_fwd_kernel(const __grid_consta
             a[j] = mul2(a[j], a[j - 1]);
         }
         s_warp[buf][warp][lane] = Pair<V>{a[kTok - 1], h[kTok - 1]};
-        if (kPacked && threadIdx.x < kTile) find_rows(p, s_rows[rb], tile + p.ranks, last);
+        if (kPacked && threadIdx.x < kTile) find_rows(p, s_rows[rb], tile + ranks, last);
+        in.template wait<1>();      // the next tile
         __syncthreads();
-        V in;           // the state before this thread's tokens
+        V before;       // the state before this thread's tokens
         if (!kCluster) {
             V s = carry;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                if (w == warp) in = s;
+                if (w == warp) before = s;
                 const Pair<V> q = s_warp[buf][w][lane];
                 const V n = fma2(q.a, s, q.b);
                 s = kPacked && mine(rows.start, w) ? q.b : n;
@@ -406,31 +503,44 @@ __global__ void __launch_bounds__(kThreads, 2) gs_fwd_kernel(const __grid_consta
                 cut = cut || c;
             }
             cooperative_groups::cluster_group cl = cooperative_groups::this_cluster();
-            if (warp < p.ranks) {       // one warp for each rank (at most eight)
+            if (warp < ranks) {         // one warp for each rank (at most eight)
                 cl.map_shared_rank(&s_rank[buf][rank][0], warp)[lane] = Pair<V>{pa, pb};
                 if (lane == 0) cl.map_shared_rank(&s_reset[buf][rank], warp)[0] = cut;
             }
             cl.sync();
             V s = carry;
-            for (int r = 0; r < p.ranks; ++r) {
-                if (r == rank) in = s;
+            for (int r = 0; r < ranks; ++r) {
+                if (r == rank) before = s;
                 const Pair<V> q = s_rank[buf][r][lane];
                 const V n = fma2(q.a, s, q.b);
                 s = kPacked && s_reset[buf][r] ? q.b : n;
             }
             carry = s;
-            if (p.marks && warp == 0 && tile < tiles) k.put(p.marks + (b * p.tiles + tile) * p.C, in);
-            const V n = fma2(ea, in, eb);
-            in = kPacked && ecut ? eb : n;
+            if (p.marks && warp == 0 && tile < tiles) k.put(p.marks + (b * p.tiles + tile) * p.C, before);
+            const V n = fma2(ea, before, eb);
+            before = kPacked && ecut ? eb : n;
         }
-        const uint32_t en = kPacked ? mine(rows.end, warp) : 0u;
 #pragma unroll
         for (int j = 0; j < kTok; ++j) {
-            const V n = fma2(a[j], in, h[j]);
+            const V n = fma2(a[j], before, h[j]);
             h[j] = kPacked && (st & ((2u << j) - 1)) ? h[j] : n;
-            if (py && k.ok && t0 + j < last && t0 + j >= first) k.store(py + (t0 + j) * p.y.token, h[j]);
+        }
+        slot = next;
+        if (py) {
+            const Live live{static_cast<int>(first > t0 ? (first - t0 < kTok ? first - t0 : kTok) : 0),
+                            static_cast<int>(last > t0 ? (last - t0 < kTok ? last - t0 : kTok) : 0)};
+            T* to = py + t0 * p.y.token;
+            if (live.all() && k.ok) {
+#pragma unroll
+                for (int j = 0; j < kTok; ++j) k.store(to + j * p.y.token, h[j]);
+            } else if (k.ok) {
+#pragma unroll
+                for (int j = 0; j < kTok; ++j)
+                    if (live(j)) k.store(to + j * p.y.token, h[j]);
+            }
         }
         if (!p.final_state) continue;
+        const uint32_t en = kPacked ? mine(rows.end, warp) : 0u;
         if (kPacked && en) {
 #pragma unroll
             for (int j = 0; j < kTok; ++j)
@@ -444,17 +554,15 @@ __global__ void __launch_bounds__(kThreads, 2) gs_fwd_kernel(const __grid_consta
     }
     // (no token at all: the state stays)
     if (!kPacked && steps == 0 && rank == 0 && warp == 0 && p.final_state) k.put(p.final_state + b * p.C, carry);
+    in.template wait<0>();
 }
 
 // ---- backward
 
-template <typename V>
-struct Trio {
-    V a, b, g;
-};
-
-template <typename T, bool kLerp, bool kGate, bool kPacked, bool kVec, bool kCluster>
+template <typename T, bool kLerp, bool kGate, bool kPacked, int kMode, bool kCluster>
 __global__ void __launch_bounds__(kThreads, 2) gs_bwd_kernel(const __grid_constant__ GsParams p) {
+    constexpr bool kVec = kMode >= 1, kStaged = kMode == 2;
+    constexpr int kTensors = kGate ? 4 : 3;
     using Col = Column<T, kVec>;
     using V = typename Col::V;
     __shared__ Pair<V> s_warp[2][kWarps][32];
@@ -462,65 +570,63 @@ __global__ void __launch_bounds__(kThreads, 2) gs_bwd_kernel(const __grid_consta
     __shared__ Pair<V> s_rank[kCluster ? 2 : 1][kCluster ? kMaxRanks : 1][32];
     __shared__ int s_reset[2][kMaxRanks];
     __shared__ Rows s_rows[kPacked ? 3 : 1];
+    extern __shared__ __align__(16) uint8_t s_tiles[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = kCluster ? static_cast<int>(blockIdx.x % p.ranks) : 0;
-    const int64_t unit = kCluster ? blockIdx.x / p.ranks : blockIdx.x;
+    const int ranks = kCluster ? p.ranks : 1;
+    const int rank = kCluster ? static_cast<int>(blockIdx.x % ranks) : 0;
+    const int64_t unit = kCluster ? blockIdx.x / ranks : blockIdx.x;
     const int share = static_cast<int>(unit / p.cols);
-    const Col k(p, static_cast<int>(unit - static_cast<int64_t>(share) * p.cols));
+    const int column = static_cast<int>(unit - static_cast<int64_t>(share) * p.cols);
+    const Col k(p, column);
     sm100::grid_dep_wait();     // the marks may still be formed
     sm100::grid_dep_launch_dependents();
     int64_t first = 0, last = p.L;
     if (kPacked) packed_span(p, &first, &last);
     const int64_t tiles = (last + kTile - 1) / kTile;
-    const int64_t steps = (tiles + p.ranks - 1) / p.ranks;
+    const int64_t steps = (tiles + ranks - 1) / ranks;
 
     const V d = k.param(p.decay);
     const V kd = kLerp ? d : each(d, [&](float v) { return -p.power * softplus(v); });
     bool small = true;
     each(kd, [&](float v) { small = small && v >= -kSeries; return v; });
-    small = __all_sync(0xffffffffu, small);
+    small = kLerp || __all_sync(0xffffffffu, small);
     if (kPacked && p.dinit) empty_sequences(p, k, rank, p.dfinal, p.dinit);
     V sum = splat<V>(0.f);
     int tick = 0;               // which of the two exchange buffers is next, across sequences
     const V zero = splat<V>(0.f);
+    Tiles<T, kVec, kStaged, kTensors> in(k, column, p.C, s_tiles);
 
     for (int64_t b = share; b < p.nb; b += p.shares) {
-        const T *px = at<const T>(p.x, b, k.c), *pr = at<const T>(p.r, b, k.c), *pd = at<const T>(p.dy, b, k.c);
-        const T* pi = kGate ? at<const T>(p.i, b, k.c) : nullptr;
-        T *qx = at<T>(p.dx, b, k.c), *qr = at<T>(p.dr, b, k.c), *qi = kGate ? at<T>(p.di, b, k.c) : nullptr;
-        uint32_t rx[kTok], rr[kTok], ri[kTok], rd[kTok];
+        in.set(0, p.x, b, column);
+        in.set(1, p.r, b, column);
+        in.set(2, p.dy, b, column);
+        if constexpr (kGate) in.set(3, p.i, b, column);
         V mark = zero;
-        const auto fetch = [&](int64_t tile) {
-            const int64_t t0 = tile * kTile + warp * kTok;
-            const bool ok = k.ok && tile >= 0;
-            mark = tile >= 0 ? k.get(p.marks + (b * p.tiles + tile) * p.C) : zero;
-#pragma unroll
-            for (int j = 0; j < kTok; ++j) {
-                const bool live = ok && t0 + j < last;
-                rx[j] = k.load(px + (t0 + j) * p.x.token, live);
-                rr[j] = k.load(pr + (t0 + j) * p.r.token, live);
-                if (kGate) ri[j] = k.load(pi + (t0 + j) * p.i.token, live);
-                rd[j] = k.load(pd + (t0 + j) * p.dy.token, live);
-            }
-        };
-        fetch(tiles - 1 - rank);
-        int rb = 0;
-        if (kPacked) {
-            if (threadIdx.x < kTile) find_rows(p, s_rows[0], tiles - 1 - rank, last);
-            __syncthreads();
+        const auto fetch = [&](int64_t tile, int slot) { in.fetch(tile < 0 ? 0 : tile, tile < 0 ? 0 : clamp_tile(last - tile * kTile), slot); };
+        const auto get_mark = [&](int64_t tile) { mark = tile >= 0 ? k.get(p.marks + (b * p.tiles + tile) * p.C) : zero; };
+        T *qx = static_cast<T*>(p.dx.p) + b * p.dx.batch + k.c, *qr = static_cast<T*>(p.dr.p) + b * p.dr.batch + k.c;
+        T* qi = kGate ? static_cast<T*>(p.di.p) + b * p.di.batch + k.c : nullptr;
+        if (steps > 0) {
+            fetch(tiles - 1 - rank, 0);
+            if (kStaged) fetch(tiles - 1 - rank - ranks, 1);
         }
+        get_mark(tiles - 1 - rank);
+        int rb = 0, slot = 0;
+        if (kPacked && threadIdx.x < kTile) find_rows(p, s_rows[0], tiles - 1 - rank, last);
+        in.template wait<1>();
+        if (kStaged || kPacked) __syncthreads();
         V carry = zero;         // G behind the tiles done so far (set where a sequence ends)
         for (int64_t step = 0; step < steps; ++step) {
-            const int64_t tile = tiles - 1 - step * p.ranks - rank, t0 = tile * kTile + warp * kTok;
+            const int64_t tile = tiles - 1 - step * ranks - rank, t0 = tile * kTile + warp * kTok;
             const int buf = tick;
             tick ^= 1;
             Rows& rows = s_rows[kPacked ? rb : 0];
             // rows that begin and end a sequence: bits of the thread's tokens
             uint32_t st, en;
+            const int tail = tile >= 0 && last - 1 - tile * kTile < kTile ? static_cast<int>(last - 1 - tile * kTile) : -1;
             const auto ends = [&](int w) {
                 if (kPacked) return mine(rows.end, w);
-                const int64_t at = last - 1 - (tile * kTile + w * kTok);
-                return tile >= 0 && at >= 0 && at < kTok ? 1u << at : 0u;
+                return tail >= 0 && tail >> 3 == w ? 1u << (tail & 7) : 0u;
             };
             if (kPacked) {
                 st = mine(rows.start, warp);
@@ -529,37 +635,57 @@ __global__ void __launch_bounds__(kThreads, 2) gs_bwd_kernel(const __grid_consta
                 st = t0 == 0 ? 1u : 0u;
             }
             en = ends(warp);
+            const Live live{static_cast<int>(first > t0 ? (first - t0 < kTok ? first - t0 : kTok) : 0),
+                            static_cast<int>(tile >= 0 && last > t0 ? (last - t0 < kTok ? last - t0 : kTok) : 0)};
+            const bool plain = st == 0 && en == 0 && live.all();
             const auto seq = [&](int j) { return kPacked ? static_cast<int64_t>(rows.seq[warp * kTok + j]) : b; };
             const auto gin = [&](int j) { return p.dfinal ? k.get(p.dfinal + seq(j) * p.C) : zero; };
             V a[kTok], h[kTok];
+            branch(small, [&](auto is_small) {
 #pragma unroll
-            for (int j = 0; j < kTok; ++j) {
-                const V x = Word<T>::unpack(rx[j]);
-                const Gates<V> g = gates<kLerp, kGate, false>(Word<T>::unpack(rr[j]), Word<T>::unpack(kGate ? ri[j] : 0u), kd, small);
-                a[j] = g.a;
-                h[j] = mul2(g.w, kGate ? mul2(g.si, x) : x);
-            }
-            V pa = a[0], pb = h[0], pg = zero;
-            if (kPacked && (st & 1) && p.init) pb = fma2(a[0], k.get(p.init + seq(0) * p.C), h[0]);
-#pragma unroll
-            for (int j = 1; j < kTok; ++j) {
-                if (kPacked && (st >> j & 1)) {
-                    pb = p.init ? fma2(a[j], k.get(p.init + seq(j) * p.C), h[j]) : h[j];
-                } else {
-                    pb = fma2(a[j], pb, h[j]);
+                for (int j = 0; j < kTok; ++j) {
+                    const V x = Word<T>::unpack(in.word(slot, 0, j));
+                    const Gates<V> g = gates<kLerp, kGate, false, decltype(is_small)::value>(in.word(slot, 1, j), kGate ? in.word(slot, kTensors - 1, j) : 0u, kd);
+                    a[j] = g.a;
+                    h[j] = mul2(g.w, kGate ? mul2(g.si, x) : x);
                 }
-                pa = mul2(pa, a[j]);
-            }
+            });
+            V pa = a[0], pb = h[0], pg = zero;
+            if (plain) {
 #pragma unroll
-            for (int j = kTok - 1; j >= 0; --j) {
-                if (en >> j & 1) pg = gin(j);
-                pg = mul2(a[j], add2(Word<T>::unpack(rd[j]), pg));
+                for (int j = 1; j < kTok; ++j) {
+                    pb = fma2(a[j], pb, h[j]);
+                    pa = mul2(pa, a[j]);
+                }
+#pragma unroll
+                for (int j = kTok - 1; j >= 0; --j) pg = mul2(a[j], add2(Word<T>::unpack(in.word(slot, 2, j)), pg));
+            } else {
+                if (kPacked && (st & 1) && p.init) pb = fma2(a[0], k.get(p.init + seq(0) * p.C), h[0]);
+#pragma unroll
+                for (int j = 1; j < kTok; ++j) {
+                    if (kPacked && (st >> j & 1)) {
+                        pb = p.init ? fma2(a[j], k.get(p.init + seq(j) * p.C), h[j]) : h[j];
+                    } else {
+                        pb = fma2(a[j], pb, h[j]);
+                    }
+                    pa = mul2(pa, a[j]);
+                }
+#pragma unroll
+                for (int j = kTok - 1; j >= 0; --j) {
+                    if (en >> j & 1) pg = gin(j);
+                    pg = mul2(a[j], add2(Word<T>::unpack(in.word(slot, 2, j)), pg));
+                }
             }
             s_warp[buf][warp][lane] = Pair<V>{pa, pb};
             s_back[buf][warp][lane] = pg;
-            if (kPacked && threadIdx.x < kTile) find_rows(p, s_rows[rb], tile - p.ranks, last);
+            if (kPacked && threadIdx.x < kTile) find_rows(p, s_rows[rb], tile - ranks, last);
+            in.template wait<0>();      // the next tile
             __syncthreads();
+            // (into the slot of the tile before, which every thread has done with)
+            const int next = slot == 2 ? 0 : slot + 1;
+            if (kStaged) fetch(tile - 2 * ranks, next == 2 ? 0 : next + 1);
             V hp = mark;        // the state before this thread's tokens
+            get_mark(tile - ranks);
 #pragma unroll
             for (int w = 0; w < kWarps - 1; ++w) {
                 if (w >= warp) break;
@@ -573,8 +699,8 @@ __global__ void __launch_bounds__(kThreads, 2) gs_bwd_kernel(const __grid_consta
 #pragma unroll
                 for (int w = kWarps - 1; w >= 0; --w) {
                     if (w == warp) G = s;
-                    const V n = fma2(s_warp[buf][w][lane].a, s, s_back[buf][w][lane]);
-                    s = ends(w) ? s_back[buf][w][lane] : n;
+                    const V back = s_back[buf][w][lane], n = fma2(s_warp[buf][w][lane].a, s, back);
+                    s = ends(w) ? back : n;
                 }
                 carry = s;
             } else {
@@ -591,13 +717,13 @@ __global__ void __launch_bounds__(kThreads, 2) gs_bwd_kernel(const __grid_consta
                     cut = cut || c;
                 }
                 cooperative_groups::cluster_group cl = cooperative_groups::this_cluster();
-                if (warp < p.ranks) {
+                if (warp < ranks) {
                     cl.map_shared_rank(&s_rank[buf][rank][0], warp)[lane] = Pair<V>{ca, cb};
                     if (lane == 0) cl.map_shared_rank(&s_reset[buf][rank], warp)[0] = cut;
                 }
                 cl.sync();
                 V s = carry;
-                for (int r = 0; r < p.ranks; ++r) {
+                for (int r = 0; r < ranks; ++r) {
                     if (r == rank) G = s;
                     const Pair<V> q = s_rank[buf][r][lane];
                     const V n = fma2(q.a, s, q.b);
@@ -615,35 +741,47 @@ __global__ void __launch_bounds__(kThreads, 2) gs_bwd_kernel(const __grid_consta
                 h[j] = hp;
                 hp = n;
             }
-#pragma unroll
-            for (int j = kTok - 1; j >= 0; --j) {
-                if (en >> j & 1) G = gin(j);
-                const V g = add2(Word<T>::unpack(rd[j]), G);
-                const V x = Word<T>::unpack(rx[j]);
-                const Gates<V> gt = gates<kLerp, kGate, true>(Word<T>::unpack(rr[j]), Word<T>::unpack(kGate ? ri[j] : 0u), kd, small);
-                const bool live = k.ok && tile >= 0 && t0 + j < last && t0 + j >= first;
+            T *tx = qx + t0 * p.dx.token, *tr = qr + t0 * p.dr.token, *ti = kGate ? qi + t0 * p.di.token : nullptr;
+            const auto token = [&](int j, auto is_plain, auto is_small) {
+                constexpr bool kPlain = decltype(is_plain)::value;
+                if (!kPlain && (en >> j & 1)) G = gin(j);
+                const V g = add2(Word<T>::unpack(in.word(slot, 2, j)), G);
+                const V x = Word<T>::unpack(in.word(slot, 0, j));
+                const Gates<V> gt = gates<kLerp, kGate, true, decltype(is_small)::value>(in.word(slot, 1, j), kGate ? in.word(slot, kTensors - 1, j) : 0u, kd);
+                const bool on = kPlain ? k.ok : k.ok && live(j);
                 const V du = mul2(g, gt.w);
                 const V dx = kGate ? mul2(du, gt.si) : du, u = kGate ? mul2(x, gt.si) : x;
-                V dr;
+                V dr, dl;
                 if (kLerp) {
-                    dr = mul2(mul2(g, add2(h[j], neg(u))), mul2(gt.a, gt.w));
-                    if (live) sum = add2(sum, dr);
+                    dl = dr = mul2(mul2(g, add2(h[j], neg(u))), mul2(a[j], gt.w));
                 } else {
-                    const V dl = mul2(g, mul2(gt.a, fma2(gt.l, h[j], neg(mul2(mul2(u, gt.a), gt.lw)))));
-                    if (live) sum = add2(sum, dl);
+                    dl = mul2(g, mul2(a[j], fma2(gt.l, h[j], neg(mul2(mul2(u, a[j]), gt.lw)))));
                     dr = mul2(dl, gt.cr);
                 }
-                G = mul2(gt.a, g);
-                if (live) {
-                    k.store(qx + (t0 + j) * p.dx.token, dx);
-                    k.store(qr + (t0 + j) * p.dr.token, dr);
-                    if (kGate) k.store(qi + (t0 + j) * p.di.token, mul2(mul2(dx, x), gt.ci));
+                if (kPlain || on) sum = add2(sum, dl);
+                G = mul2(a[j], g);
+                if (on) {
+                    k.store(tx + j * p.dx.token, dx);
+                    k.store(tr + j * p.dr.token, dr);
+                    if (kGate) k.store(ti + j * p.di.token, mul2(mul2(dx, x), gt.ci));
                 }
-                if ((st >> j & 1) && tile >= 0 && p.dinit) k.put(p.dinit + seq(j) * p.C, G);
+                if (!kPlain && (st >> j & 1) && tile >= 0 && p.dinit) k.put(p.dinit + seq(j) * p.C, G);
+            };
+            if (plain && small) {
+#pragma unroll
+                for (int j = kTok - 1; j >= 0; --j) token(j, Is<true>{}, Is<true>{});
+            } else if (plain) {
+#pragma unroll
+                for (int j = kTok - 1; j >= 0; --j) token(j, Is<true>{}, Is<kLerp>{});
+            } else {
+#pragma unroll
+                for (int j = kTok - 1; j >= 0; --j) token(j, Is<false>{}, Is<kLerp>{});
             }
-            fetch(tile - p.ranks);
+            if (!kStaged) fetch(tile - ranks, 0);
+            slot = next;
         }
-        __syncthreads();        // the next sequence's rows and pairs
+        in.template wait<0>();
+        __syncthreads();        // the next sequence's rows, tiles and pairs
         if (!kPacked && steps == 0 && rank == 0 && warp == 0 && p.dinit)
             k.put(p.dinit + b * p.C, p.dfinal ? k.get(p.dfinal + b * p.C) : zero);
     }
@@ -659,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, 2) gs_bwd_kernel(const __grid_consta
             const float s = softplus(v);
             return v < -15.f ? 1.f : 1.f / (s * (1.f + expf(-v)));
         }));
-    k.put(p.part + (static_cast<int64_t>(share) * p.ranks + rank) * p.C, total);
+    k.put(p.part + (static_cast<int64_t>(share) * ranks + rank) * p.C, total);
 }
 
 // ---- one token
@@ -683,7 +821,7 @@ __global__ void __launch_bounds__(kThreads) gs_step_kernel(const __grid_constant
     const bool in = slot >= 0 && slot < nstates;
     if (in) {
         const V kd = kLerp ? d : each(d, [&](float v) { return -p.power * softplus(v); });
-        const Gates<V> g = gates<kLerp, kGate, false>(W::unpack(rr), W::unpack(ri), kd, false);
+        const Gates<V> g = gates<kLerp, kGate, false, false>(rr, ri, kd);
         const V x = W::unpack(rx);
         h = fma2(g.a, k.get(p.init + slot * p.C), mul2(g.w, kGate ? mul2(g.si, x) : x));
         k.put(p.final_state + slot * p.C, h);
@@ -693,11 +831,16 @@ __global__ void __launch_bounds__(kThreads) gs_step_kernel(const __grid_constant
 
 // ---- launches
 
-template <typename K, typename... Args>
-cudaError_t launch(K* kernel, int64_t grid, int ranks, bool after, cudaStream_t s, const Args&... args) {
+template <typename... P, typename... Args>
+cudaError_t launch(void (*kernel)(P...), int64_t grid, int ranks, int smem, bool after, cudaStream_t s, const Args&... args) {
+    if (ranks == 1 && !after) {
+        kernel<<<static_cast<unsigned>(grid), kThreads, smem, s>>>(args...);
+        return cudaGetLastError();
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     if (ranks > 1) {
@@ -715,27 +858,39 @@ cudaError_t launch(K* kernel, int64_t grid, int ranks, bool after, cudaStream_t 
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <bool kL, bool kG, bool kP, bool kV, bool kC>
+template <bool... b>
 struct Flags {
-    static constexpr bool L = kL, G = kG, P = kP, V = kV, C = kC;
+    template <int i>
+    static constexpr bool at() {
+        constexpr bool v[] = {b...};
+        return v[i];
+    }
 };
 template <bool... B, typename F>
 auto with_bools(F&& f) { return f(Flags<B...>{}); }
 template <bool... B, typename F, typename... R>
 auto with_bools(F&& f, bool b, R... r) { return b ? with_bools<B..., true>(f, r...) : with_bools<B..., false>(f, r...); }
 
-// Columns that fill words: pointers and strides of whole words, an even number of channels.
-bool words_ok(const GsParams& p) {
-    if (p.C % 2) return false;
+// Rows of whole units of `bytes`: pointers, strides and channels; a tile's rows within 32-bit offsets.
+bool rows_of(const GsParams& p, int es, int bytes) {
+    if (p.C * static_cast<int64_t>(es) % bytes) return false;
     for (const GsTensor* t : {&p.x, &p.r, &p.i, &p.y, &p.dy, &p.dx, &p.dr, &p.di})
-        if (t->p && ((reinterpret_cast<uintptr_t>(t->p) & 3u) || t->batch % 2 || t->token % 2)) return false;
+        if (t->p && (reinterpret_cast<uintptr_t>(t->p) % bytes || t->batch * es % bytes || t->token * es % bytes ||
+                     t->token < 0 || t->token > (int64_t(1) << 25)))
+            return false;
     return true;
+}
+// 2: staged through shared memory; 1: words of two bf16 or one fp32; 0: an element at a time
+template <typename T>
+int mode_of(const GsParams& p) {
+    constexpr int es = sizeof(T);
+    return rows_of(p, es, 16) ? 2 : es == 4 || rows_of(p, es, 4) ? 1 : 0;
 }
 
 // CTAs of a column: as many as there is room for beside the other columns.
 constexpr int kPerSm = 2;
-int rank_count(int64_t units, int64_t tiles) {
-    int64_t r = kPerSm * static_cast<int64_t>(device_sm_count()) / (units > 0 ? units : 1);
+int rank_count(int64_t units, int64_t tiles, int per_sm) {
+    int64_t r = per_sm * static_cast<int64_t>(device_sm_count()) / (units > 0 ? units : 1);
     if (r > tiles) r = tiles;
     return r < 1 ? 1 : r > kMaxRanks ? kMaxRanks : static_cast<int>(r);
 }
@@ -746,26 +901,54 @@ int share_count(const GsParams& p) {
     return static_cast<int>(p.nb < want ? p.nb : want);
 }
 
+// f with the kernel's mode: element-wise code exists for bf16 alone
+template <typename T, typename F>
+cudaError_t with_mode(int mode, F&& f) {
+    if (mode == 2) return f(std::integral_constant<int, 2>{});
+    if constexpr (sizeof(T) == 2) {
+        if (mode == 0) return f(std::integral_constant<int, 0>{});
+    }
+    return f(std::integral_constant<int, 1>{});
+}
+
+template <auto K>
+cudaError_t staged_smem(int bytes) {
+    static std::atomic<uint64_t> done{0};
+    return bytes > 0 ? allow_smem(K, bytes, done) : cudaSuccess;
+}
+
 template <typename T>
 cudaError_t launch_fwd(GsParams p, bool lerp, cudaStream_t s) {
-    p.ranks = rank_count(p.nb * p.cols, p.tiles);
-    return with_bools<>([&](auto f) {
-        using F = decltype(f);
-        return launch(gs_fwd_kernel<T, F::L, F::G, F::P, F::V || sizeof(T) == 4, F::C>, p.nb * p.cols * p.ranks, p.ranks, false, s, p);
-    }, lerp, p.i.p != nullptr, p.cu != nullptr, sizeof(T) == 4 || words_ok(p), p.ranks > 1);
+    const int mode = mode_of<T>(p);
+    p.ranks = rank_count(p.nb * p.cols, p.tiles, mode == 2 ? 3 : 2);
+    return with_mode<T>(mode, [&](auto m) {
+        return with_bools<>([&](auto f) {
+            using F = decltype(f);
+            constexpr int kMode = decltype(m)::value;
+            constexpr auto kernel = gs_fwd_kernel<T, F::template at<0>(), F::template at<1>(), F::template at<2>(), kMode, F::template at<3>()>;
+            constexpr int smem = kMode == 2 ? 3 * (F::template at<1>() ? 3 : 2) * kTileBytes : 0;
+            const cudaError_t e = staged_smem<kernel>(smem);
+            return e != cudaSuccess ? e : launch(kernel, p.nb * p.cols * p.ranks, p.ranks, smem, false, s, p);
+        }, lerp, p.i.p != nullptr, p.cu != nullptr, p.ranks > 1);
+    });
 }
 
 template <typename T>
 cudaError_t launch_bwd(GsParams p, bool lerp, bool after, float* ddecay, cudaStream_t s) {
     p.shares = share_count(p);
-    p.ranks = rank_count(static_cast<int64_t>(p.shares) * p.cols, p.tiles);
+    p.ranks = rank_count(static_cast<int64_t>(p.shares) * p.cols, p.tiles, kPerSm);
     if (!ddecay) p.part = nullptr;
     else if (p.shares * p.ranks == 1) p.part = ddecay;
-    cudaError_t e = with_bools<>([&](auto f) {
-        using F = decltype(f);
-        return launch(gs_bwd_kernel<T, F::L, F::G, F::P, F::V || sizeof(T) == 4, F::C>,
-                      static_cast<int64_t>(p.shares) * p.cols * p.ranks, p.ranks, after, s, p);
-    }, lerp, p.i.p != nullptr, p.cu != nullptr, sizeof(T) == 4 || words_ok(p), p.ranks > 1);
+    const cudaError_t e = with_mode<T>(mode_of<T>(p), [&](auto m) {
+        return with_bools<>([&](auto f) {
+            using F = decltype(f);
+            constexpr int kMode = decltype(m)::value;
+            constexpr auto kernel = gs_bwd_kernel<T, F::template at<0>(), F::template at<1>(), F::template at<2>(), kMode, F::template at<3>()>;
+            constexpr int smem = kMode == 2 ? 3 * (F::template at<1>() ? 4 : 3) * kTileBytes : 0;
+            const cudaError_t e = staged_smem<kernel>(smem);
+            return e != cudaSuccess ? e : launch(kernel, static_cast<int64_t>(p.shares) * p.cols * p.ranks, p.ranks, smem, after, s, p);
+        }, lerp, p.i.p != nullptr, p.cu != nullptr, p.ranks > 1);
+    });
     if (e != cudaSuccess || !ddecay || p.shares * p.ranks == 1) return e;
     float* const outs[1] = {ddecay};
     return launch_sum_shares(p.part, p.shares * p.ranks, p.C, outs, 1, s);
@@ -776,8 +959,9 @@ cudaError_t launch_step(const GsParams& p, bool lerp, const int32_t* slots, int6
     const int64_t grid = (p.nb * p.cols + kWarps - 1) / kWarps;
     return with_bools<>([&](auto f) {
         using F = decltype(f);
-        return launch(gs_step_kernel<T, F::L, F::G, F::P || sizeof(T) == 4>, grid, 1, false, s, p, slots, nstates);
-    }, lerp, p.i.p != nullptr, sizeof(T) == 4 || words_ok(p), false, false);
+        return launch(gs_step_kernel<T, F::template at<0>(), F::template at<1>(), F::template at<2>() || sizeof(T) == 4>, grid, 1, 0, false, s,
+                      p, slots, nstates);
+    }, lerp, p.i.p != nullptr, sizeof(T) == 4 || mode_of<T>(p) > 0);
 }
 
 m3_status err(m3_status st, const char* fmt, ...) {
@@ -965,7 +1149,7 @@ size_t m3_gated_scan_bwd_workspace_bytes(const m3_gated_scan_dims* dims, int pac
     if (packed) in.cu_seqlens = &mark;
     GsParams p = make_params(dims, &in);
     p.shares = share_count(p);
-    const size_t part = up(static_cast<size_t>(p.shares) * rank_count(static_cast<int64_t>(p.shares) * p.cols, p.tiles) *
+    const size_t part = up(static_cast<size_t>(p.shares) * rank_count(static_cast<int64_t>(p.shares) * p.cols, p.tiles, kPerSm) *
                            static_cast<size_t>(p.C) * 4);
     return part + (have_marks ? 0 : marks_bytes(dims, packed));
 }
