@@ -459,7 +459,7 @@ M3_API m3_status m3_group_norm_bwd(const m3_group_norm_dims* dims, const m3_view
  * Views: batch and token strides (head is not used), channels contiguous. A sigmoid ends at 2^-62 (arguments
  * below -43), not at zero. */
 #define M3_GS_LERP 1u
-#define M3_GS_BLOCK 64      /* tokens between two marks */
+#define M3_GS_BLOCK 8       /* tokens between two marks */
 
 typedef struct {
     int64_t nseq;      /* sequences, 0 to 2^24                                             */

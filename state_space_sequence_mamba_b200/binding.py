@@ -24,7 +24,7 @@ BWD_FP32 = M3_BWD_FP32
 # m3_group_norm_dims.flags
 M3_GN_CENTER, M3_GN_SILU = 1, 2
 # m3_gated_scan_dims.flags, and the tokens between two of its marks
-M3_GS_LERP, M3_GS_BLOCK = 1, 64
+M3_GS_LERP, M3_GS_BLOCK = 1, 8
 # m3_rotary_dims.flags
 M3_ROT_INTERLEAVED, M3_ROT_INVERSE, M3_ROT_POS64 = 1, 2, 4
 # m3_block_norm_dims.flags
@@ -588,7 +588,7 @@ def gated_scan_fwd(x, r, i=None, decay=None, power=8.0, lerp=False, init=None, f
     tensors of batch 1, states [n, C]. ``final=True`` allocates the final state, ``False``/None skips it, or
     pass a tensor (it may be ``init``). ``y`` is allocated unless given (packed: zeroed, since rows of no sequence
     are not written). ``marks=True`` allocates the states that spare gated_scan_bwd a pass, [b or 1,
-    ceil(L / 64), C] fp32, or pass a tensor. Returns (y, final state or None, marks or None)."""
+    ceil(L / 8), C] fp32, or pass a tensor. Returns (y, final state or None, marks or None)."""
     return _run("gated_scan_fwd", stream, x, x, r, i, decay, power, lerp, init, final, y, cu_seqlens, marks)
 
 

@@ -4,21 +4,21 @@
 //     lerp:   a_t = sig(r_t + d),                     w_t = 1 - a_t
 //     h_t = a_t h_{t-1} + w_t u_t,  u_t = sig(i_t) x_t
 // Bound by HBM: the forward reads x, r, i and writes y once, the backward reads those and dy and writes
-// three gradients. Two tokens compose as (A, B) after (A', B') = (A A', A B' + B), so time is cut: a
-// CTA takes a tile of 64 tokens by 32 words (a word: two bf16 channels or one of fp32), a thread eight
-// tokens of one word. It reduces them to one (A, B) in registers, the warps' pairs are combined in order
-// through shared memory, and each thread then finishes its eight tokens; the next tile's loads are in
-// flight meanwhile. Where columns of channels are fewer than the device holds CTAs, the CTAs of a cluster
-// take the tiles of a column in turn and exchange one pair per tile through each other's shared memory.
-// Everything is added in a fixed order.
+// three gradients. Two tokens compose as (A, B) after (A', B') = (A A', A B' + B), so time is cut: a CTA takes a
+// tile of 8 tokens a warp by 32 words (a word: two bf16 channels or one of fp32), a thread eight tokens of one word.
+// It reduces them to one (A, B) in registers, the warps' pairs are combined in order through shared memory, and
+// each thread then finishes its eight tokens; the next tile's loads are in flight meanwhile. Where columns of
+// channels are fewer than the device holds CTAs, the CTAs of a cluster take the tiles of a column in turn and exchange
+// one pair a tile through each other's shared memory. Everything is added in a fixed order.
 //
 // Backward. With g_t = dL/dh_t and G_t = a_t g_t,
 //     g_t = dy_t + G_{t+1},   dx = g w sig(i),   di = dx x (1 - sig(i)),
 //     power:  l = log a:  l dL/dl = g (a l h_{t-1} - u a^2 l / w),  dr = (1 - sig(r)) l dL/dl,
 //             dd = sum l dL/dl sig(d) / softplus(d)      (l / w -> 0 as l -> 0: no singularity is left)
 //     lerp:   dr = g (h_{t-1} - u) a w,  dd = sum dr
-// in tiles from the last one back. h_{t-1} comes from the forward's states before each tile (marks) and
-// the same composition inside a tile, so nothing is read twice and h is not rounded.
+// in tiles from the last one back. The forward's states before every eighth token (marks, half a byte for each element)
+// give each thread its h: only G is composed, h is not rounded and nothing is read twice. A thread finds the
+// decays first (for G), then g from its last token back, then h and the gradients from its first token on.
 #include <cooperative_groups.h>
 
 #include <cmath>
@@ -35,9 +35,10 @@
 namespace m3 {
 namespace {
 
-constexpr int kWarps = 8, kTok = 8, kTile = kWarps * kTok, kThreads = 32 * kWarps;
+constexpr int kTok = 8;                             // tokens of a thread
+constexpr int kFwdWarps = 16, kBwdWarps = 8, kStepWarps = 8;
 constexpr int kMaxRanks = 8;
-static_assert(kTile == M3_GS_BLOCK, "marks lie before every tile");
+static_assert(kTok == M3_GS_BLOCK, "a mark for every thread of a tile");
 
 struct GsTensor {
     void* p;
@@ -51,11 +52,11 @@ struct GsParams {
     float* final_state;
     const float* dfinal;
     float* dinit;
-    float* marks;               // [nb][tiles][C] or null
+    float* marks;               // [nb][blocks][C] or null
     float* part;                // backward: [shares][C]
     int64_t L;
     int64_t nb;                 // batch entries (packed: 1)
-    int nseq, C, cols, ranks, tiles, shares;
+    int nseq, C, cols, ranks, blocks, shares;
     float power;
 };
 
@@ -93,8 +94,26 @@ template <typename F>
 __device__ __forceinline__ float each(float v, F&& f) { return f(v); }
 template <typename F>
 __device__ __forceinline__ float2 each(const float2& v, F&& f) { return make_float2(f(v.x), f(v.y)); }
+__device__ __forceinline__ float mul2(float a, float b) { return __fmul_rn(a, b); }
+__device__ __forceinline__ float add2(float a, float b) { return __fadd_rn(a, b); }
+__device__ __forceinline__ float fma2(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float2 mul2(const float2& a, const float2& b) { return make_float2(__fmul_rn(a.x, b.x), __fmul_rn(a.y, b.y)); }
+__device__ __forceinline__ float2 add2(const float2& a, const float2& b) { return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y)); }
+__device__ __forceinline__ float2 fma2(const float2& a, const float2& b, const float2& c) { return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y)); }
+// With a constant: an element at a time, since the instruction then carries it (a pair's would take two moves).
 template <typename V>
-__device__ __forceinline__ V neg(const V& v) { return mul2(v, splat<V>(-1.f)); }
+__device__ __forceinline__ V plus(const V& v, float c) { return each(v, [=](float x) { return __fadd_rn(x, c); }); }
+template <typename V>
+__device__ __forceinline__ V times(const V& v, float c) { return each(v, [=](float x) { return __fmul_rn(x, c); }); }
+template <typename V>
+__device__ __forceinline__ V less_from(const V& v, float c) { return each(v, [=](float x) { return __fadd_rn(c, -x); }); }   // c - v
+// c - a b
+__device__ __forceinline__ float less2(float a, float b, float c) { return fmaf(-a, b, c); }
+__device__ __forceinline__ float2 less2(const float2& a, const float2& b, const float2& c) {
+    return make_float2(fmaf(-a.x, b.x, c.x), fmaf(-a.y, b.y, c.y));
+}
+__device__ __forceinline__ float minus(float a, float b) { return __fadd_rn(a, -b); }
+__device__ __forceinline__ float2 minus(const float2& a, const float2& b) { return make_float2(__fadd_rn(a.x, -b.x), __fadd_rn(a.y, -b.y)); }
 
 // The hardware's 2^x, 1 / x and 1 / sqrt(x); the bounds keep NaN.
 __device__ __forceinline__ float hw_ex2(float v) { asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(v)); return v; }
@@ -113,71 +132,56 @@ __device__ __forceinline__ float2 bounded(const float2&, uint32_t w) {
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
 }
 template <typename V>
-__device__ __forceinline__ V exp_neg(const V& v) { return each(mul2(v, splat<V>(-kLog2e)), hw_ex2); }
+__device__ __forceinline__ V exp_neg(const V& v) { return each(times(v, -kLog2e), hw_ex2); }
 
-// 1 - e^l: the series' up to kSeries, the other beyond
 constexpr float kSeries = 0.35f;
-__device__ __forceinline__ float beyond(float l, float m, float big) { return l < -kSeries ? big : m; }
-__device__ __forceinline__ float2 beyond(const float2& l, const float2& m, const float2& big) {
-    return make_float2(beyond(l.x, m.x, big.x), beyond(l.y, m.y, big.y));
+
+// r's part: e^-r and n = 1 - a. k: power: power softplus(d), the largest -log a; lerp: d. kSmall: k <= kSeries, the
+// series of 1 - e^-t alone serves (it holds for t <= kSeries: the next term is 0.35^8 / 8! = 6e-9); otherwise e^-t from
+// the hardware's 2^x where t is larger. t = -log a is taken 1e-30 higher, so that w is not zero where sig(r) is.
+__device__ __forceinline__ float decay_of(float sr, float k) { return fmaf(k, sr, 1e-30f); }
+__device__ __forceinline__ float2 decay_of(const float2& sr, const float2& k) { return make_float2(decay_of(sr.x, k.x), decay_of(sr.y, k.y)); }
+template <bool kSmall, typename V>
+__device__ __forceinline__ V one_less(const V& t) {
+    return each(t, [](float t) {        // t (1 - t/2 (1 - t/3 (1 - ... t/7)))
+        float s = fmaf(t, 1.f / 5040.f, -1.f / 720.f);
+        s = fmaf(t, s, 1.f / 120.f);
+        s = fmaf(t, s, -1.f / 24.f);
+        s = fmaf(t, s, 1.f / 6.f);
+        s = fmaf(t, s, -0.5f);
+        s = fmaf(t, s, 1.f);
+        const float n = __fmul_rn(t, s);
+        if (kSmall) return n;
+        return t > kSeries ? __fadd_rn(1.f, -hw_ex2(__fmul_rn(t, -kLog2e))) : n;
+    });
 }
-
-// What one token does to its channels.
-template <typename V>
-struct Gates {
-    V a, w;         // decay and weight of the input
-    V si, ci;       // sig(i) and 1 - sig(i) (with an input gate)
-    V cr;           // power: 1 - sig(r)
-    V l, lw;        // power: log a and log a / w
-};
-
-// r, i: the gates' words. k: power: -power softplus(d), the largest |log a|; lerp: d. kSmall: |k| <= kSeries, the series
-// of 1 - e^l alone serves (it holds for |l| <= kSeries: the next term is 0.35^8 / 8! = 6e-9); otherwise e^l from the
-// hardware's 2^x where |l| is larger. 1 - a^2 = m (2 - m) with m = 1 - a: no digits are lost for a near 1. log a is
-// taken 1e-30 lower, so that w is not zero where sig(r) is.
-template <bool kLerp, bool kGate, bool kBack, bool kSmall, typename V>
-__device__ __forceinline__ Gates<V> gates(uint32_t rw, uint32_t iw, const V& k) {
-    Gates<V> g{};
-    const V one = splat<V>(1.f);
-    V er, sr;
-    if (kLerp) er = exp_neg(each(add2(bounded(k, rw), k), [](float v) { return at_least(v, kLeast); }));
-    else er = exp_neg(bounded(k, rw));
+template <bool kLerp, typename V>
+__device__ __forceinline__ V exp_r(uint32_t rw, const V& k) {
+    if (!kLerp) return exp_neg(bounded(k, rw));
+    return exp_neg(each(add2(bounded(k, rw), k), [](float v) { return at_least(v, kLeast); }));
+}
+// The decay and the weighted input of one token.
+template <bool kLerp, bool kGate, bool kSmall, typename V>
+__device__ __forceinline__ void gates(uint32_t rw, uint32_t iw, const V& x, const V& k, V* a, V* add) {
+    const V er = exp_r<kLerp>(rw, k), pi = plus(er, 1.f);
+    V sr, u = x;
     if (kGate) {        // one reciprocal for both sigmoids
-        const V ei = exp_neg(bounded(k, iw)), pr = add2(er, one), pi = add2(ei, one);
-        const V R = each(mul2(pr, pi), hw_rcp);
-        sr = mul2(pi, R);
-        g.si = mul2(pr, R);
-        if (kBack) g.ci = mul2(ei, g.si);
+        const V ei = exp_neg(bounded(k, iw)), pr = plus(ei, 1.f), R = each(mul2(pr, pi), hw_rcp);
+        sr = mul2(pr, R);
+        u = mul2(u, mul2(pi, R));
     } else {
-        sr = each(add2(er, one), hw_rcp);
+        sr = each(pi, hw_rcp);
     }
     if (kLerp) {
-        g.a = sr;
-        g.w = mul2(er, sr);
-        return g;
+        *a = sr;
+        *add = mul2(mul2(er, sr), u);
+        return;
     }
-    if (kBack) g.cr = mul2(er, sr);
-    const V l = fma2(k, sr, splat<V>(-1e-30f));
-    // -m = e^l - 1 = l (1 + l/2 (1 + l/3 (1 + ... l/7)))
-    V s = fma2(l, splat<V>(1.f / 5040.f), splat<V>(1.f / 720.f));
-    s = fma2(l, s, splat<V>(1.f / 120.f));
-    s = fma2(l, s, splat<V>(1.f / 24.f));
-    s = fma2(l, s, splat<V>(1.f / 6.f));
-    s = fma2(l, s, splat<V>(0.5f));
-    s = fma2(l, s, one);
-    V m = mul2(l, s);
-    if (!kSmall) {
-        const V big = each(mul2(l, splat<V>(kLog2e)), [](float x) { return hw_ex2(x) - 1.f; });
-        m = beyond(l, m, big);
-    }
-    g.a = add2(one, m);
-    const V q = mul2(neg(m), add2(splat<V>(2.f), m)), rs = each(q, hw_rsqrt);
-    g.w = mul2(q, rs);
-    if (kBack) {
-        g.l = l;
-        g.lw = mul2(l, rs);
-    }
-    return g;
+    // 1 - a^2 = n (1 + a): no digits are lost for a near 1
+    const V n = one_less<kSmall>(decay_of(sr, k));
+    *a = less_from(n, 1.f);
+    const V q = fma2(n, *a, n);
+    *add = mul2(mul2(q, each(q, hw_rsqrt)), u);
 }
 
 // softplus(d) = log(1 + e^d)
@@ -245,28 +249,31 @@ __device__ __forceinline__ T* at(const GsTensor& t, int64_t b, int c) { return s
 
 // Which of a tile's rows begin and end a sequence, and whose rows they are. Three of them: the next
 // tile's is written while the slowest warp still reads the last one's.
+template <int kTile>
 struct Rows {
-    uint32_t start[2], end[2];
+    uint32_t start[kTile / 32], end[kTile / 32];
     int seq[kTile];
 };
 
 // Rows of the packed tensor that hold tokens.
-__device__ __forceinline__ void packed_span(const GsParams& p, int64_t* first, int64_t* last) {
-    int64_t f = p.nseq > 0 ? __ldg(p.cu) : 0, l = p.nseq > 0 ? __ldg(p.cu + p.nseq) : 0;
-    *first = f < 0 ? 0 : f > p.L ? p.L : f;
-    *last = l < *first ? *first : l > p.L ? p.L : l;
+__device__ __forceinline__ void packed_span(const GsParams& p, int* first, int* last) {
+    const int L = static_cast<int>(p.L), f = p.nseq > 0 ? __ldg(p.cu) : 0, l = p.nseq > 0 ? __ldg(p.cu + p.nseq) : 0;
+    *first = min(max(f, 0), L);
+    *last = min(max(l, *first), L);
 }
 
-// threads 0 to 63: the sequence of one row each, by halves (the last that begins at or before it)
-__device__ __forceinline__ void find_rows(const GsParams& p, Rows& rows, int64_t tile, int64_t last) {
-    const int64_t row = tile * kTile + threadIdx.x;
+// the first kTile threads: the sequence of one row each, by halves (the last that begins at or before it)
+template <int kTile>
+__device__ __forceinline__ void find_rows(const GsParams& p, Rows<kTile>& rows, int tile, int last) {
+    if (threadIdx.x >= kTile) return;
+    const int row = tile * kTile + static_cast<int>(threadIdx.x);
     int lo = 0, hi = p.nseq;
     while (hi - lo > 1) {
         const int m = (lo + hi) >> 1;
         if (__ldg(p.cu + m) <= row) lo = m;
         else hi = m;
     }
-    const int64_t s = __ldg(p.cu + lo), e = __ldg(p.cu + lo + 1);
+    const int s = __ldg(p.cu + lo), e = __ldg(p.cu + lo + 1);
     const bool in = tile >= 0 && row < last && s <= row && row < e;
     const uint32_t st = __ballot_sync(0xffffffffu, in && s == row), en = __ballot_sync(0xffffffffu, in && e == row + 1);
     const int w = threadIdx.x >> 5;
@@ -278,10 +285,11 @@ __device__ __forceinline__ void find_rows(const GsParams& p, Rows& rows, int64_t
 }
 
 // the eight rows of warp w
-__device__ __forceinline__ uint32_t mine(const uint32_t (&m)[2], int w) { return (m[w >> 2] >> (8 * (w & 3))) & 0xffu; }
+template <int n>
+__device__ __forceinline__ uint32_t mine(const uint32_t (&m)[n], int w) { return (m[w >> 2] >> (8 * (w & 3))) & 0xffu; }
 
 // a sequence without tokens ends in the state it begins with
-template <typename Col>
+template <int kWarps, typename Col>
 __device__ __forceinline__ void empty_sequences(const GsParams& p, const Col& k, int rank, const float* from, float* to) {
     using V = typename Col::V;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -303,59 +311,66 @@ struct Pair {
 
 // Tiles of the input tensors. kStaged (rows of whole 16-byte words): rows of 128 bytes in shared memory, brought by
 // asynchronous copies while other tiles are worked on; otherwise each thread's own words in its registers, a tile ahead.
-constexpr int kRowBytes = 128, kTileBytes = kTile * kRowBytes;
-template <typename T, bool kVec, bool kStaged, int kTensors>
+constexpr int kRowBytes = 128;
+template <typename T, bool kVec, bool kStaged, int kTensors, int kWarps>
 struct Tiles {
+    static constexpr int kTile = kWarps * kTok, kTileBytes = kTile * kRowBytes, kPass = kTile / 2;    // rows of one copy a thread
     using Col = Column<T, kVec>;
-    const T* base[kTensors];        // kStaged: of the batch entry; otherwise of this thread's column
-    int64_t token[kTensors];
-    uint32_t at[kTensors];          // kStaged: this thread's first 16 bytes of a tile
+    const T* next[kTensors];        // this thread's place in the tile to come: its 16 bytes of the first row (kStaged), its word
+    int64_t token[kTensors], step;  // step: rows from tile to tile
     uint32_t raw[kStaged ? 1 : kTensors][kStaged ? 1 : kTok];
     uint8_t* room;
     const Col& k;
     int chunk_bytes, warp, lane;
-    __device__ __forceinline__ Tiles(const Col& col, int column, int C, uint8_t* smem) : room(smem), k(col) {
+    // step: tiles from one to the next
+    __device__ __forceinline__ Tiles(const Col& col, int column, int C, uint8_t* smem, int tiles) : step(static_cast<int64_t>(tiles) * kTile), room(smem), k(col) {
         warp = threadIdx.x >> 5;
         lane = threadIdx.x & 31;
         const int c = column * 32 * Word<T>::E + static_cast<int>(threadIdx.x & 7) * (16 / static_cast<int>(sizeof(T)));
         chunk_bytes = c < C ? 16 : 0;
     }
-    __device__ __forceinline__ void set(int n, const GsTensor& t, int64_t b, int column) {
+    // tensor n, from this tile on
+    __device__ __forceinline__ void set(int n, const GsTensor& t, int64_t b, int column, int64_t tile) {
         token[n] = t.token;
-        if (kStaged) {
-            const int c = column * 32 * Word<T>::E;
-            base[n] = static_cast<const T*>(t.p) + b * t.batch + c;
-            at[n] = (static_cast<uint32_t>(threadIdx.x >> 3) * static_cast<uint32_t>(t.token) +
-                     (chunk_bytes ? threadIdx.x & 7u : 0u) * static_cast<uint32_t>(16 / sizeof(T)));
-        } else {
-            base[n] = static_cast<const T*>(t.p) + b * t.batch + k.c;
-        }
+        const T* base = static_cast<const T*>(t.p) + b * t.batch;
+        if (kStaged)
+            next[n] = base + column * 32 * Word<T>::E + (chunk_bytes ? threadIdx.x & 7u : 0u) * (16 / sizeof(T)) +
+                      (tile * kTile + (threadIdx.x >> 3)) * t.token;
+        else
+            next[n] = base + k.c + (tile * kTile + warp * kTok) * t.token;
     }
-    // the rows of a tile, `rows` of which hold tokens, into a slot
-    __device__ __forceinline__ void fetch(int64_t tile, int rows, int slot) {
+    // the rows of the tile to come, `rows` of which hold tokens, into a slot
+    __device__ __forceinline__ void fetch(int rows, int slot) {
         if constexpr (kStaged) {
             const int r = threadIdx.x >> 3;
+            const uint32_t dst = sm100::smem_u32(room + slot * kTensors * kTileBytes + threadIdx.x * 16);
+            if (rows == kTile) {
 #pragma unroll
-            for (int n = 0; n < kTensors; ++n) {
-                const T* src = base[n] + tile * kTile * token[n];
-                uint8_t* dst = room + (slot * kTensors + n) * kTileBytes + threadIdx.x * 16;
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const bool live = r + 32 * half < rows;
-                    const T* from = live ? src + at[n] + static_cast<uint32_t>(half * 32) * static_cast<uint32_t>(token[n]) : base[n];
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sm100::smem_u32(dst + half * 4096)), "l"(from),
-                                 "r"(live ? chunk_bytes : 0) : "memory");
+                for (int n = 0; n < kTensors; ++n) {
+                    copy(dst + n * kTileBytes, next[n], chunk_bytes);
+                    copy(dst + n * kTileBytes + kTileBytes / 2, next[n] + kPass * token[n], chunk_bytes);
                 }
+            } else if (rows > 0) {      // (a row without a token is zero, read from the tile's first)
+#pragma unroll
+                for (int n = 0; n < kTensors; ++n)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const bool live = r + half * kPass < rows;
+                        copy(dst + n * kTileBytes + half * (kTileBytes / 2), next[n] + (live ? half * kPass : -r) * token[n], live ? chunk_bytes : 0);
+                    }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         } else {
 #pragma unroll
-            for (int n = 0; n < kTensors; ++n) {
-                const T* src = base[n] + (tile * kTile + warp * kTok) * token[n];
+            for (int n = 0; n < kTensors; ++n)
 #pragma unroll
-                for (int j = 0; j < kTok; ++j) raw[n][j] = k.load(src + j * token[n], k.ok && warp * kTok + j < rows);
-            }
+                for (int j = 0; j < kTok; ++j) raw[n][j] = k.load(next[n] + j * token[n], k.ok && warp * kTok + j < rows);
         }
+#pragma unroll
+        for (int n = 0; n < kTensors; ++n) next[n] += step * token[n];
+    }
+    static __device__ __forceinline__ void copy(uint32_t dst, const T* src, int bytes) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
     }
     template <int keep>
     __device__ __forceinline__ void wait() const {
@@ -374,7 +389,8 @@ struct Live {
     __device__ __forceinline__ bool all() const { return lo <= 0 && hi >= kTok; }
     __device__ __forceinline__ bool operator()(int j) const { return j >= lo && j < hi; }
 };
-__device__ __forceinline__ int clamp_tile(int64_t n) { return n < 0 ? 0 : n > kTile ? kTile : static_cast<int>(n); }
+template <int kMost>
+__device__ __forceinline__ int clamp_to(int n) { return min(max(n, 0), kMost); }
 
 template <bool k>
 struct Is {
@@ -389,15 +405,16 @@ __device__ __forceinline__ void branch(bool b, F&& f) {
 // ---- forward
 
 template <typename T, bool kLerp, bool kGate, bool kPacked, int kMode, bool kCluster>
-__global__ void __launch_bounds__(kThreads, kMode == 2 ? 3 : 2) gs_fwd_kernel(const __grid_constant__ GsParams p) {
+__global__ void __launch_bounds__(32 * kFwdWarps, kMode == 2 ? 2 : 1) gs_fwd_kernel(const __grid_constant__ GsParams p) {
     constexpr bool kVec = kMode >= 1, kStaged = kMode == 2;
-    constexpr int kTensors = kGate ? 3 : 2, kSlots = 3;
+    constexpr int kTensors = kGate ? 3 : 2, kWarps = kFwdWarps, kTile = kWarps * kTok;
     using Col = Column<T, kVec>;
     using V = typename Col::V;
     __shared__ Pair<V> s_warp[2][kWarps][32];
+    __shared__ V s_carry[2][32];            // the state behind a tile
     __shared__ Pair<V> s_rank[kCluster ? 2 : 1][kCluster ? kMaxRanks : 1][32];
     __shared__ int s_reset[2][kMaxRanks];
-    __shared__ Rows s_rows[kPacked ? 3 : 1];
+    __shared__ Rows<kTile> s_rows[kPacked ? 3 : 1];
     extern __shared__ __align__(16) uint8_t s_tiles[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int ranks = kCluster ? p.ranks : 1;
@@ -406,56 +423,49 @@ __global__ void __launch_bounds__(kThreads, kMode == 2 ? 3 : 2) gs_fwd_kernel(co
     const int64_t b = unit / p.cols;
     const int column = static_cast<int>(unit - b * p.cols);
     const Col k(p, column);
-    int64_t first = 0, last = p.L;
+    int first = 0, last = static_cast<int>(p.L);       // (up to 2^30: rows are counted in 32 bits)
     if (kPacked) packed_span(p, &first, &last);
-    const int64_t tiles = (last + kTile - 1) / kTile;
-    const int64_t steps = (tiles + ranks - 1) / ranks;
+    const int tiles = (last + kTile - 1) / kTile, steps = (tiles + ranks - 1) / ranks;
 
-    Tiles<T, kVec, kStaged, kTensors> in(k, column, p.C, s_tiles);
-    in.set(0, p.x, b, column);
-    in.set(1, p.r, b, column);
-    if constexpr (kGate) in.set(2, p.i, b, column);
-    const auto fetch = [&](int64_t tile, int slot) { in.fetch(tile, clamp_tile(last - tile * kTile), slot); };
+    Tiles<T, kVec, kStaged, kTensors, kWarps> in(k, column, p.C, s_tiles, ranks);
+    in.set(0, p.x, b, column, rank);
+    in.set(1, p.r, b, column, rank);
+    if constexpr (kGate) in.set(2, p.i, b, column, rank);
+    const auto fetch = [&](int tile, int slot) { in.fetch(clamp_to<kTile>(last - tile * kTile), slot); };
     if (steps > 0) {
         fetch(rank, 0);
         if (kStaged) fetch(rank + ranks, 1);
     }
 
     const V d = k.param(p.decay);
-    const V kd = kLerp ? d : each(d, [&](float v) { return -p.power * softplus(v); });
+    const V kd = kLerp ? d : each(d, [&](float v) { return p.power * softplus(v); });
     bool small = true;
-    each(kd, [&](float v) { small = small && v >= -kSeries; return v; });
+    each(kd, [&](float v) { small = small && v <= kSeries; return v; });
     small = kLerp || __all_sync(0xffffffffu, small);
-    if (kPacked && p.final_state) empty_sequences(p, k, rank, p.init, p.final_state);
+    if (kPacked && p.final_state) empty_sequences<kWarps>(p, k, rank, p.init, p.final_state);
     V carry = splat<V>(0.f);
     if (!kPacked && p.init) carry = k.get(p.init + b * p.C);
-    if (kPacked && threadIdx.x < kTile) find_rows(p, s_rows[0], rank, last);
+    if (!kCluster && warp == 0) s_carry[0][lane] = carry;
+    if (kPacked) find_rows(p, s_rows[0], rank, last);
     in.template wait<1>();
     if (kStaged || kPacked) __syncthreads();
 
     T* py = p.y.p ? static_cast<T*>(p.y.p) + b * p.y.batch + k.c : nullptr;
-    int rb = 0, slot = 0;
-    for (int64_t step = 0; step < steps; ++step) {
-        const int64_t tile = step * ranks + rank, t0 = tile * kTile + warp * kTok;
-        const int buf = static_cast<int>(step & 1);
-        Rows& rows = s_rows[kPacked ? rb : 0];
+    int rb = 0;
+    for (int step = 0; step < steps; ++step) {
+        const int tile = step * ranks + rank, t0 = tile * kTile + warp * kTok, buf = step & 1;
+        Rows<kTile>& rows = s_rows[kPacked ? rb : 0];
         uint32_t st = 0;
         V a[kTok], h[kTok];
         if (kPacked) {
             st = mine(rows.start, warp);
             rb = rb == 2 ? 0 : rb + 1;
         }
-        // (the slot of the tile before, which every thread has read)
-        const int next = slot == 2 ? 0 : slot + 1;
-        if (kStaged) fetch(tile + 2 * ranks, next == 2 ? 0 : next + 1);
         branch(small, [&](auto is_small) {
 #pragma unroll
-            for (int j = 0; j < kTok; ++j) {
-                const V x = Word<T>::unpack(in.word(slot, 0, j));
-                const Gates<V> g = gates<kLerp, kGate, false, decltype(is_small)::value>(in.word(slot, 1, j), kGate ? in.word(slot, kTensors - 1, j) : 0u, kd);
-                a[j] = g.a;
-                h[j] = mul2(g.w, kGate ? mul2(g.si, x) : x);
-            }
+            for (int j = 0; j < kTok; ++j)
+                gates<kLerp, kGate, decltype(is_small)::value>(in.word(buf, 1, j), kGate ? in.word(buf, kTensors - 1, j) : 0u,
+                                                               Word<T>::unpack(in.word(buf, 0, j)), kd, &a[j], &h[j]);
         });
         if (!kStaged) fetch(tile + ranks, 0);
         if (kPacked && st && p.init) {
@@ -473,26 +483,25 @@ __global__ void __launch_bounds__(kThreads, kMode == 2 ? 3 : 2) gs_fwd_kernel(co
             a[j] = mul2(a[j], a[j - 1]);
         }
         s_warp[buf][warp][lane] = Pair<V>{a[kTok - 1], h[kTok - 1]};
-        if (kPacked && threadIdx.x < kTile) find_rows(p, s_rows[rb], tile + ranks, last);
-        in.template wait<1>();      // the next tile
+        if (kPacked) find_rows(p, s_rows[rb], tile + ranks, last);
+        in.template wait<0>();      // the next tile
         __syncthreads();
+        // (into this tile's slot, which every thread has read)
+        if (kStaged) fetch(tile + 2 * ranks, buf);
         V before;       // the state before this thread's tokens
         if (!kCluster) {
-            V s = carry;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                if (w == warp) before = s;
+            before = s_carry[buf][lane];
+#pragma unroll 4
+            for (int w = 0; w < warp; ++w) {
                 const Pair<V> q = s_warp[buf][w][lane];
-                const V n = fma2(q.a, s, q.b);
-                s = kPacked && mine(rows.start, w) ? q.b : n;
+                const V n = fma2(q.a, before, q.b);
+                before = kPacked && mine(rows.start, w) ? q.b : n;
             }
-            if (p.marks && warp == 0 && tile < tiles) k.put(p.marks + (b * p.tiles + tile) * p.C, carry);
-            carry = s;
         } else {
             // the tile's pair, and that of the warps before this one
             V pa = splat<V>(1.f), pb = splat<V>(0.f), ea, eb;
             bool cut = false, ecut = false;
-#pragma unroll
+#pragma unroll 4
             for (int w = 0; w < kWarps; ++w) {
                 if (w == warp) { ea = pa; eb = pb; ecut = cut; }
                 const Pair<V> q = s_warp[buf][w][lane];
@@ -516,60 +525,60 @@ __global__ void __launch_bounds__(kThreads, kMode == 2 ? 3 : 2) gs_fwd_kernel(co
                 s = kPacked && s_reset[buf][r] ? q.b : n;
             }
             carry = s;
-            if (p.marks && warp == 0 && tile < tiles) k.put(p.marks + (b * p.tiles + tile) * p.C, before);
             const V n = fma2(ea, before, eb);
             before = kPacked && ecut ? eb : n;
         }
+        const Live live{clamp_to<kTok>(first - t0), clamp_to<kTok>(last - t0)};
+        if (p.marks && live.hi > 0) k.put(p.marks + (b * p.blocks + (tile * kWarps + warp)) * p.C, before);
 #pragma unroll
         for (int j = 0; j < kTok; ++j) {
             const V n = fma2(a[j], before, h[j]);
             h[j] = kPacked && (st & ((2u << j) - 1)) ? h[j] : n;
         }
-        slot = next;
-        if (py) {
-            const Live live{static_cast<int>(first > t0 ? (first - t0 < kTok ? first - t0 : kTok) : 0),
-                            static_cast<int>(last > t0 ? (last - t0 < kTok ? last - t0 : kTok) : 0)};
-            T* to = py + t0 * p.y.token;
-            if (live.all() && k.ok) {
+        if (!kCluster && warp == kWarps - 1) s_carry[buf ^ 1][lane] = h[kTok - 1];
+        if (py && k.ok) {
+            T* to = py + static_cast<int64_t>(t0) * p.y.token;
+            if (live.all()) {
 #pragma unroll
                 for (int j = 0; j < kTok; ++j) k.store(to + j * p.y.token, h[j]);
-            } else if (k.ok) {
+            } else {
 #pragma unroll
                 for (int j = 0; j < kTok; ++j)
                     if (live(j)) k.store(to + j * p.y.token, h[j]);
             }
         }
-        if (!p.final_state) continue;
-        const uint32_t en = kPacked ? mine(rows.end, warp) : 0u;
-        if (kPacked && en) {
+        if (p.final_state) {
+            const uint32_t en = kPacked ? mine(rows.end, warp) : 0u;
+            if (kPacked && en) {
 #pragma unroll
-            for (int j = 0; j < kTok; ++j)
-                if (en >> j & 1) k.put(p.final_state + static_cast<int64_t>(rows.seq[warp * kTok + j]) * p.C, h[j]);
-        }
-        if (!kPacked && t0 <= last - 1 && last - 1 < t0 + kTok) {
+                for (int j = 0; j < kTok; ++j)
+                    if (en >> j & 1) k.put(p.final_state + static_cast<int64_t>(rows.seq[warp * kTok + j]) * p.C, h[j]);
+            }
+            if (!kPacked && live.hi > 0 && last <= t0 + kTok) {
 #pragma unroll
-            for (int j = 0; j < kTok; ++j)
-                if (t0 + j == last - 1) k.put(p.final_state + b * p.C, h[j]);
+                for (int j = 0; j < kTok; ++j)
+                    if (t0 + j == last - 1) k.put(p.final_state + b * p.C, h[j]);
+            }
         }
     }
+    in.template wait<0>();
     // (no token at all: the state stays)
     if (!kPacked && steps == 0 && rank == 0 && warp == 0 && p.final_state) k.put(p.final_state + b * p.C, carry);
-    in.template wait<0>();
 }
 
 // ---- backward
 
 template <typename T, bool kLerp, bool kGate, bool kPacked, int kMode, bool kCluster>
-__global__ void __launch_bounds__(kThreads, 2) gs_bwd_kernel(const __grid_constant__ GsParams p) {
+__global__ void __launch_bounds__(32 * kBwdWarps, 2) gs_bwd_kernel(const __grid_constant__ GsParams p) {
     constexpr bool kVec = kMode >= 1, kStaged = kMode == 2;
-    constexpr int kTensors = kGate ? 4 : 3;
+    constexpr int kTensors = kGate ? 4 : 3, kWarps = kBwdWarps, kTile = kWarps * kTok;
     using Col = Column<T, kVec>;
     using V = typename Col::V;
     __shared__ Pair<V> s_warp[2][kWarps][32];
-    __shared__ V s_back[2][kWarps][32];
+    __shared__ V s_carry[2][32];            // G before a tile
     __shared__ Pair<V> s_rank[kCluster ? 2 : 1][kCluster ? kMaxRanks : 1][32];
     __shared__ int s_reset[2][kMaxRanks];
-    __shared__ Rows s_rows[kPacked ? 3 : 1];
+    __shared__ Rows<kTile> s_rows[kPacked ? 3 : 1];
     extern __shared__ __align__(16) uint8_t s_tiles[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int ranks = kCluster ? p.ranks : 1;
@@ -580,30 +589,32 @@ __global__ void __launch_bounds__(kThreads, 2) gs_bwd_kernel(const __grid_consta
     const Col k(p, column);
     sm100::grid_dep_wait();     // the marks may still be formed
     sm100::grid_dep_launch_dependents();
-    int64_t first = 0, last = p.L;
+    int first = 0, last = static_cast<int>(p.L);       // (up to 2^30: rows are counted in 32 bits)
     if (kPacked) packed_span(p, &first, &last);
-    const int64_t tiles = (last + kTile - 1) / kTile;
-    const int64_t steps = (tiles + ranks - 1) / ranks;
+    const int tiles = (last + kTile - 1) / kTile, steps = (tiles + ranks - 1) / ranks;
 
     const V d = k.param(p.decay);
-    const V kd = kLerp ? d : each(d, [&](float v) { return -p.power * softplus(v); });
+    const V kd = kLerp ? d : each(d, [&](float v) { return p.power * softplus(v); });
     bool small = true;
-    each(kd, [&](float v) { small = small && v >= -kSeries; return v; });
+    each(kd, [&](float v) { small = small && v <= kSeries; return v; });
     small = kLerp || __all_sync(0xffffffffu, small);
-    if (kPacked && p.dinit) empty_sequences(p, k, rank, p.dfinal, p.dinit);
+    if (kPacked && p.dinit) empty_sequences<kWarps>(p, k, rank, p.dfinal, p.dinit);
     V sum = splat<V>(0.f);
     int tick = 0;               // which of the two exchange buffers is next, across sequences
     const V zero = splat<V>(0.f);
-    Tiles<T, kVec, kStaged, kTensors> in(k, column, p.C, s_tiles);
+    Tiles<T, kVec, kStaged, kTensors, kWarps> in(k, column, p.C, s_tiles, -ranks);
 
     for (int64_t b = share; b < p.nb; b += p.shares) {
-        in.set(0, p.x, b, column);
-        in.set(1, p.r, b, column);
-        in.set(2, p.dy, b, column);
-        if constexpr (kGate) in.set(3, p.i, b, column);
+        in.set(0, p.x, b, column, tiles - 1 - rank);
+        in.set(1, p.r, b, column, tiles - 1 - rank);
+        in.set(2, p.dy, b, column, tiles - 1 - rank);
+        if constexpr (kGate) in.set(3, p.i, b, column, tiles - 1 - rank);
         V mark = zero;
-        const auto fetch = [&](int64_t tile, int slot) { in.fetch(tile < 0 ? 0 : tile, tile < 0 ? 0 : clamp_tile(last - tile * kTile), slot); };
-        const auto get_mark = [&](int64_t tile) { mark = tile >= 0 ? k.get(p.marks + (b * p.tiles + tile) * p.C) : zero; };
+        const auto fetch = [&](int tile, int slot) { in.fetch(tile < 0 ? 0 : clamp_to<kTile>(last - tile * kTile), slot); };
+        const auto get_mark = [&](int tile) {       // the state before this thread's tokens
+            const int block = tile * kWarps + warp;
+            mark = tile >= 0 && block * kTok < last ? k.get(p.marks + (b * p.blocks + block) * p.C) : zero;
+        };
         T *qx = static_cast<T*>(p.dx.p) + b * p.dx.batch + k.c, *qr = static_cast<T*>(p.dr.p) + b * p.dr.batch + k.c;
         T* qi = kGate ? static_cast<T*>(p.di.p) + b * p.di.batch + k.c : nullptr;
         if (steps > 0) {
@@ -612,18 +623,19 @@ __global__ void __launch_bounds__(kThreads, 2) gs_bwd_kernel(const __grid_consta
         }
         get_mark(tiles - 1 - rank);
         int rb = 0, slot = 0;
-        if (kPacked && threadIdx.x < kTile) find_rows(p, s_rows[0], tiles - 1 - rank, last);
+        if (kPacked) find_rows(p, s_rows[0], tiles - 1 - rank, last);
+        if (!kCluster && warp == 0) s_carry[tick][lane] = zero;
         in.template wait<1>();
-        if (kStaged || kPacked) __syncthreads();
+        __syncthreads();
         V carry = zero;         // G behind the tiles done so far (set where a sequence ends)
-        for (int64_t step = 0; step < steps; ++step) {
-            const int64_t tile = tiles - 1 - step * ranks - rank, t0 = tile * kTile + warp * kTok;
+        for (int step = 0; step < steps; ++step) {
+            const int tile = tiles - 1 - step * ranks - rank, t0 = tile * kTile + warp * kTok;
             const int buf = tick;
             tick ^= 1;
-            Rows& rows = s_rows[kPacked ? rb : 0];
+            Rows<kTile>& rows = s_rows[kPacked ? rb : 0];
             // rows that begin and end a sequence: bits of the thread's tokens
             uint32_t st, en;
-            const int tail = tile >= 0 && last - 1 - tile * kTile < kTile ? static_cast<int>(last - 1 - tile * kTile) : -1;
+            const int tail = tile >= 0 && last - 1 - tile * kTile < kTile ? last - 1 - tile * kTile : -1;
             const auto ends = [&](int w) {
                 if (kPacked) return mine(rows.end, w);
                 return tail >= 0 && tail >> 3 == w ? 1u << (tail & 7) : 0u;
@@ -635,85 +647,58 @@ __global__ void __launch_bounds__(kThreads, 2) gs_bwd_kernel(const __grid_consta
                 st = t0 == 0 ? 1u : 0u;
             }
             en = ends(warp);
-            const Live live{static_cast<int>(first > t0 ? (first - t0 < kTok ? first - t0 : kTok) : 0),
-                            static_cast<int>(tile >= 0 && last > t0 ? (last - t0 < kTok ? last - t0 : kTok) : 0)};
+            const Live live{clamp_to<kTok>(first - t0), tile >= 0 ? clamp_to<kTok>(last - t0) : 0};
             const bool plain = st == 0 && en == 0 && live.all();
             const auto seq = [&](int j) { return kPacked ? static_cast<int64_t>(rows.seq[warp * kTok + j]) : b; };
             const auto gin = [&](int j) { return p.dfinal ? k.get(p.dfinal + seq(j) * p.C) : zero; };
-            V a[kTok], h[kTok];
+            // e^-r and 1 - a (lerp: a), then the decays' product and G from zero
+            V er[kTok], n[kTok];
             branch(small, [&](auto is_small) {
 #pragma unroll
                 for (int j = 0; j < kTok; ++j) {
-                    const V x = Word<T>::unpack(in.word(slot, 0, j));
-                    const Gates<V> g = gates<kLerp, kGate, false, decltype(is_small)::value>(in.word(slot, 1, j), kGate ? in.word(slot, kTensors - 1, j) : 0u, kd);
-                    a[j] = g.a;
-                    h[j] = mul2(g.w, kGate ? mul2(g.si, x) : x);
+                    er[j] = exp_r<kLerp>(in.word(slot, 1, j), kd);
+                    n[j] = each(plus(er[j], 1.f), hw_rcp);
+                    if (!kLerp) n[j] = one_less<decltype(is_small)::value>(decay_of(n[j], kd));
                 }
             });
-            V pa = a[0], pb = h[0], pg = zero;
-            if (plain) {
+            const auto a = [&](int j) { return kLerp ? n[j] : less_from(n[j], 1.f); };
+            V pa = a(0), pg = zero;
 #pragma unroll
-                for (int j = 1; j < kTok; ++j) {
-                    pb = fma2(a[j], pb, h[j]);
-                    pa = mul2(pa, a[j]);
-                }
+            for (int j = 1; j < kTok; ++j) pa = mul2(pa, a(j));
 #pragma unroll
-                for (int j = kTok - 1; j >= 0; --j) pg = mul2(a[j], add2(Word<T>::unpack(in.word(slot, 2, j)), pg));
-            } else {
-                if (kPacked && (st & 1) && p.init) pb = fma2(a[0], k.get(p.init + seq(0) * p.C), h[0]);
-#pragma unroll
-                for (int j = 1; j < kTok; ++j) {
-                    if (kPacked && (st >> j & 1)) {
-                        pb = p.init ? fma2(a[j], k.get(p.init + seq(j) * p.C), h[j]) : h[j];
-                    } else {
-                        pb = fma2(a[j], pb, h[j]);
-                    }
-                    pa = mul2(pa, a[j]);
-                }
-#pragma unroll
-                for (int j = kTok - 1; j >= 0; --j) {
-                    if (en >> j & 1) pg = gin(j);
-                    pg = mul2(a[j], add2(Word<T>::unpack(in.word(slot, 2, j)), pg));
-                }
+            for (int j = kTok - 1; j >= 0; --j) {
+                if (!plain && (en >> j & 1)) pg = gin(j);
+                pg = mul2(a(j), add2(Word<T>::unpack(in.word(slot, 2, j)), pg));
             }
-            s_warp[buf][warp][lane] = Pair<V>{pa, pb};
-            s_back[buf][warp][lane] = pg;
-            if (kPacked && threadIdx.x < kTile) find_rows(p, s_rows[rb], tile - ranks, last);
+            s_warp[buf][warp][lane] = Pair<V>{pa, pg};
+            if (kPacked) find_rows(p, s_rows[rb], tile - ranks, last);
             in.template wait<0>();      // the next tile
             __syncthreads();
             // (into the slot of the tile before, which every thread has done with)
             const int next = slot == 2 ? 0 : slot + 1;
             if (kStaged) fetch(tile - 2 * ranks, next == 2 ? 0 : next + 1);
-            V hp = mark;        // the state before this thread's tokens
+            V hp = mark;
             get_mark(tile - ranks);
-#pragma unroll
-            for (int w = 0; w < kWarps - 1; ++w) {
-                if (w >= warp) break;
-                const Pair<V> q = s_warp[buf][w][lane];
-                const V n = fma2(q.a, hp, q.b);
-                hp = kPacked && mine(rows.start, w) ? q.b : n;
-            }
-            V G;                // G behind them
+            V G;                // G behind this thread's tokens
             if (!kCluster) {
-                V s = carry;
-#pragma unroll
-                for (int w = kWarps - 1; w >= 0; --w) {
-                    if (w == warp) G = s;
-                    const V back = s_back[buf][w][lane], n = fma2(s_warp[buf][w][lane].a, s, back);
-                    s = ends(w) ? back : n;
+                G = s_carry[buf][lane];
+#pragma unroll 4
+                for (int w = kWarps - 1; w > warp; --w) {
+                    const Pair<V> q = s_warp[buf][w][lane];
+                    const V m = fma2(q.a, G, q.b);
+                    G = ends(w) ? q.b : m;
                 }
-                carry = s;
             } else {
                 V ca = splat<V>(1.f), cb = zero, ea, eb;
                 bool cut = false, ecut = false;
 #pragma unroll
                 for (int w = kWarps - 1; w >= 0; --w) {
                     if (w == warp) { ea = ca; eb = cb; ecut = cut; }
-                    const V qa = s_warp[buf][w][lane].a, qb = s_back[buf][w][lane];
-                    const V n = fma2(qa, cb, qb);
+                    const Pair<V> q = s_warp[buf][w][lane];
+                    const V m = fma2(q.a, cb, q.b);
                     const bool c = ends(w) != 0;
-                    cb = c ? qb : n;
-                    ca = mul2(ca, qa);
+                    cb = c ? q.b : m;
+                    ca = mul2(ca, q.a);
                     cut = cut || c;
                 }
                 cooperative_groups::cluster_group cl = cooperative_groups::this_cluster();
@@ -726,57 +711,68 @@ __global__ void __launch_bounds__(kThreads, 2) gs_bwd_kernel(const __grid_consta
                 for (int r = 0; r < ranks; ++r) {
                     if (r == rank) G = s;
                     const Pair<V> q = s_rank[buf][r][lane];
-                    const V n = fma2(q.a, s, q.b);
-                    s = s_reset[buf][r] ? q.b : n;
+                    const V m = fma2(q.a, s, q.b);
+                    s = s_reset[buf][r] ? q.b : m;
                 }
                 carry = s;
-                const V n = fma2(ea, G, eb);
-                G = ecut ? eb : n;
+                const V m = fma2(ea, G, eb);
+                G = ecut ? eb : m;
             }
-            // the states before each token, then the gradients from the last token back
+            // g of each token from the last one back
+            V g[kTok];
 #pragma unroll
-            for (int j = 0; j < kTok; ++j) {
-                if (kPacked && (st >> j & 1)) hp = p.init ? k.get(p.init + seq(j) * p.C) : zero;
-                const V n = fma2(a[j], hp, h[j]);
-                h[j] = hp;
-                hp = n;
+            for (int j = kTok - 1; j >= 0; --j) {
+                if (!plain && (en >> j & 1)) G = gin(j);
+                g[j] = add2(Word<T>::unpack(in.word(slot, 2, j)), G);
+                G = mul2(a(j), g[j]);
+                if (!plain && (st >> j & 1) && tile >= 0 && p.dinit) k.put(p.dinit + seq(j) * p.C, G);
             }
-            T *tx = qx + t0 * p.dx.token, *tr = qr + t0 * p.dr.token, *ti = kGate ? qi + t0 * p.di.token : nullptr;
-            const auto token = [&](int j, auto is_plain, auto is_small) {
+            if (!kCluster && warp == 0) s_carry[buf ^ 1][lane] = G;
+            // h and the gradients from the first token on
+            const int64_t row0 = t0;
+            T *tx = qx + row0 * p.dx.token, *tr = qr + row0 * p.dr.token, *ti = kGate ? qi + row0 * p.di.token : nullptr;
+            branch(plain, [&](auto is_plain) {
                 constexpr bool kPlain = decltype(is_plain)::value;
-                if (!kPlain && (en >> j & 1)) G = gin(j);
-                const V g = add2(Word<T>::unpack(in.word(slot, 2, j)), G);
-                const V x = Word<T>::unpack(in.word(slot, 0, j));
-                const Gates<V> gt = gates<kLerp, kGate, true, decltype(is_small)::value>(in.word(slot, 1, j), kGate ? in.word(slot, kTensors - 1, j) : 0u, kd);
-                const bool on = kPlain ? k.ok : k.ok && live(j);
-                const V du = mul2(g, gt.w);
-                const V dx = kGate ? mul2(du, gt.si) : du, u = kGate ? mul2(x, gt.si) : x;
-                V dr, dl;
-                if (kLerp) {
-                    dl = dr = mul2(mul2(g, add2(h[j], neg(u))), mul2(a[j], gt.w));
-                } else {
-                    dl = mul2(g, mul2(a[j], fma2(gt.l, h[j], neg(mul2(mul2(u, a[j]), gt.lw)))));
-                    dr = mul2(dl, gt.cr);
+#pragma unroll
+                for (int j = 0; j < kTok; ++j) {
+                    if (!kPlain && kPacked && (st >> j & 1)) hp = p.init ? k.get(p.init + seq(j) * p.C) : zero;
+                    const V x = Word<T>::unpack(in.word(slot, 0, j)), pi = plus(er[j], 1.f);
+                    V sr, si, ci, u = x;
+                    if (kGate) {
+                        const V ei = exp_neg(bounded(kd, in.word(slot, kTensors - 1, j))), pr = plus(ei, 1.f);
+                        const V R = each(mul2(pr, pi), hw_rcp);
+                        sr = mul2(pr, R);
+                        si = mul2(pi, R);
+                        ci = mul2(ei, si);
+                        u = mul2(x, si);
+                    } else {
+                        sr = kLerp ? n[j] : each(pi, hw_rcp);
+                    }
+                    const V aj = a(j), cr = mul2(er[j], sr);
+                    V w, dr, dl;
+                    if (kLerp) {
+                        w = cr;
+                        dl = dr = mul2(mul2(g[j], minus(hp, u)), mul2(aj, w));
+                    } else {
+                        // with t = -log a: -l dL/dl = g a (t h - u a t / w)
+                        const V q = fma2(n[j], aj, n[j]), rs = each(q, hw_rsqrt), t = decay_of(sr, kd);
+                        w = mul2(q, rs);
+                        const V ua = mul2(mul2(u, aj), mul2(t, rs));
+                        dl = mul2(g[j], mul2(aj, less2(t, hp, ua)));
+                        dr = mul2(dl, cr);
+                    }
+                    hp = fma2(aj, hp, mul2(w, u));
+                    const V du = mul2(g[j], w), dx = kGate ? mul2(du, si) : du;
+                    if (kPlain || live(j)) {
+                        sum = add2(sum, dl);
+                        if (k.ok) {
+                            k.store(tx + j * p.dx.token, dx);
+                            k.store(tr + j * p.dr.token, dr);
+                            if (kGate) k.store(ti + j * p.di.token, mul2(mul2(dx, x), ci));
+                        }
+                    }
                 }
-                if (kPlain || on) sum = add2(sum, dl);
-                G = mul2(a[j], g);
-                if (on) {
-                    k.store(tx + j * p.dx.token, dx);
-                    k.store(tr + j * p.dr.token, dr);
-                    if (kGate) k.store(ti + j * p.di.token, mul2(mul2(dx, x), gt.ci));
-                }
-                if (!kPlain && (st >> j & 1) && tile >= 0 && p.dinit) k.put(p.dinit + seq(j) * p.C, G);
-            };
-            if (plain && small) {
-#pragma unroll
-                for (int j = kTok - 1; j >= 0; --j) token(j, Is<true>{}, Is<true>{});
-            } else if (plain) {
-#pragma unroll
-                for (int j = kTok - 1; j >= 0; --j) token(j, Is<true>{}, Is<kLerp>{});
-            } else {
-#pragma unroll
-                for (int j = kTok - 1; j >= 0; --j) token(j, Is<false>{}, Is<kLerp>{});
-            }
+            });
             if (!kStaged) fetch(tile - ranks, 0);
             slot = next;
         }
@@ -786,12 +782,12 @@ __global__ void __launch_bounds__(kThreads, 2) gs_bwd_kernel(const __grid_consta
             k.put(p.dinit + b * p.C, p.dfinal ? k.get(p.dfinal + b * p.C) : zero);
     }
     if (!p.part) return;
-    s_back[0][warp][lane] = sum;
+    s_warp[0][warp][lane].a = sum;
     __syncthreads();
     if (warp != 0) return;
     V total = zero;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) total = add2(total, s_back[0][w][lane]);
+    for (int w = 0; w < kWarps; ++w) total = add2(total, s_warp[0][w][lane].a);
     if (!kLerp)         // dlog a / dd = log a sig(d) / softplus(d); both go to zero together
         total = mul2(total, each(d, [](float v) {
             const float s = softplus(v);
@@ -803,13 +799,13 @@ __global__ void __launch_bounds__(kThreads, 2) gs_bwd_kernel(const __grid_consta
 // ---- one token
 
 template <typename T, bool kLerp, bool kGate, bool kVec>
-__global__ void __launch_bounds__(kThreads) gs_step_kernel(const __grid_constant__ GsParams p, const int32_t* __restrict__ slots,
+__global__ void __launch_bounds__(32 * kStepWarps) gs_step_kernel(const __grid_constant__ GsParams p, const int32_t* __restrict__ slots,
                                                            int64_t nstates) {
     using W = Word<T>;
     using V = typename W::V;
     using Col = Column<T, kVec>;
     // a warp takes 32 words of one sequence
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kStepWarps + (threadIdx.x >> 5);
     const int64_t b = unit / p.cols;
     if (b >= p.nb) return;
     const Col k(p, static_cast<int>(unit - b * p.cols));
@@ -820,10 +816,10 @@ __global__ void __launch_bounds__(kThreads) gs_step_kernel(const __grid_constant
     V h = splat<V>(0.f);
     const bool in = slot >= 0 && slot < nstates;
     if (in) {
-        const V kd = kLerp ? d : each(d, [&](float v) { return -p.power * softplus(v); });
-        const Gates<V> g = gates<kLerp, kGate, false, false>(rr, ri, kd);
-        const V x = W::unpack(rx);
-        h = fma2(g.a, k.get(p.init + slot * p.C), mul2(g.w, kGate ? mul2(g.si, x) : x));
+        const V kd = kLerp ? d : each(d, [&](float v) { return p.power * softplus(v); });
+        V a, add;
+        gates<kLerp, kGate, false>(rr, ri, W::unpack(rx), kd, &a, &add);
+        h = fma2(a, k.get(p.init + slot * p.C), add);
         k.put(p.final_state + slot * p.C, h);
     }
     if (k.ok) k.store(at<T>(p.y, b, k.c), h);
@@ -832,14 +828,14 @@ __global__ void __launch_bounds__(kThreads) gs_step_kernel(const __grid_constant
 // ---- launches
 
 template <typename... P, typename... Args>
-cudaError_t launch(void (*kernel)(P...), int64_t grid, int ranks, int smem, bool after, cudaStream_t s, const Args&... args) {
+cudaError_t launch(void (*kernel)(P...), int64_t grid, int threads, int ranks, int smem, bool after, cudaStream_t s, const Args&... args) {
     if (ranks == 1 && !after) {
-        kernel<<<static_cast<unsigned>(grid), kThreads, smem, s>>>(args...);
+        kernel<<<static_cast<unsigned>(grid), threads, smem, s>>>(args...);
         return cudaGetLastError();
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -888,7 +884,8 @@ int mode_of(const GsParams& p) {
 }
 
 // CTAs of a column: as many as there is room for beside the other columns.
-constexpr int kPerSm = 2;
+constexpr int kPerSm = 2;       // of the backward
+int64_t bwd_tiles(int64_t L) { return (L + kBwdWarps * kTok - 1) / (kBwdWarps * kTok); }
 int rank_count(int64_t units, int64_t tiles, int per_sm) {
     int64_t r = per_sm * static_cast<int64_t>(device_sm_count()) / (units > 0 ? units : 1);
     if (r > tiles) r = tiles;
@@ -920,15 +917,15 @@ cudaError_t staged_smem(int bytes) {
 template <typename T>
 cudaError_t launch_fwd(GsParams p, bool lerp, cudaStream_t s) {
     const int mode = mode_of<T>(p);
-    p.ranks = rank_count(p.nb * p.cols, p.tiles, mode == 2 ? 3 : 2);
+    p.ranks = rank_count(p.nb * p.cols, (p.L + kFwdWarps * kTok - 1) / (kFwdWarps * kTok), mode == 2 ? 2 : 1);
     return with_mode<T>(mode, [&](auto m) {
         return with_bools<>([&](auto f) {
             using F = decltype(f);
             constexpr int kMode = decltype(m)::value;
             constexpr auto kernel = gs_fwd_kernel<T, F::template at<0>(), F::template at<1>(), F::template at<2>(), kMode, F::template at<3>()>;
-            constexpr int smem = kMode == 2 ? 3 * (F::template at<1>() ? 3 : 2) * kTileBytes : 0;
+            constexpr int smem = kMode == 2 ? 2 * (F::template at<1>() ? 3 : 2) * kFwdWarps * kTok * kRowBytes : 0;
             const cudaError_t e = staged_smem<kernel>(smem);
-            return e != cudaSuccess ? e : launch(kernel, p.nb * p.cols * p.ranks, p.ranks, smem, false, s, p);
+            return e != cudaSuccess ? e : launch(kernel, p.nb * p.cols * p.ranks, 32 * kFwdWarps, p.ranks, smem, false, s, p);
         }, lerp, p.i.p != nullptr, p.cu != nullptr, p.ranks > 1);
     });
 }
@@ -936,7 +933,7 @@ cudaError_t launch_fwd(GsParams p, bool lerp, cudaStream_t s) {
 template <typename T>
 cudaError_t launch_bwd(GsParams p, bool lerp, bool after, float* ddecay, cudaStream_t s) {
     p.shares = share_count(p);
-    p.ranks = rank_count(static_cast<int64_t>(p.shares) * p.cols, p.tiles, kPerSm);
+    p.ranks = rank_count(static_cast<int64_t>(p.shares) * p.cols, bwd_tiles(p.L), kPerSm);
     if (!ddecay) p.part = nullptr;
     else if (p.shares * p.ranks == 1) p.part = ddecay;
     const cudaError_t e = with_mode<T>(mode_of<T>(p), [&](auto m) {
@@ -944,9 +941,9 @@ cudaError_t launch_bwd(GsParams p, bool lerp, bool after, float* ddecay, cudaStr
             using F = decltype(f);
             constexpr int kMode = decltype(m)::value;
             constexpr auto kernel = gs_bwd_kernel<T, F::template at<0>(), F::template at<1>(), F::template at<2>(), kMode, F::template at<3>()>;
-            constexpr int smem = kMode == 2 ? 3 * (F::template at<1>() ? 4 : 3) * kTileBytes : 0;
+            constexpr int smem = kMode == 2 ? 3 * (F::template at<1>() ? 4 : 3) * kBwdWarps * kTok * kRowBytes : 0;
             const cudaError_t e = staged_smem<kernel>(smem);
-            return e != cudaSuccess ? e : launch(kernel, static_cast<int64_t>(p.shares) * p.cols * p.ranks, p.ranks, smem, after, s, p);
+            return e != cudaSuccess ? e : launch(kernel, static_cast<int64_t>(p.shares) * p.cols * p.ranks, 32 * kBwdWarps, p.ranks, smem, after, s, p);
         }, lerp, p.i.p != nullptr, p.cu != nullptr, p.ranks > 1);
     });
     if (e != cudaSuccess || !ddecay || p.shares * p.ranks == 1) return e;
@@ -956,10 +953,10 @@ cudaError_t launch_bwd(GsParams p, bool lerp, bool after, float* ddecay, cudaStr
 
 template <typename T>
 cudaError_t launch_step(const GsParams& p, bool lerp, const int32_t* slots, int64_t nstates, cudaStream_t s) {
-    const int64_t grid = (p.nb * p.cols + kWarps - 1) / kWarps;
+    const int64_t grid = (p.nb * p.cols + kStepWarps - 1) / kStepWarps;
     return with_bools<>([&](auto f) {
         using F = decltype(f);
-        return launch(gs_step_kernel<T, F::template at<0>(), F::template at<1>(), F::template at<2>() || sizeof(T) == 4>, grid, 1, 0, false, s,
+        return launch(gs_step_kernel<T, F::template at<0>(), F::template at<1>(), F::template at<2>() || sizeof(T) == 4>, grid, 32 * kStepWarps, 1, 0, false, s,
                       p, slots, nstates);
     }, lerp, p.i.p != nullptr, sizeof(T) == 4 || mode_of<T>(p) > 0);
 }
@@ -1048,14 +1045,14 @@ GsParams make_params(const m3_gated_scan_dims* d, const m3_gated_scan_inputs* in
     const int per = d->in_dtype == M3_BF16 ? 64 : 32;
     p.cols = (p.C + per - 1) / per;
     p.ranks = 1;
-    p.tiles = static_cast<int>((d->seqlen + kTile - 1) / kTile);
+    p.blocks = static_cast<int>((d->seqlen + kTok - 1) / kTok);
     p.power = d->power;
     return p;
 }
 
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 size_t marks_bytes(const m3_gated_scan_dims* d, bool packed) {
-    return up(static_cast<size_t>(packed ? 1 : d->nseq) * static_cast<size_t>((d->seqlen + kTile - 1) / kTile) *
+    return up(static_cast<size_t>(packed ? 1 : d->nseq) * static_cast<size_t>((d->seqlen + kTok - 1) / kTok) *
               static_cast<size_t>(d->channels) * 4);
 }
 
@@ -1149,7 +1146,7 @@ size_t m3_gated_scan_bwd_workspace_bytes(const m3_gated_scan_dims* dims, int pac
     if (packed) in.cu_seqlens = &mark;
     GsParams p = make_params(dims, &in);
     p.shares = share_count(p);
-    const size_t part = up(static_cast<size_t>(p.shares) * rank_count(static_cast<int64_t>(p.shares) * p.cols, p.tiles, kPerSm) *
+    const size_t part = up(static_cast<size_t>(p.shares) * rank_count(static_cast<int64_t>(p.shares) * p.cols, bwd_tiles(p.L), kPerSm) *
                            static_cast<size_t>(p.C) * 4);
     return part + (have_marks ? 0 : marks_bytes(dims, packed));
 }
