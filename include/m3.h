@@ -502,7 +502,7 @@ M3_API size_t m3_gated_scan_bwd_workspace_bytes(const m3_gated_scan_dims* dims, 
 /* Gradients of sum(y * dy) + <final state, dfinal> for the call of m3_gated_scan_fwd with the same
  * dims, inputs and init. dx, dr, di (with i): in_dtype, by their views; rows of no sequence are left as they
  * were. ddecay: fp32 [C], summed over tokens and sequences, or NULL. dfinal, dinit: fp32 [nseq, C], or
- * NULL for zero / not wanted; dinit may be dfinal, not init. marks: that call's, or NULL (they are formed
+ * NULL for zero / not wanted; dinit must be neither. marks: that call's, or NULL (they are formed
  * in the workspace by a pass over the inputs). fp32 pointers 16-byte aligned, workspace 256. */
 typedef struct {
     m3_view dx, dr, di;

@@ -311,14 +311,17 @@ struct Pair {
     V a, b;
 };
 
-// Tiles of the input tensors. kStaged (rows of whole 16-byte words): rows of 128 bytes in shared memory, brought by
-// asynchronous copies while other tiles are worked on; otherwise each thread's own words in its registers, a tile ahead.
+// Tiles of the input tensors. kMode 2 (rows of whole 16-byte words) and 1 (of whole words): rows of 128 bytes in
+// shared memory, brought by asynchronous copies while other tiles are worked on; 0: each thread's own words in its
+// registers, a tile ahead.
 constexpr int kRowBytes = 128;
-template <typename T, bool kVec, bool kStaged, int kTensors, int kWarps>
+template <typename T, int kMode, int kTensors, int kWarps>
 struct Tiles {
+    static constexpr bool kVec = kMode >= 1, kStaged = kMode >= 1;
     static constexpr int kTile = kWarps * kTok, kTileBytes = kTile * kRowBytes, kPass = kTile / 2;    // rows of one copy a thread
     using Col = Column<T, kVec>;
-    const T* next[kTensors];        // this thread's place in the tile to come: its 16 bytes of the first row (kStaged), its word
+    const T* next[kTensors];        // this thread's place in the tile to come: its 16 bytes of the first row (mode 2), its first word
+    const T* first[kMode == 1 ? kTensors : 1];      // a place that can be read
     int64_t token[kTensors], step;  // step: rows from tile to tile
     uint32_t raw[kStaged ? 1 : kTensors][kStaged ? 1 : kTok];
     uint8_t* room;
@@ -335,7 +338,8 @@ struct Tiles {
     __device__ __forceinline__ void set(int n, const GsTensor& t, int64_t b, int column, int64_t tile) {
         token[n] = t.token;
         const T* base = static_cast<const T*>(t.p) + b * t.batch;
-        if (kStaged)
+        if (kMode == 1) first[kMode == 1 ? n : 0] = base;
+        if (kMode == 2)
             next[n] = base + column * 32 * Word<T>::E + (chunk_bytes ? threadIdx.x & 7u : 0u) * (16 / sizeof(T)) +
                       (tile * kTile + (threadIdx.x >> 3)) * t.token;
         else
@@ -343,7 +347,7 @@ struct Tiles {
     }
     // the rows of the tile to come, `rows` of which hold tokens, into a slot
     __device__ __forceinline__ void fetch(int rows, int slot) {
-        if constexpr (kStaged) {
+        if constexpr (kMode == 2) {
             const int r = threadIdx.x >> 3;
             const uint32_t dst = sm100::smem_u32(room + slot * kTensors * kTileBytes + threadIdx.x * 16);
             if (rows == kTile) {
@@ -360,6 +364,18 @@ struct Tiles {
                         const bool live = r + half * kPass < rows;
                         copy(dst + n * kTileBytes + half * (kTileBytes / 2), next[n] + (live ? half * kPass : -r) * token[n], live ? chunk_bytes : 0);
                     }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        } else if constexpr (kMode == 1) {
+            const uint32_t dst = sm100::smem_u32(room + slot * kTensors * kTileBytes + warp * kTok * kRowBytes + lane * 4);
+            const int mine = k.ok ? rows - warp * kTok : 0;
+#pragma unroll
+            for (int n = 0; n < kTensors; ++n) {
+                const T* q = next[n];
+#pragma unroll
+                for (int j = 0; j < kTok; ++j, q += token[n])       // (past the last token: zero, read from nowhere)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + n * kTileBytes + j * kRowBytes),
+                                 "l"(j < mine ? q : first[n]), "r"(j < mine ? 4 : 0) : "memory");
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         } else {
@@ -426,8 +442,8 @@ __device__ __forceinline__ void meet(bool sent) {
 constexpr int fwd_warps(bool cluster) { return cluster ? kFwdClusterWarps : kFwdWarps; }
 
 template <typename T, bool kLerp, bool kGate, bool kPacked, int kMode, bool kCluster>
-__global__ void __launch_bounds__(32 * fwd_warps(kCluster), kMode == 2 ? 2 : 1) gs_fwd_kernel(const __grid_constant__ GsParams p) {
-    constexpr bool kVec = kMode >= 1, kStaged = kMode == 2;
+__global__ void __launch_bounds__(32 * fwd_warps(kCluster), kMode >= 1 ? 2 : 1) gs_fwd_kernel(const __grid_constant__ GsParams p) {
+    constexpr bool kVec = kMode >= 1, kStaged = kMode >= 1;
     constexpr int kTensors = kGate ? 3 : 2, kWarps = fwd_warps(kCluster), kTile = kWarps * kTok;
     using Col = Column<T, kVec>;
     using V = typename Col::V;
@@ -448,7 +464,7 @@ __global__ void __launch_bounds__(32 * fwd_warps(kCluster), kMode == 2 ? 2 : 1) 
     if (kPacked) packed_span(p, &first, &last);
     const int tiles = (last + kTile - 1) / kTile, steps = (tiles + ranks - 1) / ranks;
 
-    Tiles<T, kVec, kStaged, kTensors, kWarps> in(k, column, p.C, s_tiles, ranks);
+    Tiles<T, kMode, kTensors, kWarps> in(k, column, p.C, s_tiles, ranks);
     in.set(0, p.x, b, column, rank);
     in.set(1, p.r, b, column, rank);
     if constexpr (kGate) in.set(2, p.i, b, column, rank);
@@ -470,6 +486,7 @@ __global__ void __launch_bounds__(32 * fwd_warps(kCluster), kMode == 2 ? 2 : 1) 
     if (kPacked) find_rows(p, s_rows[0], rank, last);
     in.template wait<1>();
     if (kStaged || kPacked) __syncthreads();
+    if (kCluster) meet(false);      // every CTA of the cluster runs
 
     T* py = p.y.p ? static_cast<T*>(p.y.p) + b * p.y.batch + k.c : nullptr;
     int rb = 0;
@@ -583,7 +600,7 @@ __global__ void __launch_bounds__(32 * fwd_warps(kCluster), kMode == 2 ? 2 : 1) 
 
 template <typename T, bool kLerp, bool kGate, bool kPacked, int kMode, bool kCluster>
 __global__ void __launch_bounds__(32 * kBwdWarps, 2) gs_bwd_kernel(const __grid_constant__ GsParams p) {
-    constexpr bool kVec = kMode >= 1, kStaged = kMode == 2;
+    constexpr bool kVec = kMode >= 1, kStaged = kMode >= 1;
     constexpr int kTensors = kGate ? 4 : 3, kWarps = kBwdWarps, kTile = kWarps * kTok;
     using Col = Column<T, kVec>;
     using V = typename Col::V;
@@ -602,6 +619,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) gs_bwd_kernel(const __grid_
     const Col k(p, column);
     sm100::grid_dep_wait();     // the marks may still be formed
     sm100::grid_dep_launch_dependents();
+    if (kCluster) meet(false);  // every CTA of the cluster runs
     int first = 0, last = static_cast<int>(p.L);       // (up to 2^30: rows are counted in 32 bits)
     if (kPacked) packed_span(p, &first, &last);
     const int tiles = (last + kTile - 1) / kTile, steps = (tiles + ranks - 1) / ranks;
@@ -615,7 +633,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) gs_bwd_kernel(const __grid_
     V sum = splat<V>(0.f);
     int tick = 0;               // which of the two exchange buffers is next, across sequences
     const V zero = splat<V>(0.f);
-    Tiles<T, kVec, kStaged, kTensors, kWarps> in(k, column, p.C, s_tiles, -ranks);
+    Tiles<T, kMode, kTensors, kWarps> in(k, column, p.C, s_tiles, -ranks);
 
     for (int64_t b = share; b < p.nb; b += p.shares) {
         in.set(0, p.x, b, column, tiles - 1 - rank);
@@ -882,7 +900,7 @@ bool rows_of(const GsParams& p, int es, int bytes) {
             return false;
     return true;
 }
-// 2: staged through shared memory; 1: words of two bf16 or one fp32; 0: an element at a time
+// 2: copied by 16 bytes; 1: by words of two bf16 or one fp32; 0: loaded an element at a time
 template <typename T>
 int mode_of(const GsParams& p) {
     constexpr int es = sizeof(T);
@@ -923,14 +941,14 @@ cudaError_t staged_smem(int bytes) {
 template <typename T>
 cudaError_t launch_fwd(GsParams p, bool lerp, cudaStream_t s) {
     const int mode = mode_of<T>(p);
-    p.ranks = rank_count(p.nb * p.cols, (p.L + kFwdClusterWarps * kTok - 1) / (kFwdClusterWarps * kTok), mode == 2 ? 2 : 1);
+    p.ranks = rank_count(p.nb * p.cols, (p.L + kFwdClusterWarps * kTok - 1) / (kFwdClusterWarps * kTok), mode >= 1 ? 2 : 1);
     return with_mode<T>(mode, [&](auto m) {
         return with_bools<>([&](auto f) {
             using F = decltype(f);
             constexpr int kMode = decltype(m)::value;
             constexpr auto kernel = gs_fwd_kernel<T, F::template at<0>(), F::template at<1>(), F::template at<2>(), kMode, F::template at<3>()>;
             constexpr int warps = fwd_warps(F::template at<3>());
-            constexpr int smem = kMode == 2 ? 2 * (F::template at<1>() ? 3 : 2) * warps * kTok * kRowBytes : 0;
+            constexpr int smem = kMode >= 1 ? 2 * (F::template at<1>() ? 3 : 2) * warps * kTok * kRowBytes : 0;
             const cudaError_t e = staged_smem<kernel>(smem);
             return e != cudaSuccess ? e : launch(kernel, p.nb * p.cols * p.ranks, 32 * warps, p.ranks, smem, false, s, p);
         }, lerp, p.i.p != nullptr, p.cu != nullptr, p.ranks > 1);
@@ -948,7 +966,7 @@ cudaError_t launch_bwd(GsParams p, bool lerp, bool after, float* ddecay, cudaStr
             using F = decltype(f);
             constexpr int kMode = decltype(m)::value;
             constexpr auto kernel = gs_bwd_kernel<T, F::template at<0>(), F::template at<1>(), F::template at<2>(), kMode, F::template at<3>()>;
-            constexpr int smem = kMode == 2 ? 3 * (F::template at<1>() ? 4 : 3) * kBwdWarps * kTok * kRowBytes : 0;
+            constexpr int smem = kMode >= 1 ? 3 * (F::template at<1>() ? 4 : 3) * kBwdWarps * kTok * kRowBytes : 0;
             const cudaError_t e = staged_smem<kernel>(smem);
             return e != cudaSuccess ? e : launch(kernel, static_cast<int64_t>(p.shares) * p.cols * p.ranks, 32 * kBwdWarps, p.ranks, smem, after, s, p);
         }, lerp, p.i.p != nullptr, p.cu != nullptr, p.ranks > 1);
@@ -1181,8 +1199,7 @@ m3_status m3_gated_scan_bwd(const m3_gated_scan_dims* dims, const m3_gated_scan_
     const Named dd{ddecay, "ddecay"}, ds{dinit, "dinit"}, df{dfinal, "dfinal"};
     if (dims->nseq > 0) {
         for (const Named* o : {&dx, &dr, &di, &dd, &ds}) {
-            if ((st = check_apart(*o, {x, r, i, g})) != M3_OK || (st = check_apart(*o, rest)) != M3_OK) return st;
-            if (o != &ds && (st = check_apart(*o, {df})) != M3_OK) return st;
+            if ((st = check_apart(*o, {x, r, i, g, df})) != M3_OK || (st = check_apart(*o, rest)) != M3_OK) return st;
         }
         if ((st = check_apart(dr, {dx})) != M3_OK || (st = check_apart(di, {dx, dr})) != M3_OK ||
             (st = check_apart(dd, {dx, dr, di})) != M3_OK || (st = check_apart(ds, {dx, dr, di, dd})) != M3_OK)
@@ -1200,7 +1217,7 @@ m3_status m3_gated_scan_bwd(const m3_gated_scan_dims* dims, const m3_gated_scan_
         cudaError_t e = cudaSuccess;
         const size_t n = static_cast<size_t>(dims->nseq) * dims->channels * 4;
         if (ddecay) e = cudaMemsetAsync(ddecay, 0, dims->channels * 4, s);
-        if (e == cudaSuccess && dinit && n && dinit != dfinal)
+        if (e == cudaSuccess && dinit && n)
             e = dfinal ? cudaMemcpyAsync(dinit, dfinal, n, cudaMemcpyDeviceToDevice, s) : cudaMemsetAsync(dinit, 0, n, s);
         return done(e, "empty gradient");
     }

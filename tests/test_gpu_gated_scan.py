@@ -207,10 +207,10 @@ def test_strides_in_place_and_versions(cuda_dev, dtype, off):
     assert torch.equal(y2, y) and torch.equal(st, fin) and torch.equal(mk2, mk)
     assert bool((wide[..., :off] == 7.0).all()) and bool((wide[..., off + 4 * C:] == 7.0).all())
     g = m3.gated_scan_bwd(d["dy"], d["x"], d["r"], d["i"], d["decay"], init=d["init"], dfinal=d["dfinal"], marks=mk)
-    ds = d["dfinal"].clone()
+    ds = torch.full_like(d["dfinal"], 7.0)
     out = torch.full_like(wide, 7.0)
     o = [out[..., off + n * C:off + (n + 1) * C] for n in range(3)]
-    g2 = m3.gated_scan_bwd(d["dy"], v[0], v[1], v[2], d["decay"], init=d["init"], dfinal=ds, marks=mk, grads=o, want_init=ds)
+    g2 = m3.gated_scan_bwd(d["dy"], v[0], v[1], v[2], d["decay"], init=d["init"], dfinal=d["dfinal"], marks=mk, grads=o, want_init=ds)
     torch.cuda.synchronize()
     assert all(torch.equal(g[k], g2[k]) for k in g) and g2["dinit"] is ds
     assert bool((out[..., :off] == 7.0).all()) and bool((out[..., off + 3 * C:] == 7.0).all())
@@ -344,6 +344,10 @@ def test_refusals(cuda_dev):
     for bad in (dict(power=0.0), dict(power=math.nan), dict(y=x)):
         with pytest.raises(m3.M3Error):
             m3.gated_scan_fwd(**{**dict(x=x, r=x, decay=d), **bad})
+    s = z(2, 64)
+    for bad in (dict(want_init=s, dfinal=s), dict(want_init=s, init=s), dict(grads=(x, z(2, 5, 64), None))):
+        with pytest.raises(m3.M3Error):
+            m3.gated_scan_bwd(x, x, x, decay=d, **bad)
     with pytest.raises(ValueError):
         m3.gated_scan_step(x[:, 0], x[:, 0], z(3, 64), decay=d)
     with pytest.raises(TypeError):
