@@ -136,19 +136,17 @@ __device__ __forceinline__ float2 bounded(const float2&, uint32_t w) {
 template <typename V>
 __device__ __forceinline__ V exp_neg(const V& v) { return each(times(v, -kLog2e), hw_ex2); }
 
-constexpr float kSeries = 0.35f;
+constexpr float kSeries = 0.125f;
 
 // r's part: e^-r and n = 1 - a. k: power: power softplus(d), the largest -log a; lerp: d. kSmall: k <= kSeries, the
-// series of 1 - e^-t alone serves (it holds for t <= kSeries: the next term is 0.35^8 / 8! = 6e-9); otherwise e^-t from
+// series of 1 - e^-t alone serves (the next term is kSeries^5 / 6! = 4e-8 of the first); otherwise e^-t from
 // the hardware's 2^x where t is larger. t = -log a is taken 1e-30 higher, so that w is not zero where sig(r) is.
 __device__ __forceinline__ float decay_of(float sr, float k) { return fmaf(k, sr, 1e-30f); }
 __device__ __forceinline__ float2 decay_of(const float2& sr, const float2& k) { return make_float2(decay_of(sr.x, k.x), decay_of(sr.y, k.y)); }
 template <bool kSmall, typename V>
 __device__ __forceinline__ V one_less(const V& t) {
-    return each(t, [](float t) {        // t (1 - t/2 (1 - t/3 (1 - ... t/7)))
-        float s = fmaf(t, 1.f / 5040.f, -1.f / 720.f);
-        s = fmaf(t, s, 1.f / 120.f);
-        s = fmaf(t, s, -1.f / 24.f);
+    return each(t, [](float t) {        // t (1 - t/2 (1 - t/3 (1 - t/4 (1 - t/5))))
+        float s = fmaf(t, 1.f / 120.f, -1.f / 24.f);
         s = fmaf(t, s, 1.f / 6.f);
         s = fmaf(t, s, -0.5f);
         s = fmaf(t, s, 1.f);
@@ -188,6 +186,10 @@ __device__ __forceinline__ void gates(uint32_t rw, uint32_t iw, const V& x, cons
 
 // softplus(d) = log(1 + e^d)
 __device__ __forceinline__ float softplus(float d) { return d > 20.f ? d : log1pf(expf(d)); }
+
+// The warp's index, the same in every lane for the compiler too: what follows from it (rows, addresses) is then worked out
+// once a warp. (Forward 742 -> 724 us for 65536 x 4096; the backward, which has more of it, loses 5 %.)
+__device__ __forceinline__ int warp_index() { return __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0); }
 
 // ---- a thread's column
 
@@ -328,8 +330,8 @@ struct Tiles {
     const Col& k;
     int chunk_bytes, warp, lane;
     // step: tiles from one to the next
-    __device__ __forceinline__ Tiles(const Col& col, int column, int C, uint8_t* smem, int tiles) : step(static_cast<int64_t>(tiles) * kTile), room(smem), k(col) {
-        warp = threadIdx.x >> 5;
+    __device__ __forceinline__ Tiles(const Col& col, int column, int C, uint8_t* smem, int tiles, int warp_) : step(static_cast<int64_t>(tiles) * kTile), room(smem), k(col) {
+        warp = warp_;
         lane = threadIdx.x & 31;
         const int c = column * 32 * Word<T>::E + static_cast<int>(threadIdx.x & 7) * (16 / static_cast<int>(sizeof(T)));
         chunk_bytes = c < C ? 16 : 0;
@@ -453,7 +455,7 @@ __global__ void __launch_bounds__(32 * fwd_warps(kCluster), kMode >= 1 ? 2 : 1) 
     __shared__ int s_reset[2][kMaxRanks];
     __shared__ Rows<kTile> s_rows[kPacked ? 3 : 1];
     extern __shared__ __align__(16) uint8_t s_tiles[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_index(), lane = threadIdx.x & 31;
     const int ranks = kCluster ? p.ranks : 1;
     const int rank = kCluster ? static_cast<int>(blockIdx.x % ranks) : 0;
     const int64_t unit = kCluster ? blockIdx.x / ranks : blockIdx.x;
@@ -464,7 +466,7 @@ __global__ void __launch_bounds__(32 * fwd_warps(kCluster), kMode >= 1 ? 2 : 1) 
     if (kPacked) packed_span(p, &first, &last);
     const int tiles = (last + kTile - 1) / kTile, steps = (tiles + ranks - 1) / ranks;
 
-    Tiles<T, kMode, kTensors, kWarps> in(k, column, p.C, s_tiles, ranks);
+    Tiles<T, kMode, kTensors, kWarps> in(k, column, p.C, s_tiles, ranks, warp);
     in.set(0, p.x, b, column, rank);
     in.set(1, p.r, b, column, rank);
     if constexpr (kGate) in.set(2, p.i, b, column, rank);
@@ -488,7 +490,7 @@ __global__ void __launch_bounds__(32 * fwd_warps(kCluster), kMode >= 1 ? 2 : 1) 
     if (kStaged || kPacked) __syncthreads();
     if (kCluster) meet(false);      // every CTA of the cluster runs
 
-    T* py = p.y.p ? static_cast<T*>(p.y.p) + b * p.y.batch + k.c : nullptr;
+    T* py = p.y.p ? static_cast<T*>(p.y.p) + b * p.y.batch : nullptr;
     int rb = 0;
     for (int step = 0; step < steps; ++step) {
         const int tile = step * ranks + rank, t0 = tile * kTile + warp * kTok, buf = step & 1;
@@ -552,8 +554,9 @@ __global__ void __launch_bounds__(32 * fwd_warps(kCluster), kMode >= 1 ? 2 : 1) 
                 carry = kPacked && s_reset[buf][r] ? q.b : n;
             }
         }
-#pragma unroll 4
-        for (int w = 0; w < warp; ++w) {
+#pragma unroll
+        for (int w = 0; w < kWarps - 1; ++w) {
+            if (w >= warp) break;
             const Pair<V> q = s_warp[buf][w][lane];
             const V n = fma2(q.a, before, q.b);
             before = kPacked && mine(rows.start, w) ? q.b : n;
@@ -570,11 +573,11 @@ __global__ void __launch_bounds__(32 * fwd_warps(kCluster), kMode >= 1 ? 2 : 1) 
             T* to = py + static_cast<int64_t>(t0) * p.y.token;
             if (live.all()) {
 #pragma unroll
-                for (int j = 0; j < kTok; ++j) k.store(to + j * p.y.token, h[j]);
+                for (int j = 0; j < kTok; ++j) k.store(to + j * p.y.token + k.c, h[j]);
             } else {
 #pragma unroll
                 for (int j = 0; j < kTok; ++j)
-                    if (live(j)) k.store(to + j * p.y.token, h[j]);
+                    if (live(j)) k.store(to + j * p.y.token + k.c, h[j]);
             }
         }
         if (p.final_state) {
@@ -633,7 +636,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) gs_bwd_kernel(const __grid_
     V sum = splat<V>(0.f);
     int tick = 0;               // which of the two exchange buffers is next, across sequences
     const V zero = splat<V>(0.f);
-    Tiles<T, kMode, kTensors, kWarps> in(k, column, p.C, s_tiles, -ranks);
+    Tiles<T, kMode, kTensors, kWarps> in(k, column, p.C, s_tiles, -ranks, warp);
 
     for (int64_t b = share; b < p.nb; b += p.shares) {
         in.set(0, p.x, b, column, tiles - 1 - rank);
@@ -736,11 +739,20 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) gs_bwd_kernel(const __grid_
                     carry = s_reset[buf][r] ? q.b : m;
                 }
             }
-#pragma unroll 4
-            for (int w = kWarps - 1; w > warp; --w) {
-                const Pair<V> q = s_warp[buf][w][lane];
-                const V m = fma2(q.a, G, q.b);
-                G = ends(w) ? q.b : m;
+            if (!kPacked && tail < 0) {
+#pragma unroll
+                for (int w = kWarps - 1; w > 0; --w) {
+                    if (w <= warp) break;
+                    const Pair<V> q = s_warp[buf][w][lane];
+                    G = fma2(q.a, G, q.b);
+                }
+            } else {
+#pragma unroll 1
+                for (int w = kWarps - 1; w > warp; --w) {
+                    const Pair<V> q = s_warp[buf][w][lane];
+                    const V m = fma2(q.a, G, q.b);
+                    G = ends(w) ? q.b : m;
+                }
             }
             // g of each token from the last one back
             V g[kTok];
