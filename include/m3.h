@@ -455,7 +455,8 @@ M3_API m3_status m3_group_norm_bwd(const m3_group_norm_dims* dims, const m3_view
  *     h_t = a_t h_{t-1} + w_t sigmoid(i_t) x_t,    y_t = h_t                 (h_{-1} = init)
  * The gates arrive as they leave their projections. The state is one value a channel: where linear
  * attention keeps a K x V state for each head, this keeps the width of the layer. State and arithmetic are
- * fp32, y is rounded once. Packed sequences lie as linear attention's do; offsets must not descend.
+ * fp32, y is rounded once. Packed sequences lie as linear attention's do; offsets must lie in [0, seqlen] and
+ * not descend (others leave states and outputs undefined, within their tensors).
  * Views: batch and token strides (head is not used), channels contiguous. A sigmoid ends at 2^-62 (arguments
  * below -43), not at zero. */
 #define M3_GS_LERP 1u

@@ -3,7 +3,7 @@
 
 Usage: ``python -m state_space_sequence_mamba_b200.build [--force] [-v] [--lib-only]``.
 No GPU is needed: nvcc cross-compiles. ``_m3torch`` needs the headers of Python and torch, and serves the
-Python entry points of linear attention and the grouped norm; ``libm3.so`` alone (``--lib-only``, or
+Python entry points of all but the scan; ``libm3.so`` alone (``--lib-only``, or
 what is there when the other fails) serves the C ABI and the scan's Python entry points.
 """
 from __future__ import annotations

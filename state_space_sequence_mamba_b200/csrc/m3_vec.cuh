@@ -42,10 +42,6 @@ __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 __device__ __forceinline__ float2 mul2(const float2& a, const float2& b) { return __fmul2_rn(a, b); }
 __device__ __forceinline__ float2 add2(const float2& a, const float2& b) { return __fadd2_rn(a, b); }
 __device__ __forceinline__ float2 fma2(const float2& a, const float2& b, const float2& c) { return __ffma2_rn(a, b, c); }
-// one element, for code that takes either (never contracted, so that every form of a kernel rounds alike)
-__device__ __forceinline__ float mul2(float a, float b) { return __fmul_rn(a, b); }
-__device__ __forceinline__ float add2(float a, float b) { return __fadd_rn(a, b); }
-__device__ __forceinline__ float fma2(float a, float b, float c) { return fmaf(a, b, c); }
 
 // 1 / (1 + e^-v) of two elements, with the hardware's 2^x and 1 / x (1 + 2^x lies in [1, inf], so that
 // denormals need no care).
