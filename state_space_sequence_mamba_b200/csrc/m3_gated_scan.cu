@@ -5,8 +5,8 @@
 //     h_t = a_t h_{t-1} + w_t u_t,  u_t = sig(i_t) x_t
 // The floor is HBM's: the forward reads x, r, i and writes y once, the backward reads those and dy and writes
 // three gradients. bf16, 4 x 2048 x 4096: forward 72 us (0.57 of what a copy reaches), gradients 135 (0.53); one sequence of
-// 65 536 x 4096: forward 687 us (0.48). What bounds them is the issue of instructions: some 48 a channel and token
-// forward, 92 backward (two exponentials, a reciprocal and a root among them, which keep that unit half busy), at three of
+// 65 536 x 4096: forward 687 us (0.48). What bounds them is the issue of instructions: some 46 a channel and token
+// forward, 90 backward (two exponentials, a reciprocal and a root among them, which keep that unit half busy), at three of
 // four a cycle; and 256 columns over 148 SMs leave an eighth of the device idle. Two tokens compose as (A, B) after (A', B') = (A A', A B' + B), so time is cut: a CTA takes a
 // tile of 8 tokens a warp by 32 words (a word: two bf16 channels or one of fp32), a thread eight tokens of one word.
 // It reduces them to one (A, B) in registers, the warps' pairs are combined in order through shared memory, and
@@ -118,6 +118,11 @@ __device__ __forceinline__ V less_from(const V& v, float c) { return each(v, [=]
 __device__ __forceinline__ float less2(float a, float b, float c) { return fmaf(-a, b, c); }
 __device__ __forceinline__ float2 less2(const float2& a, const float2& b, const float2& c) {
     return make_float2(fmaf(-a.x, b.x, c.x), fmaf(-a.y, b.y, c.y));
+}
+// a b - c
+__device__ __forceinline__ float minus_fma(float a, float b, float c) { return fmaf(a, b, -c); }
+__device__ __forceinline__ float2 minus_fma(const float2& a, const float2& b, const float2& c) {
+    return make_float2(fmaf(a.x, b.x, -c.x), fmaf(a.y, b.y, -c.y));
 }
 __device__ __forceinline__ float minus(float a, float b) { return __fadd_rn(a, -b); }
 __device__ __forceinline__ float2 minus(const float2& a, const float2& b) { return make_float2(__fadd_rn(a.x, -b.x), __fadd_rn(a.y, -b.y)); }
@@ -702,13 +707,14 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) gs_bwd_kernel(const __grid_
                 }
             });
             const auto a = [&](int j) { return kLerp ? n[j] : less_from(n[j], 1.f); };
+            const auto decayed = [&](int j, const V& v) { return kLerp ? mul2(n[j], v) : less2(n[j], v, v); };
             V pa = a(0), pg = zero;
 #pragma unroll
-            for (int j = 1; j < kTok; ++j) pa = mul2(pa, a(j));
+            for (int j = 1; j < kTok; ++j) pa = decayed(j, pa);
 #pragma unroll
             for (int j = kTok - 1; j >= 0; --j) {
                 if (!plain && (en >> j & 1)) pg = gin(j);
-                pg = mul2(a(j), add2(Word<T>::unpack(in.word(slot, 2, j)), pg));
+                pg = decayed(j, add2(Word<T>::unpack(in.word(slot, 2, j)), pg));
             }
             s_warp[buf][warp][lane] = Pair<V>{pa, pg};
             if (kPacked) find_rows(p, s_rows[rb], tile - ranks, last);
@@ -766,7 +772,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) gs_bwd_kernel(const __grid_
             for (int j = kTok - 1; j >= 0; --j) {
                 if (!plain && (en >> j & 1)) G = gin(j);
                 g[j] = add2(Word<T>::unpack(in.word(slot, 2, j)), G);
-                G = mul2(a(j), g[j]);
+                G = decayed(j, g[j]);
                 if (!plain && (st >> j & 1) && tile >= 0 && p.dinit) k.put(p.dinit + seq(j) * p.C, G);
             }
             if (!kCluster && warp == 0) s_carry[buf ^ 1][lane] = G;
@@ -796,11 +802,10 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) gs_bwd_kernel(const __grid_
                         w = cr;
                         dl = dr = mul2(mul2(g[j], minus(hp, u)), mul2(aj, w));
                     } else {
-                        // with t = -log a: -l dL/dl = g a (t h - u a t / w)
+                        // with t = -log a: l dL/dl = g a t (u a / w - h)
                         const V q = fma2(n[j], aj, n[j]), rs = each(q, hw_rsqrt), t = decay_of(sr, kd);
                         w = mul2(q, rs);
-                        const V ua = mul2(mul2(u, aj), mul2(t, rs));
-                        dl = mul2(g[j], mul2(aj, less2(t, hp, ua)));
+                        dl = mul2(mul2(mul2(g[j], aj), t), minus_fma(mul2(u, aj), rs, hp));
                         dr = mul2(dl, cr);
                     }
                     hp = fma2(aj, hp, mul2(w, u));
