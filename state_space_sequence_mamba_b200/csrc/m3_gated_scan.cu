@@ -134,9 +134,11 @@ __device__ __forceinline__ float hw_rsqrt(float v) { asm("rsqrt.approx.ftz.f32 %
 __device__ __forceinline__ float at_least(float v, float b) { asm("max.NaN.f32 %0, %0, %1;" : "+f"(v) : "f"(b)); return v; }
 
 constexpr float kLog2e = 1.4426950408889634f;
-// A gate is taken to be at least -43 (NaN stays): then (1 + e^-r)(1 + e^-i) is finite, and a sigmoid ends at 2^-62
+// A sigmoid's argument is taken to be at least -43 (NaN stays): then (1 + e^-r)(1 + e^-i) is finite, and a sigmoid ends at 2^-62
 // instead of at zero. For a pair of bf16 that is one instruction.
 constexpr float kLeast = -43.f;
+__device__ __forceinline__ float unpacked(float, uint32_t w) { return Word<float>::unpack(w); }
+__device__ __forceinline__ float2 unpacked(const float2&, uint32_t w) { return Word<__nv_bfloat16>::unpack(w); }
 __device__ __forceinline__ float bounded(float, uint32_t w) { return at_least(__uint_as_float(w), kLeast); }
 __device__ __forceinline__ float2 bounded(const float2&, uint32_t w) {
     uint32_t v;
@@ -168,7 +170,8 @@ __device__ __forceinline__ V one_less(const V& t) {
 template <bool kLerp, typename V>
 __device__ __forceinline__ V exp_r(uint32_t rw, const V& k) {
     if (!kLerp) return exp_neg(bounded(k, rw));
-    return exp_neg(each(add2(bounded(k, rw), k), [](float v) { return at_least(v, kLeast); }));
+    // (only the sum is bounded: r alone may lie far below where the bias lifts it)
+    return exp_neg(each(add2(unpacked(k, rw), k), [](float v) { return at_least(v, kLeast); }));
 }
 // The decay and the weighted input of one token.
 template <bool kLerp, bool kGate, bool kSmall, typename V>

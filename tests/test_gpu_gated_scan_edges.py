@@ -1,0 +1,67 @@
+"""The gated recurrence where its arithmetic ends, element by element against the float64 definition: gates far from
+their bias. Tolerances, fixed before the first run, count units of 2^-24 and stand beside each test.
+"""
+import math
+
+import pytest
+import torch
+
+from state_space_sequence_mamba_b200 import binding as m3
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+UNIT = 2.0 ** -24
+
+
+def close(got, ref, rel, floor, what):
+    """Every element within rel of itself (a tensor or a number), plus the floor."""
+    got = got.detach().double().cpu()
+    assert got.shape == ref.shape and bool(torch.isfinite(got).all()), what
+    off = (got - ref).abs() - rel * ref.abs() - floor
+    at = int(off.argmax())
+    assert float(off.max()) <= 0, (what, at, float(got.reshape(-1)[at]), float(ref.reshape(-1)[at]))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("gate", [False, True])
+def test_convex_gates_far_from_their_bias(cuda_dev, dtype, gate):
+    """sigmoid(r + d) where r alone lies below -43 and the sum does not: prompt, step and gradients of one token, of which
+    each result is a product of sigmoids. v = r + d is rounded, v log2 e again, the constant by a fifth: 2.2 |v| units of
+    e^-v, and four of the hardware's 2^x; 1 / x has two, the other sigmoid six, sums and products one each:
+    2.5 |v| + 24 for one product. A sigmoid of arguments below -43 ends at 2^-62."""
+    r = torch.tensor([-math.inf, -1e4, -200.0, -60.0, -50.0, -48.0, -43.5, -10.0, 0.0, 200.0]).to(dtype)
+    d = torch.tensor([-100.0, -44.0, -1.0, 0.0, 1.0, 35.0, 40.0, 44.0, 50.0, 60.0, 100.0, 199.5])
+    B, C = len(r), len(d)
+    rr = r[:, None, None].expand(B, 1, C).contiguous()
+    v = rr.double() + d.double()
+    a, w = torch.sigmoid(v), torch.sigmoid(-v)
+    ii = torch.full((B, 1, C), 0.5).to(dtype) if gate else None
+    si = 1.0 if ii is None else torch.sigmoid(ii.double())
+    rel = (2.5 * v.abs().clamp(max=43) + 24) * UNIT
+    half = 2.0 ** -8 if dtype == BF else 0.0
+    up = lambda t: None if t is None else t.to(cuda_dev)  # noqa: E731
+    zero, one = torch.zeros(B, 1, C, dtype=dtype), torch.ones(B, 1, C, dtype=dtype)
+    ones = torch.ones(B, C, device=cuda_dev)
+    args = up(rr), up(ii), up(d)
+    floor = 2.0 ** -61
+    for x, init, want in ((zero, ones, a), (one, None, w * si)):
+        y, fin, mk = m3.gated_scan_fwd(up(x), *args, lerp=True, init=init, marks=True)
+        st = ones.clone() if init is not None else torch.zeros_like(ones)
+        ys, out = m3.gated_scan_step(up(x)[:, 0], args[0][:, 0], st, None if ii is None else args[1][:, 0], args[2], lerp=True)
+        torch.cuda.synchronize()
+        close(fin, want[:, 0], rel[:, 0], floor, "final")
+        close(out, want[:, 0], rel[:, 0], floor, "state")
+        close(y, want, rel + half, floor, "y")
+        close(ys, want[:, 0], rel[:, 0] + half, floor, "step")
+        u = 0.0 if init is not None else si
+        dr = a * w if init is not None else -si * a * w     # dy = 1: (h - u) a w
+        for marks in (mk, None):
+            g = m3.gated_scan_bwd(up(one), up(x), *args, lerp=True, init=init, marks=marks)
+            torch.cuda.synchronize()
+            close(g["dinit"], a[:, 0], rel[:, 0], floor, "dinit")
+            close(g["dx"], w * si, rel + half, floor, "dx")
+            close(g["dr"], dr, 2 * rel + half, floor, "dr")
+            close(g["ddecay"], dr.sum((0, 1)), 2 * float(rel.max()), B * floor, "ddecay")
+            if gate:
+                close(g["di"], w * u * (1 - si), rel + half, floor, "di")
