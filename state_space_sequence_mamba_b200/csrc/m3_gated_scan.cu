@@ -133,6 +133,10 @@ __device__ __forceinline__ float hw_rcp(float v) { asm("rcp.approx.ftz.f32 %0, %
 __device__ __forceinline__ float hw_rsqrt(float v) { asm("rsqrt.approx.ftz.f32 %0, %0;" : "+f"(v)); return v; }
 __device__ __forceinline__ float at_least(float v, float b) { asm("max.NaN.f32 %0, %0, %1;" : "+f"(v) : "f"(b)); return v; }
 
+// The same value, which the compiler takes for another: what follows from it is worked out again, not kept.
+__device__ __forceinline__ float apart(float v) { asm("" : "+f"(v)); return v; }
+__device__ __forceinline__ float2 apart(const float2& v) { return make_float2(apart(v.x), apart(v.y)); }
+
 constexpr float kLog2e = 1.4426950408889634f;
 // A sigmoid's argument is taken to be at least -43 (NaN stays): then (1 + e^-r)(1 + e^-i) is finite, and a sigmoid ends at 2^-62
 // instead of at zero. For a pair of bf16 that is one instruction.
@@ -150,23 +154,32 @@ __device__ __forceinline__ V exp_neg(const V& v) { return each(times(v, -kLog2e)
 
 constexpr float kSeries = 0.125f;
 
-// r's part: e^-r and n = 1 - a. k: power: power softplus(d), the largest -log a; lerp: d. kSmall: k <= kSeries, the
+// r's part: e^-r, a and n = 1 - a. k: power: power softplus(d), the largest -log a; lerp: d. kSmall: k <= kSeries, the
 // series of 1 - e^-t alone serves (the next term is kSeries^5 / 6! = 4e-8 of the first); otherwise e^-t from
-// the hardware's 2^x where t is larger. t = -log a is taken 1e-30 higher, so that w is not zero where sig(r) is.
+// the hardware's 2^x where t is larger: there that is a, and n what is left of one (as one less n, an a of e^-16 would keep
+// no digits). t = -log a is taken 1e-30 higher, so that w is not zero where sig(r) is.
 __device__ __forceinline__ float decay_of(float sr, float k) { return fmaf(k, sr, 1e-30f); }
 __device__ __forceinline__ float2 decay_of(const float2& sr, const float2& k) { return make_float2(decay_of(sr.x, k.x), decay_of(sr.y, k.y)); }
-template <bool kSmall, typename V>
-__device__ __forceinline__ V one_less(const V& t) {
-    return each(t, [](float t) {        // t (1 - t/2 (1 - t/3 (1 - t/4 (1 - t/5))))
-        float s = fmaf(t, 1.f / 120.f, -1.f / 24.f);
-        s = fmaf(t, s, 1.f / 6.f);
-        s = fmaf(t, s, -0.5f);
-        s = fmaf(t, s, 1.f);
-        const float n = __fmul_rn(t, s);
-        if (kSmall) return n;
-        return t > kSeries ? __fadd_rn(1.f, -hw_ex2(__fmul_rn(t, -kLog2e))) : n;
-    });
+__device__ __forceinline__ float series(float t) {      // t (1 - t/2 (1 - t/3 (1 - t/4 (1 - t/5))))
+    float s = fmaf(t, 1.f / 120.f, -1.f / 24.f);
+    s = fmaf(t, s, 1.f / 6.f);
+    s = fmaf(t, s, -0.5f);
+    s = fmaf(t, s, 1.f);
+    return __fmul_rn(t, s);
 }
+// a of t, given n where the series has it (kSmall: everywhere)
+template <bool kSmall>
+__device__ __forceinline__ float a_of(float t, float n) {
+    const float a = __fadd_rn(1.f, -n);
+    return !kSmall && t > kSeries ? hw_ex2(__fmul_rn(t, -kLog2e)) : a;
+}
+template <bool kSmall>
+__device__ __forceinline__ float2 a_of(const float2& t, const float2& n) { return make_float2(a_of<kSmall>(t.x, n.x), a_of<kSmall>(t.y, n.y)); }
+// n of t, given a where that is 2^x
+template <bool kSmall>
+__device__ __forceinline__ float n_of(float t, float a) { return !kSmall && t > kSeries ? __fadd_rn(1.f, -a) : series(t); }
+template <bool kSmall>
+__device__ __forceinline__ float2 n_of(const float2& t, const float2& a) { return make_float2(n_of<kSmall>(t.x, a.x), n_of<kSmall>(t.y, a.y)); }
 template <bool kLerp, typename V>
 __device__ __forceinline__ V exp_r(uint32_t rw, const V& k) {
     if (!kLerp) return exp_neg(bounded(k, rw));
@@ -191,8 +204,9 @@ __device__ __forceinline__ void gates(uint32_t rw, uint32_t iw, const V& x, cons
         return;
     }
     // 1 - a^2 = n (1 + a): no digits are lost for a near 1
-    const V n = one_less<kSmall>(decay_of(sr, k));
-    *a = less_from(n, 1.f);
+    const V t = decay_of(sr, k);
+    *a = a_of<kSmall>(t, each(t, series));
+    const V n = n_of<kSmall>(t, *a);
     const V q = fma2(n, *a, n);
     *add = mul2(mul2(q, each(q, hw_rsqrt)), u);
 }
@@ -241,6 +255,11 @@ struct Column {
         if (!q) return splat<V>(0.f);
         if constexpr (W::E == 1) return ok ? q[c] : 0.f;
         else return make_float2(ok ? q[c] : 0.f, two ? q[c + 1] : 0.f);
+    }
+    // whether the channels that exist are all below (NaN is not)
+    __device__ __forceinline__ bool below(const V& v, float most) const {
+        if constexpr (W::E == 1) return !ok || v <= most;
+        else return (!ok || v.x <= most) && (!two || v.y <= most);
     }
     // fp32 values of this column (states, marks, sums); q points at the row
     __device__ __forceinline__ V get(const float* q) const {
@@ -492,9 +511,7 @@ __global__ void __launch_bounds__(32 * fwd_warps(kCluster), kMode >= 1 ? 2 : 1) 
 
     const V d = k.param(p.decay);
     const V kd = kLerp ? d : each(d, [&](float v) { return p.power * softplus(v); });
-    bool small = true;
-    each(kd, [&](float v) { small = small && v <= kSeries; return v; });
-    small = kLerp || __all_sync(0xffffffffu, small);
+    const bool small = kLerp || __all_sync(0xffffffffu, k.below(kd, kSeries));
     if (kPacked && p.final_state) empty_sequences<kWarps>(p, k, rank, p.init, p.final_state);
     V carry = splat<V>(0.f);
     if (!kPacked && p.init) carry = k.get(p.init + b * p.C);
@@ -643,9 +660,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) gs_bwd_kernel(const __grid_
 
     const V d = k.param(p.decay);
     const V kd = kLerp ? d : each(d, [&](float v) { return p.power * softplus(v); });
-    bool small = true;
-    each(kd, [&](float v) { small = small && v <= kSeries; return v; });
-    small = kLerp || __all_sync(0xffffffffu, small);
+    const bool small = kLerp || __all_sync(0xffffffffu, k.below(kd, kSeries));
     if (kPacked && p.dinit) empty_sequences<kWarps>(p, k, rank, p.dfinal, p.dinit);
     V sum = splat<V>(0.f);
     int tick = 0;               // which of the two exchange buffers is next, across sequences
@@ -676,156 +691,163 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) gs_bwd_kernel(const __grid_
         in.template wait<1>();
         __syncthreads();
         V carry = zero;         // G behind the tiles done so far (set where a sequence ends)
-        for (int step = 0; step < steps; ++step) {
-            const int tile = tiles - 1 - step * ranks - rank, t0 = tile * kTile + warp * kTok;
-            const int buf = tick;
-            tick ^= 1;
-            Rows<kTile>& rows = s_rows[kPacked ? rb : 0];
-            // rows that begin and end a sequence: bits of the thread's tokens
-            uint32_t st, en;
-            const int tail = tile >= 0 && last - 1 - tile * kTile < kTile ? last - 1 - tile * kTile : -1;
-            const auto ends = [&](int w) {
-                if (kPacked) return mine(rows.end, w);
-                return tail >= 0 && tail >> 3 == w ? 1u << (tail & 7) : 0u;
-            };
-            if (kPacked) {
-                st = mine(rows.start, warp);
-                rb = rb == 2 ? 0 : rb + 1;
-            } else {
-                st = t0 == 0 ? 1u : 0u;
-            }
-            en = ends(warp);
-            const Live live{clamp_to<kTok>(first - t0), tile >= 0 ? clamp_to<kTok>(last - t0) : 0};
-            const bool plain = st == 0 && en == 0 && live.all();
-            const auto seq = [&](int j) { return kPacked ? static_cast<int64_t>(rows.seq[warp * kTok + j]) : b; };
-            const auto gin = [&](int j) { return p.dfinal ? k.get(p.dfinal + seq(j) * p.C) : zero; };
-            // e^-r and 1 - a (lerp: a), then the decays' product and G from zero
-            V er[kTok], n[kTok];
-            branch(small, [&](auto is_small) {
+        // Every warp of the cluster has the same channels and takes the same way. Small decays are kept as n, which saves an
+        // instruction each; others as a (4 x 2048 x 4096 bf16, all of one sort: 135 and 142 us).
+        branch(small, [&](auto is_small) {
+            constexpr bool kSmall = decltype(is_small)::value, kHaveA = kLerp || !kSmall;
+            for (int step = 0; step < steps; ++step) {
+                const int tile = tiles - 1 - step * ranks - rank, t0 = tile * kTile + warp * kTok;
+                const int buf = tick;
+                tick ^= 1;
+                Rows<kTile>& rows = s_rows[kPacked ? rb : 0];
+                // rows that begin and end a sequence: bits of the thread's tokens
+                uint32_t st, en;
+                const int tail = tile >= 0 && last - 1 - tile * kTile < kTile ? last - 1 - tile * kTile : -1;
+                const auto ends = [&](int w) {
+                    if (kPacked) return mine(rows.end, w);
+                    return tail >= 0 && tail >> 3 == w ? 1u << (tail & 7) : 0u;
+                };
+                if (kPacked) {
+                    st = mine(rows.start, warp);
+                    rb = rb == 2 ? 0 : rb + 1;
+                } else {
+                    st = t0 == 0 ? 1u : 0u;
+                }
+                en = ends(warp);
+                const Live live{clamp_to<kTok>(first - t0), tile >= 0 ? clamp_to<kTok>(last - t0) : 0};
+                const bool plain = st == 0 && en == 0 && live.all();
+                const auto seq = [&](int j) { return kPacked ? static_cast<int64_t>(rows.seq[warp * kTok + j]) : b; };
+                const auto gin = [&](int j) { return p.dfinal ? k.get(p.dfinal + seq(j) * p.C) : zero; };
+                // e^-r and the decays (kSmall: n, else a), then their product and G from zero
+                V er[kTok], c[kTok];
 #pragma unroll
                 for (int j = 0; j < kTok; ++j) {
                     er[j] = exp_r<kLerp>(in.word(slot, 1, j), kd);
-                    n[j] = each(plus(er[j], 1.f), hw_rcp);
-                    if (!kLerp) n[j] = one_less<decltype(is_small)::value>(decay_of(n[j], kd));
+                    c[j] = each(plus(er[j], 1.f), hw_rcp);
+                    if (!kLerp) {
+                        const V t = decay_of(c[j], kd), n = each(t, series);
+                        c[j] = kSmall ? n : a_of<kSmall>(t, n);
+                    }
                 }
-            });
-            const auto a = [&](int j) { return kLerp ? n[j] : less_from(n[j], 1.f); };
-            const auto decayed = [&](int j, const V& v) { return kLerp ? mul2(n[j], v) : less2(n[j], v, v); };
-            V pa = a(0), pg = zero;
+                const auto a = [&](int j) { return kHaveA ? c[j] : less_from(c[j], 1.f); };
+                const auto decayed = [&](int j, const V& v) { return kHaveA ? mul2(c[j], v) : less2(c[j], v, v); };
+                V pa = a(0), pg = zero;
 #pragma unroll
-            for (int j = 1; j < kTok; ++j) pa = decayed(j, pa);
+                for (int j = 1; j < kTok; ++j) pa = decayed(j, pa);
 #pragma unroll
-            for (int j = kTok - 1; j >= 0; --j) {
-                if (!plain && (en >> j & 1)) pg = gin(j);
-                pg = decayed(j, add2(Word<T>::unpack(in.word(slot, 2, j)), pg));
-            }
-            s_warp[buf][warp][lane] = Pair<V>{pa, pg};
-            if (kPacked) find_rows(p, s_rows[rb], tile - ranks, last);
-            in.template wait<0>();      // the next tile
-            __syncthreads();
-            // (into the slot of the tile before, which every thread has done with)
-            const int next = slot == 2 ? 0 : slot + 1;
-            if (kStaged) fetch(tile - 2 * ranks, next == 2 ? 0 : next + 1);
-            V hp = mark;
-            get_mark(tile - ranks);
-            V G;                // G behind the tile, then behind this thread's tokens
-            if (!kCluster) {
-                G = s_carry[buf][lane];
-            } else {
-                if (warp < ranks) {
-                    V ca = splat<V>(1.f), cb = zero;
-                    bool cut = false;
+                for (int j = kTok - 1; j >= 0; --j) {
+                    if (!plain && (en >> j & 1)) pg = gin(j);
+                    pg = decayed(j, add2(Word<T>::unpack(in.word(slot, 2, j)), pg));
+                }
+                s_warp[buf][warp][lane] = Pair<V>{pa, pg};
+                if (kPacked) find_rows(p, s_rows[rb], tile - ranks, last);
+                in.template wait<0>();      // the next tile
+                __syncthreads();
+                // (into the slot of the tile before, which every thread has done with)
+                const int next = slot == 2 ? 0 : slot + 1;
+                if (kStaged) fetch(tile - 2 * ranks, next == 2 ? 0 : next + 1);
+                V hp = mark;
+                get_mark(tile - ranks);
+                V G;                // G behind the tile, then behind this thread's tokens
+                if (!kCluster) {
+                    G = s_carry[buf][lane];
+                } else {
+                    if (warp < ranks) {
+                        V ca = splat<V>(1.f), cb = zero;
+                        bool cut = false;
 #pragma unroll
-                    for (int w = kWarps - 1; w >= 0; --w) {
+                        for (int w = kWarps - 1; w >= 0; --w) {
+                            const Pair<V> q = s_warp[buf][w][lane];
+                            const V m = fma2(q.a, cb, q.b);
+                            const bool at_end = ends(w) != 0;
+                            cb = at_end ? q.b : m;
+                            ca = mul2(ca, q.a);
+                            cut = cut || at_end;
+                        }
+                        send(&s_rank[buf][rank][lane], Pair<V>{ca, cb}, &s_reset[buf][rank], cut, warp);
+                    }
+                    meet(warp < ranks);
+                    for (int r = 0; r < ranks; ++r) {
+                        if (r == rank) G = carry;
+                        const Pair<V> q = s_rank[buf][r][lane];
+                        const V m = fma2(q.a, carry, q.b);
+                        carry = s_reset[buf][r] ? q.b : m;
+                    }
+                }
+                if (!kPacked && tail < 0) {
+#pragma unroll
+                    for (int w = kWarps - 1; w > 0; --w) {
+                        if (w <= warp) break;
                         const Pair<V> q = s_warp[buf][w][lane];
-                        const V m = fma2(q.a, cb, q.b);
-                        const bool c = ends(w) != 0;
-                        cb = c ? q.b : m;
-                        ca = mul2(ca, q.a);
-                        cut = cut || c;
+                        G = fma2(q.a, G, q.b);
                     }
-                    send(&s_rank[buf][rank][lane], Pair<V>{ca, cb}, &s_reset[buf][rank], cut, warp);
-                }
-                meet(warp < ranks);
-                for (int r = 0; r < ranks; ++r) {
-                    if (r == rank) G = carry;
-                    const Pair<V> q = s_rank[buf][r][lane];
-                    const V m = fma2(q.a, carry, q.b);
-                    carry = s_reset[buf][r] ? q.b : m;
-                }
-            }
-            if (!kPacked && tail < 0) {
-#pragma unroll
-                for (int w = kWarps - 1; w > 0; --w) {
-                    if (w <= warp) break;
-                    const Pair<V> q = s_warp[buf][w][lane];
-                    G = fma2(q.a, G, q.b);
-                }
-            } else {
+                } else {
 #pragma unroll 1
-                for (int w = kWarps - 1; w > warp; --w) {
-                    const Pair<V> q = s_warp[buf][w][lane];
-                    const V m = fma2(q.a, G, q.b);
-                    G = ends(w) ? q.b : m;
+                    for (int w = kWarps - 1; w > warp; --w) {
+                        const Pair<V> q = s_warp[buf][w][lane];
+                        const V m = fma2(q.a, G, q.b);
+                        G = ends(w) ? q.b : m;
+                    }
                 }
-            }
-            // g of each token from the last one back
-            V g[kTok];
+                // g of each token from the last one back
+                V g[kTok];
 #pragma unroll
-            for (int j = kTok - 1; j >= 0; --j) {
-                if (!plain && (en >> j & 1)) G = gin(j);
-                g[j] = add2(Word<T>::unpack(in.word(slot, 2, j)), G);
-                G = decayed(j, g[j]);
-                if (!plain && (st >> j & 1) && tile >= 0 && p.dinit) k.put(p.dinit + seq(j) * p.C, G);
-            }
-            if (!kCluster && warp == 0) s_carry[buf ^ 1][lane] = G;
-            // h and the gradients from the first token on
-            const int64_t row0 = t0;
-            T *tx = qx + row0 * p.dx.token, *tr = qr + row0 * p.dr.token, *ti = kGate ? qi + row0 * p.di.token : nullptr;
-            branch(plain, [&](auto is_plain) {
-                constexpr bool kPlain = decltype(is_plain)::value;
+                for (int j = kTok - 1; j >= 0; --j) {
+                    if (!plain && (en >> j & 1)) G = gin(j);
+                    g[j] = add2(Word<T>::unpack(in.word(slot, 2, j)), G);
+                    G = decayed(j, g[j]);
+                    if (!plain && (st >> j & 1) && tile >= 0 && p.dinit) k.put(p.dinit + seq(j) * p.C, G);
+                }
+                if (!kCluster && warp == 0) s_carry[buf ^ 1][lane] = G;
+                // h and the gradients from the first token on (words in registers leave no room for both ways of large decays)
+                const int64_t row0 = t0;
+                T *tx = qx + row0 * p.dx.token, *tr = qr + row0 * p.dr.token, *ti = kGate ? qi + row0 * p.di.token : nullptr;
+                branch((kStaged || kSmall) && plain, [&](auto is_plain) {
+                    constexpr bool kPlain = decltype(is_plain)::value;
 #pragma unroll
-                for (int j = 0; j < kTok; ++j) {
-                    if (!kPlain && kPacked && (st >> j & 1)) hp = p.init ? k.get(p.init + seq(j) * p.C) : zero;
-                    const V x = Word<T>::unpack(in.word(slot, 0, j)), pi = plus(er[j], 1.f);
-                    V sr, si, ci, u = x;
-                    if (kGate) {
-                        const V ei = exp_neg(bounded(kd, in.word(slot, kTensors - 1, j))), pr = plus(ei, 1.f);
-                        const V R = each(mul2(pr, pi), hw_rcp);
-                        sr = mul2(pr, R);
-                        si = mul2(pi, R);
-                        ci = mul2(ei, si);
-                        u = mul2(x, si);
-                    } else {
-                        sr = kLerp ? n[j] : each(pi, hw_rcp);
-                    }
-                    const V aj = a(j), cr = mul2(er[j], sr);
-                    V w, dr, dl;
-                    if (kLerp) {
-                        w = cr;
-                        dl = dr = mul2(mul2(g[j], minus(hp, u)), mul2(aj, w));
-                    } else {
-                        // with t = -log a: l dL/dl = g a t (u a / w - h)
-                        const V q = fma2(n[j], aj, n[j]), rs = each(q, hw_rsqrt), t = decay_of(sr, kd);
-                        w = mul2(q, rs);
-                        dl = mul2(mul2(mul2(g[j], aj), t), minus_fma(mul2(u, aj), rs, hp));
-                        dr = mul2(dl, cr);
-                    }
-                    hp = fma2(aj, hp, mul2(w, u));
-                    const V du = mul2(g[j], w), dx = kGate ? mul2(du, si) : du;
-                    if (kPlain || live(j)) {
-                        sum = add2(sum, dl);
-                        if (k.ok) {
-                            k.store(tx + j * p.dx.token, dx);
-                            k.store(tr + j * p.dr.token, dr);
-                            if (kGate) k.store(ti + j * p.di.token, mul2(mul2(dx, x), ci));
+                    for (int j = 0; j < kTok; ++j) {
+                        if (!kPlain && kPacked && (st >> j & 1)) hp = p.init ? k.get(p.init + seq(j) * p.C) : zero;
+                        const V x = Word<T>::unpack(in.word(slot, 0, j)), pi = plus(kGate ? er[j] : apart(er[j]), 1.f);
+                        V sr, si, ci, u = x;
+                        if (kGate) {
+                            const V ei = exp_neg(bounded(kd, in.word(slot, kTensors - 1, j))), pr = plus(ei, 1.f);
+                            const V R = each(mul2(pr, pi), hw_rcp);
+                            sr = mul2(pr, R);
+                            si = mul2(pi, R);
+                            ci = mul2(ei, si);
+                            u = mul2(x, si);
+                        } else {
+                            sr = kLerp ? c[j] : each(pi, hw_rcp);
+                        }
+                        const V aj = a(j), cr = mul2(er[j], sr);
+                        V w, dr, dl;
+                        if (kLerp) {
+                            w = cr;
+                            dl = dr = mul2(mul2(g[j], minus(hp, u)), mul2(aj, w));
+                        } else {
+                            // with t = -log a: l dL/dl = g a t (u a / w - h)
+                            const V t = decay_of(sr, kd), n = kSmall ? c[j] : n_of<kSmall>(t, aj);
+                            const V q = fma2(n, aj, n), rs = each(q, hw_rsqrt);
+                            w = mul2(q, rs);
+                            dl = mul2(mul2(mul2(g[j], aj), t), minus_fma(mul2(u, aj), rs, hp));
+                            dr = mul2(dl, cr);
+                        }
+                        hp = fma2(aj, hp, mul2(w, u));
+                        const V du = mul2(g[j], w), dx = kGate ? mul2(du, si) : du;
+                        if (kPlain || live(j)) {
+                            sum = add2(sum, dl);
+                            if (k.ok) {
+                                k.store(tx + j * p.dx.token, dx);
+                                k.store(tr + j * p.dr.token, dr);
+                                if (kGate) k.store(ti + j * p.di.token, mul2(mul2(dx, x), ci));
+                            }
                         }
                     }
-                }
-            });
-            if (!kStaged) fetch(tile - ranks, 0);
-            slot = next;
-        }
+                });
+                if (!kStaged) fetch(tile - ranks, 0);
+                slot = next;
+            }
+        });
         in.template wait<0>();
         __syncthreads();        // the next sequence's rows, tiles and pairs
         if (!kPacked && steps == 0 && rank == 0 && warp == 0 && p.dinit)

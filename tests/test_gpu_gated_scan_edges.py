@@ -1,11 +1,12 @@
 """The gated recurrence where its arithmetic ends, element by element against the float64 definition: gates far from
-their bias. Tolerances, fixed before the first run, count units of 2^-24 and stand beside each test.
+their bias, strong decays. Tolerances, fixed before the first run, count units of 2^-24 and stand beside each test.
 """
 import math
 
 import pytest
 import torch
 
+from oracle import blocks as ob
 from state_space_sequence_mamba_b200 import binding as m3
 
 pytestmark = pytest.mark.gpu
@@ -65,3 +66,60 @@ def test_convex_gates_far_from_their_bias(cuda_dev, dtype, gate):
             close(g["ddecay"], dr.sum((0, 1)), 2 * float(rel.max()), B * floor, "ddecay")
             if gate:
                 close(g["di"], w * u * (1 - si), rel + half, floor, "di")
+
+
+def strengths(dtype):
+    """Channels whose -log a lies between 1e-3 and 20 side by side: d with 8 softplus(d) from 1e-3 to 24, and r of
+    three tokens of three sequences."""
+    k = torch.cat([torch.logspace(-2.9, math.log10(24.0), 53, dtype=torch.float64), torch.linspace(9.0, 24.0, 11, dtype=torch.float64)])
+    d = torch.log(torch.expm1(k / 8.0)).float()
+    g = torch.Generator().manual_seed(3)
+    return d, (0.3 + 1.2 * torch.rand(3, 3, len(d), generator=g)).to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("gate", [False, True])
+@pytest.mark.parametrize("packed", [False, True])
+def test_strong_decays_keep_their_digits(cuda_dev, dtype, gate, packed):
+    """Decays of e^-20 to 0.999 side by side: what is proportional to a decay is right relative to itself, element by
+    element (states carried over tokens without input, dr, ddecay, dinit), where all terms have one sign or one
+    dwarfs the other. t = -log a carries 16 units (softplus six, the sigmoid nine, a product one) and the argument of 2^x two,
+    so that a is off by 18 t + 6 units; three tokens have three of them, other factors of a result 40 in all."""
+    d, r = strengths(dtype)
+    b, L, C = r.shape
+    g = torch.Generator().manual_seed(4)
+    x = (0.5 + torch.rand(b, L, C, generator=g)).to(dtype)
+    i = torch.randn(b, L, C, generator=g).to(dtype) if gate else None
+    dy = (0.5 + torch.rand(b, L, C, generator=g)).to(dtype)
+    init = 1e4 * (1 + torch.rand(b, C, generator=g))
+    t = 8 * torch.nn.functional.softplus(d.double()) * torch.sigmoid(r.double())
+    rel = (18 * t.sum(1) + 3 * 6 + 40) * UNIT          # [b, C]
+    half = 2.0 ** -8 if dtype == BF else 0.0
+    lens = [L] * b if packed else None
+    lay = (lambda v: None if v is None else v.reshape(1, b * L, C).to(cuda_dev)) if packed else (lambda v: None if v is None else v.to(cuda_dev))
+    back = lambda v: v.reshape(b, L, C)  # noqa: E731
+    cu = torch.arange(0, b * L + 1, L, dtype=torch.int32, device=cuda_dev) if packed else None
+    kw = dict(init=init.to(cuda_dev), cu_seqlens=cu)
+    a = lay(x), lay(r), lay(i), d.to(cuda_dev)
+    none = (torch.zeros_like(a[0]), *a[1:])
+    y, fin, mk = m3.gated_scan_fwd(*none, marks=True, **kw)
+    torch.cuda.synchronize()
+    decay = torch.exp(-t)
+    carried = init.double()[:, None] * torch.cumprod(decay, 1)
+    close(back(y), carried, rel[:, None] + half, 0.0, "carried")
+    close(fin, carried[:, -1], rel, 0.0, "final")
+    st = init.to(cuda_dev)
+    for n in range(L):
+        tok = [None if v is None else v[:, n].to(cuda_dev) for v in (torch.zeros_like(x), r, i)]
+        _, st = m3.gated_scan_step(tok[0], tok[1], st, tok[2], a[3])
+    close(st, carried[:, -1], rel, 0.0, "steps")
+    flat = (lambda v: None if v is None else v.reshape(1, b * L, C)) if packed else (lambda v: v)
+    ref = ob.scan_gradients(flat(dy), flat(x), flat(r), flat(i), d, init=init, lens=lens)
+    y, fin, mk = m3.gated_scan_fwd(*a, marks=True, **kw)
+    for marks in (mk, None):
+        got = m3.gated_scan_bwd(lay(dy), *a, marks=marks, **kw)
+        torch.cuda.synchronize()
+        close(got["dinit"], ref[4], rel, 0.0, "dinit")
+        close(back(got["dr"]), ref[1].reshape(b, L, C), rel[:, None] + half, 0.0, "dr")
+        close(got["ddecay"], ref[3], rel.max(0).values, 0.0, "ddecay")
+        close(back(got["dx"]), ref[0].reshape(b, L, C), rel[:, None] + half, 0.0, "dx")
