@@ -123,3 +123,23 @@ def test_strong_decays_keep_their_digits(cuda_dev, dtype, gate, packed):
         close(back(got["dr"]), ref[1].reshape(b, L, C), rel[:, None] + half, 0.0, "dr")
         close(got["ddecay"], ref[3], rel.max(0).values, 0.0, "ddecay")
         close(back(got["dx"]), ref[0].reshape(b, L, C), rel[:, None] + half, 0.0, "dx")
+
+
+def test_weights_on_both_sides_of_the_series_end(cuda_dev):
+    """w = sqrt(1 - a^2) of -log a from 0.01 to 4, where softplus(d) = d and sigmoid(r) = 1 to fp32 and the power is one of two:
+    -log a is exact but for 1 / x (two units, a product one). In units of w, the root halving what stands under it: -log a 1.5,
+    the series 1.4, 1 - a^2 from it 1, 1 / sqrt(x) 2.1, two products 2: 8. Beyond 1/8, 2^x is off by four units and its
+    argument's rounding by 1.2 t, of which a / (1 - a) reaches 1 - a, halved again, and one less a by a half: 24 at 1/8, 10 at 1."""
+    for power, lo, hi in ((2.0 ** -11, 20.5, 256.0), (2.0 ** -8, 32.0, 1024.0)):
+        d = torch.linspace(lo, hi, 40000)
+        t = d.double() * power
+        w = torch.sqrt(-torch.expm1(-2 * t))
+        a = torch.exp(-t)
+        rel = torch.where(t <= 0.125, 8.0, 8.5 + (4 + 1.2 * t) * a / (1 - a) / 2) * UNIT
+        one = torch.ones(1, 1, len(d), device=cuda_dev)
+        y, fin, _ = m3.gated_scan_fwd(one, 30 * one, None, d.to(cuda_dev), power=power)
+        ys, out = m3.gated_scan_step(one[0], 30 * one[0], torch.zeros(1, len(d), device=cuda_dev), None, d.to(cuda_dev), power=power)
+        g = m3.gated_scan_bwd(one, one, 30 * one, None, d.to(cuda_dev), power=power)    # dx = w
+        torch.cuda.synchronize()
+        for n, v in (("y", y[0]), ("final", fin), ("step", ys), ("state", out), ("dx", g["dx"][0])):
+            close(v, w[None], rel, 0.0, n)
