@@ -520,8 +520,8 @@ M3_API m3_status m3_gated_scan_bwd(const m3_gated_scan_dims* dims, const m3_gate
  * (M3_ROT_INVERSE: turned back, which is the gradient); the other dimensions are copied. Linear
  * attention with a constant decay knows positions by its decay alone; its layers turn q and k. The scan's
  * own rotation is data-dependent and part of it. freq: fp64 [rotdim / 2], radians per position, finite
- * (scaled as the layer was trained). The angle is exact to 2^-54 turns a position, sine and cosine to some
- * 1e-7; fp32 arithmetic, one rounding. */
+ * (scaled as the layer was trained). The angle is exact to 2^-54 turns a position (frequencies up to 2^40), sine
+ * and cosine to some 1e-7; fp32 arithmetic, one rounding. */
 #define M3_ROT_INTERLEAVED 1u
 #define M3_ROT_INVERSE 2u
 #define M3_ROT_POS64 4u         /* positions are int64, otherwise int32 */

@@ -5,6 +5,8 @@ Shares no code with the GPU path.
 """
 from __future__ import annotations
 
+from fractions import Fraction
+
 import torch
 
 
@@ -77,6 +79,14 @@ def scan_gradients(dy, x, r, i=None, decay=None, power=8.0, lerp=False, init=Non
 
 
 # ---------------------------------------------------------------- rotary positions
+
+TWO_PI = Fraction(6283185307179586476925286766559005768394338798750211641949889, 10 ** 60)
+
+
+def turns(freq, pos):
+    """pos * freq modulo one turn of a stored frequency (a double) and an integer position, exactly, in [0, 1)."""
+    return Fraction(freq) * pos / TWO_PI % 1
+
 
 def rotary(x, freq, positions, interleaved=False, inverse=False, scale=1.0):
     """x [..., L, heads, D] at positions [..., L] (one for each token), as complex numbers."""

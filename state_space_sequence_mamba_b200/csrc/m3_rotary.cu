@@ -6,7 +6,7 @@
 // pairs of one token and walks over up to eight heads, so the sines are formed once for them. Angles of far positions lose their
 // digits in fp32 (position 65 536 at one radian: 4e-3), so they are counted in turns, as 64-bit fractions:
 // freq / 2 pi modulo one, times 2^64, multiplied by the position modulo 2^64, is the angle
-// modulo one turn to 2^-54 turns a position, for any integer position, without a division. The top
+// modulo one turn to 2^-54 turns a position, for any integer position and frequencies up to 2^40, without a division. The top
 // 32 bits, reduced to an eighth of a turn either way, go through the series of sine and cosine.
 #include <cmath>
 #include <cstdarg>
@@ -40,7 +40,7 @@ struct RotParams {
     float scale, sign;
 };
 
-// sine and cosine of a 32-bit fraction of a turn. Up to pi / 4 the series' next terms are 2e-9 and 2e-9.
+// sine and cosine of a 32-bit fraction of a turn. Up to pi / 4 the series' next terms are 2e-9 and 1.2e-10.
 __device__ __forceinline__ float2 turn(uint32_t u) {
     const uint32_t q = (u + 0x20000000u) >> 30;
     const float t = static_cast<float>(static_cast<int32_t>(u - (q << 30))) * 1.4629180792671596e-9f;     // 2 pi / 2^32
@@ -125,9 +125,12 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
     __shared__ uint64_t s_turns[kMaxPairs];
     constexpr int kTwo = PP == 1 ? 1 : PP;      // elements of one of an item's two parts
     for (int j = threadIdx.x; j < p.rot / 2; j += kThreads) {
-        double t = p.freq[j] * 0.15915494309189535;
-        t -= floor(t);
-        s_turns[j] = static_cast<uint64_t>(t * 18446744073709551616.0);
+        // 1 / 2 pi in two parts, the whole turns taken off before the digits that the product lost are added
+        const double f = p.freq[j], whole = f * 0.15915494309189535;
+        const double lost = fma(f, -9.839338337591243e-18, fma(f, 0.15915494309189535, -whole));
+        double t = (whole - rint(whole)) + lost;
+        t -= rint(t);
+        s_turns[j] = static_cast<uint64_t>(__double2ll_rn(t * 18446744073709551616.0));     // (one half: saturates, 2^-64 off)
     }
     __syncthreads();
     const uint32_t idx = blockIdx.x * kThreads + threadIdx.x;
