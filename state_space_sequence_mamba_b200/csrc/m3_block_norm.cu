@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(block_threads<W>(), 512 / block_threads<W>()) 
             team.sum(a);
             if (p.pre != kNone) {
                 r2 = rsqrtf(fmaf(a[0], inv, p.eps));
-                k2 = -r2 * r2 * r2 * a[1] * inv;
+                k2 = -r2 * (r2 * (r2 * (a[1] * inv)));     // (r2^3 alone may leave fp32)
             }
             if (p.post != kNone) m1 = -(a[2] + (p.pre != kNone ? fmaf(r2, a[3], k2 * a[4]) : 0.f)) * inv * r1;
             next = a[5];
@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(block_threads<W>(), 512 / block_threads<W>()) 
             team.sum(a);
             if (p.pre != kNone) {
                 r2 = rsqrtf(fmaf(a[0], inv, p.eps));
-                k2 = -r2 * r2 * r2 * a[1] * inv;
+                k2 = -r2 * (r2 * (r2 * (a[1] * inv)));
                 if (p.pre == kLayerNorm) m2 = -r2 * a[6] * inv;
             }
             const bool pre = p.pre != kNone;
