@@ -181,6 +181,10 @@ template <bool kSmall>
 __device__ __forceinline__ float n_of(float t, float a) { return !kSmall && t > kSeries ? __fadd_rn(1.f, -a) : series(t); }
 template <bool kSmall>
 __device__ __forceinline__ float2 n_of(const float2& t, const float2& a) { return make_float2(n_of<kSmall>(t.x, a.x), n_of<kSmall>(t.y, a.y)); }
+// 1 / p from the hardware's, which leans by a quarter of 2^-24 where p is near one: a convex decay is that at every token, and
+// a memory of thousands adds it up. One step of Newton's leaves roundings alone.
+template <typename V>
+__device__ __forceinline__ V settled(const V& s, const V& p) { return fma2(s, less2(p, s, splat<V>(1.f)), s); }
 template <bool kLerp, typename V>
 __device__ __forceinline__ V exp_r(uint32_t rw, const V& k) {
     if (!kLerp) return exp_neg(bounded(k, rw));
@@ -200,7 +204,7 @@ __device__ __forceinline__ void gates(uint32_t rw, uint32_t iw, const V& x, cons
         sr = each(pi, hw_rcp);
     }
     if (kLerp) {
-        *a = sr;
+        *a = settled(sr, pi);
         *add = mul2(mul2(er, sr), u);
         return;
     }
@@ -724,8 +728,11 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) gs_bwd_kernel(const __grid_
 #pragma unroll
                 for (int j = 0; j < kTok; ++j) {
                     er[j] = exp_r<kLerp>(in.word(slot, 1, j), kd);
-                    c[j] = each(plus(er[j], 1.f), hw_rcp);
-                    if (!kLerp) {
+                    const V p = plus(er[j], 1.f);
+                    c[j] = each(p, hw_rcp);
+                    if (kLerp) {
+                        c[j] = settled(c[j], p);
+                    } else {
                         const V t = decay_of(c[j], kd), n = each(t, series);
                         c[j] = kSmall ? n : a_of<kSmall>(t, n);
                     }

@@ -143,3 +143,31 @@ def test_weights_on_both_sides_of_the_series_end(cuda_dev):
         torch.cuda.synchronize()
         for n, v in (("y", y[0]), ("final", fin), ("step", ys), ("state", out), ("dx", g["dx"][0])):
             close(v, w[None], rel, 0.0, n)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("lerp", [False, True])
+@pytest.mark.parametrize("gate", [False, True])
+def test_decays_near_one_lean_to_neither_side(cuda_dev, dtype, lerp, gate):
+    """What a decay is off by, on the mean over many: a long memory multiplies thousands of them. Roundings of a and of 1 + e^-v
+    lean to neither side: a mean of 2^17 of them, each below one unit, strays by 0.02 at most. What is off relative to 1 - a
+    (2^x, its argument, the sigmoid, the softplus: 16 units) may lean, but counts 1 - a alone, which is 0.001 and less."""
+    B, C = 32, 4096
+    g = torch.Generator().manual_seed(1)
+    u = 0.999 + 0.0009 * torch.rand(C, generator=g)
+    d = torch.logit(u) if lerp else torch.log(torch.expm1(-torch.log(u) / 8))
+    r = torch.randn(B, 1, C, generator=g).to(dtype)
+    i = torch.randn(B, 1, C, generator=g).to(dtype).to(cuda_dev) if gate else None
+    v = r.double()
+    a = (torch.sigmoid(v + d.double()) if lerp
+         else torch.exp(-8 * torch.nn.functional.softplus(d.double()) * torch.sigmoid(v)))[:, 0]
+    z = torch.zeros(B, 1, C, dtype=dtype, device=cuda_dev)
+    one = torch.ones(B, C, device=cuda_dev)
+    t = z, r.to(cuda_dev), i, d.to(cuda_dev)
+    _, fin, mk = m3.gated_scan_fwd(*t, lerp=lerp, init=one, marks=True)
+    _, out = m3.gated_scan_step(z[:, 0], t[1][:, 0], one, None if i is None else i[:, 0], t[3], lerp=lerp, state_out=torch.empty_like(one))
+    grads = m3.gated_scan_bwd(z, *t, lerp=lerp, init=one, dfinal=one, marks=mk)
+    torch.cuda.synchronize()
+    for name, got in (("final", fin), ("state", out), ("dinit", grads["dinit"])):
+        lean = float((got.double().cpu() - a).mean()) / UNIT
+        assert abs(lean) <= 0.02 + 16 * float((1 - a).mean()), (name, lean)
