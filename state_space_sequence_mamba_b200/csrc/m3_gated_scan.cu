@@ -5,10 +5,11 @@
 //     h_t = a_t h_{t-1} + w_t u_t,  u_t = sig(i_t) x_t
 // The floor is HBM's: the forward reads x, r, i and writes y once, the backward reads those and dy and writes
 // three gradients. bf16, 4 x 2048 x 4096: forward 72 us (0.57 of what a copy reaches), gradients 135 (0.53); one sequence of
-// 65 536 x 4096: forward 687 us (0.48). What bounds them is the issue of instructions: some 46 a channel and token
+// 65 536 x 4096: forward 687 us (0.48). What bounds a batch is the issue of instructions: some 46 a channel and token
 // forward, 90 backward (two exponentials, a reciprocal and a root among them, which keep that unit half busy), at three of
-// four a cycle; and 256 columns over 148 SMs leave an eighth of the device idle. Two tokens compose as (A, B) after (A', B') = (A A', A B' + B), so time is cut: a CTA takes a
-// tile of 8 tokens a warp by 32 words (a word: two bf16 channels or one of fp32), a thread eight tokens of one word.
+// four a cycle; and 256 columns over 148 SMs leave an eighth of the device idle. One sequence, in clusters, waits at the
+// meeting of every tile (issue at 61 % of what it could be, fp32 documents at 46 and 41). Two tokens compose as (A, B) after
+// (A', B') = (A A', A B' + B), so time is cut: a CTA takes a tile of 8 tokens a warp by 32 words (a word: two bf16 channels or one of fp32), a thread eight tokens of one word.
 // It reduces them to one (A, B) in registers, the warps' pairs are combined in order through shared memory, and
 // each thread then finishes its eight tokens; the next tile's loads are in flight meanwhile. Where columns of
 // channels are fewer than the device holds CTAs, the CTAs of a cluster take the tiles of a column in turn and exchange
