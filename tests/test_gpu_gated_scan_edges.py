@@ -125,6 +125,38 @@ def test_strong_decays_keep_their_digits(cuda_dev, dtype, gate, packed):
         close(back(got["dx"]), ref[0].reshape(b, L, C), rel[:, None] + half, 0.0, "dx")
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("gate", [False, True])
+@pytest.mark.parametrize("C", [64, 66, 67])
+@pytest.mark.parametrize("lens", [None, [150, 0, 1, 99]])
+def test_strong_decays_over_tiles_and_clusters(cuda_dev, dtype, gate, C, lens):
+    """The same over 250 tokens of channels that all decay by e^-8 to e^-16 a token, in rows of 16-byte words, of words and of neither: a state
+    is its last token's and h, what dr is proportional to, of one sign. 18 t + 6 units for a token's decay and 60 for the rest."""
+    b, L = (2, 250) if lens is None else (1, 250)
+    g = torch.Generator().manual_seed(C)
+    d = torch.linspace(2.0, 2.6, C)
+    r = (0.3 + 0.7 * torch.rand(b, L, C, generator=g)).to(dtype)
+    x, dy = ((0.5 + torch.rand(b, L, C, generator=g)).to(dtype) for _ in range(2))
+    i = torch.randn(b, L, C, generator=g).to(dtype) if gate else None
+    n = b if lens is None else len(lens)
+    init, dfinal = (0.5 + torch.rand(n, C, generator=g) for _ in range(2))
+    t = 8 * torch.nn.functional.softplus(d.double()) * torch.sigmoid(r.double())
+    assert 8 < float(t.min()) and float(t.max()) < 17
+    rel, half = (18 * t + 66) * UNIT, 2.0 ** -8 if dtype == BF else 0.0
+    up = lambda v: None if v is None else v.to(cuda_dev)  # noqa: E731
+    cu = None if lens is None else torch.tensor([0] + list(torch.tensor(lens).cumsum(0)), dtype=torch.int32, device=cuda_dev)
+    a, kw = (up(x), up(r), up(i), up(d)), dict(init=up(init), cu_seqlens=cu)
+    ref = ob.scan_gradients(dy, x, r, i, d, init=init, dfinal=dfinal, lens=lens)
+    _, _, mk = m3.gated_scan_fwd(*a, marks=True, **kw)
+    for marks in (mk, None):
+        got = m3.gated_scan_bwd(up(dy), *a, dfinal=up(dfinal), marks=marks, **kw)
+        torch.cuda.synchronize()
+        close(got["dx"], ref[0], rel + half, 0.0, "dx")
+        close(got["dr"], ref[1], rel + half, 0.0, "dr")
+        close(got["ddecay"], ref[3], float(rel.max()), 0.0, "ddecay")
+        close(got["dinit"], ref[4], float(rel.max()), 0.0, "dinit")
+
+
 def test_weights_on_both_sides_of_the_series_end(cuda_dev):
     """w = sqrt(1 - a^2) of -log a from 0.01 to 4, where softplus(d) = d and sigmoid(r) = 1 to fp32 and the power is one of two:
     -log a is exact but for 1 / x (two units, a product one). In units of w, the root halving what stands under it: -log a 1.5,
